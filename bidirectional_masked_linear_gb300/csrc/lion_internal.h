@@ -145,6 +145,22 @@ int reorder_bwd_launches(int mask_kind);
 cudaError_t launch_reordered_bwd(const Problem& p, const int* order, const float* dy, float* dq, float* dk, float* dv,
                                  float* dll, void* ws, int* status, cudaStream_t s);
 
+// The state space block (ssm_*.cu), on checked arguments; a workspace of the
+// queried size where one is taken.
+cudaError_t launch_layernorm_fwd(const lion_layernorm_args& a, cudaStream_t s);
+size_t layernorm_bwd_workspace_bytes(int rows, int cols);
+cudaError_t launch_layernorm_bwd(const lion_layernorm_bwd_args& a, void* ws, cudaStream_t s);
+cudaError_t launch_conv_fwd(const lion_conv_args& a, cudaStream_t s);
+size_t conv_bwd_workspace_bytes(int B, int L, int D, int K);
+cudaError_t launch_conv_bwd(const lion_conv_bwd_args& a, void* ws, cudaStream_t s);
+cudaError_t launch_conv_step(const void* x, void* state, const float* weight, const float* bias, void* y, int B, int D,
+                             int K, int act, int dtype, cudaStream_t s);
+size_t scan_workspace_bytes(int B, int L, int D, int N, int G);
+cudaError_t launch_scan_fwd(const lion_scan_args& a, void* ws, cudaStream_t s);
+size_t scan_bwd_workspace_bytes(int B, int L, int D, int N, int G, bool have_states);
+cudaError_t launch_scan_bwd(const lion_scan_bwd_args& a, void* ws, cudaStream_t s);
+cudaError_t launch_scan_step(const lion_scan_step_args& a, cudaStream_t s);
+
 // y (fp32, n values) rounded to nearest even bfloat16.
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, cudaStream_t s);
 

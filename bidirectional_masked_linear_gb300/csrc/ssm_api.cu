@@ -1,0 +1,216 @@
+// ssm_api.cu -- the C ABI of the state space block declared in include/lion.h:
+// argument checks, workspaces and the launches.
+#include <stdint.h>
+
+#include "../../include/lion.h"
+#include "lion_internal.h"
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool device_accessible(const void* p) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) return true;
+  return at.type == cudaMemoryTypeHost && at.devicePointer != nullptr;
+}
+
+bool need(const void* p, size_t a) { return p && aligned(p, a) && device_accessible(p); }
+bool maybe(const void* p, size_t a) { return !p || (aligned(p, a) && device_accessible(p)); }
+bool dtype_ok(int t) { return t == LION_DTYPE_BF16 || t == LION_DTYPE_FP32; }
+size_t esize(int t) { return t == LION_DTYPE_BF16 ? 2 : 4; }
+bool flag(int v) { return v == 0 || v == 1; }
+bool stride_ok(long long ld, long long width) { return ld == 0 || ld >= width; }
+
+constexpr long long kMaxGrid = 0x7fffffffLL;
+
+lion_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return LION_OK;
+  if (e == cudaErrorMemoryAllocation) return LION_ERR_NO_MEMORY;
+  return LION_ERR_CUDA;
+}
+
+// Runs `go(workspace)` on the caller's workspace or on a stream-ordered one.
+template <typename F>
+lion_status with_workspace(void* ws, size_t ws_bytes, size_t want, cudaStream_t s, F go) {
+  if (want == 0) return from_cuda(go(nullptr));
+  if (ws) {
+    if (!aligned(ws, 256) || !device_accessible(ws) || ws_bytes < want) return LION_ERR_INVALID_ARG;
+    return from_cuda(go(ws));
+  }
+  cudaError_t e = cudaMallocAsync(&ws, want, s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return from_cuda(e);
+  }
+  e = go(ws);
+  const cudaError_t f = cudaFreeAsync(ws, s);
+  return from_cuda(e != cudaSuccess ? e : f);
+}
+
+lion_status norm_sizes(int rows, int cols, long long x_row, int dtype) {
+  if (rows < 1 || cols < 1 || !dtype_ok(dtype) || !stride_ok(x_row, cols)) return LION_ERR_INVALID_ARG;
+  return cols > LION_LAYERNORM_MAX_COLS ? LION_ERR_UNSUPPORTED : LION_OK;
+}
+
+lion_status conv_sizes(int B, int L, int D, int K, int act, int reverse, int dtype, long long x_token) {
+  if (B < 1 || L < 1 || D < 1 || K < 1 || !dtype_ok(dtype) || !flag(reverse) || !stride_ok(x_token, D) ||
+      (act != LION_ACT_NONE && act != LION_ACT_SILU))
+    return LION_ERR_INVALID_ARG;
+  if (K < 2 || K > 4) return LION_ERR_UNSUPPORTED;
+  // a CTA for 128 vectors of channels of a run of tokens, on one grid axis
+  if ((long long)B * (L / 8 + 1) > kMaxGrid / (((long long)D + 7) / 8) * 128) return LION_ERR_UNSUPPORTED;
+  return LION_OK;
+}
+
+lion_status scan_sizes(int B, int L, int D, int N, int G, int softplus, int reverse, int dtype) {
+  if (B < 1 || L < 1 || D < 1 || N < 1 || G < 1 || D % G != 0 || !flag(softplus) || !flag(reverse) || !dtype_ok(dtype))
+    return LION_ERR_INVALID_ARG;
+  if (N != 8 && N != 16 && N != 32 && N != 64) return LION_ERR_UNSUPPORTED;
+  // CTAs on one grid axis, with as many segments as a sequence can have
+  if ((long long)B * G > kMaxGrid / ((long long)D / G + 1) / ((long long)L / 64 + 1)) return LION_ERR_UNSUPPORTED;
+  return LION_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lion_status lion_layernorm_fwd(const lion_layernorm_args* a) {
+  if (!a) return LION_ERR_INVALID_ARG;
+  const lion_status st = norm_sizes(a->rows, a->cols, a->x_row, a->dtype);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(a->dtype);
+  if (!need(a->x, es) || !need(a->weight, 4) || !maybe(a->bias, 4) || !need(a->y, es) || !maybe(a->mean, 4) ||
+      !maybe(a->rstd, 4) || !a->mean != !a->rstd || !(a->eps >= 0.f))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return from_cuda(lion::launch_layernorm_fwd(*a, a->stream));
+}
+
+size_t lion_layernorm_bwd_workspace_bytes(int rows, int cols) {
+  if (rows < 1 || cols < 1 || cols > LION_LAYERNORM_MAX_COLS) return 0;
+  return lion::layernorm_bwd_workspace_bytes(rows, cols);
+}
+
+lion_status lion_layernorm_bwd(const lion_layernorm_bwd_args* a) {
+  if (!a) return LION_ERR_INVALID_ARG;
+  const lion_status st = norm_sizes(a->rows, a->cols, a->x_row, a->dtype);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(a->dtype);
+  if (!need(a->dy, es) || !need(a->x, es) || !need(a->weight, 4) || !need(a->mean, 4) || !need(a->rstd, 4) ||
+      !need(a->dx, es) || !need(a->dweight, 4) || !maybe(a->dbias, 4))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return with_workspace(a->workspace, a->workspace_bytes, lion::layernorm_bwd_workspace_bytes(a->rows, a->cols),
+                        a->stream, [&](void* ws) { return lion::launch_layernorm_bwd(*a, ws, a->stream); });
+}
+
+lion_status lion_conv_fwd(const lion_conv_args* a) {
+  if (!a) return LION_ERR_INVALID_ARG;
+  const lion_status st = conv_sizes(a->B, a->L, a->D, a->K, a->act, a->reverse, a->dtype, a->x_token);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(a->dtype);
+  if (!need(a->x, es) || !need(a->weight, 4) || !maybe(a->bias, 4) || !maybe(a->state, es) || !maybe(a->lengths, 4) ||
+      !need(a->y, es) || !maybe(a->state_out, es) || (a->state && a->state_out == a->state))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return from_cuda(lion::launch_conv_fwd(*a, a->stream));
+}
+
+size_t lion_conv_bwd_workspace_bytes(int B, int L, int D, int K) {
+  if (conv_sizes(B, L, D, K, 0, 0, 0, 0) != LION_OK) return 0;
+  return lion::conv_bwd_workspace_bytes(B, L, D, K);
+}
+
+lion_status lion_conv_bwd(const lion_conv_bwd_args* a) {
+  if (!a) return LION_ERR_INVALID_ARG;
+  const lion_status st = conv_sizes(a->B, a->L, a->D, a->K, a->act, a->reverse, a->dtype, a->x_token);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(a->dtype);
+  if (!need(a->dy, es) || !need(a->x, es) || !need(a->weight, 4) || !maybe(a->bias, 4) || !maybe(a->state, es) ||
+      !maybe(a->lengths, 4) || !need(a->dx, es) || !need(a->dweight, 4) || !maybe(a->dbias, 4) ||
+      !maybe(a->dstate, es))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return with_workspace(a->workspace, a->workspace_bytes, lion::conv_bwd_workspace_bytes(a->B, a->L, a->D, a->K),
+                        a->stream, [&](void* ws) { return lion::launch_conv_bwd(*a, ws, a->stream); });
+}
+
+lion_status lion_conv_step(const void* x, void* state, const float* weight, const float* bias, void* y, int B, int D,
+                           int K, int act, int dtype, cudaStream_t stream) {
+  const lion_status st = conv_sizes(B, 1, D, K, act, 0, dtype, 0);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(dtype);
+  if (!need(x, es) || !need(state, es) || !need(weight, 4) || !maybe(bias, 4) || !need(y, es))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return from_cuda(lion::launch_conv_step(x, state, weight, bias, y, B, D, K, act, dtype, stream));
+}
+
+size_t lion_scan_workspace_bytes(int B, int L, int D, int N, int G) {
+  if (scan_sizes(B, L, D, N, G, 0, 0, 0) != LION_OK) return 0;
+  return lion::scan_workspace_bytes(B, L, D, N, G);
+}
+
+lion_status lion_scan_fwd(const lion_scan_args* a) {
+  if (!a) return LION_ERR_INVALID_ARG;
+  const lion_status st = scan_sizes(a->B, a->L, a->D, a->N, a->G, a->dt_softplus, a->reverse, a->dtype);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(a->dtype);
+  const long long gn = (long long)a->G * a->N;
+  if (!stride_ok(a->u_token, a->D) || !stride_ok(a->dt_token, a->D) || !stride_ok(a->z_token, a->D) ||
+      !stride_ok(a->b_token, gn) || !stride_ok(a->c_token, gn))
+    return LION_ERR_INVALID_ARG;
+  if (!need(a->u, es) || !need(a->dt, es) || !need(a->A, 16) || !need(a->Bm, es) || !need(a->Cm, es) ||
+      !maybe(a->Dskip, 4) || !maybe(a->z, es) || !maybe(a->dt_bias, 4) || !maybe(a->h0, 16) ||
+      !maybe(a->lengths, 4) || !need(a->out, es) || !maybe(a->h_out, 16) || !maybe(a->states, 16))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return with_workspace(a->workspace, a->workspace_bytes, lion::scan_workspace_bytes(a->B, a->L, a->D, a->N, a->G),
+                        a->stream, [&](void* ws) { return lion::launch_scan_fwd(*a, ws, a->stream); });
+}
+
+size_t lion_scan_bwd_workspace_bytes(int B, int L, int D, int N, int G, int have_states) {
+  if (scan_sizes(B, L, D, N, G, 0, 0, 0) != LION_OK) return 0;
+  return lion::scan_bwd_workspace_bytes(B, L, D, N, G, have_states != 0);
+}
+
+lion_status lion_scan_bwd(const lion_scan_bwd_args* a) {
+  if (!a) return LION_ERR_INVALID_ARG;
+  const lion_status st = scan_sizes(a->B, a->L, a->D, a->N, a->G, a->dt_softplus, a->reverse, a->dtype);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(a->dtype);
+  const long long gn = (long long)a->G * a->N;
+  if (!stride_ok(a->u_token, a->D) || !stride_ok(a->dt_token, a->D) || !stride_ok(a->z_token, a->D) ||
+      !stride_ok(a->b_token, gn) || !stride_ok(a->c_token, gn))
+    return LION_ERR_INVALID_ARG;
+  if (!need(a->dout, es) || !need(a->u, es) || !need(a->dt, es) || !need(a->A, 16) || !need(a->Bm, es) ||
+      !need(a->Cm, es) || !maybe(a->Dskip, 4) || !maybe(a->z, es) || !maybe(a->dt_bias, 4) || !maybe(a->h0, 16) ||
+      !maybe(a->lengths, 4) || !maybe(a->states, 16) || !need(a->du, es) || !need(a->ddt, es) || !need(a->dA, 16) ||
+      !need(a->dB, es) || !need(a->dC, es) || !maybe(a->dDskip, 4) || !maybe(a->dz, es) || !a->z != !a->dz ||
+      !maybe(a->ddt_bias, 4) || !maybe(a->dh0, 16))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return with_workspace(a->workspace, a->workspace_bytes,
+                        lion::scan_bwd_workspace_bytes(a->B, a->L, a->D, a->N, a->G, a->states != nullptr), a->stream,
+                        [&](void* ws) { return lion::launch_scan_bwd(*a, ws, a->stream); });
+}
+
+lion_status lion_scan_step(const lion_scan_step_args* a) {
+  if (!a) return LION_ERR_INVALID_ARG;
+  const lion_status st = scan_sizes(a->B, 1, a->D, a->N, a->G, a->dt_softplus, 0, a->dtype);
+  if (st == LION_ERR_INVALID_ARG) return st;
+  const size_t es = esize(a->dtype);
+  if (!need(a->h, 16) || !need(a->u, es) || !need(a->dt, es) || !need(a->A, 16) || !need(a->Bm, es) ||
+      !need(a->Cm, es) || !maybe(a->Dskip, 4) || !maybe(a->z, es) || !maybe(a->dt_bias, 4) || !need(a->out, es))
+    return LION_ERR_INVALID_ARG;
+  if (st != LION_OK) return st;
+  return from_cuda(lion::launch_scan_step(*a, a->stream));
+}
+
+}  // extern "C"

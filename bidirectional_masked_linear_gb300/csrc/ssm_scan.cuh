@@ -1,0 +1,173 @@
+// ssm_scan.cuh -- what the selective scan's kernels share.
+//
+//   h_i[n] = a_i[n] h_{i-1}[n] + b_i[n],  a = exp(delta A[n]),  b = delta u B[n]
+//
+// A CTA holds adjacent channels of one group and walks a segment of one
+// sequence in tiles of N tokens.  For the element-wise parts (loads, softplus,
+// gate, stores) a thread holds eight adjacent channels of one token of the
+// tile; for the recurrence it holds four adjacent states of two channels, so
+// that one read of B, C serves two channels, one read of delta serves four
+// states, and a sum over the states is log2(N/4) shuffle steps.  The two
+// meet in shared memory.
+#pragma once
+
+#include "lion_internal.h"
+#include "ssm_common.cuh"
+
+namespace lion {
+
+struct ScanP {
+  const void* u;
+  const void* dt;
+  const void* z;
+  const void* Bm;
+  const void* Cm;
+  const void* dout;
+  const float* A;
+  const float* Dskip;
+  const float* dt_bias;
+  const float* h0;
+  const int* lengths;
+  void* out;
+  float* h_out;
+  float* states;        // [B][nst][D][N]
+  // gradients
+  void* du;
+  void* ddt;
+  void* dz;
+  float* dh0;
+  float* part_bc;       // [channel block of a group][B][L][G][2][N]
+  float* part_par;      // [B * nseg][D*N | D | D], rows padded to four
+  // segments
+  float* seg_state;     // [B][nseg][D][N]: a segment's own contribution to the state that leaves it
+  float* seg_sum;       // [B][nseg][D]: its sum of delta
+  long long u_ld, dt_ld, z_ld, b_ld, c_ld;
+  int B, L, D, N, G, Dg;
+  int nblk, nseg, seglen, nst;
+  int softplus, reverse;
+  bool u_wide, dt_wide, z_wide, o_wide, d_wide;   // o: tight activations, d: dout
+};
+
+namespace {
+
+// LN lanes hold the N = 4 LN states of a channel.
+template <int LN_, int W_>
+struct ScanTile {
+  static constexpr int LN = LN_, W = W_;
+  static constexpr int N = 4 * LN;
+  static constexpr int LC = 32 / LN;        // channel lanes of a warp
+  static constexpr int CW = 2 * LC;         // channels of a warp
+  static constexpr int CB = W * CW;         // channels of a CTA
+  static constexpr int TT = N;              // tokens of a tile: eight elements a thread
+  static constexpr int NT = 32 * W;
+  static constexpr int VPT = CB / 8;        // vectors of a token
+  static constexpr int SLOT = CB + CB / 8;  // a token's row of per-channel slots, one slot of padding after eight:
+                                            // the element threads' 16-byte accesses then start on different banks
+  static_assert(TT * CB == 8 * NT, "eight elements a thread");
+};
+__device__ __forceinline__ int slot_of(int c) { return c + (c >> 3); }
+
+
+// A CTA's place: channel block, segment and sequence.
+struct ScanAt {
+  int g, blk, seg, b;
+  int d0;       // first channel within D
+  int nch;      // channels of the block
+  int i0, i1;   // processing indices of the segment
+  int v0, v1;   // processing indices with a token
+};
+__device__ __forceinline__ ScanAt scan_at(const ScanP& p, int CB) {
+  ScanAt w;
+  unsigned x = blockIdx.x;
+  w.blk = x % p.nblk;
+  x /= p.nblk;
+  w.g = x % p.G;
+  x /= p.G;
+  w.seg = x % p.nseg;
+  w.b = x / p.nseg;
+  w.d0 = w.g * p.Dg + w.blk * CB;
+  w.nch = min(CB, p.Dg - w.blk * CB);
+  w.i0 = w.seg * p.seglen;
+  w.i1 = min(p.L, w.i0 + p.seglen);
+  const int len = p.lengths ? min(max(p.lengths[w.b], 0), p.L) : p.L;
+  w.v0 = p.reverse ? p.L - len : 0;
+  w.v1 = p.reverse ? p.L : len;
+  return w;
+}
+__device__ __forceinline__ int token_of(const ScanP& p, int i) { return p.reverse ? p.L - 1 - i : i; }
+
+// B or C of a tile's tokens as fp32 rows of N (tokens outside [v0, v1): 0).
+template <typename T, int N, int TT, int NT>
+__device__ __forceinline__ void load_bc(const ScanP& p, const ScanAt& w, const void* src, long long ld, int i0,
+                                        float* dst) {
+#pragma unroll 4
+  for (int k = threadIdx.x; k < TT * N; k += NT) {
+    const int i = i0 + k / N;
+    float v = 0.f;
+    if (i >= w.v0 && i < w.v1 && i < w.i1)
+      v = to_f32(static_cast<const T*>(src)[((long long)w.b * p.L + token_of(p, i)) * ld + w.g * N + k % N]);
+    dst[k] = v;
+  }
+}
+
+// The state's four values of a channel, or of the decays (scaled by log2 e).
+__device__ __forceinline__ void load_pair(const float* src, bool there, f2 (&v)[2], float scale = 1.f) {
+  const float4 x = there ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+  v[0] = pack2(x.x * scale, x.y * scale);
+  v[1] = pack2(x.z * scale, x.w * scale);
+}
+__device__ __forceinline__ void store_pair(float* dst, const f2 (&v)[2]) {
+  const float2 a = unpack2(v[0]), b = unpack2(v[1]);
+  *reinterpret_cast<float4*>(dst) = make_float4(a.x, a.y, b.x, b.y);
+}
+
+// The sums over the LN lanes of a channel of V = LN values, the k-th left in
+// the lane whose place is k: each step halves the values that a lane carries.
+template <int LN>
+__device__ __forceinline__ float sum_states(float (&v)[LN], int ln) {
+#pragma unroll
+  for (int w = LN / 2; w >= 1; w /= 2) {
+    const bool up = ln & w;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+    }
+  }
+  return v[0];
+}
+
+// delta of eight channels from the step sizes read.
+__device__ __forceinline__ void deltas(const ScanP& p, int d, int n, float (&dt)[8], float (&raw)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    raw[e] = p.dt_bias && e < n ? dt[e] + p.dt_bias[d + e] : dt[e];
+    dt[e] = e < n ? (p.softplus ? softplus(raw[e]) : raw[e]) : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+#define LION_SCAN_DISPATCH(RUN, dtype, N, ...)                                        \
+  (dtype == DT_BF16 ? (N == 8    ? RUN<__nv_bfloat16, 2>(__VA_ARGS__)                 \
+                       : N == 16 ? RUN<__nv_bfloat16, 4>(__VA_ARGS__)                 \
+                       : N == 32 ? RUN<__nv_bfloat16, 8>(__VA_ARGS__)                 \
+                                 : RUN<__nv_bfloat16, 16>(__VA_ARGS__))               \
+                    : (N == 8    ? RUN<float, 2>(__VA_ARGS__)                         \
+                       : N == 16 ? RUN<float, 4>(__VA_ARGS__)                         \
+                       : N == 32 ? RUN<float, 8>(__VA_ARGS__)                         \
+                                 : RUN<float, 16>(__VA_ARGS__)))
+
+inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+inline int scan_channels(int N, int W) { return W * 2 * 32 / (N / 4); }
+
+}  // namespace
+
+// Segments of a sequence for kernels whose CTAs hold `cb` channels.
+struct ScanPlan {
+  int nblk, nseg, seglen;
+};
+void fill_scan(ScanP& p, const lion_scan_args& a);   // everything but the plan and the workspace
+ScanPlan scan_plan(int B, int L, int D, int N, int G, int W);
+
+}  // namespace lion

@@ -404,6 +404,254 @@ lion_status lion_attn_bwd_reordered(const lion_reorder_bwd_args* a);
 size_t lion_attn_reordered_bwd_workspace_bytes(int B, int H, int L, int d);
 
 /*
+ * The state space block beside the attention operator: layer norm, a short
+ * causal depthwise convolution and the selective scan with a decay per
+ * channel and state (the diagonal form, of which the operator's lambda is the
+ * scalar one: rebuttal page, "scalar version of Lambda_i").  Conventions of
+ * these entry points, besides those above:
+ *   - Activations are token-major: [B][L][D] (a batch row per sequence, then
+ *     the token, then the channel), in `dtype` (BF16 or FP32); parameters,
+ *     states and their gradients are float32.  Arithmetic and every sum are
+ *     float32; a bfloat16 result is rounded once, to nearest even.
+ *   - A field `*_token` is the distance in elements between a tensor's tokens,
+ *     0 for the tight one (so an input may be a slice of a wider projection's
+ *     output); a sequence starts L tokens after the one before it.
+ *     Activations and vectors need the alignment of their elements only
+ *     (16-byte aligned rows take the wide loads); A, dA and the float32
+ *     states h, h0, h_out, states and dh0 are 16-byte aligned.
+ *   - lengths: NULL, or device int32 [B]: only the first lengths[b] tokens of
+ *     sequence b exist (values outside 0..L are clamped into it).  The rest
+ *     is not used: it advances no state, its outputs and gradients are 0.
+ *   - reverse: 0 walks a sequence from its first token, 1 from its last one
+ *     (the second direction of a bidirectional block).
+ *   - Outputs must not overlap inputs or each other.  No entry point reduces
+ *     with atomics: the same call gives the same bits.
+ *   - workspace: device, 256-byte aligned, of the queried size, or NULL for a
+ *     stream-ordered allocation.
+ */
+
+/* Largest row lion_layernorm_* take. */
+#define LION_LAYERNORM_MAX_COLS 16384
+
+/*
+ * lion_layernorm_fwd -- y = (x - mean) * rstd * weight + bias over each row's
+ * `cols` values, rstd = 1 / sqrt(var + eps) with the biased variance.
+ *   x      rows of `cols` values, x_row elements apart (0: cols).
+ *   weight [cols]; bias [cols] or NULL; y [rows][cols] in dtype.
+ *   mean, rstd  [rows] float32 out, for the gradients (both or neither NULL).
+ * cols > LION_LAYERNORM_MAX_COLS: LION_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  const void* x;
+  const float* weight;
+  const float* bias;
+  void* y;
+  float* mean;
+  float* rstd;
+  long long x_row;
+  int rows, cols;
+  float eps;                 /* >= 0 */
+  int dtype;                 /* lion_dtype of x and y */
+  cudaStream_t stream;
+} lion_layernorm_args;
+lion_status lion_layernorm_fwd(const lion_layernorm_args* a);
+
+/*
+ * lion_layernorm_bwd -- with xh = (x - mean) rstd and g = weight dy:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)),  dweight = sum_rows dy xh,
+ *   dbias = sum_rows dy.
+ *   dy [rows][cols] and dx [rows][cols] in dtype; mean, rstd from the forward;
+ *   dweight [cols], dbias [cols] or NULL, float32.
+ */
+typedef struct {
+  const void* dy;
+  const void* x;
+  const float* weight;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  float* dweight;
+  float* dbias;
+  long long x_row;
+  int rows, cols;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} lion_layernorm_bwd_args;
+lion_status lion_layernorm_bwd(const lion_layernorm_bwd_args* a);
+size_t lion_layernorm_bwd_workspace_bytes(int rows, int cols);
+
+typedef enum { LION_ACT_NONE = 0, LION_ACT_SILU = 1 } lion_act;
+
+/*
+ * lion_conv_fwd -- causal depthwise convolution of width K along the tokens,
+ * in the order they are walked (i counts processed tokens):
+ *   y_i = act(bias + sum_{j < K} weight[c][K-1-j] x_{i-j}).
+ *   x [B][L][D]; weight [D][K]; bias [D] or NULL; y [B][L][D]; K in {2, 3, 4}
+ *   (else LION_ERR_UNSUPPORTED); act: lion_act.
+ *   state      [B][K-1][D] in dtype: the K-1 inputs before the first token,
+ *              oldest first, or NULL for zeros.
+ *   state_out  [B][K-1][D]: the last K-1 inputs, to go on from, or NULL.  May
+ *              not be `state` itself.
+ */
+typedef struct {
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const void* state;
+  const int* lengths;
+  void* y;
+  void* state_out;
+  long long x_token;
+  int B, L, D, K;
+  int act;
+  int reverse;
+  int dtype;
+  cudaStream_t stream;
+} lion_conv_args;
+lion_status lion_conv_fwd(const lion_conv_args* a);
+
+/*
+ * lion_conv_bwd -- gradients of a loss through lion_conv_fwd's y, given dy
+ * ([B][L][D] in dtype): dx [B][L][D] and dstate [B][K-1][D] (or NULL) in
+ * dtype, dweight [D][K] and dbias [D] (or NULL) float32.
+ */
+typedef struct {
+  const void* dy;
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const void* state;
+  const int* lengths;
+  void* dx;
+  float* dweight;
+  float* dbias;
+  void* dstate;
+  long long x_token;
+  int B, L, D, K;
+  int act;
+  int reverse;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} lion_conv_bwd_args;
+lion_status lion_conv_bwd(const lion_conv_bwd_args* a);
+size_t lion_conv_bwd_workspace_bytes(int B, int L, int D, int K);
+
+/*
+ * lion_conv_step -- one token: x [B][D] -> y [B][D], the window in state
+ * [B][K-1][D] moved on in place.  Arguments as lion_conv_fwd.
+ */
+lion_status lion_conv_step(const void* x, void* state, const float* weight, const float* bias, void* y, int B, int D,
+                           int K, int act, int dtype, cudaStream_t stream);
+
+/*
+ * lion_scan_fwd -- the selective scan.  Per sequence and channel c of group
+ * g = c / (D / G), over the states n < N:
+ *   delta_t = softplus(dt_t + dt_bias)  (dt_softplus = 0: dt_t + dt_bias)
+ *   h_t[n]  = exp(delta_t A[c][n]) h_{t-1}[n] + delta_t u_t B_t[g][n]
+ *   out_t   = (sum_n C_t[g][n] h_t[n] + Dskip[c] u_t) silu(z_t)
+ *   u, dt, z  [B][L][D] (z NULL: no gate);  B, C  [B][L][G][N];  A [D][N];
+ *   Dskip, dt_bias [D] or NULL;  h0 [B][D][N] or NULL for zeros.
+ *   out [B][L][D];  h_out [B][D][N] or NULL: the state after the last token.
+ *   states [B][ceil(L/N)][D][N] float32 or NULL: the state before every N-th
+ *   processed token, which spares lion_scan_bwd the recomputation.
+ *   N in {8, 16, 32, 64} (else LION_ERR_UNSUPPORTED), G divides D.
+ */
+typedef struct {
+  const void* u;
+  const void* dt;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dskip;
+  const void* z;
+  const float* dt_bias;
+  const float* h0;
+  const int* lengths;
+  void* out;
+  float* h_out;
+  float* states;
+  long long u_token, dt_token, z_token, b_token, c_token;
+  int B, L, D, N, G;
+  int dt_softplus;
+  int reverse;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} lion_scan_args;
+lion_status lion_scan_fwd(const lion_scan_args* a);
+size_t lion_scan_workspace_bytes(int B, int L, int D, int N, int G);
+
+/*
+ * lion_scan_bwd -- gradients of a loss through lion_scan_fwd's out, given
+ * dout [B][L][D] in dtype.  Inputs as the forward's; states: the forward's
+ * (NULL: recomputed in the workspace).
+ *   du, ddt, dz [B][L][D] and dB, dC [B][L][G][N] in dtype, tight; dA [D][N],
+ *   dDskip, ddt_bias [D], dh0 [B][D][N] float32.  dz is given with z;
+ *   dDskip, ddt_bias and dh0 may be NULL, the others not.
+ */
+typedef struct {
+  const void* dout;
+  const void* u;
+  const void* dt;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dskip;
+  const void* z;
+  const float* dt_bias;
+  const float* h0;
+  const int* lengths;
+  const float* states;
+  void* du;
+  void* ddt;
+  float* dA;
+  void* dB;
+  void* dC;
+  float* dDskip;
+  void* dz;
+  float* ddt_bias;
+  float* dh0;
+  long long u_token, dt_token, z_token, b_token, c_token;
+  int B, L, D, N, G;
+  int dt_softplus;
+  int reverse;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} lion_scan_bwd_args;
+lion_status lion_scan_bwd(const lion_scan_bwd_args* a);
+/* have_states: 1 if the call passes the forward's states. */
+size_t lion_scan_bwd_workspace_bytes(int B, int L, int D, int N, int G, int have_states);
+
+/*
+ * lion_scan_step -- one token: u, dt, z, out [B][D], B, C [B][G][N], all
+ * tight, the state h [B][D][N] updated in place.
+ */
+typedef struct {
+  float* h;
+  const void* u;
+  const void* dt;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dskip;
+  const void* z;
+  const float* dt_bias;
+  void* out;
+  int B, D, N, G;
+  int dt_softplus;
+  int dtype;
+  cudaStream_t stream;
+} lion_scan_step_args;
+lion_status lion_scan_step(const lion_scan_step_args* a);
+
+/*
  * Testing aids for the bound on device-side waits (no counterpart in the
  * pages; not needed in normal use).
  * lion_debug_set_wait_cycles -- the bound, in SM clock cycles, on every
