@@ -87,52 +87,16 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// log(1 + e) for e in [0, 1] as 2 artanh(s), s = e / (2 + e) <= 1/3, by
-// artanh's power series: the first term left out is below 2e-8 of the sum, and
-// a small e keeps its relative accuracy.
-__device__ __forceinline__ float log1p_unit(float e) {
-  const float s = __fdividef(e, 2.f + e), q = s * s;
-  float r = 1.f / 13.f;
-  r = fmaf(r, q, 1.f / 11.f);
-  r = fmaf(r, q, 1.f / 9.f);
-  r = fmaf(r, q, 1.f / 7.f);
-  r = fmaf(r, q, 1.f / 5.f);
-  r = fmaf(r, q, 1.f / 3.f);
-  r = fmaf(r, q, 1.f);
-  return 2.f * s * r;
-}
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1p_unit(__expf(-fabsf(x))); }
-
 // ---------------------------------------------------------------- fp32 pairs
 
 // Two fp32 values in one 64-bit register: an instruction issues for both, at
 // the same rate of values, which leaves issue slots for everything else.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(f2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+typedef float2 f2;
+__device__ __forceinline__ f2 pack2(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ float2 unpack2(f2 x) { return x; }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ f2 ex2_2(f2 x) {
   const float2 v = unpack2(x);
   return pack2(ex2(v.x), ex2(v.y));
@@ -140,6 +104,33 @@ __device__ __forceinline__ f2 ex2_2(f2 x) {
 __device__ __forceinline__ float sum2(f2 x) {
   const float2 v = unpack2(x);
   return v.x + v.y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|).  With s = e / (2 + e)
+// <= 1/3 the logarithm is 2 artanh(s) = s P(s^2), P fitted to the series in
+// the Chebyshev sense on [0, 1/9] to 8e-9 of the result, so that a small e
+// keeps its relative accuracy.
+__device__ __forceinline__ f2 softplus2(float x0, float x1) {
+  const f2 e = pack2(ex2(fabsf(x0) * -kLog2e), ex2(fabsf(x1) * -kLog2e));
+  const float2 den = unpack2(add2(e, pack2(2.f, 2.f)));
+  const f2 s = mul2(e, pack2(rcp(den.x), rcp(den.y))), q = mul2(s, s);
+  f2 r = fma2(q, pack2(0.2817465663f, 0.2817465663f), pack2(0.2796141803f, 0.2796141803f));
+  r = fma2(r, q, pack2(0.4002485275f, 0.4002485275f));
+  r = fma2(r, q, pack2(0.6666631699f, 0.6666631699f));
+  r = fma2(r, q, pack2(2.f, 2.f));
+  return fma2(s, r, pack2(fmaxf(x0, 0.f), fmaxf(x1, 0.f)));
+}
+__device__ __forceinline__ float softplus(float x) { return unpack2(softplus2(x, 0.f)).x; }
+
+// z sigmoid(z) of a pair, times o.
+__device__ __forceinline__ f2 gate2(f2 o, float z0, float z1) {
+  const float2 d = unpack2(add2(pack2(ex2(z0 * -kLog2e), ex2(z1 * -kLog2e)), pack2(1.f, 1.f)));
+  return mul2(mul2(o, pack2(z0, z1)), pack2(rcp(d.x), rcp(d.y)));
 }
 
 // Whether rows of es-byte elements, `stride` elements apart, all start on 16 bytes.

@@ -39,13 +39,14 @@ struct ScanP {
   float* part_bc;       // [channel block of a group][B][L][G][2][N]
   float* part_par;      // [B * nseg][D*N | D | D], rows padded to four
   // segments
-  float* seg_state;     // [B][nseg][D][N]: a segment's own contribution to the state that leaves it
+  float* seg_state;     // [B][nseg][D][N]: a segment's own contribution to the state that leaves it, then
+                        // (chained) the state that enters it
   float* seg_sum;       // [B][nseg][D]: its sum of delta
   long long u_ld, dt_ld, z_ld, b_ld, c_ld;
   int B, L, D, N, G, Dg;
   int nblk, nseg, seglen, nst;
   int softplus, reverse;
-  bool u_wide, dt_wide, z_wide, o_wide, d_wide;   // o: tight activations, d: dout
+  bool u_wide, dt_wide, z_wide, b_wide, c_wide, o_wide, d_wide;   // o: tight activations, d: dout
 };
 
 namespace {
@@ -123,15 +124,16 @@ __device__ __forceinline__ void store_pair(float* dst, const f2 (&v)[2]) {
 
 // The sums over the LN lanes of a channel of V = LN values, the k-th left in
 // the lane whose place is k: each step halves the values that a lane carries.
+// `step`: the distance between neighbouring places in lanes.
 template <int LN>
-__device__ __forceinline__ float sum_states(float (&v)[LN], int ln) {
+__device__ __forceinline__ float sum_states(float (&v)[LN], int ln, int step = 1) {
 #pragma unroll
   for (int w = LN / 2; w >= 1; w /= 2) {
     const bool up = ln & w;
 #pragma unroll
     for (int i = 0; i < w; ++i) {
       const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w * step);
     }
   }
   return v[0];
@@ -149,14 +151,14 @@ __device__ __forceinline__ void deltas(const ScanP& p, int d, int n, float (&dt)
 // ---------------------------------------------------------------- host side
 
 #define LION_SCAN_DISPATCH(RUN, dtype, N, ...)                                        \
-  (dtype == DT_BF16 ? (N == 8    ? RUN<__nv_bfloat16, 2>(__VA_ARGS__)                 \
-                       : N == 16 ? RUN<__nv_bfloat16, 4>(__VA_ARGS__)                 \
-                       : N == 32 ? RUN<__nv_bfloat16, 8>(__VA_ARGS__)                 \
-                                 : RUN<__nv_bfloat16, 16>(__VA_ARGS__))               \
-                    : (N == 8    ? RUN<float, 2>(__VA_ARGS__)                         \
-                       : N == 16 ? RUN<float, 4>(__VA_ARGS__)                         \
-                       : N == 32 ? RUN<float, 8>(__VA_ARGS__)                         \
-                                 : RUN<float, 16>(__VA_ARGS__)))
+  (dtype == DT_BF16 ? (N == 8    ? RUN<__nv_bfloat16, 8>(__VA_ARGS__)                 \
+                       : N == 16 ? RUN<__nv_bfloat16, 16>(__VA_ARGS__)                \
+                       : N == 32 ? RUN<__nv_bfloat16, 32>(__VA_ARGS__)                \
+                                 : RUN<__nv_bfloat16, 64>(__VA_ARGS__))               \
+                    : (N == 8    ? RUN<float, 8>(__VA_ARGS__)                         \
+                       : N == 16 ? RUN<float, 16>(__VA_ARGS__)                        \
+                       : N == 32 ? RUN<float, 32>(__VA_ARGS__)                        \
+                                 : RUN<float, 64>(__VA_ARGS__)))
 
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline int scan_channels(int N, int W) { return W * 2 * 32 / (N / 4); }
@@ -168,6 +170,7 @@ struct ScanPlan {
   int nblk, nseg, seglen;
 };
 void fill_scan(ScanP& p, const lion_scan_args& a);   // everything but the plan and the workspace
-ScanPlan scan_plan(int B, int L, int D, int N, int G, int W);
+ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int warps, long long enough, long long want);
+cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cudaStream_t s);
 
 }  // namespace lion

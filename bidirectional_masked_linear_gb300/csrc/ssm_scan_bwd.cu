@@ -31,26 +31,6 @@ struct BwdSmem {
   float red[W * kSub * 2 * S::N];             // dB, dC of a sub-block, one part a warp
 };
 
-// What the segments after this one pass back into it (0 behind the last).
-template <int LN, int W>
-__device__ __forceinline__ void enter_back(const ScanP& p, const ScanAt& w, const int (&d)[2], const bool (&live)[2],
-                                           int n0, const f2 (&A)[2][2], f2 (&g)[2][2]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    g[k][0] = g[k][1] = pack2(0.f, 0.f);
-#pragma unroll 4
-    for (int s = p.nseg - 1; s > w.seg; --s) {
-      const size_t at = ((size_t)w.b * p.nseg + s) * p.D + d[k];
-      f2 own[2];
-      load_pair(p.seg_state + at * p.N + n0, live[k], own);
-      const float sum = live[k] ? p.seg_sum[at] : 0.f;
-      const f2 s2 = pack2(sum, sum);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) g[k][q] = fma2(ex2_2(mul2(s2, A[k][q])), g[k][q], own[q]);
-    }
-  }
-}
-
 // A segment's own contribution to what it passes back, and its sum of delta.
 template <typename T, int LN, int W>
 __global__ void __launch_bounds__(32 * W) scan_bwd_segment_kernel(ScanP p) {
@@ -148,7 +128,9 @@ __global__ void __launch_bounds__(32 * W) scan_bwd_kernel(ScanP p) {
     load_pair(p.A + (size_t)d[k] * N + 4 * ln, live[k], A[k], kLog2e);
     dA[k][0] = dA[k][1] = pack2(0.f, 0.f);
   }
-  enter_back<LN, W>(p, w, d, live, 4 * ln, A, g);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)   // what the segments after this one pass back into it
+    load_pair(p.seg_state + (((size_t)w.b * p.nseg + w.seg) * p.D + d[k]) * N + 4 * ln, live[k] && p.nseg > 1, g[k]);
   float skip[8], dskip[8], dbias[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -400,8 +382,9 @@ struct BwdW {
   static constexpr int W = kBwdWarps;
 };
 
-template <typename T, int LN>
+template <typename T, int N>
 cudaError_t run_bwd(const ScanP& p, cudaStream_t s) {
+  constexpr int LN = N / 4;
   constexpr int W = BwdW<LN>::W;
   using S = ScanTile<LN, W>;
   const unsigned ctas = (unsigned)p.nblk * p.G * p.nseg * p.B;
@@ -409,6 +392,7 @@ cudaError_t run_bwd(const ScanP& p, cudaStream_t s) {
     auto seg = scan_bwd_segment_kernel<T, LN, W>;
     seg<<<ctas, S::NT, sizeof(float) * S::TT * S::N, s>>>(p);
     cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_scan_chain(p, true, nullptr, s);
     if (e != cudaSuccess) return e;
   }
   auto kern = scan_bwd_kernel<T, LN, W>;
@@ -434,7 +418,7 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(int B, int L, int D, int N, int G, bool have_states) {
   BwdPlan q;
-  q.r = scan_plan(B, L, D, N, G, kBwdWarps);
+  q.r = scan_plan(B, L, D, G, scan_channels(N, kBwdWarps), kBwdWarps, 8 * kSmCount, 32 * kSmCount);
   size_t at = 0;
   auto take = [&](size_t floats) {
     const size_t here = at;

@@ -1,200 +1,436 @@
 // ssm_scan_fwd.cu -- the selective scan, forward, and its one-token step.
+//
+// A warp walks a segment of one sequence for its CW channels in tiles of TT
+// tokens, alone: no barrier wider than the warp.  Raw inputs arrive in shared
+// memory a tile ahead (asynchronous copies); the element lanes turn them into
+// delta and delta u once; the recurrence lanes, 32 states each (all of a
+// channel's up to 16, of as many channels as that allows), read those and B,
+// C, and leave sum_n C h in delta's place for the element lanes, which gate and
+// store.  32 states a lane are what keeps shared memory from being the bound:
+// a token costs a lane one read of delta and one of delta u for them, and B
+// and C are broadcasts.
 #include "ssm_scan.cuh"
 
 namespace lion {
 namespace {
 
-template <typename T, int LN, int W>
-struct FwdSmem {
-  using S = ScanTile<LN, W>;
-  float4 dt[S::TT * S::SLOT];       // {delta, delta, delta u, delta u}
-  float y[S::TT * S::SLOT];
-  float Bm[S::TT * S::N];
-  float Cm[S::TT * S::N];
+constexpr int kFwdWarps = 4;
+
+template <typename T, int N_>
+struct FwdTile {
+  static constexpr int N = N_;
+  static constexpr int RN = N < 16 ? N : 16;          // states of a channel in a lane
+  static constexpr int LN = N / RN;                   // lanes of a channel
+  static constexpr int RC = 32 / RN;                  // adjacent channels of a lane
+  static constexpr int CW = 32 / LN * RC;             // channels of a warp
+  static constexpr int TT = N == 64 ? 16 : 512 / CW;  // tokens of a tile
+  static constexpr int VT = CW / 4;                   // vectors of four channels: of a token,
+  static constexpr int VL = TT * VT / 32;             // and of a lane, 32 / VT tokens apart
+  static constexpr bool kConvert = sizeof(T) == 2;    // B and C: fp32 copies of raw bf16
+};
+template <typename T, int N_>
+struct FwdWarp {
+  using S = FwdTile<T, N_>;
+  alignas(16) float dt[S::TT * S::CW];   // delta, then sum_n C h
+  alignas(16) float du[S::TT * S::CW];   // delta u
+  alignas(16) float Bf[S::kConvert ? S::TT * S::N : 4];
+  alignas(16) float Cf[S::kConvert ? S::TT * S::N : 4];
+  struct Raw {
+    alignas(16) T u[S::TT * S::CW];
+    alignas(16) T dt[S::TT * S::CW];
+    alignas(16) T z[S::TT * S::CW];
+    alignas(16) T Bm[S::TT * S::N];
+    alignas(16) T Cm[S::TT * S::N];
+  } raw[2];
 };
 
-// The state that enters the CTA's segment from the ones before it (h0 before the first).
-template <int LN, int W>
-__device__ __forceinline__ void enter_segment(const ScanP& p, const ScanAt& w, const int (&d)[2], const bool (&live)[2],
-                                              int n0, const f2 (&A)[2][2], f2 (&h)[2][2]) {
+// Four adjacent elements of shared or global memory.
+__device__ __forceinline__ void get(const float* p, float (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void get(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void put(float* p, int n, bool wide, const float (&v)[4]) {
+  if (wide && n >= 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    load_pair(p.h0 + ((size_t)w.b * p.D + d[k]) * p.N + n0, live[k] && p.h0, h[k]);
-#pragma unroll 4
-    for (int s = 0; s < w.seg; ++s) {
-      const size_t at = ((size_t)w.b * p.nseg + s) * p.D + d[k];
-      f2 own[2];
-      load_pair(p.seg_state + at * p.N + n0, live[k], own);
-      const float sum = live[k] ? p.seg_sum[at] : 0.f;
-      const f2 s2 = pack2(sum, sum);
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+__device__ __forceinline__ void put(__nv_bfloat16* p, int n, bool wide, const float (&v)[4]) {
+  if (wide && n >= 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+  } else {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) h[k][q] = fma2(ex2_2(mul2(s2, A[k][q])), h[k][q], own[q]);
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+// n <= V = 16 bytes' worth of elements to shared memory, zeros behind them.
+template <typename T>
+__device__ __forceinline__ void fetch(T* dst, const T* src, int n, bool wide) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (wide && n >= V) {
+    copy_async16(dst, src);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[e] = e < n ? src[e] : from_f32<T>(0.f);
+  }
+}
+
+// A warp's copies of [TT][W] rows in pieces of 16 bytes: piece q = lane + 32 k
+// is PV elements of token q / PPR.  The source moves on a tile at a time.
+template <typename T, int TT, int W>
+struct Feed {
+  static constexpr int PV = 16 / (int)sizeof(T), PPR = W / PV, PIECES = TT * PPR, PK = (PIECES + 31) / 32;
+  static_assert(PPR <= 32 && 32 % PPR == 0, "a lane's pieces have one place in their tokens");
+  const T* src;
+  long long hop;   // elements from a lane's piece to its next, 32 / PPR tokens on
+  int n;           // elements there are of a piece
+  __device__ __forceinline__ void start(const void* base, long long ld, long long off, const ScanP& p, const ScanAt& w,
+                                        int i0, int lane, int width) {
+    const int c = lane % PPR * PV;
+    src = static_cast<const T*>(base) + ((long long)w.b * p.L + token_of(p, i0 + lane / PPR)) * ld + off + c;
+    hop = (p.reverse ? -(32 / PPR) : 32 / PPR) * ld;
+    n = min(PV, width - c);
+  }
+  __device__ __forceinline__ void next(T* dst, int lo, int hi, int lane, bool wide, bool whole, long long tile) {
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < PK; ++k) {
+        const int q = lane + 32 * k;
+        if (PIECES % 32 == 0 || q < PIECES) copy_async16(dst + q * PV, src + k * hop);
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < PK; ++k) {
+        const int q = lane + 32 * k, t = q / PPR;
+        if (PIECES % 32 == 0 || q < PIECES)
+          fetch<T>(dst + q * PV, src + k * hop, t >= lo && t < hi ? n : 0, wide);
+      }
     }
+    src += tile;
+  }
+};
+
+template <int COUNT>
+__device__ __forceinline__ const float* as_fp32(const float* raw, float*, int) { return raw; }
+template <int COUNT>
+__device__ __forceinline__ const float* as_fp32(const __nv_bfloat16* raw, float* dst, int lane) {
+#pragma unroll
+  for (int k = 0; k < (COUNT / 4 + 31) / 32; ++k) {
+    const int q = lane + 32 * k;
+    if (COUNT / 4 % 32 == 0 || q < COUNT / 4) {
+      float v[4];
+      get(raw + 4 * q, v);
+      *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  return dst;
+}
+
+// R adjacent floats.
+template <int R>
+__device__ __forceinline__ void get_some(const float* p, float (&v)[R]) {
+  if (R == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x; v[1] = x.y; v[R - 2] = x.z; v[R - 1] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x; v[1] = x.y;
+  }
+}
+
+// RN states of a channel (fp32, 16-byte aligned) as pairs.
+template <int RN>
+__device__ __forceinline__ void load_states(const float* src, bool there, f2 (&v)[RN / 2], float scale = 1.f) {
+#pragma unroll
+  for (int k = 0; k < RN / 4; ++k) {
+    f2 x[2];
+    load_pair(src + 4 * k, there, x, scale);
+    v[2 * k] = x[0];
+    v[2 * k + 1] = x[1];
+  }
+}
+template <int RN>
+__device__ __forceinline__ void store_states(float* dst, const f2 (&v)[RN / 2]) {
+#pragma unroll
+  for (int k = 0; k < RN / 4; ++k) {
+    const f2 x[2] = {v[2 * k], v[2 * k + 1]};
+    store_pair(dst + 4 * k, x);
   }
 }
 
 // MAIN: outputs, states, final state.  Otherwise: a segment's own
 // contribution to the state that leaves it, from a zero state, and its sum of
 // delta.
-template <typename T, int LN, int W, bool MAIN>
-__global__ void __launch_bounds__(32 * W) scan_fwd_kernel(ScanP p) {
-  using S = ScanTile<LN, W>;
-  constexpr int N = S::N, LC = S::LC, TT = S::TT;
+template <typename T, int N, bool MAIN>
+__global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kernel(ScanP p) {
+  using S = FwdTile<T, N>;
+  typedef typename FwdWarp<T, N>::Raw Raw;
+  constexpr int RN = S::RN, LN = S::LN, RC = S::RC, TT = S::TT, CW = S::CW, VT = S::VT, VL = S::VL;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  FwdSmem<T, LN, W>& sm = *reinterpret_cast<FwdSmem<T, LN, W>*>(smem_raw);
-  const ScanAt w = scan_at(p, S::CB);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  FwdWarp<T, N>& sm = reinterpret_cast<FwdWarp<T, N>*>(smem_raw)[warp];
+  ScanAt w = scan_at(p, kFwdWarps * CW);
+  w.d0 += warp * CW;
+  w.nch = min(CW, w.nch - warp * CW);
+  if (w.nch <= 0) return;
   if (!MAIN && w.seg == p.nseg - 1) return;   // nothing comes after it
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // element role
-  const int vt = tid / S::VPT, vc = 8 * (tid % S::VPT), vd = w.d0 + vc, vn = min(8, w.nch - vc);
-  // recurrence role
-  const int ln = lane % LN, cl = warp * S::CW + lane / LN;
-  const int d[2] = {w.d0 + cl, w.d0 + cl + LC};
-  const bool live[2] = {cl < w.nch, cl + LC < w.nch};
-  f2 A[2][2], h[2][2];
+  // element role: VL vectors of four channels, 32 / VT tokens apart
+  const int vt = lane / VT, vc = lane % VT * 4, vd = w.d0 + vc, vn = min(4, w.nch - vc);
+  // recurrence role: states n0 .. n0 + RN - 1 of RC adjacent channels; with two
+  // lanes a channel the odd one holds them in the other order, so that the
+  // first step of a sum over the states sends the same register from both
+  const int ln = lane % LN, n0 = ln * RN, odd = RC == 2 ? ln & 1 : 0, c0 = lane / LN * RC;
+  f2 A[RC][RN / 2], h[RC][RN / 2];
+  const size_t state_at = (size_t)(w.d0 + c0) * N + n0;
+  bool live[RC];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    load_pair(p.A + (size_t)d[k] * N + 4 * ln, live[k], A[k], kLog2e);
-    h[k][0] = h[k][1] = pack2(0.f, 0.f);
+  for (int k = 0; k < RC; ++k) {
+    live[k] = c0 + (k ^ odd) < w.nch;
+    load_states<RN>(p.A + state_at + (k ^ odd) * N, live[k], A[k], kLog2e);
+#pragma unroll
+    for (int q = 0; q < RN / 2; ++q) h[k][q] = pack2(0.f, 0.f);
   }
-  if (MAIN) enter_segment<LN, W>(p, w, d, live, 4 * ln, A, h);
-  float total[8], skip[8];
+  float total[4], bias[4], skip[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 4; ++e) {
     total[e] = 0.f;
+    bias[e] = p.dt_bias && e < vn ? p.dt_bias[vd + e] : 0.f;
     skip[e] = MAIN && p.Dskip && e < vn ? p.Dskip[vd + e] : 0.f;
   }
+  const bool plain = w.nch == CW && p.u_wide && p.dt_wide && p.b_wide && p.c_wide && (!p.z || p.z_wide) && p.o_wide;
+  // the tiles that have tokens; MAIN visits the others to write zeros and states
+  const int a0 = max(w.i0, w.v0 - w.v0 % TT), a1 = min(w.i1, w.v1), r0 = max(w.i0, w.v0);
+  Feed<T, TT, CW> fu, fdt, fz;
+  Feed<T, TT, N> fb, fc;
+  fu.start(p.u, p.u_ld, w.d0, p, w, a0, lane, w.nch);
+  fdt.start(p.dt, p.dt_ld, w.d0, p, w, a0, lane, w.nch);
+  fz.start(p.z, p.z_ld, w.d0, p, w, a0, lane, w.nch);
+  fb.start(p.Bm, p.b_ld, w.g * N, p, w, a0, lane, N);
+  fc.start(p.Cm, p.c_ld, w.g * N, p, w, a0, lane, N);
+  const int dir = p.reverse ? -TT : TT;
+  auto fetch_tile = [&](Raw& to, int i0) {
+    const int lo = r0 - i0, hi = a1 - i0;
+    const bool whole = plain && lo <= 0 && hi >= TT;
+    fu.next(to.u, lo, hi, lane, p.u_wide, whole, dir * p.u_ld);
+    fdt.next(to.dt, lo, hi, lane, p.dt_wide, whole, dir * p.dt_ld);
+    if (MAIN && p.z) fz.next(to.z, lo, hi, lane, p.z_wide, whole, dir * p.z_ld);
+    fb.next(to.Bm, lo, hi, lane, p.b_wide, whole, dir * p.b_ld);
+    if (MAIN) fc.next(to.Cm, lo, hi, lane, p.c_wide, whole, dir * p.c_ld);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (a0 < a1) fetch_tile(sm.raw[0], a0);
+  if (MAIN) {
+    const float* from = p.nseg > 1 ? p.seg_state + ((size_t)w.b * p.nseg + w.seg) * p.D * N
+                        : p.h0     ? p.h0 + (size_t)w.b * p.D * N
+                                   : nullptr;
+#pragma unroll
+    for (int k = 0; k < RC; ++k) load_states<RN>(from + state_at + (k ^ odd) * N, live[k] && from, h[k]);
+  }
+  T* out = nullptr;
+  long long out_hop = 0;   // from a lane's vector to its next
+  if (MAIN && p.out) {
+    out = static_cast<T*>(p.out) + ((long long)w.b * p.L + token_of(p, w.i0 + vt)) * p.D + vd;
+    out_hop = (long long)(p.reverse ? -(32 / VT) : 32 / VT) * p.D;
+  }
 
-  for (int i0 = w.i0; i0 < w.i1; i0 += TT) {
-    const int i = i0 + vt;
-    if (MAIN && p.states) {
+  int stage = 0;
+  for (int i0 = MAIN ? w.i0 : a0; i0 < (MAIN ? w.i1 : a1); i0 += TT) {
+    if (MAIN && p.states && i0 % N == 0) {
+      float* to = p.states + ((size_t)w.b * p.nst + i0 / N) * p.D * N + state_at;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (live[k]) store_pair(p.states + (((size_t)w.b * p.nst + i0 / TT) * p.D + d[k]) * N + 4 * ln, h[k]);
+      for (int k = 0; k < RC; ++k)
+        if (live[k]) store_states<RN>(to + (k ^ odd) * N, h[k]);
     }
-    const bool real = i >= w.v0 && i < w.v1 && i < w.i1;
-    const long long row = (long long)w.b * p.L + token_of(p, i);
-    const bool some = i0 + TT > w.v0 && i0 < w.v1;   // the tile has a token
-    float u[8], z[8];
+    const bool some = i0 >= a0 && i0 < a1;
+    const bool whole = plain && i0 >= r0 && i0 + TT <= a1;   // every lane has full vectors of tokens
+    Raw& raw = sm.raw[stage];
     if (some) {
-      float dt[8], raw[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = dt[e] = z[e] = 0.f;
-      if (real && vn > 0) {
-        load8(static_cast<const T*>(p.u) + row * p.u_ld + vd, vn, p.u_wide, u);
-        load8(static_cast<const T*>(p.dt) + row * p.dt_ld + vd, vn, p.dt_wide, dt);
-        if (MAIN && p.z) load8(static_cast<const T*>(p.z) + row * p.z_ld + vd, vn, p.z_wide, z);
-        deltas(p, vd, vn, dt, raw);
+      if (i0 + TT < a1) {
+        fetch_tile(sm.raw[stage ^ 1], i0 + TT);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
+      __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float du = dt[e] * u[e];
-        sm.dt[vt * S::SLOT + slot_of(vc + e)] = make_float4(dt[e], dt[e], du, du);
-        total[e] += dt[e];
+      for (int j = 0; j < VL; ++j) {
+        const int at = (lane + 32 * j) * 4, i = i0 + vt + j * (32 / VT);
+        float u[4], dt[4];
+        get(raw.u + at, u);
+        get(raw.dt + at, dt);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          f2 x = add2(pack2(dt[e], dt[e + 1]), pack2(bias[e], bias[e + 1]));
+          if (p.softplus) {
+            const float2 r = unpack2(x);
+            x = softplus2(r.x, r.y);
+          }
+          if (!whole) {
+            const bool real = i >= r0 && i < a1;
+            x = pack2(real && e < vn ? unpack2(x).x : 0.f, real && e + 1 < vn ? unpack2(x).y : 0.f);
+          }
+          const float2 dl = unpack2(x), d2 = unpack2(mul2(x, pack2(u[e], u[e + 1])));
+          dt[e] = dl.x; dt[e + 1] = dl.y;
+          u[e] = d2.x; u[e + 1] = d2.y;
+          if (!MAIN) {
+            total[e] += dl.x;
+            total[e + 1] += dl.y;
+          }
+        }
+        *reinterpret_cast<float4*>(sm.dt + at) = make_float4(dt[0], dt[1], dt[2], dt[3]);
+        *reinterpret_cast<float4*>(sm.du + at) = make_float4(u[0], u[1], u[2], u[3]);
       }
-      load_bc<T, N, TT, S::NT>(p, w, p.Bm, p.b_ld, i0, sm.Bm);
-      if (MAIN) load_bc<T, N, TT, S::NT>(p, w, p.Cm, p.c_ld, i0, sm.Cm);
-      __syncthreads();
-      constexpr int TG = LN / 2;   // tokens whose sums over the states are taken together
-#pragma unroll 2
-      for (int t0 = 0; t0 < TT; t0 += TG) {
-        float v[LN];
+      const float* Bt = as_fp32<TT * N>(raw.Bm, sm.Bf, lane) + n0;
+      const float* Ct = MAIN ? as_fp32<TT * N>(raw.Cm, sm.Cf, lane) + n0 : nullptr;
+      __syncwarp();
+#pragma unroll(TT < 4 ? TT : 4)
+      for (int t = 0; t < TT; ++t) {
+        float dt[RC], du[RC];
+        get_some<RC>(sm.dt + t * CW + c0, dt);
+        get_some<RC>(sm.du + t * CW + c0, du);
+        if (RC == 2 && LN > 1) {   // the odd lane's order
+          const float a = dt[0], b = du[0];
+          dt[0] = odd ? dt[1] : a; dt[1] = odd ? a : dt[1];
+          du[0] = odd ? du[1] : b; du[1] = odd ? b : du[1];
+        }
+        f2 y[RC];
 #pragma unroll
-        for (int t = 0; t < TG; ++t) {
-          const float4 b4 = *reinterpret_cast<const float4*>(sm.Bm + (t0 + t) * N + 4 * ln);
-          const f2 Bt[2] = {pack2(b4.x, b4.y), pack2(b4.z, b4.w)};
-          f2 Ct[2];
+        for (int n = 0; n < RN / 4; ++n) {
+          const float4 b4 = *reinterpret_cast<const float4*>(Bt + t * N + 4 * n);
+          const f2 b2[2] = {pack2(b4.x, b4.y), pack2(b4.z, b4.w)};
+          f2 c2[2];
           if (MAIN) {
-            const float4 c4 = *reinterpret_cast<const float4*>(sm.Cm + (t0 + t) * N + 4 * ln);
-            Ct[0] = pack2(c4.x, c4.y);
-            Ct[1] = pack2(c4.z, c4.w);
+            const float4 c4 = *reinterpret_cast<const float4*>(Ct + t * N + 4 * n);
+            c2[0] = pack2(c4.x, c4.y);
+            c2[1] = pack2(c4.z, c4.w);
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4 q4 = sm.dt[(t0 + t) * S::SLOT + slot_of(cl + k * LC)];
-            const f2 dt2 = pack2(q4.x, q4.y), du2 = pack2(q4.z, q4.w);
-            f2 y;
+          for (int k = 0; k < RC; ++k) {
+            const f2 dt2 = pack2(dt[k], dt[k]), du2 = pack2(du[k], du[k]);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              h[k][q] = fma2(ex2_2(mul2(dt2, A[k][q])), h[k][q], mul2(du2, Bt[q]));
-              if (MAIN) y = q == 0 ? mul2(Ct[0], h[k][0]) : fma2(Ct[q], h[k][q], y);
+              f2& s = h[k][2 * n + q];
+              s = fma2(ex2_2(mul2(dt2, A[k][2 * n + q])), s, mul2(du2, b2[q]));
+              if (MAIN) y[k] = n + q == 0 ? mul2(c2[q], s) : fma2(c2[q], s, y[k]);
             }
-            if (MAIN) v[2 * t + k] = sum2(y);
           }
         }
         if (MAIN) {
-          const float y = sum_states<LN>(v, ln);
-          sm.y[(t0 + (ln >> 1)) * S::SLOT + slot_of(cl + (ln & 1) * LC)] = y;
-        }
-      }
-      __syncthreads();
-    }
-    if (MAIN && p.out && i < w.i1 && vn > 0) {
-      float o[8];
+          float v[RC];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        o[e] = 0.f;
-        if (real) {
-          o[e] = fmaf(skip[e], u[e], sm.y[vt * S::SLOT + slot_of(vc + e)]);
-          if (p.z) o[e] *= z[e] * sigmoid(z[e]);
+          for (int k = 0; k < RC; ++k) v[k] = sum2(y[k]);
+          float* yo = sm.dt + t * CW + c0;
+          if (LN > 1) {
+            float r = v[0] + __shfl_xor_sync(0xffffffffu, v[RC - 1], 1);
+#pragma unroll
+            for (int o = 2; o < LN; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+            yo[odd] = r;   // lanes of one parity hold the same sum
+          } else if (RC == 4) {
+            *reinterpret_cast<float4*>(yo) = make_float4(v[0], v[1], v[RC - 2], v[RC - 1]);
+          } else {
+            *reinterpret_cast<float2*>(yo) = make_float2(v[0], v[1]);
+          }
         }
       }
-      store8(static_cast<T*>(p.out) + row * p.D + vd, vn, p.o_wide, o);
+      __syncwarp();
+    }
+    if (MAIN && out) {
+#pragma unroll
+      for (int j = 0; j < VL; ++j) {
+        const int at = (lane + 32 * j) * 4, i = i0 + vt + j * (32 / VT);
+        if (whole || (i < w.i1 && vn > 0)) {
+          float o[4] = {0.f, 0.f, 0.f, 0.f};
+          if (whole || (i >= r0 && i < a1)) {
+            float u[4];
+            get(raw.u + at, u);
+            get(sm.dt + at, o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(skip[e], u[e], o[e]);
+            if (p.z) {
+              float z[4];
+              get(raw.z + at, z);
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const float2 g = unpack2(gate2(pack2(o[e], o[e + 1]), z[e], z[e + 1]));
+                o[e] = g.x;
+                o[e + 1] = g.y;
+              }
+            }
+          }
+          put(out, whole ? 4 : vn, whole || p.o_wide, o);
+        }
+        out += out_hop;
+      }
+    }
+    if (some) {
+      stage ^= 1;
+      __syncwarp();   // this tile's raw inputs are read before the copies after next overwrite them
     }
   }
 
   if (MAIN) {
     if (p.h_out && w.seg == p.nseg - 1) {
+      float* to = p.h_out + (size_t)w.b * p.D * N + state_at;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (live[k]) store_pair(p.h_out + ((size_t)w.b * p.D + d[k]) * N + 4 * ln, h[k]);
+      for (int k = 0; k < RC; ++k)
+        if (live[k]) store_states<RN>(to + (k ^ odd) * N, h[k]);
     }
   } else {
     const size_t at = ((size_t)w.b * p.nseg + w.seg) * p.D;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (live[k]) store_pair(p.seg_state + (at + d[k]) * N + 4 * ln, h[k]);
-    // the threads of a channel vector add up their tokens' delta
-    __syncthreads();
+    for (int k = 0; k < RC; ++k)
+      if (live[k]) store_states<RN>(p.seg_state + at * N + state_at + (k ^ odd) * N, h[k]);
+    // a channel's delta: over the lanes that hold its tokens
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sm.y[vt * S::SLOT + slot_of(vc + e)] = total[e];
-    __syncthreads();
-    for (int c = tid; c < w.nch; c += S::NT) {
-      float s = 0.f;
-#pragma unroll 8
-      for (int t = 0; t < TT; ++t) s += sm.y[t * S::SLOT + slot_of(c)];
-      p.seg_sum[at + w.d0 + c] = s;
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int o = VT; o < 32; o <<= 1) total[e] += __shfl_xor_sync(0xffffffffu, total[e], o);
+      if (vt == 0 && e < vn) p.seg_sum[at + vd + e] = total[e];
     }
   }
 }
 
-constexpr int kFwdWarps = 4;
-
-template <typename T, int LN, bool MAIN>
+template <typename T, int N, bool MAIN>
 cudaError_t run_kernel(const ScanP& p, cudaStream_t s) {
-  using S = ScanTile<LN, kFwdWarps>;
-  auto kern = scan_fwd_kernel<T, LN, kFwdWarps, MAIN>;
-  const size_t smem = sizeof(FwdSmem<T, LN, kFwdWarps>);
+  auto kern = scan_fwd_kernel<T, N, MAIN>;
+  const size_t smem = sizeof(FwdWarp<T, N>) * kFwdWarps;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)p.nblk * p.G * p.nseg * p.B, S::NT, smem, s>>>(p);
+  kern<<<(unsigned)p.nblk * p.G * p.nseg * p.B, 32 * kFwdWarps, smem, s>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, int LN>
+template <typename T, int N>
 cudaError_t run_fwd(const ScanP& p, cudaStream_t s) {
   if (p.nseg > 1) {
-    cudaError_t e = run_kernel<T, LN, false>(p, s);
+    cudaError_t e = run_kernel<T, N, false>(p, s);
+    if (e == cudaSuccess) e = launch_scan_chain(p, false, p.h0, s);
     if (e != cudaSuccess) return e;
   }
-  return run_kernel<T, LN, true>(p, s);
+  return run_kernel<T, N, true>(p, s);
 }
 
 // One token: a thread holds four states of a channel; bound by the states'
 // traffic, read and written once, 16 bytes a thread.
-template <typename T, int LN>
+template <typename T, int N>
 __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a) {
-  constexpr int N = 4 * LN;
+  constexpr int LN = N / 4;
   const long long item = (long long)blockIdx.x * 128 + threadIdx.x;
   const int ln = (int)(item % LN);
   const long long ch = item / LN;   // b * D + d
@@ -234,24 +470,68 @@ __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a) {
   }
 }
 
-template <typename T, int LN>
+template <typename T, int N>
 cudaError_t run_step(const lion_scan_step_args& a, cudaStream_t s) {
-  const long long n = (long long)a.B * a.D * LN;
-  scan_step_kernel<T, LN><<<(unsigned)((n + 127) / 128), 128, 0, s>>>(a);
+  const long long n = (long long)a.B * a.D * (N / 4);
+  scan_step_kernel<T, N><<<(unsigned)((n + 127) / 128), 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+// Turns the segments' own contributions into the states that enter them, in
+// place: X_{s+1} = exp(A sum_s) X_s + own_s from the walk's start, or, back,
+// X_{s-1} = exp(A sum_s) X_s + own_s from its end.  A thread has four states
+// of a channel and reads eight segments ahead.
+namespace {
+__global__ void __launch_bounds__(128) scan_chain_kernel(ScanP p, bool back, const float* first) {
+  const int per = p.N / 4;
+  const long long k = (long long)blockIdx.x * 128 + threadIdx.x;
+  if (k >= (long long)p.B * p.D * per) return;
+  const int n0 = 4 * (int)(k % per);
+  const long long bd = k / per;
+  const int b = (int)(bd / p.D), d = (int)(bd - (long long)b * p.D);
+  f2 A[2], x[2];
+  load_pair(p.A + (size_t)d * p.N + n0, true, A, kLog2e);
+  load_pair(first + bd * p.N + n0, first != nullptr, x);
+  for (int s0 = 0; s0 < p.nseg; s0 += 8) {
+    f2 own[8][2];
+    float sum[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      // the last of the walk has no contribution: nothing follows it
+      const bool there = s0 + q < p.nseg - 1;
+      const int s = back ? p.nseg - 1 - s0 - q : s0 + q;
+      const size_t at = ((size_t)b * p.nseg + s) * p.D + d;
+      load_pair(p.seg_state + at * p.N + n0, there, own[q]);
+      sum[q] = there ? p.seg_sum[at] : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (s0 + q >= p.nseg) break;
+      const int s = back ? p.nseg - 1 - s0 - q : s0 + q;
+      store_pair(p.seg_state + (((size_t)b * p.nseg + s) * p.D + d) * p.N + n0, x);
+      const f2 s2 = pack2(sum[q], sum[q]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) x[e] = fma2(ex2_2(mul2(s2, A[e])), x[e], own[q][e]);
+    }
+  }
+}
+}  // namespace
+
+cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cudaStream_t s) {
+  const long long n = (long long)p.B * p.D * (p.N / 4);
+  scan_chain_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, back, first);
+  return cudaGetLastError();
+}
+
 // A sequence is cut into segments only while its channels alone leave the SMs
-// short of CTAs: each cut costs a second pass over the exponentials.
-ScanPlan scan_plan(int B, int L, int D, int N, int G, int W) {
+// short of warps: a cut costs a second pass over the exponentials.
+ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int warps, long long enough, long long want) {
   ScanPlan r;
-  const int cb = scan_channels(N, W);
-  r.nblk = (D / G + cb - 1) / cb;
-  const long long ctas = (long long)B * G * r.nblk;
-  const long long want = kSmCount * (16 / W);
-  long long nseg = ctas >= want / 2 ? 1 : (want + ctas - 1) / ctas;
+  r.nblk = (D / G + cta_channels - 1) / cta_channels;
+  const long long have = (long long)B * G * r.nblk * warps;
+  long long nseg = have >= enough ? 1 : (want + have - 1) / have;
   const long long most = L / 128 > 1 ? L / 128 : 1;
   if (nseg > most) nseg = most;
   long long len = (L + nseg - 1) / nseg;
@@ -260,9 +540,15 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, int W) {
   r.nseg = (int)((L + len - 1) / len);
   return r;
 }
+namespace {
+ScanPlan fwd_plan(int B, int L, int D, int N, int G) {
+  const int cw = N == 8 ? 128 : 1024 / N;
+  return scan_plan(B, L, D, G, kFwdWarps * cw, kFwdWarps, 4 * kSmCount, 48 * kSmCount);
+}
+}  // namespace
 
 size_t scan_workspace_bytes(int B, int L, int D, int N, int G) {
-  const ScanPlan r = scan_plan(B, L, D, N, G, kFwdWarps);
+  const ScanPlan r = fwd_plan(B, L, D, N, G);
   if (r.nseg == 1) return 0;
   return up256(sizeof(float) * (size_t)B * r.nseg * D * N) + up256(sizeof(float) * (size_t)B * r.nseg * D);
 }
@@ -301,12 +587,14 @@ void fill_scan(ScanP& p, const lion_scan_args& a) {
   p.dt_wide = whole && rows_wide(a.dt, p.dt_ld, es);
   p.z_wide = whole && rows_wide(a.z, p.z_ld, es);
   p.o_wide = whole && rows_wide(a.out, a.D, es);
+  p.b_wide = rows_wide(a.Bm, p.b_ld, es);
+  p.c_wide = rows_wide(a.Cm, p.c_ld, es);
 }
 
 cudaError_t launch_scan_fwd(const lion_scan_args& a, void* ws, cudaStream_t s) {
   ScanP p = {};
   fill_scan(p, a);
-  const ScanPlan r = scan_plan(a.B, a.L, a.D, a.N, a.G, kFwdWarps);
+  const ScanPlan r = fwd_plan(a.B, a.L, a.D, a.N, a.G);
   p.nblk = r.nblk;
   p.nseg = r.nseg;
   p.seglen = r.seglen;
