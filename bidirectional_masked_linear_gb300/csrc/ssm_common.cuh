@@ -127,10 +127,14 @@ __device__ __forceinline__ f2 softplus2(float x0, float x1) {
 }
 __device__ __forceinline__ float softplus(float x) { return unpack2(softplus2(x, 0.f)).x; }
 
+__device__ __forceinline__ f2 sigmoid2(float x0, float x1) {
+  const f2 d = add2(pack2(ex2(x0 * -kLog2e), ex2(x1 * -kLog2e)), pack2(1.f, 1.f));
+  return pack2(rcp(d.x), rcp(d.y));
+}
+
 // z sigmoid(z) of a pair, times o.
 __device__ __forceinline__ f2 gate2(f2 o, float z0, float z1) {
-  const float2 d = unpack2(add2(pack2(ex2(z0 * -kLog2e), ex2(z1 * -kLog2e)), pack2(1.f, 1.f)));
-  return mul2(mul2(o, pack2(z0, z1)), pack2(rcp(d.x), rcp(d.y)));
+  return mul2(mul2(o, pack2(z0, z1)), sigmoid2(z0, z1));
 }
 
 // Whether rows of es-byte elements, `stride` elements apart, all start on 16 bytes.

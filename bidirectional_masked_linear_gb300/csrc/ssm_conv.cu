@@ -5,10 +5,10 @@
 //   dx_i = sum_{j<K} w[K-1-j] dp_{i+j},  dp = dy act'(p)
 //   dw[K-1-j] = sum_{b,i} dp_i x_{i-j},  dbias = sum_{b,i} dp_i
 // with i the order in which tokens are walked.  2 K operations a value: bound
-// by HBM.  A thread walks a run of tokens for eight channels with the window
-// in registers, so an input is read once plus K-1 tokens before each run (and
-// behind it, for the gradients), which the neighbouring runs' reads leave in
-// the caches; a warp reads 32 x 8 adjacent channels.
+// by HBM.  A thread walks a run of tokens for four channels with the window in
+// registers; the next few tokens are read while it works on the last ones, so
+// an input is read once plus K-1 tokens before each run (and behind it, for
+// the gradients), which the neighbouring runs leave in the caches.
 #include "lion_internal.h"
 #include "ssm_common.cuh"
 
@@ -28,7 +28,8 @@ struct ConvP {
   long long x_ld;
   int B, L, D;
   int act, reverse;
-  int nvec, runs;     // channel vectors; runs of tokens a sequence
+  int nvec;           // vectors of four channels
+  int run, runs;      // tokens of a run; runs of a sequence
   bool x_wide, o_wide, s_wide;
 };
 
@@ -36,72 +37,161 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int L) {
   return lengths ? min(max(lengths[b], 0), L) : L;
 }
 
-constexpr int kRun = 16;
+// Tokens read ahead: 8 bytes of bfloat16 or 16 of fp32 a token and thread.
+template <typename T>
+struct Ahead {
+  static constexpr int N = sizeof(T) == 2 ? 8 : 4;
+};
+
+// Four raw elements.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 r;
+  __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool wide) {
+    if (wide) {
+      r = *reinterpret_cast<const uint2*>(p);
+    } else {
+      unsigned short h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = e < n ? reinterpret_cast<const unsigned short*>(p)[e] : 0;
+      r = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  }
+};
+template <>
+struct Raw4<float> {
+  float4 r;
+  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p, int n, bool wide) {
+    if (wide) r = *reinterpret_cast<const float4*>(p);
+    else r = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+  }
+  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+};
+__device__ __forceinline__ void store4(float* p, int n, bool wide, const float (&v)[4]) {
+  if (wide) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, int n, bool wide, const float (&v)[4]) {
+  if (wide) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = __float2bfloat16_rn(v[e]);
+  }
+}
 
 template <int K>
-__device__ __forceinline__ void load_taps(const float* weight, int c0, int n, float (&w)[K][8]) {
+__device__ __forceinline__ void load_taps(const float* weight, int c0, int n, float (&w)[K][4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
+  for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int k = 0; k < K; ++k) w[k][e] = e < n ? weight[(size_t)(c0 + e) * K + k] : 0.f;
 }
 
-// The input processed i-th (i < 0: from the state; 0 where there is none).
+// A thread's line: four channels of one sequence.
 template <typename T, int K>
-__device__ __forceinline__ void load_at(const ConvP& p, int b, int len, int i, int c0, int n, float (&v)[8]) {
-  if (i >= 0 && i < len) {
-    const int t = p.reverse ? len - 1 - i : i;
-    load8(static_cast<const T*>(p.x) + ((long long)b * p.L + t) * p.x_ld + c0, n, p.x_wide, v);
-  } else if (i < 0 && i >= -(K - 1) && p.state) {
-    load8(static_cast<const T*>(p.state) + ((long long)b * (K - 1) + K - 1 + i) * p.D + c0, n, p.s_wide, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+struct Line {
+  int b, c0, n, len;
+  bool xw, ow, sw;   // whole aligned vectors: x, the tight activations, the states
+  __device__ __forceinline__ Line(const ConvP& p, int b_, int c0_) : b(b_), c0(c0_) {
+    n = p.D - c0;
+    len = clamp_len(p.lengths, b, p.L);
+    xw = p.x_wide && n >= 4;
+    ow = p.o_wide && n >= 4;
+    sw = p.s_wide && n >= 4;
   }
-}
+  __device__ __forceinline__ int token(const ConvP& p, int i) const { return p.reverse ? len - 1 - i : i; }
+  // The input processed i-th (i < 0: from the state; zeros where there is none).
+  __device__ __forceinline__ void at(const ConvP& p, int i, float (&v)[4]) const {
+    Raw4<T> r;
+    r.zero();
+    if (i >= 0 && i < len)
+      r.load(static_cast<const T*>(p.x) + ((long long)b * p.L + token(p, i)) * p.x_ld + c0, n, xw);
+    else if (i < 0 && i >= -(K - 1) && p.state)
+      r.load(static_cast<const T*>(p.state) + ((long long)b * (K - 1) + K - 1 + i) * p.D + c0, n, sw);
+    r.get(v);
+  }
+};
 
 template <typename T, int K>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(ConvP p) {
-  const long long item = (long long)blockIdx.x * 128 + threadIdx.x;
-  const long long line = item / p.nvec;
-  const int c0 = 8 * (int)(item - line * p.nvec), n = p.D - c0;
-  const int b = (int)(line / p.runs), i0 = (int)(line - (long long)b * p.runs) * kRun;
+  constexpr int A = Ahead<T>::N;
+  const long long item = (long long)blockIdx.x * 128 + threadIdx.x, line = item / p.nvec;
+  const int b = (int)(line / p.runs), i0 = (int)(line - (long long)b * p.runs) * p.run;
   if (b >= p.B) return;
-  const int len = clamp_len(p.lengths, b, p.L);
-  const int i1 = min(i0 + kRun, p.L);
-  float w[K][8], bias[8], win[K][8];
-  load_taps<K>(p.weight, c0, n, w);
+  const Line<T, K> l(p, b, 4 * (int)(item - line * p.nvec));
+  const int i1 = min(i0 + p.run, p.L);
+  float w[K][4], bias[4], win[K][4];
+  load_taps<K>(p.weight, l.c0, l.n, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) bias[e] = p.bias && e < n ? p.bias[c0 + e] : 0.f;
+  for (int e = 0; e < 4; ++e) bias[e] = p.bias && e < l.n ? p.bias[l.c0 + e] : 0.f;
+  const long long x_hop = p.reverse ? -p.x_ld : p.x_ld, y_hop = p.reverse ? -p.D : p.D;
+  const T* x = static_cast<const T*>(p.x) + ((long long)b * p.L + l.token(p, i0)) * p.x_ld + l.c0;
+  T* y = static_cast<T*>(p.out) + ((long long)b * p.L + l.token(p, i0)) * p.D + l.c0;
+  const int real = min(i1, l.len) - i0;   // tokens of the run that there are
+  Raw4<T> next[A];
+  auto read = [&](int j) {
 #pragma unroll
-  for (int k = 1; k < K; ++k) load_at<T, K>(p, b, len, i0 - K + k, c0, n, win[k]);
-  T* y = static_cast<T*>(p.out);
-#pragma unroll 4
-  for (int i = i0; i < i1; ++i) {
-#pragma unroll
-    for (int k = 0; k + 1 < K; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) win[k][e] = win[k + 1][e];
-    load_at<T, K>(p, b, len, i, c0, n, win[K - 1]);
-    float o[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float a = bias[e];
-#pragma unroll
-      for (int k = 0; k < K; ++k) a = fmaf(w[k][e], win[k][e], a);
-      o[e] = i < len ? (p.act ? a * sigmoid(a) : a) : 0.f;
+    for (int a = 0; a < A; ++a) {
+      next[a].zero();
+      if (j + a < real) next[a].load(x + a * x_hop, l.n, l.xw);
     }
-    // tokens past the length are not part of the walk: each is written as it lies
-    const int t = p.reverse && i < len ? len - 1 - i : i;
-    store8(y + ((long long)b * p.L + t) * p.D + c0, n, p.o_wide, o);
+    x += A * x_hop;
+  };
+  read(0);
+#pragma unroll
+  for (int k = 1; k < K; ++k) l.at(p, i0 - K + k, win[k]);
+  for (int j = 0; j < real; j += A) {
+    Raw4<T> now[A];
+#pragma unroll
+    for (int a = 0; a < A; ++a) now[a] = next[a];
+    if (j + A < real) read(j + A);
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+#pragma unroll
+      for (int k = 0; k + 1 < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) win[k][e] = win[k + 1][e];
+      now[a].get(win[K - 1]);
+      float o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float s = bias[e];
+#pragma unroll
+        for (int k = 0; k < K; ++k) s = fmaf(w[k][e], win[k][e], s);
+        o[e] = p.act ? s * sigmoid(s) : s;
+      }
+      if (j + a < real) store4(y + a * y_hop, l.n, l.ow, o);
+    }
+    y += A * y_hop;
   }
+  // tokens past the length are not part of the walk: zeros where they lie
+  const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = max(i0, l.len); i < i1; ++i)
+    store4(static_cast<T*>(p.out) + ((long long)b * p.L + i) * p.D + l.c0, l.n, l.ow, zero);
   if (p.state_out && i0 == 0) {
-    T* st = static_cast<T*>(p.state_out) + (long long)b * (K - 1) * p.D + c0;
+    T* st = static_cast<T*>(p.state_out) + (long long)b * (K - 1) * p.D + l.c0;
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
-      float v[8];
-      load_at<T, K>(p, b, len, len - (K - 1) + k, c0, n, v);
-      store8(st + (long long)k * p.D, n, p.s_wide, v);
+      float v[4];
+      l.at(p, l.len - (K - 1) + k, v);
+      store4(st + (long long)k * p.D, l.n, l.sw, v);
     }
   }
 }
@@ -110,104 +200,129 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(ConvP p) {
 // channels' share of dweight and dbias over all the runs it walks.
 template <typename T, int K>
 __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvP p) {
-  __shared__ float sh[8][32][8];
+  constexpr int A = sizeof(T) == 2 ? 4 : 4;
+  __shared__ float sh[8][32][4];
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int vec = blockIdx.x * 32 + lane, c0 = 8 * vec, n = p.D - c0;
-  const bool live = n > 0;
-  float w[K][8], bias[8], dw[K][8], db[8];
-  load_taps<K>(p.weight, c0, live ? n : 0, w);
+  const int c0 = 4 * (blockIdx.x * 32 + lane);
+  const bool live = c0 < p.D;
+  float w[K][4], bias[4], dw[K][4], db[4];
+  load_taps<K>(p.weight, c0, p.D - c0, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    bias[e] = p.bias && e < n ? p.bias[c0 + e] : 0.f;
+  for (int e = 0; e < 4; ++e) {
+    bias[e] = p.bias && c0 + e < p.D ? p.bias[c0 + e] : 0.f;
     db[e] = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) dw[k][e] = 0.f;
   }
+  const long long x_hop = p.reverse ? -p.x_ld : p.x_ld, d_hop = p.reverse ? -p.D : p.D;
   const long long lines = (long long)p.B * p.runs;
   for (long long line = (long long)blockIdx.y * 8 + r; live && line < lines; line += (long long)gridDim.y * 8) {
-    const int b = (int)(line / p.runs), i0 = (int)(line - (long long)b * p.runs) * kRun;
-    const int len = clamp_len(p.lengths, b, p.L);
-    const int i1 = min(i0 + kRun, p.L);
-    // win[k] = x_{i-K+1+k}; dp[k] = dp_{i-K+1+k}
-    float win[K][8], dp[K][8];
+    const int b = (int)(line / p.runs), i0 = (int)(line - (long long)b * p.runs) * p.run;
+    const Line<T, K> l(p, b, c0);
+    const int i1 = min(i0 + p.run, p.L), mine = min(i1, l.len) - i0;
+    // the sums that end in the run need dp up to K-1 tokens behind it
+    const int real = mine > 0 || (i0 == 0 && p.state_out) ? min(i1 + K - 1, l.len) - i0 : 0;
+    const T* x = static_cast<const T*>(p.x) + ((long long)b * p.L + l.token(p, i0)) * p.x_ld + c0;
+    const T* dy = static_cast<const T*>(p.dy) + ((long long)b * p.L + l.token(p, i0)) * p.D + c0;
+    T* dx = static_cast<T*>(p.out) + ((long long)b * p.L + l.token(p, i0)) * p.D + c0;
+    Raw4<T> nx[A], ny[A];
+    auto read = [&](int j) {
+#pragma unroll
+      for (int a = 0; a < A; ++a) {
+        nx[a].zero();
+        ny[a].zero();
+        if (j + a < real) {
+          nx[a].load(x + a * x_hop, l.n, l.xw);
+          ny[a].load(dy + a * d_hop, l.n, l.ow);
+        }
+      }
+      x += A * x_hop;
+      dy += A * d_hop;
+    };
+    read(0);
+    // win[k] = x_{i-K+1+k}, dp[k] = dp_{i-K+1+k}
+    float win[K][4], dp[K][4];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dp[k][e] = 0.f;
+      for (int e = 0; e < 4; ++e) dp[k][e] = 0.f;
 #pragma unroll
-    for (int k = 1; k < K; ++k) load_at<T, K>(p, b, len, i0 - K + k, c0, n, win[k]);
-    // the state's gradient takes the sums that end before the first token
-    const bool head = i0 == 0 && p.state_out;
-    for (int i = i0; i < i1 + K - 1; ++i) {
+    for (int k = 1; k < K; ++k) l.at(p, i0 - K + k, win[k]);
+    const int last = mine + K - 1;   // steps until the run's last dx is complete
+    for (int j = 0; j < last; j += A) {
+      Raw4<T> vx[A], vy[A];
 #pragma unroll
-      for (int k = 0; k + 1 < K; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          win[k][e] = win[k + 1][e];
-          dp[k][e] = dp[k + 1][e];
-        }
-      load_at<T, K>(p, b, len, i, c0, n, win[K - 1]);
-      const bool real = i < len;
-      float g[8];
-      if (real) {
-        const int t = p.reverse ? len - 1 - i : i;
-        load8(static_cast<const T*>(p.dy) + ((long long)b * p.L + t) * p.D + c0, n, p.o_wide, g);
+      for (int a = 0; a < A; ++a) {
+        vx[a] = nx[a];
+        vy[a] = ny[a];
       }
-      const bool mine = i < i1;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float d = 0.f;
-        if (real) {
-          d = g[e];
-          if (p.act) {
-            float a = bias[e];
-#pragma unroll
-            for (int k = 0; k < K; ++k) a = fmaf(w[k][e], win[k][e], a);
-            const float sg = sigmoid(a);
-            d *= sg * fmaf(a, 1.f - sg, 1.f);
-          }
-          if (mine) {
-            db[e] += d;
-#pragma unroll
-            for (int k = 0; k < K; ++k) dw[k][e] = fmaf(d, win[k][e], dw[k][e]);
-          }
-        }
-        dp[K - 1][e] = d;
-      }
-      // dx_m for m = i - K + 1 is complete: sum_j w[K-1-j] dp_{m+j}
-      const int m = i - K + 1;
-      if (m < i0 && !(head && m < 0)) continue;
-      float o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float a = 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) a = fmaf(w[K - 1 - j][e], dp[j][e], a);
-        o[e] = m < len ? a : 0.f;
-      }
-      if (m < 0) {
-        store8(static_cast<T*>(p.state_out) + ((long long)b * (K - 1) + K - 1 + m) * p.D + c0, n, p.s_wide, o);
+      if (j + A < real) {
+        read(j + A);
       } else {
-        const int t = p.reverse && m < len ? len - 1 - m : m;
-        store8(static_cast<T*>(p.out) + ((long long)b * p.L + t) * p.D + c0, n, p.o_wide, o);
+#pragma unroll
+        for (int a = 0; a < A; ++a) {
+          nx[a].zero();
+          ny[a].zero();
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < A; ++a) {
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            win[k][e] = win[k + 1][e];
+            dp[k][e] = dp[k + 1][e];
+          }
+        float g[4], o[4];
+        vx[a].get(win[K - 1]);
+        vy[a].get(g);   // 0 where there is no token, and so is dp
+        const bool count = j + a < mine;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float d = g[e];
+          if (p.act) {
+            float s = bias[e];
+#pragma unroll
+            for (int k = 0; k < K; ++k) s = fmaf(w[k][e], win[k][e], s);
+            const float sg = sigmoid(s);
+            d *= sg * fmaf(s, 1.f - sg, 1.f);
+          }
+          d = j + a < real ? d : 0.f;
+          dp[K - 1][e] = d;
+          const float dm = count ? d : 0.f;
+          db[e] += dm;
+#pragma unroll
+          for (int k = 0; k < K; ++k) dw[k][e] = fmaf(dm, win[k][e], dw[k][e]);
+          // dx_m for m = i - K + 1 is complete
+          o[e] = 0.f;
+#pragma unroll
+          for (int q = 0; q < K; ++q) o[e] = fmaf(w[K - 1 - q][e], dp[q][e], o[e]);
+        }
+        const int m = j + a - K + 1;
+        if (m >= 0 && m < mine)
+          store4(dx + m * d_hop, l.n, l.ow, o);
+        else if (m < 0 && i0 == 0 && p.state_out)
+          store4(static_cast<T*>(p.state_out) + ((long long)b * (K - 1) + K - 1 + m) * p.D + c0, l.n, l.sw, o);
       }
     }
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = max(i0, l.len); i < i1; ++i)
+      store4(static_cast<T*>(p.out) + ((long long)b * p.L + i) * p.D + c0, l.n, l.ow, zero);
   }
   float* part = p.part + (size_t)blockIdx.y * p.D * (K + 1);
 #pragma unroll
   for (int k = 0; k <= K; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sh[r][lane][e] = k < K ? dw[k < K ? k : 0][e] : db[e];
+    for (int e = 0; e < 4; ++e) sh[r][lane][e] = k < K ? dw[k < K ? k : 0][e] : db[e];
     __syncthreads();
-    // thread (lane, r): channel c0 + r
-    float s = 0.f;
+    if (r < 4 && c0 + r < p.D) {   // thread (lane, r): channel c0 + r
+      float s = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += sh[q][lane][r];
-    const int c = c0 + r;
-    if (c < p.D) {
-      if (k < K) part[(size_t)c * K + k] = s;
-      else part[(size_t)p.D * K + c] = s;
+      for (int q = 0; q < 8; ++q) s += sh[q][lane][r];
+      if (k < K) part[(size_t)(c0 + r) * K + k] = s;
+      else part[(size_t)p.D * K + c0 + r] = s;
     }
   }
 }
@@ -259,18 +374,30 @@ cudaError_t run_step(const void* x, void* state, const float* weight, const floa
   return cudaGetLastError();
 }
 
-// CTAs along the runs: enough to fill the SMs twice with the channels' CTAs.
-int conv_parts(int B, int L, int D) {
-  const long long lines = (long long)B * ((L + kRun - 1) / kRun);
-  const int across = (D + 255) / 256;
-  const long long want = (lines + 7) / 8, most = (4 * kSmCount + across - 1) / across;
+// Tokens of a run: as many as leave each SM some `threads` threads, in steps
+// of the tokens read ahead (less K - 1 in the gradients, whose runs end K - 1
+// tokens later); 64 at most, where the K - 1 tokens read twice are 5%.
+int run_length(int B, int L, int D, int behind, int threads) {
+  const long long vecs = (long long)B * ((D + 3) / 4);
+  const long long want = (vecs * L + (long long)kSmCount * threads - 1) / ((long long)kSmCount * threads);
+  int run = (int)(want < 8 ? 8 : want > 64 ? 64 : (want + 7) / 8 * 8);
+  return run - behind > 0 ? run - behind : 8;
+}
+int bwd_run(int B, int L, int D, int K) { return run_length(B, L, D, K - 1, 512); }
+
+// CTAs along the runs in the gradients: what the SMs hold at once.
+int conv_parts(int B, int L, int D, int K) {
+  const int run = bwd_run(B, L, D, K);
+  const long long lines = (long long)B * ((L + run - 1) / run);
+  const int across = (D + 127) / 128;
+  const long long want = (lines + 7) / 8, most = (2 * kSmCount + across - 1) / across;
   return (int)(want < most ? want : most);
 }
 
 }  // namespace
 
 size_t conv_bwd_workspace_bytes(int B, int L, int D, int K) {
-  return sizeof(float) * (size_t)conv_parts(B, L, D) * D * (K + 1);
+  return sizeof(float) * (size_t)conv_parts(B, L, D, K) * D * (K + 1);
 }
 
 cudaError_t launch_conv_fwd(const lion_conv_args& a, cudaStream_t s) {
@@ -288,8 +415,9 @@ cudaError_t launch_conv_fwd(const lion_conv_args& a, cudaStream_t s) {
   p.D = a.D;
   p.act = a.act;
   p.reverse = a.reverse;
-  p.nvec = (a.D + 7) / 8;
-  p.runs = (a.L + kRun - 1) / kRun;
+  p.nvec = (a.D + 3) / 4;
+  p.run = run_length(a.B, a.L, a.D, 0, 1024);
+  p.runs = (a.L + p.run - 1) / p.run;
   const int es = a.dtype == DT_BF16 ? 2 : 4;
   p.x_wide = rows_wide(a.x, p.x_ld, es);
   p.o_wide = rows_wide(a.y, a.D, es);
@@ -314,13 +442,14 @@ cudaError_t launch_conv_bwd(const lion_conv_bwd_args& a, void* ws, cudaStream_t 
   p.D = a.D;
   p.act = a.act;
   p.reverse = a.reverse;
-  p.nvec = (a.D + 7) / 8;
-  p.runs = (a.L + kRun - 1) / kRun;
+  p.nvec = (a.D + 3) / 4;
+  p.run = bwd_run(a.B, a.L, a.D, a.K);
+  p.runs = (a.L + p.run - 1) / p.run;
   const int es = a.dtype == DT_BF16 ? 2 : 4;
   p.x_wide = rows_wide(a.x, p.x_ld, es);
   p.o_wide = rows_wide(a.dx, a.D, es) && rows_wide(a.dy, a.D, es);
   p.s_wide = rows_wide(a.state, a.D, es) && rows_wide(a.dstate, a.D, es);
-  const int parts = conv_parts(a.B, a.L, a.D);
+  const int parts = conv_parts(a.B, a.L, a.D, a.K);
   cudaError_t e = LION_CONV_DISPATCH(run_bwd, a.dtype, a.K, p, parts, s);
   if (e != cudaSuccess) return e;
   return launch_sum_parts(p.part, parts, (long long)a.D * (a.K + 1), (long long)a.D * a.K, a.dweight, a.D, a.dbias, 0, nullptr, s);

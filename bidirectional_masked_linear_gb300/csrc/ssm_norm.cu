@@ -90,79 +90,136 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) layernorm_fwd_kernel(No
   }
 }
 
-// dx, and the CTA's share of dweight and dbias: each thread keeps the same
-// columns for every row it takes and adds them up in registers.
-template <typename T, int TPR, int NV>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) layernorm_bwd_kernel(NormP p) {
-  __shared__ float red[32];
-  extern __shared__ float sp[];   // [4][2][cols] for the warp form
-  constexpr int RPC = TPR == 32 ? 4 : 1;
-  const int r = TPR == 32 ? threadIdx.x >> 5 : 0, lane = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
-  const float inv = 1.f / p.cols;
-  float dw[NV][8], db[NV][8];
+// Eight raw elements as they lie in memory, read ahead of their use.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool wide) {
+    if (wide && n >= 8) {
+      r = *reinterpret_cast<const uint4*>(p);
+    } else {
+      unsigned short h[8];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+      for (int e = 0; e < 8; ++e) h[e] = e < n ? reinterpret_cast<const unsigned short*>(p)[e] : 0;
+      r = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack8(r, v); }
+};
+template <>
+struct Raw8<float> {
+  float f[8];
+  __device__ __forceinline__ void load(const float* p, int n, bool wide) { load8(p, n, wide, f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = f[e];
+  }
+};
+
+// dx, and the CTA's share of dweight and dbias.  A row is shared by NW warps,
+// eight columns a thread (NV times over), so that a thread's sums for its
+// columns and the next row, read ahead, fit few registers and many rows are
+// under way; RS rows at a time in a CTA, each with a barrier of its own.
+template <typename T, int NW, int NV, int RS>
+__global__ void __launch_bounds__(32 * NW * RS) layernorm_bwd_kernel(NormP p) {
+  constexpr int TPR = 32 * NW;
+  constexpr bool kAhead = NV <= 2;   // the next row is read ahead where it fits the registers
+  __shared__ float2 red[RS][2][NW];
+  extern __shared__ float sp[];   // [RS][2][cols] where RS > 1
+  const int rs = threadIdx.x / TPR, tid = threadIdx.x % TPR, lane = tid & 31;
+  const float inv = 1.f / p.cols;
+  float dw[NV][8], db[NV][8], w[NV][8];
+  int n[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    n[j] = max(0, p.cols - 8 * (tid + j * TPR));
+    load8(p.weight + 8 * (tid + j * TPR), n[j], p.w_wide, w[j]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[j][e] = db[j][e] = 0.f;
-  for (long long row = (long long)blockIdx.x * RPC + r; row < p.rows; row += (long long)gridDim.x * RPC) {
-    const T* x = static_cast<const T*>(p.x) + row * p.x_row;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.cols;
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float v[NV][8], g[NV][8], s1 = 0.f, s2 = 0.f;
+  }
+  const long long hop = (long long)gridDim.x * RS;
+  long long row = (long long)blockIdx.x * RS + rs;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_row + 8 * tid;
+  const T* dy = static_cast<const T*>(p.dy) + row * p.cols + 8 * tid;
+  T* dx = static_cast<T*>(p.out) + row * p.cols + 8 * tid;
+  Raw8<T> rx[NV], ry[NV];
+  float mean = 0.f, rstd = 0.f;
+  auto read = [&](long long r) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (lane + j * TPR), n = max(0, p.cols - c);
-      load8(x + c, n, p.x_wide, v[j]);
-      load8(dy + c, n, p.o_wide, g[j]);
-      float w[8];
-      load8(p.weight + c, n, p.w_wide, w);
+      rx[j].load(x + 8 * j * TPR, n[j], p.x_wide);
+      ry[j].load(dy + 8 * j * TPR, n[j], p.o_wide);
+    }
+    mean = p.mean[r];
+    rstd = p.rstd[r];
+    x += hop * p.x_row;
+    dy += hop * p.cols;
+  };
+  if (kAhead && row < p.rows) read(row);
+  for (int turn = 0; row < p.rows; row += hop, turn ^= 1) {
+    if (!kAhead) read(row);
+    float v[NV][8], g[NV][8], s1 = 0.f, s2 = 0.f;
+    const float rs_now = rstd;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      rx[j].get(v[j]);
+      ry[j].get(g[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[j][e] = e < n ? (v[j][e] - mean) * rstd : 0.f;
+        v[j][e] = e < n[j] ? (v[j][e] - mean) * rs_now : 0.f;
         dw[j][e] = fmaf(g[j][e], v[j][e], dw[j][e]);
         db[j][e] += g[j][e];
-        g[j][e] *= w[e];
+        g[j][e] *= w[j][e];
         s1 += g[j][e];
         s2 = fmaf(g[j][e], v[j][e], s2);
       }
     }
-    s1 = row_sum<TPR>(s1, red) * inv;
-    s2 = row_sum<TPR>(s2, red) * inv;
-    T* dx = static_cast<T*>(p.out) + row * p.cols;
+    if (kAhead && row + hop < p.rows) read(row + hop);
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (NW > 1) {
+      if (lane == 0) red[rs][turn][tid >> 5] = make_float2(s1, s2);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + rs), "n"(TPR) : "memory");
+      s1 = s2 = 0.f;
+#pragma unroll
+      for (int q = 0; q < NW; ++q) {
+        const float2 t = red[rs][turn][q];
+        s1 += t.x;
+        s2 += t.y;
+      }
+    }
+    s1 *= inv;
+    s2 *= inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (lane + j * TPR), n = p.cols - c;
-      if (n <= 0) break;
+      if (n[j] <= 0) break;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = rstd * (g[j][e] - fmaf(v[j][e], s2, s1));
-      store8(dx + c, n, p.o_wide, v[j]);
+      for (int e = 0; e < 8; ++e) v[j][e] = rs_now * (g[j][e] - fmaf(v[j][e], s2, s1));
+      store8(dx + 8 * j * TPR, n[j], p.o_wide, v[j]);
     }
+    dx += hop * p.cols;
   }
   float* part = p.part + (size_t)blockIdx.x * 2 * p.cols;
-  if (TPR == 32) {
+  float* mine = RS > 1 ? sp + rs * 2 * p.cols : part;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (lane + j * TPR);
+  for (int j = 0; j < NV; ++j) {
+    const int c = 8 * (tid + j * TPR);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < p.cols) {
-          sp[(2 * r) * p.cols + c + e] = dw[j][e];
-          sp[(2 * r + 1) * p.cols + c + e] = db[j][e];
-        }
-    }
+    for (int e = 0; e < 8; ++e)
+      if (e < n[j]) {
+        mine[c + e] = dw[j][e];
+        mine[p.cols + c + e] = db[j][e];
+      }
+  }
+  if (RS > 1) {
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * p.cols; c += 128)
-      part[c] = (sp[c] + sp[2 * p.cols + c]) + (sp[4 * p.cols + c] + sp[6 * p.cols + c]);
-  } else {
+    for (int c = threadIdx.x; c < 2 * p.cols; c += TPR * RS) {
+      float s = sp[c];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (lane + j * TPR);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < p.cols) {
-          part[c + e] = dw[j][e];
-          part[p.cols + c + e] = db[j][e];
-        }
+      for (int q = 1; q < RS; ++q) s += sp[q * 2 * p.cols + c];
+      part[c] = s;
     }
   }
 }
@@ -173,51 +230,68 @@ cudaError_t run_fwd(const NormP& p, cudaStream_t s) {
   layernorm_fwd_kernel<T, TPR, NV><<<(unsigned)((p.rows + RPC - 1) / RPC), TPR == 32 ? 128 : TPR, 0, s>>>(p);
   return cudaGetLastError();
 }
-template <typename T, int TPR, int NV>
+template <typename T, int NW, int NV, int RS>
 cudaError_t run_bwd(const NormP& p, int ctas, cudaStream_t s) {
-  layernorm_bwd_kernel<T, TPR, NV>
-      <<<ctas, TPR == 32 ? 128 : TPR, TPR == 32 ? sizeof(float) * 8 * p.cols : 0, s>>>(p);
+  layernorm_bwd_kernel<T, NW, NV, RS>
+      <<<ctas, 32 * NW * RS, RS > 1 ? sizeof(float) * RS * 2 * p.cols : 0, s>>>(p);
   return cudaGetLastError();
 }
 
 // The row's threads and vectors by its length.
-#define LION_NORM_DISPATCH(RUN, T, ...)                                   \
-  (p.cols <= 256     ? RUN<T, 32, 1>(__VA_ARGS__)                         \
-   : p.cols <= 512   ? RUN<T, 32, 2>(__VA_ARGS__)                         \
-   : p.cols <= 768   ? RUN<T, 32, 3>(__VA_ARGS__)                         \
-   : p.cols <= 1024  ? RUN<T, 32, 4>(__VA_ARGS__)                         \
-   : p.cols <= 2048  ? RUN<T, 256, 1>(__VA_ARGS__)                        \
-   : p.cols <= 4096  ? RUN<T, 256, 2>(__VA_ARGS__)                        \
-   : p.cols <= 8192  ? RUN<T, 512, 2>(__VA_ARGS__)                        \
-                     : RUN<T, 512, 4>(__VA_ARGS__))
-
-constexpr int kNormMaxCtas = 4 * kSmCount;
-int norm_ctas(int rows, int cols) {
-  const long long per = cols <= 1024 ? 4 : 1;
-  const long long want = (rows + per - 1) / per;
-  return (int)(want < kNormMaxCtas ? want : kNormMaxCtas);
+template <typename T>
+cudaError_t run_fwd_any(const NormP& p, cudaStream_t s) {
+  return p.cols <= 256    ? run_fwd<T, 32, 1>(p, s)
+         : p.cols <= 512  ? run_fwd<T, 32, 2>(p, s)
+         : p.cols <= 768  ? run_fwd<T, 32, 3>(p, s)
+         : p.cols <= 1024 ? run_fwd<T, 32, 4>(p, s)
+         : p.cols <= 2048 ? run_fwd<T, 256, 1>(p, s)
+         : p.cols <= 4096 ? run_fwd<T, 256, 2>(p, s)
+         : p.cols <= 8192 ? run_fwd<T, 512, 2>(p, s)
+                          : run_fwd<T, 512, 4>(p, s);
+}
+template <typename T>
+cudaError_t run_bwd_any(const NormP& p, int ctas, cudaStream_t s) {
+  return p.cols <= 256    ? run_bwd<T, 1, 1, 8>(p, ctas, s)
+         : p.cols <= 512  ? run_bwd<T, 2, 1, 4>(p, ctas, s)
+         : p.cols <= 768  ? run_bwd<T, 3, 1, 4>(p, ctas, s)
+         : p.cols <= 1024 ? run_bwd<T, 4, 1, 4>(p, ctas, s)
+         : p.cols <= 2048 ? run_bwd<T, 8, 1, 1>(p, ctas, s)
+         : p.cols <= 4096 ? run_bwd<T, 16, 1, 1>(p, ctas, s)
+         : p.cols <= 8192 ? run_bwd<T, 16, 2, 1>(p, ctas, s)
+                          : run_bwd<T, 16, 4, 1>(p, ctas, s);
 }
 
-// part[p * stride + i] summed over p: 8 threads an element, each every eighth p.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* part, int P, long long stride, long long n1,
-                                                        float* out1, long long n2, float* out2, long long n3, float* out3) {
-  __shared__ float sh[8][33];
+// CTAs of the gradients: what the SMs hold at once, as far as there are rows.
+int norm_ctas(int rows, int cols) {
+  const int per = cols <= 256 ? 8 : cols <= 1024 ? 4 : 1;
+  const int most = kSmCount * (cols <= 512 ? 4 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1);
+  const long long want = ((long long)rows + per - 1) / per;
+  return (int)(want < most ? want : most);
+}
+
+// part[p * stride + i] summed over p: 32 threads an element, each every 32nd p.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int P, long long stride, long long n1,
+                                                         float* out1, long long n2, float* out2, long long n3,
+                                                         float* out3) {
+  __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const long long n = n1 + n2 + n3, i = (long long)blockIdx.x * 32 + lane;
+  const long long n = n1 + n2 + n3, i0 = (long long)blockIdx.x * 32, i = i0 + lane;
   float s = 0.f;
-  if (i < n)
-    for (int q = r; q < P; q += 8) s += part[q * stride + i];
+  if (i < n) {
+#pragma unroll 4
+    for (int q = r; q < P; q += 32) s += part[q * stride + i];
+  }
   sh[r][lane] = s;
   __syncthreads();
-  if (r == 0 && i < n) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) s += sh[k][lane];
-    if (i < n1) {
-      if (out1) out1[i] = s;
-    } else if (i < n1 + n2) {
-      if (out2) out2[i - n1] = s;
+  const long long o = i0 + r;   // warp r: element r of the CTA's 32
+  s = warp_sum(sh[lane][r]);
+  if (lane == 0 && o < n) {
+    if (o < n1) {
+      if (out1) out1[o] = s;
+    } else if (o < n1 + n2) {
+      if (out2) out2[o - n1] = s;
     } else if (out3) {
-      out3[i - n1 - n2] = s;
+      out3[o - n1 - n2] = s;
     }
   }
 }
@@ -227,7 +301,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* part, int P
 cudaError_t launch_sum_parts(const float* part, int P, long long stride, long long n1, float* out1, long long n2, float* out2,
                              long long n3, float* out3, cudaStream_t s) {
   const long long n = n1 + n2 + n3;
-  sum_parts_kernel<<<(unsigned)((n + 31) / 32), 256, 0, s>>>(part, P, stride, n1, out1, n2, out2, n3, out3);
+  sum_parts_kernel<<<(unsigned)((n + 31) / 32), 1024, 0, s>>>(part, P, stride, n1, out1, n2, out2, n3, out3);
   return cudaGetLastError();
 }
 
@@ -247,7 +321,7 @@ cudaError_t launch_layernorm_fwd(const lion_layernorm_args& a, cudaStream_t s) {
   p.x_wide = rows_wide(a.x, p.x_row, es);
   p.o_wide = rows_wide(a.y, a.cols, es);
   p.w_wide = rows_wide(a.weight, 0, 4) && rows_wide(a.bias, 0, 4);
-  return a.dtype == DT_BF16 ? LION_NORM_DISPATCH(run_fwd, __nv_bfloat16, p, s) : LION_NORM_DISPATCH(run_fwd, float, p, s);
+  return a.dtype == DT_BF16 ? run_fwd_any<__nv_bfloat16>(p, s) : run_fwd_any<float>(p, s);
 }
 
 size_t layernorm_bwd_workspace_bytes(int rows, int cols) {
@@ -271,8 +345,7 @@ cudaError_t launch_layernorm_bwd(const lion_layernorm_bwd_args& a, void* ws, cud
   p.o_wide = rows_wide(a.dx, a.cols, es) && rows_wide(a.dy, a.cols, es);
   p.w_wide = rows_wide(a.weight, 0, 4);
   const int ctas = norm_ctas(a.rows, a.cols);
-  cudaError_t e = a.dtype == DT_BF16 ? LION_NORM_DISPATCH(run_bwd, __nv_bfloat16, p, ctas, s)
-                                     : LION_NORM_DISPATCH(run_bwd, float, p, ctas, s);
+  cudaError_t e = a.dtype == DT_BF16 ? run_bwd_any<__nv_bfloat16>(p, ctas, s) : run_bwd_any<float>(p, ctas, s);
   if (e != cudaSuccess) return e;
   return launch_sum_parts(p.part, ctas, 2LL * a.cols, a.cols, a.dweight, a.cols, a.dbias, 0, nullptr, s);
 }

@@ -16,6 +16,8 @@
 
 namespace lion {
 
+constexpr int kStateEvery = LION_SCAN_STATE_EVERY;
+
 struct ScanP {
   const void* u;
   const void* dt;
@@ -122,22 +124,87 @@ __device__ __forceinline__ void store_pair(float* dst, const f2 (&v)[2]) {
   *reinterpret_cast<float4*>(dst) = make_float4(a.x, a.y, b.x, b.y);
 }
 
-// The sums over the LN lanes of a channel of V = LN values, the k-th left in
-// the lane whose place is k: each step halves the values that a lane carries.
-// `step`: the distance between neighbouring places in lanes.
-template <int LN>
-__device__ __forceinline__ float sum_states(float (&v)[LN], int ln, int step = 1) {
-#pragma unroll
-  for (int w = LN / 2; w >= 1; w /= 2) {
-    const bool up = ln & w;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w * step);
-    }
-  }
-  return v[0];
+// Four adjacent elements of shared or global memory.
+__device__ __forceinline__ void get(const float* p, float (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
 }
+__device__ __forceinline__ void get(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void put(float* p, int n, bool wide, const float (&v)[4]) {
+  if (wide && n >= 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+__device__ __forceinline__ void put(__nv_bfloat16* p, int n, bool wide, const float (&v)[4]) {
+  if (wide && n >= 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+// n <= V = 16 bytes' worth of elements to shared memory, zeros behind them.
+template <typename T>
+__device__ __forceinline__ void fetch(T* dst, const T* src, int n, bool wide) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (wide && n >= V) {
+    copy_async16(dst, src);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[e] = e < n ? src[e] : from_f32<T>(0.f);
+  }
+}
+
+// A warp's copies of [TT][W] rows in pieces of 16 bytes: piece q = lane + 32 k
+// is PV elements of token q / PPR.  The source moves on a tile at a time.
+template <typename T, int TT, int W>
+struct Feed {
+  static constexpr int PV = 16 / (int)sizeof(T), PPR = W / PV, PIECES = TT * PPR, PK = (PIECES + 31) / 32;
+  static_assert(PPR <= 32 && 32 % PPR == 0, "a lane's pieces have one place in their tokens");
+  const T* src;
+  long long hop;   // elements from a lane's piece to its next, 32 / PPR tokens on
+  int n;           // elements there are of a piece
+  __device__ __forceinline__ void start(const void* base, long long ld, long long off, const ScanP& p, const ScanAt& w,
+                                        int i0, int lane, int width) {
+    const int c = lane % PPR * PV;
+    src = static_cast<const T*>(base) + ((long long)w.b * p.L + token_of(p, i0 + lane / PPR)) * ld + off + c;
+    hop = (p.reverse ? -(32 / PPR) : 32 / PPR) * ld;
+    n = min(PV, width - c);
+  }
+  __device__ __forceinline__ void next(T* dst, int lo, int hi, int lane, bool wide, bool whole, long long tile) {
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < PK; ++k) {
+        const int q = lane + 32 * k;
+        if (PIECES % 32 == 0 || q < PIECES) copy_async16(dst + q * PV, src + k * hop);
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < PK; ++k) {
+        const int q = lane + 32 * k, t = q / PPR;
+        if (PIECES % 32 == 0 || q < PIECES)
+          fetch<T>(dst + q * PV, src + k * hop, t >= lo && t < hi ? n : 0, wide);
+      }
+    }
+    src += tile;
+  }
+};
 
 // delta of eight channels from the step sizes read.
 __device__ __forceinline__ void deltas(const ScanP& p, int d, int n, float (&dt)[8], float (&raw)[8]) {

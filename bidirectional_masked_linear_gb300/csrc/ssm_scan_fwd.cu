@@ -44,88 +44,6 @@ struct FwdWarp {
   } raw[2];
 };
 
-// Four adjacent elements of shared or global memory.
-__device__ __forceinline__ void get(const float* p, float (&v)[4]) {
-  const float4 x = *reinterpret_cast<const float4*>(p);
-  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-}
-__device__ __forceinline__ void get(const __nv_bfloat16* p, float (&v)[4]) {
-  const uint2 r = *reinterpret_cast<const uint2*>(p);
-  const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-}
-__device__ __forceinline__ void put(float* p, int n, bool wide, const float (&v)[4]) {
-  if (wide && n >= 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) p[e] = v[e];
-  }
-}
-__device__ __forceinline__ void put(__nv_bfloat16* p, int n, bool wide, const float (&v)[4]) {
-  if (wide && n >= 4) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) p[e] = __float2bfloat16_rn(v[e]);
-  }
-}
-
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-}
-// n <= V = 16 bytes' worth of elements to shared memory, zeros behind them.
-template <typename T>
-__device__ __forceinline__ void fetch(T* dst, const T* src, int n, bool wide) {
-  constexpr int V = 16 / (int)sizeof(T);
-  if (wide && n >= V) {
-    copy_async16(dst, src);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) dst[e] = e < n ? src[e] : from_f32<T>(0.f);
-  }
-}
-
-// A warp's copies of [TT][W] rows in pieces of 16 bytes: piece q = lane + 32 k
-// is PV elements of token q / PPR.  The source moves on a tile at a time.
-template <typename T, int TT, int W>
-struct Feed {
-  static constexpr int PV = 16 / (int)sizeof(T), PPR = W / PV, PIECES = TT * PPR, PK = (PIECES + 31) / 32;
-  static_assert(PPR <= 32 && 32 % PPR == 0, "a lane's pieces have one place in their tokens");
-  const T* src;
-  long long hop;   // elements from a lane's piece to its next, 32 / PPR tokens on
-  int n;           // elements there are of a piece
-  __device__ __forceinline__ void start(const void* base, long long ld, long long off, const ScanP& p, const ScanAt& w,
-                                        int i0, int lane, int width) {
-    const int c = lane % PPR * PV;
-    src = static_cast<const T*>(base) + ((long long)w.b * p.L + token_of(p, i0 + lane / PPR)) * ld + off + c;
-    hop = (p.reverse ? -(32 / PPR) : 32 / PPR) * ld;
-    n = min(PV, width - c);
-  }
-  __device__ __forceinline__ void next(T* dst, int lo, int hi, int lane, bool wide, bool whole, long long tile) {
-    if (whole) {
-#pragma unroll
-      for (int k = 0; k < PK; ++k) {
-        const int q = lane + 32 * k;
-        if (PIECES % 32 == 0 || q < PIECES) copy_async16(dst + q * PV, src + k * hop);
-      }
-    } else {
-#pragma unroll 1
-      for (int k = 0; k < PK; ++k) {
-        const int q = lane + 32 * k, t = q / PPR;
-        if (PIECES % 32 == 0 || q < PIECES)
-          fetch<T>(dst + q * PV, src + k * hop, t >= lo && t < hi ? n : 0, wide);
-      }
-    }
-    src += tile;
-  }
-};
-
 template <int COUNT>
 __device__ __forceinline__ const float* as_fp32(const float* raw, float*, int) { return raw; }
 template <int COUNT>
@@ -251,8 +169,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kern
 
   int stage = 0;
   for (int i0 = MAIN ? w.i0 : a0; i0 < (MAIN ? w.i1 : a1); i0 += TT) {
-    if (MAIN && p.states && i0 % N == 0) {
-      float* to = p.states + ((size_t)w.b * p.nst + i0 / N) * p.D * N + state_at;
+    if (MAIN && p.states && i0 % kStateEvery == 0) {
+      float* to = p.states + ((size_t)w.b * p.nst + i0 / kStateEvery) * p.D * N + state_at;
 #pragma unroll
       for (int k = 0; k < RC; ++k)
         if (live[k]) store_states<RN>(to + (k ^ odd) * N, h[k]);
@@ -532,7 +450,7 @@ ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int warps, long
   r.nblk = (D / G + cta_channels - 1) / cta_channels;
   const long long have = (long long)B * G * r.nblk * warps;
   long long nseg = have >= enough ? 1 : (want + have - 1) / have;
-  const long long most = L / 128 > 1 ? L / 128 : 1;
+  const long long most = L / 64 > 1 ? L / 64 : 1;
   if (nseg > most) nseg = most;
   long long len = (L + nseg - 1) / nseg;
   len = (len + 63) / 64 * 64;   // whole tiles
@@ -580,7 +498,7 @@ void fill_scan(ScanP& p, const lion_scan_args& a) {
   p.c_ld = a.c_token ? a.c_token : (long long)a.G * a.N;
   p.softplus = a.dt_softplus;
   p.reverse = a.reverse;
-  p.nst = (a.L + a.N - 1) / a.N;
+  p.nst = (a.L + kStateEvery - 1) / kStateEvery;
   const int es = a.dtype == DT_BF16 ? 2 : 4;
   const bool whole = a.G == 1 || p.Dg * es % 16 == 0;   // a group's first channel keeps the alignment
   p.u_wide = whole && rows_wide(a.u, p.u_ld, es);

@@ -27,6 +27,7 @@ ACT_NONE, ACT_SILU = 0, 1
 ACTIVATIONS = {"none": ACT_NONE, None: ACT_NONE, "silu": ACT_SILU}
 LAYERNORM_MAX_COLS = 16384
 STATE_SIZES = (8, 16, 32, 64)
+STATE_EVERY = 16
 
 _vp, _i, _ll, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
 
@@ -451,7 +452,7 @@ def scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus=Tru
     with _on(stream):
         y = torch.empty((B, L, D), dtype=u.dtype, device=u.device) if out is None else out
         h = torch.empty((B, D, N), dtype=torch.float32, device=u.device) if return_state else None
-        states = (torch.empty((B, -(-L // N), D, N), dtype=torch.float32, device=u.device) if save_states
+        states = (torch.empty((B, -(-L // STATE_EVERY), D, N), dtype=torch.float32, device=u.device) if save_states
                   else None)
         ws, nb, keep = _workspace(workspace, 0 if workspace is not None
                                   else lib.lion_scan_workspace_bytes(B, L, D, N, G), u)
@@ -475,7 +476,7 @@ def scan_bwd(dout, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softpl
     B, L, D, N, G, tokens = _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths)
     _same("dout", dout, u.dtype)
     _tight("dout", dout, (B, L, D))
-    _f32("states", states, (B, -(-L // N), D, N))
+    _f32("states", states, (B, -(-L // STATE_EVERY), D, N))
     _cuda(dout, states)
     with _on(stream):
         du = torch.empty((B, L, D), dtype=u.dtype, device=u.device)

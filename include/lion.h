@@ -556,10 +556,12 @@ lion_status lion_conv_step(const void* x, void* state, const float* weight, cons
  *   u, dt, z  [B][L][D] (z NULL: no gate);  B, C  [B][L][G][N];  A [D][N];
  *   Dskip, dt_bias [D] or NULL;  h0 [B][D][N] or NULL for zeros.
  *   out [B][L][D];  h_out [B][D][N] or NULL: the state after the last token.
- *   states [B][ceil(L/N)][D][N] float32 or NULL: the state before every N-th
- *   processed token, which spares lion_scan_bwd the recomputation.
+ *   states [B][ceil(L/16)][D][N] float32 or NULL: the state before every
+ *   LION_SCAN_STATE_EVERY-th processed token, which spares lion_scan_bwd the
+ *   recomputation.
  *   N in {8, 16, 32, 64} (else LION_ERR_UNSUPPORTED), G divides D.
  */
+#define LION_SCAN_STATE_EVERY 16
 typedef struct {
   const void* u;
   const void* dt;

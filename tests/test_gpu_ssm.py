@@ -277,14 +277,14 @@ def test_scan(B, L, D, N, G, lens, off, reverse, dtype):
 
 @pytest.mark.parametrize("N", (8, 16, 32, 64))
 def test_scan_states(N):
-    """The saved states are the states before every N-th token."""
-    B, L, D = 2, 3 * N + 5, 37
+    """The saved states are the states before every 16th token."""
+    B, L, D, E = 2, 3 * ssm.STATE_EVERY + 5, 37, ssm.STATE_EVERY
     a, _ = _scan_inputs(B, L, D, N, 1, "fp32", True, True, True, True, True, seed=N)
     dev = {k: v.cuda() for k, v in a.items()}
     f = ssm.scan_fwd(**dev, save_states=True)
     assert torch.equal(f.states[:, 0], dev["h0"])
     for k in range(1, f.states.shape[1]):
-        cut = {q: v[:, :k * N].contiguous() if q in ("u", "dt", "Bm", "Cm", "z") else v for q, v in dev.items()}
+        cut = {q: v[:, :k * E].contiguous() if q in ("u", "dt", "Bm", "Cm", "z") else v for q, v in dev.items()}
         h = ssm.scan_fwd(**cut, return_state=True).h
         err = (h - f.states[:, k]).abs().max()
         assert float(err) <= 1e-5 * float(h.abs().max())
