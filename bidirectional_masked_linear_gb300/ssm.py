@@ -14,14 +14,13 @@ workspaces belong to it; inputs made on another stream have to be ready on it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import lion
-from .lion import _check, _dtype_code, _ptr
+from .lion import _check, _ptr
 
 ACT_NONE, ACT_SILU = 0, 1
 ACTIVATIONS = {"none": ACT_NONE, None: ACT_NONE, "silu": ACT_SILU}
@@ -106,14 +105,37 @@ def load():
 
 
 # ------------------------------------------------------------ argument checks
+#
+# A one-token call takes some ten microseconds, most of them here: the checks
+# test for the right argument first and look for what is wrong only after.
 
-def _on(stream):
-    """The context that makes outputs and workspaces belong to `stream`."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+_CODES = {torch.bfloat16: lion.DTYPE_BF16, torch.float32: lion.DTYPE_FP32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _handle(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
+
+
+def _new(stream, shape, dtype, like):
+    """An uninitialised tensor that belongs to `stream`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _code(x):
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"activations must be bfloat16 or float32, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    return code
 
 
 def _act(activation):
@@ -122,39 +144,37 @@ def _act(activation):
     return ACTIVATIONS[activation]
 
 
-def _f32(name, t, shape):
-    if t is None:
-        return
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be float32, got {t.dtype}")
-    _tight(name, t, shape)
-
-
-def _tight(name, t, shape):
+def _tight(name, t, dtype, shape):
+    """The address of a contiguous tensor of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _same(name, t, dtype):
-    if t.dtype != dtype:
+def _maybe(name, t, dtype, shape):
+    return None if t is None else _tight(name, t, dtype, shape)
+
+
+def _token(name, t, dtype, shape):
+    """(address, distance between tokens) of a [B, L, ...] activation whose
+    last dimensions are adjacent."""
+    width = shape[2] if len(shape) == 3 else shape[2] * shape[3]
+    if t.dtype is dtype and t.shape == shape and t.is_cuda:
+        if t.is_contiguous():
+            return t.data_ptr(), width
+    elif t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} as the other activations, got {t.dtype}")
-
-
-def _lengths(lengths, B):
-    if lengths is None:
-        return
-    if lengths.dtype != torch.int32:
-        raise TypeError(f"lengths must be int32, got {lengths.dtype}")
-    _tight("lengths", lengths, (B,))
-
-
-def _token(name, t, B, L, width):
-    """The distance between tokens of a [B, L, ...] activation whose last
-    dimensions, `width` values in all, are adjacent."""
-    if t.is_contiguous():
-        return width
+    elif not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    else:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    B, L = shape[:2]
     s, run = t.stride(), 1
     for k in range(t.dim() - 1, 1, -1):
         if t.shape[k] != 1 and s[k] != run:
@@ -168,24 +188,19 @@ def _token(name, t, B, L, width):
             raise ValueError(f"{name}: sequences must lie L tokens apart")
     if ld < width:
         raise ValueError(f"{name}: tokens must not overlap")
-    return ld
+    return t.data_ptr(), ld
 
 
-def _cuda(*tensors):
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("tensors must be on the GPU")
-
-
-def _workspace(workspace, nbytes, like):
-    """(pointer, bytes) of the caller's workspace, or of one from PyTorch's
-    allocator (kept alive by the third value)."""
+def _workspace(workspace, nbytes, like, stream):
+    """(address, bytes, owner) of the caller's workspace, or of one from
+    PyTorch's allocator (which reuses it once the stream has passed the call)."""
     if workspace is not None:
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    if nbytes == 0:
+    n = nbytes()
+    if n == 0:
         return None, 0, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    return ws.data_ptr(), nbytes, ws
+    ws = _new(stream, n, torch.uint8, like)
+    return ws.data_ptr(), n, ws
 
 
 # ------------------------------------------------------------------ layer norm
@@ -207,20 +222,15 @@ def layernorm_bwd_workspace_bytes(rows, cols) -> int:
 def layernorm_fwd(x, weight, bias=None, eps=1e-5, save_stats=False, out=None, stream=None):
     """Layer norm over the last dimension: ``y``, or ``(y, mean, rstd)`` with
     ``save_stats`` (float32, one per row, for :func:`layernorm_bwd`)."""
-    lib = load()
+    lib, code = load(), _code(x)
     rows, cols, ld = _rows(x)
-    code = _dtype_code(x)
-    _f32("weight", weight, (cols,))
-    _f32("bias", bias, (cols,))
-    _cuda(x, weight, bias, out)
-    with _on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if save_stats else None
-        rstd = torch.empty_like(mean) if save_stats else None
-    _same("out", y, x.dtype)
-    _tight("out", y, x.shape)
-    a = _NormArgs(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), ld, rows, cols, eps, code,
-                  _handle(stream))
+    w, b = _tight("weight", weight, torch.float32, (cols,)), _maybe("bias", bias, torch.float32, (cols,))
+    y = _new(stream, x.shape, x.dtype, x) if out is None else out
+    yp = _tight("out", y, x.dtype, x.shape)
+    mean = rstd = None
+    if save_stats:
+        mean, rstd = (_new(stream, x.shape[:-1], torch.float32, x) for _ in range(2))
+    a = _NormArgs(x.data_ptr(), w, b, yp, _ptr(mean), _ptr(rstd), ld, rows, cols, eps, code, _handle(stream))
     _check(lib.lion_layernorm_fwd(ctypes.byref(a)))
     return (y, mean, rstd) if save_stats else y
 
@@ -228,23 +238,15 @@ def layernorm_fwd(x, weight, bias=None, eps=1e-5, save_stats=False, out=None, st
 def layernorm_bwd(dy, x, weight, mean, rstd, bias=True, workspace=None, stream=None):
     """``(dx, dweight, dbias)`` given ``dy`` and the forward's ``mean`` and
     ``rstd``; ``dbias`` is None with ``bias=False``."""
-    lib = load()
+    lib, code = load(), _code(x)
     rows, cols, ld = _rows(x)
-    code = _dtype_code(x)
-    _same("dy", dy, x.dtype)
-    _tight("dy", dy, x.shape)
-    _f32("weight", weight, (cols,))
-    _f32("mean", mean, x.shape[:-1])
-    _f32("rstd", rstd, x.shape[:-1])
-    _cuda(dy, x, weight, mean, rstd)
-    with _on(stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(cols, dtype=torch.float32, device=x.device)
-        db = torch.empty_like(dw) if bias else None
-        ws, nb, keep = _workspace(workspace, 0 if workspace is not None
-                                  else lib.lion_layernorm_bwd_workspace_bytes(rows, cols), x)
-    a = _NormBwdArgs(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), ld,
-                     rows, cols, code, ws, nb, _handle(stream))
+    f32, per = torch.float32, x.shape[:-1]
+    ptrs = (_tight("dy", dy, x.dtype, x.shape), x.data_ptr(), _tight("weight", weight, f32, (cols,)),
+            _tight("mean", mean, f32, per), _tight("rstd", rstd, f32, per))
+    dx, dw = _new(stream, x.shape, x.dtype, x), _new(stream, (cols,), f32, x)
+    db = _new(stream, (cols,), f32, x) if bias else None
+    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_layernorm_bwd_workspace_bytes(rows, cols), x, stream)
+    a = _NormBwdArgs(*ptrs, dx.data_ptr(), dw.data_ptr(), _ptr(db), ld, rows, cols, code, ws, nb, _handle(stream))
     _check(lib.lion_layernorm_bwd(ctypes.byref(a)))
     return dx, dw, db
 
@@ -276,19 +278,20 @@ class ConvGrads(NamedTuple):
     dstate: Optional[torch.Tensor]
 
 
-def _conv_args(x, weight, bias, state, lengths):
-    B, L, D = x.shape
+def _taps(weight, D):
     if weight.dim() != 2:
         raise ValueError("weight must have shape [D, K]")
     K = weight.shape[1]
-    _f32("weight", weight, (D, K))
-    _f32("bias", bias, (D,))
-    if state is not None:
-        _same("state", state, x.dtype)
-        _tight("state", state, (B, K - 1, D))
-    _lengths(lengths, B)
-    _cuda(x, weight, bias, state, lengths)
-    return B, L, D, K, _token("x", x, B, L, D)
+    return _tight("weight", weight, torch.float32, (D, K)), K
+
+
+def _conv_args(x, weight, bias, state, lengths):
+    shape = B, L, D = x.shape
+    w, K = _taps(weight, D)
+    xp, ld = _token("x", x, x.dtype, shape)
+    return (B, L, D, K), ld, (xp, w, _maybe("bias", bias, torch.float32, (D,)),
+                              _maybe("state", state, x.dtype, (B, K - 1, D)),
+                              _maybe("lengths", lengths, torch.int32, (B,)))
 
 
 def conv_bwd_workspace_bytes(B, L, D, K) -> int:
@@ -302,17 +305,12 @@ def conv_fwd(x, weight, bias=None, activation="silu", state=None, lengths=None, 
     inputs, [B, K-1, D], for the next call or :func:`conv_step`).  ``state``:
     the inputs before the first token.  ``lengths``: int32 [B], the tokens
     each sequence has.  ``reverse``: walk from the last token."""
-    lib = load()
-    code = _dtype_code(x)
-    B, L, D, K, ld = _conv_args(x, weight, bias, state, lengths)
-    with _on(stream):
-        y = torch.empty((B, L, D), dtype=x.dtype, device=x.device) if out is None else out
-        new = torch.empty((B, K - 1, D), dtype=x.dtype, device=x.device) if return_state else None
-    _same("out", y, x.dtype)
-    _tight("out", y, (B, L, D))
-    _cuda(y)
-    a = _ConvArgs(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(lengths), _ptr(y), _ptr(new), ld, B, L, D, K,
-                  _act(activation), int(reverse), code, _handle(stream))
+    lib, code = load(), _code(x)
+    (B, L, D, K), ld, ptrs = _conv_args(x, weight, bias, state, lengths)
+    y = _new(stream, x.shape, x.dtype, x) if out is None else out
+    new = _new(stream, (B, K - 1, D), x.dtype, x) if return_state else None
+    a = _ConvArgs(*ptrs, _tight("out", y, x.dtype, x.shape), _ptr(new), ld, B, L, D, K, _act(activation),
+                  int(reverse), code, _handle(stream))
     _check(lib.lion_conv_fwd(ctypes.byref(a)))
     return (y, new) if return_state else y
 
@@ -321,22 +319,16 @@ def conv_bwd(dy, x, weight, bias=None, activation="silu", state=None, lengths=No
              stream=None):
     """Gradients through :func:`conv_fwd`'s ``y``: :class:`ConvGrads`
     (``dbias`` and ``dstate`` None where there is no bias or state)."""
-    lib = load()
-    code = _dtype_code(x)
-    B, L, D, K, ld = _conv_args(x, weight, bias, state, lengths)
-    _same("dy", dy, x.dtype)
-    _tight("dy", dy, (B, L, D))
-    _cuda(dy)
-    with _on(stream):
-        dx = torch.empty((B, L, D), dtype=x.dtype, device=x.device)
-        dw = torch.empty((D, K), dtype=torch.float32, device=x.device)
-        db = None if bias is None else torch.empty(D, dtype=torch.float32, device=x.device)
-        ds = None if state is None else torch.empty_like(state)
-        ws, nb, keep = _workspace(workspace, 0 if workspace is not None
-                                  else lib.lion_conv_bwd_workspace_bytes(B, L, D, K), x)
-    a = _ConvBwdArgs(_ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(lengths), _ptr(dx), _ptr(dw),
-                     _ptr(db), _ptr(ds), ld, B, L, D, K, _act(activation), int(reverse), code, ws, nb,
-                     _handle(stream))
+    lib, code = load(), _code(x)
+    (B, L, D, K), ld, ptrs = _conv_args(x, weight, bias, state, lengths)
+    dyp = _tight("dy", dy, x.dtype, x.shape)
+    f32 = torch.float32
+    dx, dw = _new(stream, x.shape, x.dtype, x), _new(stream, (D, K), f32, x)
+    db = None if bias is None else _new(stream, (D,), f32, x)
+    ds = None if state is None else _new(stream, state.shape, x.dtype, x)
+    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_conv_bwd_workspace_bytes(B, L, D, K), x, stream)
+    a = _ConvBwdArgs(dyp, *ptrs, dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds), ld, B, L, D, K, _act(activation),
+                     int(reverse), code, ws, nb, _handle(stream))
     _check(lib.lion_conv_bwd(ctypes.byref(a)))
     return ConvGrads(dx, dw, db, ds)
 
@@ -344,24 +336,13 @@ def conv_bwd(dy, x, weight, bias=None, activation="silu", state=None, lengths=No
 def conv_step(x, state, weight, bias=None, activation="silu", out=None, stream=None):
     """One token ``x`` [B, D]: its output, with the window in ``state``
     [B, K-1, D] moved on in place."""
-    lib = load()
-    code = _dtype_code(x)
+    lib, code = load(), _code(x)
     B, D = x.shape
-    if weight.dim() != 2:
-        raise ValueError("weight must have shape [D, K]")
-    K = weight.shape[1]
-    _f32("weight", weight, (D, K))
-    _f32("bias", bias, (D,))
-    _tight("x", x, (B, D))
-    _same("state", state, x.dtype)
-    _tight("state", state, (B, K - 1, D))
-    with _on(stream):
-        y = torch.empty((B, D), dtype=x.dtype, device=x.device) if out is None else out
-    _same("out", y, x.dtype)
-    _tight("out", y, (B, D))
-    _cuda(x, weight, bias, state, y)
-    _check(lib.lion_conv_step(_ptr(x), _ptr(state), _ptr(weight), _ptr(bias), _ptr(y), B, D, K, _act(activation),
-                              code, _handle(stream)))
+    w, K = _taps(weight, D)
+    y = _new(stream, (B, D), x.dtype, x) if out is None else out
+    _check(lib.lion_conv_step(_tight("x", x, x.dtype, (B, D)), _tight("state", state, x.dtype, (B, K - 1, D)), w,
+                              _maybe("bias", bias, torch.float32, (D,)), _tight("out", y, x.dtype, (B, D)), B, D, K,
+                              _act(activation), code, _handle(stream)))
     return y
 
 
@@ -403,29 +384,29 @@ class ScanGrads(NamedTuple):
     dh0: Optional[torch.Tensor]
 
 
-def _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths):
-    B, L, D = u.shape
+def _states(A, D):
     if A.dim() != 2 or A.shape[0] != D:
         raise ValueError("A must have shape [D, N]")
-    N = A.shape[1]
+    return A.shape[1]
+
+
+def _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths):
+    """Sizes, addresses in the structures' order, distances between tokens."""
+    shape = B, L, D = u.shape
+    N, T, f32 = _states(A, D), u.dtype, torch.float32
     if Bm.dim() == 3:   # one group
         Bm, Cm = Bm.unsqueeze(2), Cm.unsqueeze(2)
     G = Bm.shape[2]
-    for name, t, shape in (("dt", dt, (B, L, D)), ("Bm", Bm, (B, L, G, N)), ("Cm", Cm, (B, L, G, N)),
-                           ("z", z, (B, L, D))):
-        if t is not None:
-            _same(name, t, u.dtype)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    _f32("A", A, (D, N))
-    _f32("Dskip", Dskip, (D,))
-    _f32("dt_bias", dt_bias, (D,))
-    _f32("h0", h0, (B, D, N))
-    _lengths(lengths, B)
-    _cuda(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths)
-    tokens = (_token("u", u, B, L, D), _token("dt", dt, B, L, D), 0 if z is None else _token("z", z, B, L, D),
-              _token("Bm", Bm, B, L, G * N), _token("Cm", Cm, B, L, G * N))
-    return B, L, D, N, G, tokens
+    up, ul = _token("u", u, T, shape)
+    dp, dl = _token("dt", dt, T, shape)
+    bp, bl = _token("Bm", Bm, T, (B, L, G, N))
+    cp, cl = _token("Cm", Cm, T, (B, L, G, N))
+    zp, zl = (None, 0) if z is None else _token("z", z, T, shape)
+    return ((B, L, D, N, G),
+            (up, dp, _tight("A", A, f32, (D, N)), bp, cp, _maybe("Dskip", Dskip, f32, (D,)), zp,
+             _maybe("dt_bias", dt_bias, f32, (D,)), _maybe("h0", h0, f32, (B, D, N)),
+             _maybe("lengths", lengths, torch.int32, (B,))),
+            (ul, dl, zl, bl, cl))
 
 
 def scan_workspace_bytes(B, L, D, N, G=1) -> int:
@@ -446,22 +427,15 @@ def scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus=Tru
     ``save_states`` the ``states`` that spare :func:`scan_bwd` the
     recomputation.  ``h0``: the state before the first token; ``lengths``,
     ``reverse``: as :func:`conv_fwd`."""
-    lib = load()
-    code = _dtype_code(u)
-    B, L, D, N, G, tokens = _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths)
-    with _on(stream):
-        y = torch.empty((B, L, D), dtype=u.dtype, device=u.device) if out is None else out
-        h = torch.empty((B, D, N), dtype=torch.float32, device=u.device) if return_state else None
-        states = (torch.empty((B, -(-L // STATE_EVERY), D, N), dtype=torch.float32, device=u.device) if save_states
-                  else None)
-        ws, nb, keep = _workspace(workspace, 0 if workspace is not None
-                                  else lib.lion_scan_workspace_bytes(B, L, D, N, G), u)
-    _same("out", y, u.dtype)
-    _tight("out", y, (B, L, D))
-    _cuda(y)
-    a = _ScanArgs(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z), _ptr(dt_bias), _ptr(h0),
-                  _ptr(lengths), _ptr(y), _ptr(h), _ptr(states), *tokens, B, L, D, N, G, int(dt_softplus),
-                  int(reverse), code, ws, nb, _handle(stream))
+    lib, code = load(), _code(u)
+    sizes, ptrs, tokens = _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths)
+    B, L, D, N, G = sizes
+    y = _new(stream, u.shape, u.dtype, u) if out is None else out
+    h = _new(stream, (B, D, N), torch.float32, u) if return_state else None
+    states = _new(stream, (B, -(-L // STATE_EVERY), D, N), torch.float32, u) if save_states else None
+    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_scan_workspace_bytes(*sizes), u, stream)
+    a = _ScanArgs(*ptrs, _tight("out", y, u.dtype, u.shape), _ptr(h), _ptr(states), *tokens, *sizes,
+                  int(dt_softplus), int(reverse), code, ws, nb, _handle(stream))
     _check(lib.lion_scan_fwd(ctypes.byref(a)))
     return ScanOut(y, h, states)
 
@@ -471,29 +445,24 @@ def scan_bwd(dout, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softpl
     """Gradients through :func:`scan_fwd`'s ``out`` given ``dout`` [B, L, D]:
     :class:`ScanGrads`, with None for what was not given.  ``states``: the
     forward's (recomputed if None)."""
-    lib = load()
-    code = _dtype_code(u)
-    B, L, D, N, G, tokens = _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths)
-    _same("dout", dout, u.dtype)
-    _tight("dout", dout, (B, L, D))
-    _f32("states", states, (B, -(-L // STATE_EVERY), D, N))
-    _cuda(dout, states)
-    with _on(stream):
-        du = torch.empty((B, L, D), dtype=u.dtype, device=u.device)
-        ddt = torch.empty_like(du)
-        dz = None if z is None else torch.empty_like(du)
-        dB = torch.empty(Bm.shape, dtype=u.dtype, device=u.device)
-        dC = torch.empty_like(dB)
-        dA = torch.empty((D, N), dtype=torch.float32, device=u.device)
-        dD = None if Dskip is None else torch.empty(D, dtype=torch.float32, device=u.device)
-        dbias = None if dt_bias is None else torch.empty(D, dtype=torch.float32, device=u.device)
-        dh0 = None if h0 is None else torch.empty((B, D, N), dtype=torch.float32, device=u.device)
-        ws, nb, keep = _workspace(workspace, 0 if workspace is not None else
-                                  lib.lion_scan_bwd_workspace_bytes(B, L, D, N, G, int(states is not None)), u)
-    a = _ScanBwdArgs(_ptr(dout), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z),
-                     _ptr(dt_bias), _ptr(h0), _ptr(lengths), _ptr(states), _ptr(du), _ptr(ddt), _ptr(dA), _ptr(dB),
-                     _ptr(dC), _ptr(dD), _ptr(dz), _ptr(dbias), _ptr(dh0), *tokens, B, L, D, N, G,
-                     int(dt_softplus), int(reverse), code, ws, nb, _handle(stream))
+    lib, code = load(), _code(u)
+    sizes, ptrs, tokens = _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths)
+    B, L, D, N, G = sizes
+    f32 = torch.float32
+    dop = _tight("dout", dout, u.dtype, u.shape)
+    sp = _maybe("states", states, f32, (B, -(-L // STATE_EVERY), D, N))
+    du, ddt = (_new(stream, u.shape, u.dtype, u) for _ in range(2))
+    dB, dC = (_new(stream, Bm.shape, u.dtype, u) for _ in range(2))
+    dz = None if z is None else _new(stream, u.shape, u.dtype, u)
+    dA = _new(stream, (D, N), f32, u)
+    dD = None if Dskip is None else _new(stream, (D,), f32, u)
+    dbias = None if dt_bias is None else _new(stream, (D,), f32, u)
+    dh0 = None if h0 is None else _new(stream, (B, D, N), f32, u)
+    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_scan_bwd_workspace_bytes(*sizes, int(states is not None)),
+                               u, stream)
+    a = _ScanBwdArgs(dop, *ptrs, sp, du.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(),
+                     _ptr(dD), _ptr(dz), _ptr(dbias), _ptr(dh0), *tokens, *sizes, int(dt_softplus), int(reverse),
+                     code, ws, nb, _handle(stream))
     _check(lib.lion_scan_bwd(ctypes.byref(a)))
     return ScanGrads(du, ddt, dA, dB, dC, dD, dz, dbias, dh0)
 
@@ -502,31 +471,17 @@ def scan_step(h, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus
     """One token: ``u``, ``dt``, ``z`` [B, D], ``Bm``, ``Cm`` [B, G, N] or
     [B, N]; returns its output [B, D], with the state ``h`` [B, D, N]
     updated in place."""
-    lib = load()
-    code = _dtype_code(u)
-    B, D = u.shape
-    if A.dim() != 2 or A.shape[0] != D:
-        raise ValueError("A must have shape [D, N]")
-    N = A.shape[1]
+    lib, code = load(), _code(u)
+    shape = B, D = u.shape
+    N, T, f32 = _states(A, D), u.dtype, torch.float32
     G = Bm.shape[1] if Bm.dim() == 3 else 1
-    for name, t in (("u", u), ("dt", dt), ("z", z)):
-        if t is not None:
-            _same(name, t, u.dtype)
-            _tight(name, t, (B, D))
-    for name, t in (("Bm", Bm), ("Cm", Cm)):
-        _same(name, t, u.dtype)
-        _tight(name, t, (B, G, N) if Bm.dim() == 3 else (B, N))
-    _f32("h", h, (B, D, N))
-    _f32("A", A, (D, N))
-    _f32("Dskip", Dskip, (D,))
-    _f32("dt_bias", dt_bias, (D,))
-    with _on(stream):
-        y = torch.empty((B, D), dtype=u.dtype, device=u.device) if out is None else out
-    _same("out", y, u.dtype)
-    _tight("out", y, (B, D))
-    _cuda(h, u, dt, A, Bm, Cm, Dskip, z, dt_bias, y)
-    a = _ScanStepArgs(_ptr(h), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z), _ptr(dt_bias),
-                      _ptr(y), B, D, N, G, int(dt_softplus), code, _handle(stream))
+    bc = (B, G, N) if Bm.dim() == 3 else (B, N)
+    y = _new(stream, shape, T, u) if out is None else out
+    a = _ScanStepArgs(_tight("h", h, f32, (B, D, N)), _tight("u", u, T, shape), _tight("dt", dt, T, shape),
+                      _tight("A", A, f32, (D, N)), _tight("Bm", Bm, T, bc), _tight("Cm", Cm, T, bc),
+                      _maybe("Dskip", Dskip, f32, (D,)), _maybe("z", z, T, shape),
+                      _maybe("dt_bias", dt_bias, f32, (D,)), _tight("out", y, T, shape), B, D, N, G,
+                      int(dt_softplus), code, _handle(stream))
     _check(lib.lion_scan_step(ctypes.byref(a)))
     return y
 
