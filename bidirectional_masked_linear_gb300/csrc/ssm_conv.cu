@@ -30,7 +30,7 @@ struct ConvP {
   int act, reverse;
   int nvec;           // vectors of four channels
   int run, runs;      // tokens of a run; runs of a sequence
-  bool x_wide, o_wide, s_wide;
+  bool x_wide, o_wide, s_wide, w_wide, items32;
 };
 
 __device__ __forceinline__ int clamp_len(const int* lengths, int b, int L) {
@@ -42,6 +42,19 @@ template <typename T>
 struct Ahead {
   static constexpr int N = sizeof(T) == 2 ? 8 : 4;
 };
+
+// Four channels as two pairs.
+struct Quad {
+  f2 p[2];
+  __device__ __forceinline__ Quad() {}
+  __device__ __forceinline__ explicit Quad(const float (&v)[4]) { p[0] = pack2(v[0], v[1]); p[1] = pack2(v[2], v[3]); }
+  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = p[0].x; v[1] = p[0].y; v[2] = p[1].x; v[3] = p[1].y; }
+};
+__device__ __forceinline__ Quad zero4() {
+  Quad q;
+  q.p[0] = q.p[1] = pack2(0.f, 0.f);
+  return q;
+}
 
 // Four raw elements.
 template <typename T>
@@ -60,9 +73,11 @@ struct Raw4<__nv_bfloat16> {
       r = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
     }
   }
-  __device__ __forceinline__ void get(float (&v)[4]) const {
-    const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  __device__ __forceinline__ Quad get() const {
+    Quad q;
+    q.p[0] = unpack_bf16(r.x);
+    q.p[1] = unpack_bf16(r.y);
+    return q;
   }
 };
 template <>
@@ -73,9 +88,16 @@ struct Raw4<float> {
     if (wide) r = *reinterpret_cast<const float4*>(p);
     else r = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
   }
-  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+  __device__ __forceinline__ Quad get() const {
+    Quad q;
+    q.p[0] = pack2(r.x, r.y);
+    q.p[1] = pack2(r.z, r.w);
+    return q;
+  }
 };
-__device__ __forceinline__ void store4(float* p, int n, bool wide, const float (&v)[4]) {
+__device__ __forceinline__ void store4(float* p, int n, bool wide, const Quad& q) {
+  float v[4];
+  q.get(v);
   if (wide) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
@@ -84,7 +106,9 @@ __device__ __forceinline__ void store4(float* p, int n, bool wide, const float (
       if (e < n) p[e] = v[e];
   }
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, int n, bool wide, const float (&v)[4]) {
+__device__ __forceinline__ void store4(__nv_bfloat16* p, int n, bool wide, const Quad& q) {
+  float v[4];
+  q.get(v);
   if (wide) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
     *reinterpret_cast<uint2*>(p) =
@@ -96,12 +120,29 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, int n, bool wide, const
   }
 }
 
+// The taps of channels c0 .. c0 + 3 (adjacent in memory) and their bias.
 template <int K>
-__device__ __forceinline__ void load_taps(const float* weight, int c0, int n, float (&w)[K][4]) {
+__device__ __forceinline__ void load_taps(const ConvP& p, int c0, Quad (&w)[K], Quad& bias) {
+  float f[4 * K], b[4];
+  const int n = p.D - c0;
+  if (p.w_wide && n >= 4) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
+    for (int k = 0; k < K; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(p.weight + (size_t)c0 * K + 4 * k);
+      f[4 * k] = x.x; f[4 * k + 1] = x.y; f[4 * k + 2] = x.z; f[4 * k + 3] = x.w;
+    }
+  } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k][e] = e < n ? weight[(size_t)(c0 + e) * K + k] : 0.f;
+    for (int k = 0; k < 4 * K; ++k) f[k] = k < n * K ? p.weight[(size_t)c0 * K + k] : 0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = p.bias && e < n ? p.bias[c0 + e] : 0.f;
+  bias = Quad(b);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const float v[4] = {f[k], f[K + k], f[2 * K + k], f[3 * K + k]};
+    w[k] = Quad(v);
+  }
 }
 
 // A thread's line: four channels of one sequence.
@@ -118,29 +159,36 @@ struct Line {
   }
   __device__ __forceinline__ int token(const ConvP& p, int i) const { return p.reverse ? len - 1 - i : i; }
   // The input processed i-th (i < 0: from the state; zeros where there is none).
-  __device__ __forceinline__ void at(const ConvP& p, int i, float (&v)[4]) const {
+  __device__ __forceinline__ Raw4<T> at(const ConvP& p, int i) const {
     Raw4<T> r;
     r.zero();
     if (i >= 0 && i < len)
       r.load(static_cast<const T*>(p.x) + ((long long)b * p.L + token(p, i)) * p.x_ld + c0, n, xw);
     else if (i < 0 && i >= -(K - 1) && p.state)
       r.load(static_cast<const T*>(p.state) + ((long long)b * (K - 1) + K - 1 + i) * p.D + c0, n, sw);
-    r.get(v);
+    return r;
   }
 };
+
+// bias + sum_k w_k win_k
+template <int K>
+__device__ __forceinline__ f2 taps(const Quad (&w)[K], const Quad (&win)[K], f2 bias, int h) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) bias = fma2(w[k].p[h], win[k].p[h], bias);
+  return bias;
+}
 
 template <typename T, int K>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(ConvP p) {
   constexpr int A = Ahead<T>::N;
-  const long long item = (long long)blockIdx.x * 128 + threadIdx.x, line = item / p.nvec;
-  const int b = (int)(line / p.runs), i0 = (int)(line - (long long)b * p.runs) * p.run;
+  const unsigned long long item = (unsigned long long)blockIdx.x * 128 + threadIdx.x;
+  // divisions in 32 bits wherever the problem allows
+  const unsigned line = p.items32 ? (unsigned)item / (unsigned)p.nvec : (unsigned)(item / (unsigned)p.nvec);
+  const int b = (int)(line / (unsigned)p.runs), i0 = (int)(line - (unsigned)b * p.runs) * p.run;
   if (b >= p.B) return;
-  const Line<T, K> l(p, b, 4 * (int)(item - line * p.nvec));
+  const Line<T, K> l(p, b, 4 * (int)(item - (unsigned long long)line * p.nvec));
   const int i1 = min(i0 + p.run, p.L);
-  float w[K][4], bias[4], win[K][4];
-  load_taps<K>(p.weight, l.c0, l.n, w);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) bias[e] = p.bias && e < l.n ? p.bias[l.c0 + e] : 0.f;
+  Quad w[K], bias, win[K];
   const long long x_hop = p.reverse ? -p.x_ld : p.x_ld, y_hop = p.reverse ? -p.D : p.D;
   const T* x = static_cast<const T*>(p.x) + ((long long)b * p.L + l.token(p, i0)) * p.x_ld + l.c0;
   T* y = static_cast<T*>(p.out) + ((long long)b * p.L + l.token(p, i0)) * p.D + l.c0;
@@ -156,68 +204,60 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(ConvP p) {
   };
   read(0);
 #pragma unroll
-  for (int k = 1; k < K; ++k) l.at(p, i0 - K + k, win[k]);
+  for (int k = 1; k < K; ++k) win[k] = l.at(p, i0 - K + k).get();
+  load_taps<K>(p, l.c0, w, bias);
   for (int j = 0; j < real; j += A) {
     Raw4<T> now[A];
 #pragma unroll
     for (int a = 0; a < A; ++a) now[a] = next[a];
     if (j + A < real) read(j + A);
+    const bool full = l.ow && j + A <= real;
 #pragma unroll
     for (int a = 0; a < A; ++a) {
 #pragma unroll
-      for (int k = 0; k + 1 < K; ++k)
+      for (int k = 0; k + 1 < K; ++k) win[k] = win[k + 1];
+      win[K - 1] = now[a].get();
+      Quad o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) win[k][e] = win[k + 1][e];
-      now[a].get(win[K - 1]);
-      float o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float s = bias[e];
-#pragma unroll
-        for (int k = 0; k < K; ++k) s = fmaf(w[k][e], win[k][e], s);
-        o[e] = p.act ? s * sigmoid(s) : s;
+      for (int h = 0; h < 2; ++h) {
+        const f2 s = taps<K>(w, win, bias.p[h], h);
+        o.p[h] = p.act ? mul2(s, sigmoid2(s.x, s.y)) : s;
       }
-      if (j + a < real) store4(y + a * y_hop, l.n, l.ow, o);
+      if (full) store4(y + a * y_hop, 4, true, o);
+      else if (j + a < real) store4(y + a * y_hop, l.n, l.ow, o);
     }
     y += A * y_hop;
   }
   // tokens past the length are not part of the walk: zeros where they lie
-  const float zero[4] = {0.f, 0.f, 0.f, 0.f};
   for (int i = max(i0, l.len); i < i1; ++i)
-    store4(static_cast<T*>(p.out) + ((long long)b * p.L + i) * p.D + l.c0, l.n, l.ow, zero);
+    store4(static_cast<T*>(p.out) + ((long long)b * p.L + i) * p.D + l.c0, l.n, l.ow, zero4());
   if (p.state_out && i0 == 0) {
     T* st = static_cast<T*>(p.state_out) + (long long)b * (K - 1) * p.D + l.c0;
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) {
-      float v[4];
-      l.at(p, l.len - (K - 1) + k, v);
-      store4(st + (long long)k * p.D, l.n, l.sw, v);
-    }
+    for (int k = 0; k < K - 1; ++k)
+      store4(st + (long long)k * p.D, l.n, l.sw, l.at(p, l.len - (K - 1) + k).get());
   }
 }
 
-// One CTA: 32 channel vectors (lanes) x 8 rows of runs.  Each thread keeps its
+constexpr int kBwdRows = 8;   // runs that a CTA walks at a time
+
+// One CTA: 32 channel vectors (lanes) x kBwdRows runs.  Each thread keeps its
 // channels' share of dweight and dbias over all the runs it walks.
 template <typename T, int K>
-__global__ void __launch_bounds__(256) conv_bwd_kernel(ConvP p) {
-  constexpr int A = sizeof(T) == 2 ? 4 : 4;
-  __shared__ float sh[8][32][4];
+__global__ void __launch_bounds__(32 * kBwdRows, 2) conv_bwd_kernel(ConvP p) {
+  constexpr int A = sizeof(T) == 2 ? 4 : 2;   // tokens read ahead, of both inputs
+  __shared__ float sh[kBwdRows][32][4];
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int c0 = 4 * (blockIdx.x * 32 + lane);
   const bool live = c0 < p.D;
-  float w[K][4], bias[4], dw[K][4], db[4];
-  load_taps<K>(p.weight, c0, p.D - c0, w);
+  Quad w[K], bias, dw[K], db = zero4();
+  load_taps<K>(p, live ? c0 : p.D, w, bias);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    bias[e] = p.bias && c0 + e < p.D ? p.bias[c0 + e] : 0.f;
-    db[e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) dw[k][e] = 0.f;
-  }
+  for (int k = 0; k < K; ++k) dw[k] = zero4();
   const long long x_hop = p.reverse ? -p.x_ld : p.x_ld, d_hop = p.reverse ? -p.D : p.D;
-  const long long lines = (long long)p.B * p.runs;
-  for (long long line = (long long)blockIdx.y * 8 + r; live && line < lines; line += (long long)gridDim.y * 8) {
-    const int b = (int)(line / p.runs), i0 = (int)(line - (long long)b * p.runs) * p.run;
+  const int lines = p.B * p.runs;
+  for (int line = blockIdx.y * kBwdRows + r; live && line < lines; line += gridDim.y * kBwdRows) {
+    const int b = line / p.runs, i0 = (line - b * p.runs) * p.run;
     const Line<T, K> l(p, b, c0);
     const int i1 = min(i0 + p.run, p.L), mine = min(i1, l.len) - i0;
     // the sums that end in the run need dp up to K-1 tokens behind it
@@ -241,13 +281,11 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvP p) {
     };
     read(0);
     // win[k] = x_{i-K+1+k}, dp[k] = dp_{i-K+1+k}
-    float win[K][4], dp[K][4];
+    Quad win[K], dp[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) dp[k] = zero4();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dp[k][e] = 0.f;
-#pragma unroll
-    for (int k = 1; k < K; ++k) l.at(p, i0 - K + k, win[k]);
+    for (int k = 1; k < K; ++k) win[k] = l.at(p, i0 - K + k).get();
     const int last = mine + K - 1;   // steps until the run's last dx is complete
     for (int j = 0; j < last; j += A) {
       Raw4<T> vx[A], vy[A];
@@ -256,71 +294,64 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvP p) {
         vx[a] = nx[a];
         vy[a] = ny[a];
       }
-      if (j + A < real) {
-        read(j + A);
-      } else {
-#pragma unroll
-        for (int a = 0; a < A; ++a) {
-          nx[a].zero();
-          ny[a].zero();
-        }
-      }
+      if (j + A < last) read(j + A);
+      // every token of the batch counts, and every sum that it completes is one of the run's
+      const bool full = l.ow && j >= K - 1 && j + A <= mine;
 #pragma unroll
       for (int a = 0; a < A; ++a) {
 #pragma unroll
-        for (int k = 0; k + 1 < K; ++k)
+        for (int k = 0; k + 1 < K; ++k) {
+          win[k] = win[k + 1];
+          dp[k] = dp[k + 1];
+        }
+        win[K - 1] = vx[a].get();
+        const Quad g = vy[a].get();   // 0 where there is no token
+        Quad o;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            win[k][e] = win[k + 1][e];
-            dp[k][e] = dp[k + 1][e];
-          }
-        float g[4], o[4];
-        vx[a].get(win[K - 1]);
-        vy[a].get(g);   // 0 where there is no token, and so is dp
-        const bool count = j + a < mine;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float d = g[e];
+        for (int h = 0; h < 2; ++h) {
+          f2 d = g.p[h];
           if (p.act) {
-            float s = bias[e];
-#pragma unroll
-            for (int k = 0; k < K; ++k) s = fmaf(w[k][e], win[k][e], s);
-            const float sg = sigmoid(s);
-            d *= sg * fmaf(s, 1.f - sg, 1.f);
+            const f2 s = taps<K>(w, win, bias.p[h], h), sg = sigmoid2(s.x, s.y);
+            // silu'(s) = sg + s sg (1 - sg)
+            d = mul2(d, fma2(mul2(s, sg), fma2(sg, pack2(-1.f, -1.f), pack2(1.f, 1.f)), sg));
           }
-          d = j + a < real ? d : 0.f;
-          dp[K - 1][e] = d;
-          const float dm = count ? d : 0.f;
-          db[e] += dm;
+          if (!full && j + a >= real) d = pack2(0.f, 0.f);
+          dp[K - 1].p[h] = d;
+          f2 dm = d;
+          if (!full && j + a >= mine) dm = pack2(0.f, 0.f);
+          db.p[h] = add2(db.p[h], dm);
 #pragma unroll
-          for (int k = 0; k < K; ++k) dw[k][e] = fmaf(dm, win[k][e], dw[k][e]);
+          for (int k = 0; k < K; ++k) dw[k].p[h] = fma2(dm, win[k].p[h], dw[k].p[h]);
           // dx_m for m = i - K + 1 is complete
-          o[e] = 0.f;
+          o.p[h] = mul2(w[K - 1].p[h], dp[0].p[h]);
 #pragma unroll
-          for (int q = 0; q < K; ++q) o[e] = fmaf(w[K - 1 - q][e], dp[q][e], o[e]);
+          for (int q = 1; q < K; ++q) o.p[h] = fma2(w[K - 1 - q].p[h], dp[q].p[h], o.p[h]);
         }
         const int m = j + a - K + 1;
-        if (m >= 0 && m < mine)
+        if (full)
+          store4(dx + m * d_hop, 4, true, o);
+        else if (m >= 0 && m < mine)
           store4(dx + m * d_hop, l.n, l.ow, o);
         else if (m < 0 && i0 == 0 && p.state_out)
           store4(static_cast<T*>(p.state_out) + ((long long)b * (K - 1) + K - 1 + m) * p.D + c0, l.n, l.sw, o);
       }
     }
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     for (int i = max(i0, l.len); i < i1; ++i)
-      store4(static_cast<T*>(p.out) + ((long long)b * p.L + i) * p.D + c0, l.n, l.ow, zero);
+      store4(static_cast<T*>(p.out) + ((long long)b * p.L + i) * p.D + c0, l.n, l.ow, zero4());
   }
   float* part = p.part + (size_t)blockIdx.y * p.D * (K + 1);
 #pragma unroll
   for (int k = 0; k <= K; ++k) {
+    float v[4];
+    (k < K ? dw[k < K ? k : 0] : db).get(v);
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sh[r][lane][e] = k < K ? dw[k < K ? k : 0][e] : db[e];
+    for (int e = 0; e < 4; ++e) sh[r][lane][e] = v[e];
     __syncthreads();
     if (r < 4 && c0 + r < p.D) {   // thread (lane, r): channel c0 + r
       float s = 0.f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s += sh[q][lane][r];
+      for (int q = 0; q < kBwdRows; ++q) s += sh[q][lane][r];
       if (k < K) part[(size_t)(c0 + r) * K + k] = s;
       else part[(size_t)p.D * K + c0 + r] = s;
     }
@@ -357,12 +388,14 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const T* x, T* state, co
 template <typename T, int K>
 cudaError_t run_fwd(const ConvP& p, cudaStream_t s) {
   const long long items = (long long)p.B * p.runs * p.nvec;
-  conv_fwd_kernel<T, K><<<(unsigned)((items + 127) / 128), 128, 0, s>>>(p);
+  ConvP q = p;
+  q.items32 = items + 128 < 0x100000000LL;
+  conv_fwd_kernel<T, K><<<(unsigned)((items + 127) / 128), 128, 0, s>>>(q);
   return cudaGetLastError();
 }
 template <typename T, int K>
 cudaError_t run_bwd(const ConvP& p, int parts, cudaStream_t s) {
-  conv_bwd_kernel<T, K><<<dim3((p.nvec + 31) / 32, parts), 256, 0, s>>>(p);
+  conv_bwd_kernel<T, K><<<dim3((p.nvec + 31) / 32, parts), 32 * kBwdRows, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int K>
@@ -390,7 +423,8 @@ int conv_parts(int B, int L, int D, int K) {
   const int run = bwd_run(B, L, D, K);
   const long long lines = (long long)B * ((L + run - 1) / run);
   const int across = (D + 127) / 128;
-  const long long want = (lines + 7) / 8, most = (2 * kSmCount + across - 1) / across;
+  const long long want = (lines + kBwdRows - 1) / kBwdRows,
+                  most = (2 * kSmCount + across - 1) / across;
   return (int)(want < most ? want : most);
 }
 
@@ -415,6 +449,7 @@ cudaError_t launch_conv_fwd(const lion_conv_args& a, cudaStream_t s) {
   p.D = a.D;
   p.act = a.act;
   p.reverse = a.reverse;
+  p.w_wide = rows_wide(a.weight, 0, 4);
   p.nvec = (a.D + 3) / 4;
   p.run = run_length(a.B, a.L, a.D, 0, 1024);
   p.runs = (a.L + p.run - 1) / p.run;
@@ -442,6 +477,7 @@ cudaError_t launch_conv_bwd(const lion_conv_bwd_args& a, void* ws, cudaStream_t 
   p.D = a.D;
   p.act = a.act;
   p.reverse = a.reverse;
+  p.w_wide = rows_wide(a.weight, 0, 4);
   p.nvec = (a.D + 3) / 4;
   p.run = bwd_run(a.B, a.L, a.D, a.K);
   p.runs = (a.L + p.run - 1) / p.run;

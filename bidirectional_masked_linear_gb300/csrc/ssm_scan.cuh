@@ -48,7 +48,9 @@ struct ScanP {
   int B, L, D, N, G, Dg;
   int nblk, nseg, seglen, nst;
   int softplus, reverse;
-  bool u_wide, dt_wide, z_wide, b_wide, c_wide, o_wide, d_wide;   // o: tight activations, d: dout
+  // the alignment in bytes, 16 at most, of every row of a tensor (d: dout)
+  int u_align, dt_align, z_align, b_align, c_align, d_align;
+  bool o_wide;   // the outputs' rows lie on 16 bytes
 };
 
 namespace {
@@ -155,19 +157,33 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, int n, bool wide, const fl
   }
 }
 
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
   const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
 }
-// n <= V = 16 bytes' worth of elements to shared memory, zeros behind them.
+// n <= V = 16 bytes' worth of elements to shared memory, zeros behind them,
+// asynchronously as far as the source's alignment (in bytes) allows.
 template <typename T>
-__device__ __forceinline__ void fetch(T* dst, const T* src, int n, bool wide) {
+__device__ __forceinline__ void fetch(T* dst, const T* src, int n, int align) {
   constexpr int V = 16 / (int)sizeof(T);
-  if (wide && n >= V) {
-    copy_async16(dst, src);
+  if (n >= V && align >= 4) {
+    if (align == 16) {
+      copy_async<16>(dst, src);
+    } else if (align == 8) {
+      copy_async<8>(dst, src);
+      copy_async<8>(dst + V / 2, src + V / 2);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e += V / 4) copy_async<4>(dst + e, src + e);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) dst[e] = e < n ? src[e] : from_f32<T>(0.f);
+    for (int e = 0; e < V; ++e) {
+      if (sizeof(T) == 4 && e < n) copy_async<4>(dst + e, src + e);
+      else dst[e] = e < n ? src[e] : from_f32<T>(0.f);
+    }
   }
 }
 
@@ -187,19 +203,19 @@ struct Feed {
     hop = (p.reverse ? -(32 / PPR) : 32 / PPR) * ld;
     n = min(PV, width - c);
   }
-  __device__ __forceinline__ void next(T* dst, int lo, int hi, int lane, bool wide, bool whole, long long tile) {
+  __device__ __forceinline__ void next(T* dst, int lo, int hi, int lane, int align, bool whole, long long tile) {
     if (whole) {
 #pragma unroll
       for (int k = 0; k < PK; ++k) {
         const int q = lane + 32 * k;
-        if (PIECES % 32 == 0 || q < PIECES) copy_async16(dst + q * PV, src + k * hop);
+        if (PIECES % 32 == 0 || q < PIECES) copy_async<16>(dst + q * PV, src + k * hop);
       }
     } else {
-#pragma unroll 1
+#pragma unroll 2
       for (int k = 0; k < PK; ++k) {
         const int q = lane + 32 * k, t = q / PPR;
         if (PIECES % 32 == 0 || q < PIECES)
-          fetch<T>(dst + q * PV, src + k * hop, t >= lo && t < hi ? n : 0, wide);
+          fetch<T>(dst + q * PV, src + k * hop, t >= lo && t < hi ? n : 0, align);
       }
     }
     src += tile;
@@ -227,6 +243,12 @@ __device__ __forceinline__ void deltas(const ScanP& p, int d, int n, float (&dt)
                        : N == 32 ? RUN<float, 32>(__VA_ARGS__)                        \
                                  : RUN<float, 64>(__VA_ARGS__)))
 
+// 16, 8, 4 or 2: what divides the address, the distance between rows and that between groups.
+inline int rows_align(const void* p, long long stride, long long group, int es) {
+  const unsigned long long x =
+      reinterpret_cast<uintptr_t>(p) | (unsigned long long)stride * es | (unsigned long long)group * es;
+  return x % 16 == 0 ? 16 : x % 8 == 0 ? 8 : x % 4 == 0 ? 4 : 2;
+}
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline int scan_channels(int N, int W) { return W * 2 * 32 / (N / 4); }
 

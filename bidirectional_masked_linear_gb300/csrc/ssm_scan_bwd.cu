@@ -50,11 +50,11 @@ __global__ void __launch_bounds__(32 * W) scan_bwd_segment_kernel(ScanP p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) dt[e] = dy[e] = 0.f;
     if (real) {
-      load8(static_cast<const T*>(p.dt) + row * p.dt_ld + vd, vn, p.dt_wide, dt);
-      load8(static_cast<const T*>(p.dout) + row * p.D + vd, vn, p.d_wide, dy);
+      load8(static_cast<const T*>(p.dt) + row * p.dt_ld + vd, vn, p.dt_align == 16, dt);
+      load8(static_cast<const T*>(p.dout) + row * p.D + vd, vn, p.d_align == 16, dy);
       if (p.z) {
         float z[8];
-        load8(static_cast<const T*>(p.z) + row * p.z_ld + vd, vn, p.z_wide, z);
+        load8(static_cast<const T*>(p.z) + row * p.z_ld + vd, vn, p.z_align == 16, z);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dy[e] *= z[e] * sigmoid(z[e]);
       }
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
     dskip[e] = dbias[e] = 0.f;
   }
   const int r0 = max(w.i0, w.v0), r1 = min(w.i1, w.v1);   // the tokens that there are
-  const bool plain = w.nch == CW && p.u_wide && p.dt_wide && p.d_wide && (!GATE || p.z_wide) && p.o_wide;
+  const bool plain = w.nch == CW && p.o_wide && (p.u_align & p.dt_align & p.d_align & (GATE ? p.z_align : 16)) == 16;
 
   for (int i0 = w.i0 + (w.i1 - w.i0 - 1) / TT * TT; i0 >= w.i0; i0 -= TT) {
     const bool some = i0 + TT > r0 && i0 < r1;
@@ -211,20 +211,20 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
       {
         Feed<T, TT, CW> f;
         f.start(p.u, p.u_ld, w.d0, p, w, i0, lane, w.nch);
-        f.next(sm.ru, lo, hi, lane, p.u_wide, whole, 0);
+        f.next(sm.ru, lo, hi, lane, p.u_align, whole, 0);
         f.start(p.dt, p.dt_ld, w.d0, p, w, i0, lane, w.nch);
-        f.next(sm.rdt, lo, hi, lane, p.dt_wide, whole, 0);
+        f.next(sm.rdt, lo, hi, lane, p.dt_align, whole, 0);
         f.start(p.dout, p.D, w.d0, p, w, i0, lane, w.nch);
-        f.next(sm.rdo, lo, hi, lane, p.d_wide, whole, 0);
+        f.next(sm.rdo, lo, hi, lane, p.d_align, whole, 0);
         if (GATE) {
           f.start(p.z, p.z_ld, w.d0, p, w, i0, lane, w.nch);
-          f.next(sm.rz, lo, hi, lane, p.z_wide, whole, 0);
+          f.next(sm.rz, lo, hi, lane, p.z_align, whole, 0);
         }
         // B by the first warp, C by the second
         Feed<T, TT, N> fb;
         if (warp < 2) {
           fb.start(warp ? p.Cm : p.Bm, warp ? p.c_ld : p.b_ld, w.g * N, p, w, i0, lane, N);
-          fb.next(warp ? sh.rC : sh.rB, lo, hi, lane, warp ? p.c_wide : p.b_wide, false, 0);
+          fb.next(warp ? sh.rC : sh.rB, lo, hi, lane, warp ? p.c_align : p.b_align, false, 0);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -595,10 +595,11 @@ cudaError_t launch_scan_bwd(const lion_scan_bwd_args& a, void* ws, cudaStream_t 
   ScanP p = {};
   fill_scan(p, f);
   const int es = a.dtype == DT_BF16 ? 2 : 4;
-  const bool whole = a.G == 1 || p.Dg * es % 16 == 0;
+  const long long group = a.G > 1 ? p.Dg : 0;
   p.dout = a.dout;
-  p.d_wide = whole && rows_wide(a.dout, a.D, es);
-  p.o_wide = whole && rows_wide(a.du, a.D, es) && rows_wide(a.ddt, a.D, es) && rows_wide(a.dz, a.D, es);
+  p.d_align = rows_align(a.dout, a.D, group, es);
+  p.o_wide = (rows_align(a.du, a.D, group, es) & rows_align(a.ddt, a.D, group, es) &
+              rows_align(a.dz, a.D, group, es)) == 16;
   p.du = a.du;
   p.ddt = a.ddt;
   p.dz = a.dz;

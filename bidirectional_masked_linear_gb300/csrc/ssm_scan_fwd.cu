@@ -63,12 +63,14 @@ __device__ __forceinline__ const float* as_fp32(const __nv_bfloat16* raw, float*
 // R adjacent floats.
 template <int R>
 __device__ __forceinline__ void get_some(const float* p, float (&v)[R]) {
-  if (R == 4) {
+  if (R == 1) {
+    v[0] = p[0];
+  } else if (R == 4) {
     const float4 x = *reinterpret_cast<const float4*>(p);
-    v[0] = x.x; v[1] = x.y; v[R - 2] = x.z; v[R - 1] = x.w;
+    v[0] = x.x; v[R > 1 ? 1 : 0] = x.y; v[R > 2 ? R - 2 : 0] = x.z; v[R - 1] = x.w;
   } else {
     const float2 x = *reinterpret_cast<const float2*>(p);
-    v[0] = x.x; v[1] = x.y;
+    v[0] = x.x; v[R - 1] = x.y;
   }
 }
 
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kern
     bias[e] = p.dt_bias && e < vn ? p.dt_bias[vd + e] : 0.f;
     skip[e] = MAIN && p.Dskip && e < vn ? p.Dskip[vd + e] : 0.f;
   }
-  const bool plain = w.nch == CW && p.u_wide && p.dt_wide && p.b_wide && p.c_wide && (!p.z || p.z_wide) && p.o_wide;
+  const bool plain = w.nch == CW && p.o_wide && (p.u_align & p.dt_align & p.b_align & p.c_align & (p.z ? p.z_align : 16)) == 16;
   // the tiles that have tokens; MAIN visits the others to write zeros and states
   const int a0 = max(w.i0, w.v0 - w.v0 % TT), a1 = min(w.i1, w.v1), r0 = max(w.i0, w.v0);
   Feed<T, TT, CW> fu, fdt, fz;
@@ -145,11 +147,11 @@ __global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kern
   auto fetch_tile = [&](Raw& to, int i0) {
     const int lo = r0 - i0, hi = a1 - i0;
     const bool whole = plain && lo <= 0 && hi >= TT;
-    fu.next(to.u, lo, hi, lane, p.u_wide, whole, dir * p.u_ld);
-    fdt.next(to.dt, lo, hi, lane, p.dt_wide, whole, dir * p.dt_ld);
-    if (MAIN && p.z) fz.next(to.z, lo, hi, lane, p.z_wide, whole, dir * p.z_ld);
-    fb.next(to.Bm, lo, hi, lane, p.b_wide, whole, dir * p.b_ld);
-    if (MAIN) fc.next(to.Cm, lo, hi, lane, p.c_wide, whole, dir * p.c_ld);
+    fu.next(to.u, lo, hi, lane, p.u_align, whole, dir * p.u_ld);
+    fdt.next(to.dt, lo, hi, lane, p.dt_align, whole, dir * p.dt_ld);
+    if (MAIN && p.z) fz.next(to.z, lo, hi, lane, p.z_align, whole, dir * p.z_ld);
+    fb.next(to.Bm, lo, hi, lane, p.b_align, whole, dir * p.b_ld);
+    if (MAIN) fc.next(to.Cm, lo, hi, lane, p.c_align, whole, dir * p.c_ld);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   if (a0 < a1) fetch_tile(sm.raw[0], a0);
@@ -217,15 +219,15 @@ __global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kern
       const float* Bt = as_fp32<TT * N>(raw.Bm, sm.Bf, lane) + n0;
       const float* Ct = MAIN ? as_fp32<TT * N>(raw.Cm, sm.Cf, lane) + n0 : nullptr;
       __syncwarp();
-#pragma unroll(TT < 4 ? TT : 4)
+#pragma unroll(TT < 8 ? TT : 8)
       for (int t = 0; t < TT; ++t) {
         float dt[RC], du[RC];
         get_some<RC>(sm.dt + t * CW + c0, dt);
         get_some<RC>(sm.du + t * CW + c0, du);
         if (RC == 2 && LN > 1) {   // the odd lane's order
           const float a = dt[0], b = du[0];
-          dt[0] = odd ? dt[1] : a; dt[1] = odd ? a : dt[1];
-          du[0] = odd ? du[1] : b; du[1] = odd ? b : du[1];
+          dt[0] = odd ? dt[RC - 1] : a; dt[RC - 1] = odd ? a : dt[RC - 1];
+          du[0] = odd ? du[RC - 1] : b; du[RC - 1] = odd ? b : du[RC - 1];
         }
         f2 y[RC];
 #pragma unroll
@@ -255,14 +257,16 @@ __global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kern
           for (int k = 0; k < RC; ++k) v[k] = sum2(y[k]);
           float* yo = sm.dt + t * CW + c0;
           if (LN > 1) {
-            float r = v[0] + __shfl_xor_sync(0xffffffffu, v[RC - 1], 1);
+            float r = v[0] + __shfl_xor_sync(0xffffffffu, v[RC - 1], 1);   // RC == 1: both lanes' own
 #pragma unroll
             for (int o = 2; o < LN; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
             yo[odd] = r;   // lanes of one parity hold the same sum
           } else if (RC == 4) {
-            *reinterpret_cast<float4*>(yo) = make_float4(v[0], v[1], v[RC - 2], v[RC - 1]);
+            *reinterpret_cast<float4*>(yo) = make_float4(v[0], v[RC > 1 ? 1 : 0], v[RC > 2 ? RC - 2 : 0], v[RC - 1]);
+          } else if (RC == 2) {
+            *reinterpret_cast<float2*>(yo) = make_float2(v[0], v[RC - 1]);
           } else {
-            *reinterpret_cast<float2*>(yo) = make_float2(v[0], v[1]);
+            yo[0] = v[0];
           }
         }
       }
@@ -453,7 +457,7 @@ ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int warps, long
   const long long most = L / 64 > 1 ? L / 64 : 1;
   if (nseg > most) nseg = most;
   long long len = (L + nseg - 1) / nseg;
-  len = (len + 63) / 64 * 64;   // whole tiles
+  len = (len + 15) / 16 * 16;   // whole tiles
   r.seglen = (int)len;
   r.nseg = (int)((L + len - 1) / len);
   return r;
@@ -500,13 +504,13 @@ void fill_scan(ScanP& p, const lion_scan_args& a) {
   p.reverse = a.reverse;
   p.nst = (a.L + kStateEvery - 1) / kStateEvery;
   const int es = a.dtype == DT_BF16 ? 2 : 4;
-  const bool whole = a.G == 1 || p.Dg * es % 16 == 0;   // a group's first channel keeps the alignment
-  p.u_wide = whole && rows_wide(a.u, p.u_ld, es);
-  p.dt_wide = whole && rows_wide(a.dt, p.dt_ld, es);
-  p.z_wide = whole && rows_wide(a.z, p.z_ld, es);
-  p.o_wide = whole && rows_wide(a.out, a.D, es);
-  p.b_wide = rows_wide(a.Bm, p.b_ld, es);
-  p.c_wide = rows_wide(a.Cm, p.c_ld, es);
+  const long long group = a.G > 1 ? p.Dg : 0;
+  p.u_align = rows_align(a.u, p.u_ld, group, es);
+  p.dt_align = rows_align(a.dt, p.dt_ld, group, es);
+  p.z_align = rows_align(a.z, p.z_ld, group, es);
+  p.b_align = rows_align(a.Bm, p.b_ld, 0, es);
+  p.c_align = rows_align(a.Cm, p.c_ld, 0, es);
+  p.o_wide = rows_align(a.out, a.D, group, es) == 16;
 }
 
 cudaError_t launch_scan_fwd(const lion_scan_args& a, void* ws, cudaStream_t s) {
