@@ -120,8 +120,8 @@ struct BwdSmem {
   using S = BwdTile<T, N>;
   struct Warp {
     alignas(16) float dt[S::TT * S::CW];   // delta
-    alignas(16) float du[S::TT * S::CW];   // delta u, then sum_n G B
-    alignas(16) float dy[S::TT * S::CW];   // dy, then sum_n q A (A scaled by log2 e)
+    alignas(16) float du[S::TT * S::CW];   // delta u, then sum_n q A (A scaled by log2 e)
+    alignas(16) float dy[S::TT * S::CW];   // dy, then sum_n G B
     alignas(16) float y[S::TT * S::CW];    // sum_n C h
     alignas(16) float hs[S::NB][S::RN * S::RC / 4][32][4];   // states at the blocks' starts, a lane's own
     alignas(16) float part[2][kBlock][S::GS];   // dB, dC of a block: [lane group][N]
@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
             }
             gb[k] = sum2(sgb);
             qa[k] = sum2(sqa);
+            asm volatile("" : "+f"(qa[k]) : "f"(du1));   // qa takes delta u's place: its reads come first
             if (GATE) y[k] = sum2(sy);
           }
           // over the states
@@ -369,9 +370,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
               if (GATE) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
             }
           }
-          sm.du[t * CW + c[0]] = gb[0];   // lanes of one parity hold the same sums
-          sm.dy[t * CW + c[0]] = qa[0];
-          if (GATE) sm.y[t * CW + c[0]] = y[0];
+          put_shared(sm.dy + t * CW + c[0], gb[0]);   // lanes of one parity hold the same sums
+          put_shared(sm.du + t * CW + c[0], qa[0]);
+          if (GATE) put_shared(sm.y + t * CW + c[0], y[0]);
           // over the channels, LN lanes apart: first between lanes that hold the blocks of states in opposite
           // order, the rest in shared memory
           float r[8];
@@ -383,8 +384,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
             r[4 + 2 * q + 1] = dC[q].y + __shfl_xor_sync(0xffffffffu, dC[q + 2].y, LN);
           }
           const int at_r = (lc >> 1) * N + n0;
-          *reinterpret_cast<float4*>(sm.part[0][s] + at_r) = make_float4(r[0], r[1], r[2], r[3]);
-          *reinterpret_cast<float4*>(sm.part[1][s] + at_r) = make_float4(r[4], r[5], r[6], r[7]);
+          put_shared(sm.part[0][s] + at_r, r[0], r[1], r[2], r[3]);
+          put_shared(sm.part[1][s] + at_r, r[4], r[5], r[6], r[7]);
         }
         __syncwarp();
 #pragma unroll
@@ -425,8 +426,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
         get(sm.rdt + at, raw);
         get(sm.rdo + at, dout);
         get(sm.dt + at, dl);
-        get(sm.du + at, gb);
-        get(sm.dy + at, qa);
+        get(sm.dy + at, gb);
+        get(sm.du + at, qa);
         float z[4], y[4];
         if (GATE) {
           get(sm.rz + at, z);

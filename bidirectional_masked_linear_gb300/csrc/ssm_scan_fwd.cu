@@ -260,13 +260,13 @@ __global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kern
             float r = v[0] + __shfl_xor_sync(0xffffffffu, v[RC - 1], 1);   // RC == 1: both lanes' own
 #pragma unroll
             for (int o = 2; o < LN; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-            yo[odd] = r;   // lanes of one parity hold the same sum
+            put_shared(yo + odd, r);   // lanes of one parity hold the same sum
           } else if (RC == 4) {
-            *reinterpret_cast<float4*>(yo) = make_float4(v[0], v[RC > 1 ? 1 : 0], v[RC > 2 ? RC - 2 : 0], v[RC - 1]);
+            put_shared(yo, v[0], v[RC > 1 ? 1 : 0], v[RC > 2 ? RC - 2 : 0], v[RC - 1]);
           } else if (RC == 2) {
-            *reinterpret_cast<float2*>(yo) = make_float2(v[0], v[RC - 1]);
+            put_shared(yo, v[0], v[RC - 1]);
           } else {
-            yo[0] = v[0];
+            put_shared(yo, v[0]);
           }
         }
       }
