@@ -9,6 +9,8 @@
 // forwards to the states at every fourth token, then takes the four-token
 // blocks from the last one: forwards once more, the four states and decays
 // staying in registers, and back through them.
+#include <algorithm>
+
 #include "ssm_scan.cuh"
 
 namespace lion {
@@ -534,9 +536,9 @@ struct BwdPlan {
   ScanPlan r;
   size_t fwd, states, seg_state, seg_sum, bc, par, total;
 };
-BwdPlan bwd_plan(int B, int L, int D, int N, int G, bool have_states) {
+BwdPlan bwd_plan(int B, int L, int D, int N, int G, bool have_states, bool ragged) {
   BwdPlan q;
-  q.r = scan_plan(B, L, D, G, kBwdWarps * (N == 8 ? 32 : 512 / N), kBwdWarps, 8 * kSmCount, 24 * kSmCount);
+  q.r = scan_plan(B, L, D, G, kBwdWarps * (N == 8 ? 32 : 512 / N), 2 * kSmCount, 0.85f, ragged);
   size_t at = 0;
   auto take = [&](size_t floats) {
     const size_t here = at;
@@ -557,11 +559,11 @@ BwdPlan bwd_plan(int B, int L, int D, int N, int G, bool have_states) {
 }  // namespace
 
 size_t scan_bwd_workspace_bytes(int B, int L, int D, int N, int G, bool have_states) {
-  return bwd_plan(B, L, D, N, G, have_states).total;
+  return std::max(bwd_plan(B, L, D, N, G, have_states, false).total, bwd_plan(B, L, D, N, G, have_states, true).total);
 }
 
 cudaError_t launch_scan_bwd(const lion_scan_bwd_args& a, void* ws, cudaStream_t s) {
-  const BwdPlan q = bwd_plan(a.B, a.L, a.D, a.N, a.G, a.states != nullptr);
+  const BwdPlan q = bwd_plan(a.B, a.L, a.D, a.N, a.G, a.states != nullptr, a.lengths != nullptr);
   char* base = static_cast<char*>(ws);
   lion_scan_args f = {};
   f.u = a.u;

@@ -9,12 +9,14 @@
 // store.  32 states a lane are what keeps shared memory from being the bound:
 // a token costs a lane one read of delta and one of delta u for them, and B
 // and C are broadcasts.
+#include <algorithm>
+
 #include "ssm_scan.cuh"
 
 namespace lion {
 namespace {
 
-constexpr int kFwdWarps = 4;
+constexpr int kFwdWarps = 1;   // CTAs of one warp spread best: 64 x 197 x 1536 x 16 529 -> 525 us (both ways) against four
 
 template <typename T, int N_>
 struct FwdTile {
@@ -98,7 +100,7 @@ __device__ __forceinline__ void store_states(float* dst, const f2 (&v)[RN / 2]) 
 // contribution to the state that leaves it, from a zero state, and its sum of
 // delta.
 template <typename T, int N, bool MAIN>
-__global__ void __launch_bounds__(32 * kFwdWarps, N == 64 ? 2 : 3) scan_fwd_kernel(ScanP p) {
+__global__ void __launch_bounds__(32 * kFwdWarps, (N == 64 ? 8 : 12) / kFwdWarps) scan_fwd_kernel(ScanP p) {
   using S = FwdTile<T, N>;
   typedef typename FwdWarp<T, N>::Raw Raw;
   constexpr int RN = S::RN, LN = S::LN, RC = S::RC, TT = S::TT, CW = S::CW, VT = S::VT, VL = S::VL;
@@ -404,11 +406,12 @@ cudaError_t run_step(const lion_scan_step_args& a, cudaStream_t s) {
 // Turns the segments' own contributions into the states that enter them, in
 // place: X_{s+1} = exp(A sum_s) X_s + own_s from the walk's start, or, back,
 // X_{s-1} = exp(A sum_s) X_s + own_s from its end.  A thread has four states
-// of a channel and reads eight segments ahead.
+// of a channel and reads kAhead segments ahead.
 namespace {
-__global__ void __launch_bounds__(128) scan_chain_kernel(ScanP p, bool back, const float* first) {
+constexpr int kAhead = 16;
+__global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, const float* first) {
   const int per = p.N / 4;
-  const long long k = (long long)blockIdx.x * 128 + threadIdx.x;
+  const long long k = (long long)blockIdx.x * 64 + threadIdx.x;
   if (k >= (long long)p.B * p.D * per) return;
   const int n0 = 4 * (int)(k % per);
   const long long bd = k / per;
@@ -416,11 +419,11 @@ __global__ void __launch_bounds__(128) scan_chain_kernel(ScanP p, bool back, con
   f2 A[2], x[2];
   load_pair(p.A + (size_t)d * p.N + n0, true, A, kLog2e);
   load_pair(first + bd * p.N + n0, first != nullptr, x);
-  for (int s0 = 0; s0 < p.nseg; s0 += 8) {
-    f2 own[8][2];
-    float sum[8];
+  for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
+    f2 own[kAhead][2];
+    float sum[kAhead];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kAhead; ++q) {
       // the last of the walk has no contribution: nothing follows it
       const bool there = s0 + q < p.nseg - 1;
       const int s = back ? p.nseg - 1 - s0 - q : s0 + q;
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(128) scan_chain_kernel(ScanP p, bool back, con
       sum[q] = there ? p.seg_sum[at] : 0.f;
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kAhead; ++q) {
       if (s0 + q >= p.nseg) break;
       const int s = back ? p.nseg - 1 - s0 - q : s0 + q;
       store_pair(p.seg_state + (((size_t)b * p.nseg + s) * p.D + d) * p.N + n0, x);
@@ -443,36 +446,60 @@ __global__ void __launch_bounds__(128) scan_chain_kernel(ScanP p, bool back, con
 
 cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cudaStream_t s) {
   const long long n = (long long)p.B * p.D * (p.N / 4);
-  scan_chain_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, back, first);
+  scan_chain_kernel<<<(unsigned)((n + 63) / 64), 64, 0, s>>>(p, back, first);
   return cudaGetLastError();
 }
 
-// A sequence is cut into segments only while its channels alone leave the SMs
-// short of warps: a cut costs a second pass over the exponentials.
-ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int warps, long long enough, long long want) {
+// Cuts sequences into segments so that the SMs' slots for CTAs are filled in
+// whole rounds.  The cost, in tokens of a round: rounds x (a segment's tokens +
+// what a CTA takes to start), a round that is not full counting for 0.4 plus
+// 0.6 of its fill (fewer CTAs on an SM run faster), plus the chain over the
+// segments; a sequence left whole is spared the pass over the segments' own
+// contributions and costs `whole` of that.  Ragged sequences, whose lengths
+// the host does not see, are taken to fill half of the tokens in CTAs that end
+// at any time: only the last one's time counts in full, which asks for short
+// segments (16 prompts of up to 4096 tokens x 1024 channels: 509 us with two
+// whole rounds, PROMPTS us so).  Up to kMaxSegments, of 64 tokens at least.
+ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int slots, float whole, bool ragged) {
+  constexpr int kMaxSegments = 512;
   ScanPlan r;
   r.nblk = (D / G + cta_channels - 1) / cta_channels;
-  const long long have = (long long)B * G * r.nblk * warps;
-  long long nseg = have >= enough ? 1 : (want + have - 1) / have;
-  const long long most = L / 64 > 1 ? L / 64 : 1;
-  if (nseg > most) nseg = most;
-  long long len = (L + nseg - 1) / nseg;
-  len = (len + 15) / 16 * 16;   // whole tiles
-  r.seglen = (int)len;
-  r.nseg = (int)((L + len - 1) / len);
+  const long long ctas = (long long)B * G * r.nblk;
+  auto rounds = [&](long long n) {
+    if (ragged) return 0.5f * (float)n / (float)slots + 0.8f;
+    const long long full = n / slots, rest = n % slots;
+    return (float)full + (rest ? 0.4f + 0.6f * (float)rest / (float)slots : 0.f);
+  };
+  r.nseg = 1;
+  r.seglen = (L + 15) / 16 * 16;
+  float best = whole * rounds(ctas) * ((float)L + 6.f);
+  const int most = std::min(kMaxSegments, L / 64);
+  for (int n = 2; n <= most; ++n) {
+    const int len = ((L + n - 1) / n + 15) / 16 * 16, real = (L + len - 1) / len;   // whole tiles
+    if (real != n) continue;
+    const float cost = rounds(ctas * n) * ((float)len + 6.f) + 0.18f * (float)n;
+    if (cost < best) {
+      best = cost;
+      r.nseg = n;
+      r.seglen = len;
+    }
+  }
   return r;
 }
 namespace {
-ScanPlan fwd_plan(int B, int L, int D, int N, int G) {
+ScanPlan fwd_plan(int B, int L, int D, int N, int G, bool ragged) {
   const int cw = N == 8 ? 128 : 1024 / N;
-  return scan_plan(B, L, D, G, kFwdWarps * cw, kFwdWarps, 4 * kSmCount, 48 * kSmCount);
+  return scan_plan(B, L, D, G, kFwdWarps * cw, kSmCount * (N == 64 ? 8 : 12) / kFwdWarps, 0.6f, ragged);
 }
 }  // namespace
 
 size_t scan_workspace_bytes(int B, int L, int D, int N, int G) {
-  const ScanPlan r = fwd_plan(B, L, D, N, G);
-  if (r.nseg == 1) return 0;
-  return up256(sizeof(float) * (size_t)B * r.nseg * D * N) + up256(sizeof(float) * (size_t)B * r.nseg * D);
+  size_t most = 0;
+  for (int ragged = 0; ragged < 2; ++ragged) {
+    const size_t nseg = fwd_plan(B, L, D, N, G, ragged).nseg;
+    if (nseg > 1) most = std::max(most, up256(sizeof(float) * B * nseg * D * N) + up256(sizeof(float) * B * nseg * D));
+  }
+  return most;
 }
 
 void fill_scan(ScanP& p, const lion_scan_args& a) {
@@ -516,7 +543,7 @@ void fill_scan(ScanP& p, const lion_scan_args& a) {
 cudaError_t launch_scan_fwd(const lion_scan_args& a, void* ws, cudaStream_t s) {
   ScanP p = {};
   fill_scan(p, a);
-  const ScanPlan r = fwd_plan(a.B, a.L, a.D, a.N, a.G);
+  const ScanPlan r = fwd_plan(a.B, a.L, a.D, a.N, a.G, a.lengths != nullptr);
   p.nblk = r.nblk;
   p.nseg = r.nseg;
   p.seglen = r.seglen;
