@@ -9,6 +9,9 @@
 // registers; the next few tokens are read while it works on the last ones, so
 // an input is read once plus K-1 tokens before each run (and behind it, for
 // the gradients), which the neighbouring runs leave in the caches.
+#include <algorithm>
+#include <cmath>
+
 #include "lion_internal.h"
 #include "ssm_common.cuh"
 
@@ -407,31 +410,50 @@ cudaError_t run_step(const void* x, void* state, const float* weight, const floa
   return cudaGetLastError();
 }
 
-// Tokens of a run: as many as leave each SM some `threads` threads, in steps
-// of the tokens read ahead (less K - 1 in the gradients, whose runs end K - 1
-// tokens later); 64 at most, where the K - 1 tokens read twice are 5%.
-int run_length(int B, int L, int D, int behind, int threads) {
-  const long long vecs = (long long)B * ((D + 3) / 4);
-  const long long want = (vecs * L + (long long)kSmCount * threads - 1) / ((long long)kSmCount * threads);
-  int run = (int)(want < 8 ? 8 : want > 64 ? 64 : (want + 7) / 8 * 8);
-  return run - behind > 0 ? run - behind : 8;
+// Tokens of a run (a multiple of eight, less what the gradients read behind
+// it): the length that fills the SMs' slots in the fewest rounds of run +
+// kStart tokens, kStart being what a thread takes to begin; a round that is
+// not full counts for 0.4 plus 0.6 of its fill.  runs_of(run): how many slots
+// the runs of that length take.
+constexpr int kStart = 8;
+template <typename F>
+int best_run(int L, int behind, F slots_of) {
+  int best = 8 - behind;
+  float least = 3e38f;
+  for (int m = 8; m <= 72; m += 8) {
+    const int run = m - behind;
+    const float x = slots_of((L + run - 1) / run), full = floorf(x);
+    const float cost = (full + (x > full ? 0.4f + 0.6f * (x - full) : 0.f)) * (float)(run + kStart);
+    if (cost < least) {
+      least = cost;
+      best = run;
+    }
+    if (run >= L) break;
+  }
+  return best;
 }
-int bwd_run(int B, int L, int D, int K) { return run_length(B, L, D, K - 1, 512); }
+int fwd_run(int B, int L, int D) {
+  return best_run(L, 0, [&](int runs) { return (float)B * runs * ((D + 3) / 4) / (float)(kSmCount * 5 * 128); });
+}
 
-// CTAs along the runs in the gradients: what the SMs hold at once.
-int conv_parts(int B, int L, int D, int K) {
-  const int run = bwd_run(B, L, D, K);
-  const long long lines = (long long)B * ((L + run - 1) / run);
-  const int across = (D + 127) / 128;
-  const long long want = (lines + kBwdRows - 1) / kBwdRows,
-                  most = (2 * kSmCount + across - 1) / across;
-  return (int)(want < most ? want : most);
+// CTAs along the runs in the gradients: at most what the SMs hold at once.
+int conv_parts(int B, int L, int D, int run) {
+  const int across = (D + 127) / 128, most = std::max(1, 2 * kSmCount / across);
+  const long long want = ((long long)B * ((L + run - 1) / run) + kBwdRows - 1) / kBwdRows;
+  return (int)std::min<long long>(want, most);
+}
+int bwd_run(int B, int L, int D, int K) {
+  const int across = (D + 127) / 128, most = std::max(1, 2 * kSmCount / across);
+  return best_run(L, K - 1, [&](int runs) {
+    const float turns = ceilf((float)B * runs / (float)(most * kBwdRows));   // a CTA's lines follow one another
+    return turns <= 1.f ? (float)B * runs / (float)(most * kBwdRows) : turns;
+  });
 }
 
 }  // namespace
 
 size_t conv_bwd_workspace_bytes(int B, int L, int D, int K) {
-  return sizeof(float) * (size_t)conv_parts(B, L, D, K) * D * (K + 1);
+  return sizeof(float) * (size_t)conv_parts(B, L, D, bwd_run(B, L, D, K)) * D * (K + 1);
 }
 
 cudaError_t launch_conv_fwd(const lion_conv_args& a, cudaStream_t s) {
@@ -451,7 +473,7 @@ cudaError_t launch_conv_fwd(const lion_conv_args& a, cudaStream_t s) {
   p.reverse = a.reverse;
   p.w_wide = rows_wide(a.weight, 0, 4);
   p.nvec = (a.D + 3) / 4;
-  p.run = run_length(a.B, a.L, a.D, 0, 1024);
+  p.run = fwd_run(a.B, a.L, a.D);
   p.runs = (a.L + p.run - 1) / p.run;
   const int es = a.dtype == DT_BF16 ? 2 : 4;
   p.x_wide = rows_wide(a.x, p.x_ld, es);
@@ -485,7 +507,7 @@ cudaError_t launch_conv_bwd(const lion_conv_bwd_args& a, void* ws, cudaStream_t 
   p.x_wide = rows_wide(a.x, p.x_ld, es);
   p.o_wide = rows_wide(a.dx, a.D, es) && rows_wide(a.dy, a.D, es);
   p.s_wide = rows_wide(a.state, a.D, es) && rows_wide(a.dstate, a.D, es);
-  const int parts = conv_parts(a.B, a.L, a.D, a.K);
+  const int parts = conv_parts(a.B, a.L, a.D, p.run);
   cudaError_t e = LION_CONV_DISPATCH(run_bwd, a.dtype, a.K, p, parts, s);
   if (e != cudaSuccess) return e;
   return launch_sum_parts(p.part, parts, (long long)a.D * (a.K + 1), (long long)a.D * a.K, a.dweight, a.D, a.dbias, 0, nullptr, s);
