@@ -15,12 +15,14 @@ workspaces belong to it; inputs made on another stream have to be ready on it.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import lion
-from .lion import _check, _ptr
+from .lion import _check
 
 ACT_NONE, ACT_SILU = 0, 1
 ACTIVATIONS = {"none": ACT_NONE, None: ACT_NONE, "silu": ACT_SILU}
@@ -79,9 +81,21 @@ class _ScanStepArgs(ctypes.Structure):
                 ("dt_softplus", _i), ("dtype", _i), ("stream", _vp)]
 
 
+def _layout(args):
+    """A structure's fields in struct's notation: packing bytes takes a third
+    of the time of a ctypes structure, a microsecond of a one-token call."""
+    codes = {_vp: "P", _i: "i", _ll: "q", _sz: "N", ctypes.c_float: "f"}
+    packed = struct.Struct("@" + "".join(codes[t] for _, t in args._fields_))
+    assert packed.size <= ctypes.sizeof(args)   # but for the padding behind the last field
+    return packed.pack
+
+
 EXPORTS = ("lion_layernorm_fwd", "lion_layernorm_bwd", "lion_layernorm_bwd_workspace_bytes", "lion_conv_fwd",
            "lion_conv_bwd", "lion_conv_bwd_workspace_bytes", "lion_conv_step", "lion_scan_fwd",
            "lion_scan_workspace_bytes", "lion_scan_bwd", "lion_scan_bwd_workspace_bytes", "lion_scan_step")
+
+_Norm_pack, _NormBwd_pack, _Conv_pack, _ConvBwd_pack, _Scan_pack, _ScanBwd_pack, _ScanStep_pack = (
+    _layout(c) for c in (_NormArgs, _NormBwdArgs, _ConvArgs, _ConvBwdArgs, _ScanArgs, _ScanBwdArgs, _ScanStepArgs))
 
 _lib = None
 
@@ -91,11 +105,9 @@ def load():
     global _lib
     if _lib is None:
         lib = lion.load()
-        for name, args in (("layernorm_fwd", _NormArgs), ("layernorm_bwd", _NormBwdArgs), ("conv_fwd", _ConvArgs),
-                           ("conv_bwd", _ConvBwdArgs), ("scan_fwd", _ScanArgs), ("scan_bwd", _ScanBwdArgs),
-                           ("scan_step", _ScanStepArgs)):
+        for name in ("layernorm_fwd", "layernorm_bwd", "conv_fwd", "conv_bwd", "scan_fwd", "scan_bwd", "scan_step"):
             f = getattr(lib, "lion_" + name)
-            f.argtypes, f.restype = [ctypes.POINTER(args)], _i
+            f.argtypes, f.restype = [ctypes.c_char_p], _i
         lib.lion_conv_step.argtypes, lib.lion_conv_step.restype = [_vp] * 5 + [_i] * 5 + [_vp], _i
         for name, n in (("layernorm_bwd", 2), ("conv_bwd", 4), ("scan", 5), ("scan_bwd", 6)):
             f = getattr(lib, f"lion_{name}_workspace_bytes")
@@ -113,12 +125,12 @@ _CODES = {torch.bfloat16: lion.DTYPE_BF16, torch.float32: lion.DTYPE_FP32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _handle(stream):
+def _handle(stream, x):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream(x.device).cuda_stream
+    return _raw_stream(x.get_device())
 
 
 def _new(stream, shape, dtype, like):
@@ -144,34 +156,35 @@ def _act(activation):
     return ACTIVATIONS[activation]
 
 
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
 def _tight(name, t, dtype, shape):
-    """The address of a contiguous tensor of this type and shape."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+    """The address of a contiguous tensor of this type and shape (the library
+    refuses one that is not the GPU's)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("tensors must be on the GPU")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
 def _maybe(name, t, dtype, shape):
-    return None if t is None else _tight(name, t, dtype, shape)
+    return 0 if t is None else _tight(name, t, dtype, shape)
 
 
 def _token(name, t, dtype, shape):
     """(address, distance between tokens) of a [B, L, ...] activation whose
     last dimensions are adjacent."""
     width = shape[2] if len(shape) == 3 else shape[2] * shape[3]
-    if t.dtype is dtype and t.shape == shape and t.is_cuda:
+    if t.dtype is dtype and t.shape == shape:
         if t.is_contiguous():
             return t.data_ptr(), width
     elif t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} as the other activations, got {t.dtype}")
-    elif not t.is_cuda:
-        raise ValueError("tensors must be on the GPU")
     else:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     B, L = shape[:2]
@@ -191,14 +204,19 @@ def _token(name, t, dtype, shape):
     return t.data_ptr(), ld
 
 
-def _workspace(workspace, nbytes, like, stream):
+@functools.lru_cache(maxsize=256)
+def _query(name, *sizes):
+    return int(getattr(load(), f"lion_{name}_workspace_bytes")(*sizes))
+
+
+def _workspace(workspace, like, stream, name, *sizes):
     """(address, bytes, owner) of the caller's workspace, or of one from
     PyTorch's allocator (which reuses it once the stream has passed the call)."""
     if workspace is not None:
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    n = nbytes()
+    n = _query(name, *sizes)
     if n == 0:
-        return None, 0, None
+        return 0, 0, None
     ws = _new(stream, n, torch.uint8, like)
     return ws.data_ptr(), n, ws
 
@@ -216,7 +234,7 @@ def _rows(x):
 
 
 def layernorm_bwd_workspace_bytes(rows, cols) -> int:
-    return int(load().lion_layernorm_bwd_workspace_bytes(rows, cols))
+    return _query("layernorm_bwd", rows, cols)
 
 
 def layernorm_fwd(x, weight, bias=None, eps=1e-5, save_stats=False, out=None, stream=None):
@@ -225,13 +243,16 @@ def layernorm_fwd(x, weight, bias=None, eps=1e-5, save_stats=False, out=None, st
     lib, code = load(), _code(x)
     rows, cols, ld = _rows(x)
     w, b = _tight("weight", weight, torch.float32, (cols,)), _maybe("bias", bias, torch.float32, (cols,))
-    y = _new(stream, x.shape, x.dtype, x) if out is None else out
-    yp = _tight("out", y, x.dtype, x.shape)
+    if out is None:
+        y = _new(stream, x.shape, x.dtype, x)
+        yp = y.data_ptr()
+    else:
+        y, yp = out, _tight("out", out, x.dtype, x.shape)
     mean = rstd = None
     if save_stats:
         mean, rstd = (_new(stream, x.shape[:-1], torch.float32, x) for _ in range(2))
-    a = _NormArgs(x.data_ptr(), w, b, yp, _ptr(mean), _ptr(rstd), ld, rows, cols, eps, code, _handle(stream))
-    _check(lib.lion_layernorm_fwd(ctypes.byref(a)))
+    a = _Norm_pack(x.data_ptr(), w, b, yp, _ptr(mean), _ptr(rstd), ld, rows, cols, eps, code, _handle(stream, x))
+    _check(lib.lion_layernorm_fwd(a))
     return (y, mean, rstd) if save_stats else y
 
 
@@ -243,11 +264,12 @@ def layernorm_bwd(dy, x, weight, mean, rstd, bias=True, workspace=None, stream=N
     f32, per = torch.float32, x.shape[:-1]
     ptrs = (_tight("dy", dy, x.dtype, x.shape), x.data_ptr(), _tight("weight", weight, f32, (cols,)),
             _tight("mean", mean, f32, per), _tight("rstd", rstd, f32, per))
-    dx, dw = _new(stream, x.shape, x.dtype, x), _new(stream, (cols,), f32, x)
+    dx = _new(stream, x.shape, x.dtype, x)
+    dw = _new(stream, (cols,), f32, x)
     db = _new(stream, (cols,), f32, x) if bias else None
-    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_layernorm_bwd_workspace_bytes(rows, cols), x, stream)
-    a = _NormBwdArgs(*ptrs, dx.data_ptr(), dw.data_ptr(), _ptr(db), ld, rows, cols, code, ws, nb, _handle(stream))
-    _check(lib.lion_layernorm_bwd(ctypes.byref(a)))
+    ws, nb, _keep = _workspace(workspace, x, stream, "layernorm_bwd", rows, cols)
+    a = _NormBwd_pack(*ptrs, dx.data_ptr(), dw.data_ptr(), _ptr(db), ld, rows, cols, code, ws, nb, _handle(stream, x))
+    _check(lib.lion_layernorm_bwd(a))
     return dx, dw, db
 
 
@@ -295,7 +317,7 @@ def _conv_args(x, weight, bias, state, lengths):
 
 
 def conv_bwd_workspace_bytes(B, L, D, K) -> int:
-    return int(load().lion_conv_bwd_workspace_bytes(B, L, D, K))
+    return _query("conv_bwd", B, L, D, K)
 
 
 def conv_fwd(x, weight, bias=None, activation="silu", state=None, lengths=None, reverse=False, return_state=False,
@@ -309,9 +331,9 @@ def conv_fwd(x, weight, bias=None, activation="silu", state=None, lengths=None, 
     (B, L, D, K), ld, ptrs = _conv_args(x, weight, bias, state, lengths)
     y = _new(stream, x.shape, x.dtype, x) if out is None else out
     new = _new(stream, (B, K - 1, D), x.dtype, x) if return_state else None
-    a = _ConvArgs(*ptrs, _tight("out", y, x.dtype, x.shape), _ptr(new), ld, B, L, D, K, _act(activation),
-                  int(reverse), code, _handle(stream))
-    _check(lib.lion_conv_fwd(ctypes.byref(a)))
+    a = _Conv_pack(*ptrs, _tight("out", y, x.dtype, x.shape), _ptr(new), ld, B, L, D, K, _act(activation),
+                  int(reverse), code, _handle(stream, x))
+    _check(lib.lion_conv_fwd(a))
     return (y, new) if return_state else y
 
 
@@ -326,10 +348,10 @@ def conv_bwd(dy, x, weight, bias=None, activation="silu", state=None, lengths=No
     dx, dw = _new(stream, x.shape, x.dtype, x), _new(stream, (D, K), f32, x)
     db = None if bias is None else _new(stream, (D,), f32, x)
     ds = None if state is None else _new(stream, state.shape, x.dtype, x)
-    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_conv_bwd_workspace_bytes(B, L, D, K), x, stream)
-    a = _ConvBwdArgs(dyp, *ptrs, dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds), ld, B, L, D, K, _act(activation),
-                     int(reverse), code, ws, nb, _handle(stream))
-    _check(lib.lion_conv_bwd(ctypes.byref(a)))
+    ws, nb, _keep = _workspace(workspace, x, stream, "conv_bwd", B, L, D, K)
+    a = _ConvBwd_pack(dyp, *ptrs, dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds), ld, B, L, D, K, _act(activation),
+                     int(reverse), code, ws, nb, _handle(stream, x))
+    _check(lib.lion_conv_bwd(a))
     return ConvGrads(dx, dw, db, ds)
 
 
@@ -339,10 +361,14 @@ def conv_step(x, state, weight, bias=None, activation="silu", out=None, stream=N
     lib, code = load(), _code(x)
     B, D = x.shape
     w, K = _taps(weight, D)
-    y = _new(stream, (B, D), x.dtype, x) if out is None else out
+    if out is None:
+        y = _new(stream, (B, D), x.dtype, x)
+        yp = y.data_ptr()
+    else:
+        y, yp = out, _tight("out", out, x.dtype, (B, D))
     _check(lib.lion_conv_step(_tight("x", x, x.dtype, (B, D)), _tight("state", state, x.dtype, (B, K - 1, D)), w,
-                              _maybe("bias", bias, torch.float32, (D,)), _tight("out", y, x.dtype, (B, D)), B, D, K,
-                              _act(activation), code, _handle(stream)))
+                              _maybe("bias", bias, torch.float32, (D,)), yp, B, D, K,
+                              _act(activation), code, _handle(stream, x)))
     return y
 
 
@@ -401,7 +427,7 @@ def _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths):
     dp, dl = _token("dt", dt, T, shape)
     bp, bl = _token("Bm", Bm, T, (B, L, G, N))
     cp, cl = _token("Cm", Cm, T, (B, L, G, N))
-    zp, zl = (None, 0) if z is None else _token("z", z, T, shape)
+    zp, zl = (0, 0) if z is None else _token("z", z, T, shape)
     return ((B, L, D, N, G),
             (up, dp, _tight("A", A, f32, (D, N)), bp, cp, _maybe("Dskip", Dskip, f32, (D,)), zp,
              _maybe("dt_bias", dt_bias, f32, (D,)), _maybe("h0", h0, f32, (B, D, N)),
@@ -410,11 +436,11 @@ def _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths):
 
 
 def scan_workspace_bytes(B, L, D, N, G=1) -> int:
-    return int(load().lion_scan_workspace_bytes(B, L, D, N, G))
+    return _query("scan", B, L, D, N, G)
 
 
 def scan_bwd_workspace_bytes(B, L, D, N, G=1, have_states=True) -> int:
-    return int(load().lion_scan_bwd_workspace_bytes(B, L, D, N, G, int(have_states)))
+    return _query("scan_bwd", B, L, D, N, G, int(have_states))
 
 
 def scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus=True, h0=None, lengths=None,
@@ -433,10 +459,10 @@ def scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus=Tru
     y = _new(stream, u.shape, u.dtype, u) if out is None else out
     h = _new(stream, (B, D, N), torch.float32, u) if return_state else None
     states = _new(stream, (B, -(-L // STATE_EVERY), D, N), torch.float32, u) if save_states else None
-    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_scan_workspace_bytes(*sizes), u, stream)
-    a = _ScanArgs(*ptrs, _tight("out", y, u.dtype, u.shape), _ptr(h), _ptr(states), *tokens, *sizes,
-                  int(dt_softplus), int(reverse), code, ws, nb, _handle(stream))
-    _check(lib.lion_scan_fwd(ctypes.byref(a)))
+    ws, nb, _keep = _workspace(workspace, u, stream, "scan", *sizes)
+    a = _Scan_pack(*ptrs, _tight("out", y, u.dtype, u.shape), _ptr(h), _ptr(states), *tokens, *sizes,
+                  int(dt_softplus), int(reverse), code, ws, nb, _handle(stream, u))
+    _check(lib.lion_scan_fwd(a))
     return ScanOut(y, h, states)
 
 
@@ -458,12 +484,11 @@ def scan_bwd(dout, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softpl
     dD = None if Dskip is None else _new(stream, (D,), f32, u)
     dbias = None if dt_bias is None else _new(stream, (D,), f32, u)
     dh0 = None if h0 is None else _new(stream, (B, D, N), f32, u)
-    ws, nb, _keep = _workspace(workspace, lambda: lib.lion_scan_bwd_workspace_bytes(*sizes, int(states is not None)),
-                               u, stream)
-    a = _ScanBwdArgs(dop, *ptrs, sp, du.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(),
+    ws, nb, _keep = _workspace(workspace, u, stream, "scan_bwd", *sizes, int(states is not None))
+    a = _ScanBwd_pack(dop, *ptrs, sp, du.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(),
                      _ptr(dD), _ptr(dz), _ptr(dbias), _ptr(dh0), *tokens, *sizes, int(dt_softplus), int(reverse),
-                     code, ws, nb, _handle(stream))
-    _check(lib.lion_scan_bwd(ctypes.byref(a)))
+                     code, ws, nb, _handle(stream, u))
+    _check(lib.lion_scan_bwd(a))
     return ScanGrads(du, ddt, dA, dB, dC, dD, dz, dbias, dh0)
 
 
@@ -476,13 +501,16 @@ def scan_step(h, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus
     N, T, f32 = _states(A, D), u.dtype, torch.float32
     G = Bm.shape[1] if Bm.dim() == 3 else 1
     bc = (B, G, N) if Bm.dim() == 3 else (B, N)
-    y = _new(stream, shape, T, u) if out is None else out
-    a = _ScanStepArgs(_tight("h", h, f32, (B, D, N)), _tight("u", u, T, shape), _tight("dt", dt, T, shape),
+    if out is None:
+        y = _new(stream, shape, T, u)
+        yp = y.data_ptr()
+    else:
+        y, yp = out, _tight("out", out, T, shape)
+    a = _ScanStep_pack(_tight("h", h, f32, (B, D, N)), _tight("u", u, T, shape), _tight("dt", dt, T, shape),
                       _tight("A", A, f32, (D, N)), _tight("Bm", Bm, T, bc), _tight("Cm", Cm, T, bc),
                       _maybe("Dskip", Dskip, f32, (D,)), _maybe("z", z, T, shape),
-                      _maybe("dt_bias", dt_bias, f32, (D,)), _tight("out", y, T, shape), B, D, N, G,
-                      int(dt_softplus), code, _handle(stream))
-    _check(lib.lion_scan_step(ctypes.byref(a)))
+                      _maybe("dt_bias", dt_bias, f32, (D,)), yp, B, D, N, G, int(dt_softplus), code, _handle(stream, u))
+    _check(lib.lion_scan_step(a))
     return y
 
 

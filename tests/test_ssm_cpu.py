@@ -51,7 +51,7 @@ NEEDED = {
 
 def _call(ssm, name, **kw):
     struct, base = BASE[name]
-    return getattr(ssm.load(), "lion_" + name)(ctypes.byref(getattr(ssm, struct)(**{**base, **kw})))
+    return getattr(ssm.load(), "lion_" + name)(bytes(getattr(ssm, struct)(**{**base, **kw})))
 
 
 @pytest.mark.parametrize("name", sorted(BASE))
