@@ -187,22 +187,6 @@ __device__ __forceinline__ void fetch(T* dst, const T* src, int n, int align) {
   }
 }
 
-// Stores to shared memory that the compiler takes for plain side effects: it
-// may move the reads of later tokens above them, which it would not above a
-// store that could overlap them.  What is read of the place beforehand has to
-// go into the value stored, and what is read of it afterwards to come behind a
-// barrier.
-__device__ __forceinline__ void put_shared(float* p, float x) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"((unsigned)__cvta_generic_to_shared(p)), "f"(x));
-}
-__device__ __forceinline__ void put_shared(float* p, float x, float y) {
-  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"((unsigned)__cvta_generic_to_shared(p)), "f"(x), "f"(y));
-}
-__device__ __forceinline__ void put_shared(float* p, float x, float y, float z, float w) {
-  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"((unsigned)__cvta_generic_to_shared(p)), "f"(x), "f"(y),
-               "f"(z), "f"(w));
-}
-
 // A warp's copies of [TT][W] rows in pieces of 16 bytes: piece q = lane + 32 k
 // is PV elements of token q / PPR.  The source moves on a tile at a time.
 template <typename T, int TT, int W>
@@ -237,6 +221,22 @@ struct Feed {
     src += tile;
   }
 };
+
+template <int COUNT>
+__device__ __forceinline__ const float* as_fp32(const float* raw, float*, int) { return raw; }
+template <int COUNT>
+__device__ __forceinline__ const float* as_fp32(const __nv_bfloat16* raw, float* dst, int lane) {
+#pragma unroll
+  for (int k = 0; k < (COUNT / 4 + 31) / 32; ++k) {
+    const int q = lane + 32 * k;
+    if (COUNT / 4 % 32 == 0 || q < COUNT / 4) {
+      float v[4];
+      get(raw + 4 * q, v);
+      *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  return dst;
+}
 
 // delta of eight channels from the step sizes read.
 __device__ __forceinline__ void deltas(const ScanP& p, int d, int n, float (&dt)[8], float (&raw)[8]) {

@@ -331,17 +331,29 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
             }
           }
         }
+        // A token's reads stand before the stores of the token walked before it: a read does not pass a store ahead
+        // of it that could go to its place, and the tokens would wait for one another's sums.
+        f2 b2[4], c2[4];
+        float vt_[RC], vu_[RC], vy_[RC];
+        auto read_token = [&](int t) {
+          row4(sh.Bm, t, b2);
+          row4(sh.Cm, t, c2);
+#pragma unroll
+          for (int k = 0; k < RC; ++k) {
+            vt_[k] = sm.dt[t * CW + c[k]];
+            vu_[k] = sm.du[t * CW + c[k]];
+            vy_[k] = sm.dy[t * CW + c[k]];
+          }
+        };
+        read_token(blk * kBlock + kBlock - 1);
 #pragma unroll
         for (int s = kBlock - 1; s >= 0; --s) {
           const int t = blk * kBlock + s;
-          f2 b2[4], c2[4], dB[4], dC[4];
-          row4(sh.Bm, t, b2);
-          row4(sh.Cm, t, c2);
+          f2 dB[4], dC[4];
           float gb[RC], qa[RC], y[RC];
 #pragma unroll
           for (int k = 0; k < RC; ++k) {
-            const float dt1 = sm.dt[t * CW + c[k]], du1 = sm.du[t * CW + c[k]], dy1 = sm.dy[t * CW + c[k]];
-            const f2 dt2 = pack2(dt1, dt1), du2 = pack2(du1, du1), dy2 = pack2(dy1, dy1);
+            const f2 dt2 = pack2(vt_[k], vt_[k]), du2 = pack2(vu_[k], vu_[k]), dy2 = pack2(vy_[k], vy_[k]);
             f2 sgb, sqa, sy;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -357,9 +369,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
             }
             gb[k] = sum2(sgb);
             qa[k] = sum2(sqa);
-            asm volatile("" : "+f"(qa[k]) : "f"(du1));   // qa takes delta u's place: its reads come first
             if (GATE) y[k] = sum2(sy);
           }
+          if (s > 0) read_token(t - 1);
           // over the states
           if (LN > 1) {
             gb[0] += __shfl_xor_sync(0xffffffffu, gb[RC - 1], 1);
@@ -372,9 +384,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
               if (GATE) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
             }
           }
-          put_shared(sm.dy + t * CW + c[0], gb[0]);   // lanes of one parity hold the same sums
-          put_shared(sm.du + t * CW + c[0], qa[0]);
-          if (GATE) put_shared(sm.y + t * CW + c[0], y[0]);
+          sm.dy[t * CW + c[0]] = gb[0];   // lanes of one parity hold the same sums
+          sm.du[t * CW + c[0]] = qa[0];
+          if (GATE) sm.y[t * CW + c[0]] = y[0];
           // over the channels, LN lanes apart: first between lanes that hold the blocks of states in opposite
           // order, the rest in shared memory
           float r[8];
@@ -386,8 +398,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
             r[4 + 2 * q + 1] = dC[q].y + __shfl_xor_sync(0xffffffffu, dC[q + 2].y, LN);
           }
           const int at_r = (lc >> 1) * N + n0;
-          put_shared(sm.part[0][s] + at_r, r[0], r[1], r[2], r[3]);
-          put_shared(sm.part[1][s] + at_r, r[4], r[5], r[6], r[7]);
+          *reinterpret_cast<float4*>(sm.part[0][s] + at_r) = make_float4(r[0], r[1], r[2], r[3]);
+          *reinterpret_cast<float4*>(sm.part[1][s] + at_r) = make_float4(r[4], r[5], r[6], r[7]);
         }
         __syncwarp();
 #pragma unroll
