@@ -318,8 +318,7 @@ template <typename T, int N, bool MAIN>
 cudaError_t run_kernel(const ScanP& p, cudaStream_t s) {
   auto kern = scan_fwd_kernel<T, N, MAIN>;
   const size_t smem = sizeof(FwdWarp<T, N>) * kFwdWarps;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  static_assert(sizeof(FwdWarp<T, N>) * kFwdWarps <= 48 * 1024, "more shared memory has to be asked for");
   kern<<<(unsigned)p.nblk * p.G * p.nseg * p.B, 32 * kFwdWarps, smem, s>>>(p);
   return cudaGetLastError();
 }

@@ -382,6 +382,70 @@ def test_scan_long():
     assert bool(((f.h - h).abs() <= tol * mh).all())
 
 
+def test_lengths_out_of_range_are_clamped():
+    B, L, D, N = 3, 40, 24, 16
+    a, dout = _scan_inputs(B, L, D, N, 1, "bf16", True, True, True, True, True, seed=21)
+    dev = {k: v.cuda() for k, v in a.items()}
+    w, b = torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda")
+    got = []
+    for n in ([-5, 1000, 7], [0, L, 7]):
+        lt = torch.tensor(n, dtype=torch.int32, device="cuda")
+        f = ssm.scan_fwd(**dev, lengths=lt, return_state=True, save_states=True)
+        g = ssm.scan_bwd(dout.cuda(), **dev, lengths=lt, states=f.states)
+        y, st = ssm.conv_fwd(dev["u"], w, b, lengths=lt, return_state=True)
+        c = ssm.conv_bwd(dout.cuda(), dev["u"], w, b, lengths=lt)
+        got.append([*f, *g, y, st, c.dx, c.dweight, c.dbias])
+    assert all(torch.equal(p, s) for p, s in zip(*got))
+
+
+def test_scan_offsets_past_32_bits():
+    """More than 2^31 values: the last sequence against the same sequence alone (cut differently)."""
+    B, L, D, N = 3, 360000, 2048, 8
+    big = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_()  # noqa: E731
+    u, dt, Bm, Cm = big(B, L, D), big(B, L, D).mul_(0.1), big(B, L, N), big(B, L, N)
+    A = -(0.5 + torch.rand(D, N, device="cuda"))
+    f = ssm.scan_fwd(u, dt, A, Bm, Cm, return_state=True)
+    last = ssm.scan_fwd(u[-1:], dt[-1:], A, Bm[-1:], Cm[-1:], return_state=True)
+    # states of order one that forget within some ten tokens: a cut moves the fp32 sums by a few roundings
+    assert float((f.h[-1:] - last.h).abs().max()) <= 1e-5 * float(last.h.abs().max())
+    for lo in range(0, L, 40000):   # half a bfloat16 unit apart at most where the sums round differently
+        p, q = f.out[-1, lo:lo + 40000].float(), last.out[0, lo:lo + 40000].float()
+        assert bool(((p - q).abs() <= 2.0 ** -7 * q.abs() + 1e-4).all())
+
+
+def test_layernorm_offsets_past_32_bits():
+    x = torch.empty(280000, 8192, dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.randn(8192, device="cuda")
+    y, mean, rstd = ssm.layernorm_fwd(x, w, save_stats=True)
+    assert torch.equal(y[-3:], ssm.layernorm_fwd(x[-3:], w))
+    dx, _, _ = ssm.layernorm_bwd(x, x, w, mean, rstd, bias=False)
+    last, _, _ = ssm.layernorm_bwd(x[-3:], x[-3:], w, mean[-3:], rstd[-3:], bias=False)
+    assert torch.equal(dx[-3:], last)
+
+
+def test_scan_captured_in_a_graph():
+    """A prompt's scan with segments, its gradients, conv and norm replay to the same bits."""
+    B, L, D, N = 1, 700, 32, 16
+    a, dout = _scan_inputs(B, L, D, N, 1, "bf16", True, True, True, True, True, seed=31)
+    dev, dout = {k: v.cuda() for k, v in a.items()}, dout.cuda()
+    w, nw = torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda")
+
+    def run():
+        f = ssm.scan_fwd(**dev, save_states=True)
+        c = ssm.conv_bwd(dout, dev["u"], w)
+        return [f.out, f.states, *ssm.scan_bwd(dout, **dev, states=f.states), c.dx, c.dweight,
+                ssm.layernorm_fwd(dev["u"], nw)]
+
+    want = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, s) for p, s in zip(got, want))
+
+
 def test_autograd_functions():
     """The three ops in one graph: gradients equal the entry points' own."""
     B, L, D, N = 2, 40, 32, 16
@@ -425,6 +489,9 @@ def test_refusals():
     ws = torch.empty(64, dtype=torch.uint8, device="cuda")
     with pytest.raises(lion.LionError) as e:   # a workspace that is too small
         ssm.scan_bwd(x, x, x, A, Bm, Bm, workspace=ws)
+    assert e.value.status == lion.ERR_INVALID_ARG
+    with pytest.raises(lion.LionError) as e:   # host memory
+        ssm.conv_fwd(x, w.cpu())
     assert e.value.status == lion.ERR_INVALID_ARG
     for bad in (lambda: ssm.conv_fwd(x.double(), w), lambda: ssm.conv_fwd(x, w.bfloat16()),
                 lambda: ssm.conv_fwd(x, w, lengths=torch.ones(2, device="cuda")),
