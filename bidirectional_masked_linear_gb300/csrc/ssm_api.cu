@@ -203,7 +203,8 @@ lion_status lion_scan_bwd(const lion_scan_bwd_args* a) {
 
 lion_status lion_scan_step(const lion_scan_step_args* a) {
   if (!a) return LION_ERR_INVALID_ARG;
-  const lion_status st = scan_sizes(a->B, 1, a->D, a->N, a->G, a->dt_softplus, 0, a->dtype);
+  lion_status st = scan_sizes(a->B, 1, a->D, a->N, a->G, a->dt_softplus, 0, a->dtype);
+  if (st == LION_OK && a->B > 2 * 65535) st = LION_ERR_UNSUPPORTED;   // two sequences a CTA on a grid's second axis
   if (st == LION_ERR_INVALID_ARG) return st;
   const size_t es = esize(a->dtype);
   if (!need(a->h, 16) || !need(a->u, es) || !need(a->dt, es) || !need(a->A, 16) || !need(a->Bm, es) ||

@@ -269,29 +269,31 @@ int norm_ctas(int rows, int cols) {
   return (int)(want < most ? want : most);
 }
 
-// part[p * stride + i] summed over p: 32 threads an element, each every 32nd p.
-__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int P, long long stride, long long n1,
-                                                         float* out1, long long n2, float* out2, long long n3,
-                                                         float* out3) {
-  __shared__ float sh[32][33];
+// part[p * stride + i] summed over p: R threads an element, each every R-th p.
+template <int R>
+__global__ void __launch_bounds__(32 * R) sum_parts_kernel(const float* part, int P, long long stride, long long n1,
+                                                           float* out1, long long n2, float* out2, long long n3,
+                                                           float* out3) {
+  __shared__ float sh[R][33];
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const long long n = n1 + n2 + n3, i0 = (long long)blockIdx.x * 32, i = i0 + lane;
+  const long long n = n1 + n2 + n3, i = (long long)blockIdx.x * 32 + lane;
   float s = 0.f;
   if (i < n) {
 #pragma unroll 4
-    for (int q = r; q < P; q += 32) s += part[q * stride + i];
+    for (int q = r; q < P; q += R) s += part[q * stride + i];
   }
   sh[r][lane] = s;
   __syncthreads();
-  const long long o = i0 + r;   // warp r: element r of the CTA's 32
-  s = warp_sum(sh[lane][r]);
-  if (lane == 0 && o < n) {
-    if (o < n1) {
-      if (out1) out1[o] = s;
-    } else if (o < n1 + n2) {
-      if (out2) out2[o - n1] = s;
+  if (r == 0 && i < n) {
+    s = sh[0][lane];
+#pragma unroll
+    for (int k = 1; k < R; ++k) s += sh[k][lane];
+    if (i < n1) {
+      if (out1) out1[i] = s;
+    } else if (i < n1 + n2) {
+      if (out2) out2[i - n1] = s;
     } else if (out3) {
-      out3[o - n1 - n2] = s;
+      out3[i - n1 - n2] = s;
     }
   }
 }
@@ -301,7 +303,11 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int 
 cudaError_t launch_sum_parts(const float* part, int P, long long stride, long long n1, float* out1, long long n2, float* out2,
                              long long n3, float* out3, cudaStream_t s) {
   const long long n = n1 + n2 + n3;
-  sum_parts_kernel<<<(unsigned)((n + 31) / 32), 1024, 0, s>>>(part, P, stride, n1, out1, n2, out2, n3, out3);
+  // few parts and many elements: smaller CTAs, of which more are under way (64 parts of 27648: 4.6 against 8.7 us)
+  if (P <= 128)
+    sum_parts_kernel<8><<<(unsigned)((n + 31) / 32), 256, 0, s>>>(part, P, stride, n1, out1, n2, out2, n3, out3);
+  else
+    sum_parts_kernel<32><<<(unsigned)((n + 31) / 32), 1024, 0, s>>>(part, P, stride, n1, out1, n2, out2, n3, out3);
   return cudaGetLastError();
 }
 

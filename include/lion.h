@@ -633,7 +633,8 @@ size_t lion_scan_bwd_workspace_bytes(int B, int L, int D, int N, int G, int have
 
 /*
  * lion_scan_step -- one token: u, dt, z, out [B][D], B, C [B][G][N], all
- * tight, the state h [B][D][N] updated in place.
+ * tight, the state h [B][D][N] updated in place; B <= 131070 (else
+ * LION_ERR_UNSUPPORTED).
  */
 typedef struct {
   float* h;
