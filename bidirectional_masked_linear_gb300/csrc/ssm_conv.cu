@@ -8,7 +8,10 @@
 // by HBM.  A thread walks a run of tokens for four channels with the window in
 // registers; the next few tokens are read while it works on the last ones, so
 // an input is read once plus K-1 tokens before each run (and behind it, for
-// the gradients), which the neighbouring runs leave in the caches.
+// the gradients), which the neighbouring runs leave in the caches.  Measured at
+// 64 x 197 x 1536, K = 4, bf16: 22 us forward and 34 us for the gradients (79
+// and 116 MB: 3.6 and 3.4 TB/s; 63 and 199 with eight channels a thread and
+// reads as they are needed); 16 prompts of up to 4096 x 1024: 44 us, 4.6 TB/s.
 #include <algorithm>
 #include <cmath>
 

@@ -2,13 +2,11 @@
 //
 //   h_i[n] = a_i[n] h_{i-1}[n] + b_i[n],  a = exp(delta A[n]),  b = delta u B[n]
 //
-// A CTA holds adjacent channels of one group and walks a segment of one
-// sequence in tiles of N tokens.  For the element-wise parts (loads, softplus,
-// gate, stores) a thread holds eight adjacent channels of one token of the
-// tile; for the recurrence it holds four adjacent states of two channels, so
-// that one read of B, C serves two channels, one read of delta serves four
-// states, and a sum over the states is log2(N/4) shuffle steps.  The two
-// meet in shared memory.
+// Channels are cut into blocks within their group and sequences, where that
+// leaves too few CTAs, into segments; a walk goes tile by tile.  For the
+// element-wise parts (loads, softplus, gate, stores) a lane holds adjacent
+// channels of one token of the tile; for the recurrence it holds some states of
+// some channels over all of its tokens.  The two meet in shared memory.
 #pragma once
 
 #include "lion_internal.h"
@@ -55,7 +53,8 @@ struct ScanP {
 
 namespace {
 
-// LN lanes hold the N = 4 LN states of a channel.
+// The tile of the gradients' segment pass: a lane holds four states of two
+// channels, LN lanes a channel's N = 4 LN.
 template <int LN_, int W_>
 struct ScanTile {
   static constexpr int LN = LN_, W = W_;

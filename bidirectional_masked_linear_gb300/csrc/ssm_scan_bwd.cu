@@ -9,6 +9,17 @@
 // forwards to the states at every fourth token, then takes the four-token
 // blocks from the last one: forwards once more, the four states and decays
 // staying in registers, and back through them.
+//
+// What bounds it: twelve fp32 operations a token, channel and state at the
+// least, 14 with the first walk, against 22 bytes a token and channel (64 x 197
+// x 1536 x 16: 98 us of operations, 68 us of bytes), and the sums over states
+// and over channels, which go through shuffles and shared memory.  The states
+// and decays of a block take the registers, so that two warps share a scheduler
+// and cover half of their latencies: measured 380 us, 47% of the issue slots,
+// 39% of the fp32 pipe.  Eight products a lane instead of sixteen doubles the
+// warps and, with them, the shared-memory traffic of the sums, which then is
+// the bound (570 us); inputs read a tile ahead cost more instructions than they
+// hide (443 us).
 #include <algorithm>
 
 #include "ssm_scan.cuh"

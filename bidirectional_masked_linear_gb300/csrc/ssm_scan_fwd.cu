@@ -6,9 +6,28 @@
 // delta and delta u once; the recurrence lanes, 32 states each (all of a
 // channel's up to 16, of as many channels as that allows), read those and B,
 // C, and leave sum_n C h in delta's place for the element lanes, which gate and
-// store.  32 states a lane are what keeps shared memory from being the bound:
-// a token costs a lane one read of delta and one of delta u for them, and B
-// and C are broadcasts.
+// store.
+//
+// What bounds it: a token, channel and state costs one exponential (32 a clock
+// and SM) and four fp32 operations (128 a clock and SM), which at N = 16 is more
+// than the 8 bytes a token and channel of HBM traffic (2 x 24337 x 1536 x 16:
+// 126 us of exponentials, 90 us of bytes).  With packed pairs a scheduler
+// reaches about 45 clocks for the exponentials and products of 16 channels'
+// token against 32 at the pipes' rates; loads, softplus, gate and stores add
+// about 40.  Measured: 86 clocks, 329 us (14.5e12 operations a second with the
+// segments' pass, 559 us; 1576 in the first form).  32 states a lane are what
+// keeps shared memory from being the bound: a token costs a lane one read of
+// delta and one of delta u for them, and B and C are broadcasts (four states of
+// four channels a lane: 689 us, bound by shared-memory reads; of two: 865).
+// More warps an SM than the 12 that 168 registers leave do not help, fewer
+// hurt (8: 615 us).
+//
+// Few channels: the sequences are cut into segments.  A first launch takes each
+// segment's own contribution to the state that leaves it (the same walk without
+// C, gate and outputs), a small one chains them, and the main launch starts
+// every segment from its state.  (A warp that only has the recurrence, four
+// lanes a channel, with another one preparing its tiles and no segments, took
+// 130 clocks a token, its latencies one after the other: 1711 us.)
 #include <algorithm>
 
 #include "ssm_scan.cuh"
@@ -337,7 +356,8 @@ cudaError_t run_fwd(const ScanP& p, cudaStream_t s) {
 // bound by the states' traffic, read and written once, 16 bytes a thread and
 // sequence with the rows' reads in flight together.  Of a channel's lanes the
 // r-th takes what there is one of for row r: the step size and the gate.  256 x
-// 2048 x 16: 10 us at the kernel, 6.6 TB/s (15 with every lane taking both).
+// 2048 x 16, 67 MB of states: 10.3 us with them in L2, 20.4 from HBM (every lane
+// taking both: 12.3 and 22; four rows or rows read ahead in a loop: no faster).
 constexpr int kStepRows = 2;   // at most the lanes of a channel at N = 8
 
 template <typename T>
@@ -470,7 +490,7 @@ cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cud
 // the host does not see, are taken to fill half of the tokens in CTAs that end
 // at any time: only the last one's time counts in full, which asks for short
 // segments (16 prompts of up to 4096 tokens x 1024 channels: 509 us with two
-// whole rounds, PROMPTS us so).  Up to kMaxSegments, of 64 tokens at least.
+// whole rounds, 331 us so).  Up to kMaxSegments, of 64 tokens at least.
 ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int slots, float whole, bool ragged) {
   constexpr int kMaxSegments = 512;
   ScanPlan r;
