@@ -68,14 +68,13 @@ struct FwdWarp {
 // R adjacent floats.
 template <int R>
 __device__ __forceinline__ void get_some(const float* p, float (&v)[R]) {
-  if (R == 1) {
-    v[0] = p[0];
-  } else if (R == 4) {
+  static_assert(R == 2 || R == 4, "");
+  if (R == 4) {
     const float4 x = *reinterpret_cast<const float4*>(p);
-    v[0] = x.x; v[R > 1 ? 1 : 0] = x.y; v[R > 2 ? R - 2 : 0] = x.z; v[R - 1] = x.w;
+    v[0] = x.x; v[1] = x.y; v[R - 2] = x.z; v[R - 1] = x.w;
   } else {
     const float2 x = *reinterpret_cast<const float2*>(p);
-    v[0] = x.x; v[R - 1] = x.y;
+    v[0] = x.x; v[1] = x.y;
   }
 }
 
@@ -231,8 +230,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, (N == 64 ? 8 : 12) / kFwdWarps
         get_some<RC>(sm.du + t * CW + c0, du);
         if (RC == 2 && LN > 1) {   // the odd lane's order
           const float a = dt[0], b = du[0];
-          dt[0] = odd ? dt[RC - 1] : a; dt[RC - 1] = odd ? a : dt[RC - 1];
-          du[0] = odd ? du[RC - 1] : b; du[RC - 1] = odd ? b : du[RC - 1];
+          dt[0] = odd ? dt[1] : a; dt[1] = odd ? a : dt[1];
+          du[0] = odd ? du[1] : b; du[1] = odd ? b : du[1];
         }
         f2 y[RC];
 #pragma unroll
@@ -262,16 +261,14 @@ __global__ void __launch_bounds__(32 * kFwdWarps, (N == 64 ? 8 : 12) / kFwdWarps
           for (int k = 0; k < RC; ++k) v[k] = sum2(y[k]);
           float* yo = sm.dt + t * CW + c0;
           if (LN > 1) {
-            float r = v[0] + __shfl_xor_sync(0xffffffffu, v[RC - 1], 1);   // RC == 1: both lanes' own
+            float r = v[0] + __shfl_xor_sync(0xffffffffu, v[1], 1);
 #pragma unroll
             for (int o = 2; o < LN; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
             yo[odd] = r;   // lanes of one parity hold the same sum
           } else if (RC == 4) {
-            *reinterpret_cast<float4*>(yo) = make_float4(v[0], v[RC > 1 ? 1 : 0], v[RC > 2 ? RC - 2 : 0], v[RC - 1]);
-          } else if (RC == 2) {
-            *reinterpret_cast<float2*>(yo) = make_float2(v[0], v[RC - 1]);
+            *reinterpret_cast<float4*>(yo) = make_float4(v[0], v[1], v[RC - 2], v[RC - 1]);
           } else {
-            yo[0] = v[0];
+            *reinterpret_cast<float2*>(yo) = make_float2(v[0], v[1]);
           }
         }
       }
@@ -469,7 +466,11 @@ __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, cons
       store_pair(p.seg_state + (((size_t)b * p.nseg + s) * p.D + d) * p.N + n0, x);
       const f2 s2 = pack2(sum[q], sum[q]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) x[e] = fma2(ex2_2(mul2(s2, A[e])), x[e], own[q][e]);
+      for (int e = 0; e < 2; ++e) {
+        // a growing state's factor can overflow where nothing has grown yet
+        const f2 f = ex2_2(mul2(s2, A[e]));
+        x[e] = fma2(pack2(x[e].x == 0.f ? 0.f : f.x, x[e].y == 0.f ? 0.f : f.y), x[e], own[q][e]);
+      }
     }
   }
 }

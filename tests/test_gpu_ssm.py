@@ -446,6 +446,19 @@ def test_scan_captured_in_a_graph():
     assert all(torch.equal(p, s) for p, s in zip(got, want))
 
 
+def test_scan_growing_states():
+    """A > 0 over several segments: nothing before the first input, whatever the factors overflow to."""
+    B, L, D, N = 1, 1600, 8, 16
+    u, dt = torch.zeros(B, L, D, device="cuda"), torch.ones(B, L, D, device="cuda")
+    u[:, -20:] = 1.0
+    A = torch.full((D, N), 0.5, device="cuda")
+    ones = torch.ones(B, L, N, device="cuda")
+    f = ssm.scan_fwd(u, dt, A, ones, ones, dt_softplus=False, return_state=True)
+    h = sum(np.exp(0.5 * k) for k in range(20))
+    assert bool((f.out[:, :-20] == 0).all())
+    assert float((f.h / h - 1).abs().max()) <= 20 * 16 * E
+
+
 def test_autograd_functions():
     """The three ops in one graph: gradients equal the entry points' own."""
     B, L, D, N = 2, 40, 32, 16
