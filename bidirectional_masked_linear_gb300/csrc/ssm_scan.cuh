@@ -274,7 +274,7 @@ struct ScanPlan {
   int nblk, nseg, seglen;
 };
 void fill_scan(ScanP& p, const lion_scan_args& a);   // everything but the plan and the workspace
-ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int slots, float whole,
+ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slots, float whole,
                    bool ragged);
 cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cudaStream_t s);
 

@@ -561,7 +561,7 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(int B, int L, int D, int N, int G, bool have_states, bool ragged) {
   BwdPlan q;
-  q.r = scan_plan(B, L, D, G, kBwdWarps * (N == 8 ? 32 : 512 / N), 2 * kSmCount, 0.85f, ragged);
+  q.r = scan_plan(B, L, D, N, G, kBwdWarps * (N == 8 ? 32 : 512 / N), 2 * kSmCount, 0.85f, ragged);
   size_t at = 0;
   auto take = [&](size_t floats) {
     const size_t here = at;

@@ -486,13 +486,13 @@ cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cud
 // whole rounds.  The cost, in tokens of a round: rounds x (a segment's tokens +
 // what a CTA takes to start), a round that is not full counting for 0.4 plus
 // 0.6 of its fill (fewer CTAs on an SM run faster), plus the chain over the
-// segments; a sequence left whole is spared the pass over the segments' own
+// segments and their states' way through HBM; a sequence left whole is spared the pass over the segments' own
 // contributions and costs `whole` of that.  Ragged sequences, whose lengths
 // the host does not see, are taken to fill half of the tokens in CTAs that end
 // at any time: only the last one's time counts in full, which asks for short
 // segments (16 prompts of up to 4096 tokens x 1024 channels: 509 us with two
 // whole rounds, 331 us so).  Up to kMaxSegments, of 64 tokens at least.
-ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int slots, float whole, bool ragged) {
+ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slots, float whole, bool ragged) {
   constexpr int kMaxSegments = 512;
   ScanPlan r;
   r.nblk = (D / G + cta_channels - 1) / cta_channels;
@@ -502,6 +502,8 @@ ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int slots, floa
     const long long full = n / slots, rest = n % slots;
     return (float)full + (rest ? 0.4f + 0.6f * (float)rest / (float)slots : 0.f);
   };
+  // a token of a round is some 0.85 us; a segment's states cross HBM four times
+  const float states = 4.f * 4.f * (float)B * (float)D * (float)N / (6.7e6f * 0.85f);
   r.nseg = 1;
   r.seglen = (L + 15) / 16 * 16;
   float best = whole * rounds(ctas) * ((float)L + 6.f);
@@ -509,7 +511,7 @@ ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int slots, floa
   for (int n = 2; n <= most; ++n) {
     const int len = ((L + n - 1) / n + 15) / 16 * 16, real = (L + len - 1) / len;   // whole tiles
     if (real != n) continue;
-    const float cost = rounds(ctas * n) * ((float)len + 6.f) + 0.18f * (float)n;
+    const float cost = rounds(ctas * n) * ((float)len + 6.f) + (0.18f + states) * (float)n;
     if (cost < best) {
       best = cost;
       r.nseg = n;
@@ -521,7 +523,7 @@ ScanPlan scan_plan(int B, int L, int D, int G, int cta_channels, int slots, floa
 namespace {
 ScanPlan fwd_plan(int B, int L, int D, int N, int G, bool ragged) {
   const int cw = N == 8 ? 128 : 1024 / N;
-  return scan_plan(B, L, D, G, kFwdWarps * cw, kSmCount * (N == 64 ? 8 : 12) / kFwdWarps, 0.6f, ragged);
+  return scan_plan(B, L, D, N, G, kFwdWarps * cw, kSmCount * (N == 64 ? 8 : 12) / kFwdWarps, 0.6f, ragged);
 }
 }  // namespace
 
