@@ -172,10 +172,6 @@ def _tight(name, t, dtype, shape):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _maybe(name, t, dtype, shape):
-    return 0 if t is None else _tight(name, t, dtype, shape)
-
-
 def _token(name, t, dtype, shape):
     """(address, distance between tokens) of a [B, L, ...] activation whose
     last dimensions are adjacent."""
@@ -242,7 +238,8 @@ def layernorm_fwd(x, weight, bias=None, eps=1e-5, save_stats=False, out=None, st
     ``save_stats`` (float32, one per row, for :func:`layernorm_bwd`)."""
     lib, code = load(), _code(x)
     rows, cols, ld = _rows(x)
-    w, b = _tight("weight", weight, torch.float32, (cols,)), _maybe("bias", bias, torch.float32, (cols,))
+    w = _tight("weight", weight, torch.float32, (cols,))
+    b = 0 if bias is None else _tight("bias", bias, torch.float32, (cols,))
     if out is None:
         y = _new(stream, x.shape, x.dtype, x)
         yp = y.data_ptr()
@@ -300,20 +297,14 @@ class ConvGrads(NamedTuple):
     dstate: Optional[torch.Tensor]
 
 
-def _taps(weight, D):
-    if weight.dim() != 2:
-        raise ValueError("weight must have shape [D, K]")
-    K = weight.shape[1]
-    return _tight("weight", weight, torch.float32, (D, K)), K
-
-
 def _conv_args(x, weight, bias, state, lengths):
     shape = B, L, D = x.shape
-    w, K = _taps(weight, D)
+    K = weight.shape[-1]
+    w = _tight("weight", weight, torch.float32, (D, K))
     xp, ld = _token("x", x, x.dtype, shape)
-    return (B, L, D, K), ld, (xp, w, _maybe("bias", bias, torch.float32, (D,)),
-                              _maybe("state", state, x.dtype, (B, K - 1, D)),
-                              _maybe("lengths", lengths, torch.int32, (B,)))
+    return (B, L, D, K), ld, (xp, w, 0 if bias is None else _tight("bias", bias, torch.float32, (D,)),
+                              0 if state is None else _tight("state", state, x.dtype, (B, K - 1, D)),
+                              0 if lengths is None else _tight("lengths", lengths, torch.int32, (B,)))
 
 
 def conv_bwd_workspace_bytes(B, L, D, K) -> int:
@@ -360,14 +351,15 @@ def conv_step(x, state, weight, bias=None, activation="silu", out=None, stream=N
     [B, K-1, D] moved on in place."""
     lib, code = load(), _code(x)
     B, D = x.shape
-    w, K = _taps(weight, D)
+    K = weight.shape[-1]
+    w = _tight("weight", weight, torch.float32, (D, K))
     if out is None:
         y = _new(stream, (B, D), x.dtype, x)
         yp = y.data_ptr()
     else:
         y, yp = out, _tight("out", out, x.dtype, (B, D))
     _check(lib.lion_conv_step(_tight("x", x, x.dtype, (B, D)), _tight("state", state, x.dtype, (B, K - 1, D)), w,
-                              _maybe("bias", bias, torch.float32, (D,)), yp, B, D, K,
+                              0 if bias is None else _tight("bias", bias, torch.float32, (D,)), yp, B, D, K,
                               _act(activation), code, _handle(stream, x)))
     return y
 
@@ -410,16 +402,10 @@ class ScanGrads(NamedTuple):
     dh0: Optional[torch.Tensor]
 
 
-def _states(A, D):
-    if A.dim() != 2 or A.shape[0] != D:
-        raise ValueError("A must have shape [D, N]")
-    return A.shape[1]
-
-
 def _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths):
     """Sizes, addresses in the structures' order, distances between tokens."""
     shape = B, L, D = u.shape
-    N, T, f32 = _states(A, D), u.dtype, torch.float32
+    N, T, f32 = A.shape[-1], u.dtype, torch.float32
     if Bm.dim() == 3:   # one group
         Bm, Cm = Bm.unsqueeze(2), Cm.unsqueeze(2)
     G = Bm.shape[2]
@@ -429,9 +415,11 @@ def _scan_args(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths):
     cp, cl = _token("Cm", Cm, T, (B, L, G, N))
     zp, zl = (0, 0) if z is None else _token("z", z, T, shape)
     return ((B, L, D, N, G),
-            (up, dp, _tight("A", A, f32, (D, N)), bp, cp, _maybe("Dskip", Dskip, f32, (D,)), zp,
-             _maybe("dt_bias", dt_bias, f32, (D,)), _maybe("h0", h0, f32, (B, D, N)),
-             _maybe("lengths", lengths, torch.int32, (B,))),
+            (up, dp, _tight("A", A, f32, (D, N)), bp, cp,
+             0 if Dskip is None else _tight("Dskip", Dskip, f32, (D,)), zp,
+             0 if dt_bias is None else _tight("dt_bias", dt_bias, f32, (D,)),
+             0 if h0 is None else _tight("h0", h0, f32, (B, D, N)),
+             0 if lengths is None else _tight("lengths", lengths, torch.int32, (B,))),
             (ul, dl, zl, bl, cl))
 
 
@@ -476,7 +464,7 @@ def scan_bwd(dout, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softpl
     B, L, D, N, G = sizes
     f32 = torch.float32
     dop = _tight("dout", dout, u.dtype, u.shape)
-    sp = _maybe("states", states, f32, (B, -(-L // STATE_EVERY), D, N))
+    sp = 0 if states is None else _tight("states", states, f32, (B, -(-L // STATE_EVERY), D, N))
     du, ddt = (_new(stream, u.shape, u.dtype, u) for _ in range(2))
     dB, dC = (_new(stream, Bm.shape, u.dtype, u) for _ in range(2))
     dz = None if z is None else _new(stream, u.shape, u.dtype, u)
@@ -498,7 +486,7 @@ def scan_step(h, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus
     updated in place."""
     lib, code = load(), _code(u)
     shape = B, D = u.shape
-    N, T, f32 = _states(A, D), u.dtype, torch.float32
+    N, T, f32 = A.shape[-1], u.dtype, torch.float32
     G = Bm.shape[1] if Bm.dim() == 3 else 1
     bc = (B, G, N) if Bm.dim() == 3 else (B, N)
     if out is None:
@@ -508,8 +496,10 @@ def scan_step(h, u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, dt_softplus
         y, yp = out, _tight("out", out, T, shape)
     a = _ScanStep_pack(_tight("h", h, f32, (B, D, N)), _tight("u", u, T, shape), _tight("dt", dt, T, shape),
                       _tight("A", A, f32, (D, N)), _tight("Bm", Bm, T, bc), _tight("Cm", Cm, T, bc),
-                      _maybe("Dskip", Dskip, f32, (D,)), _maybe("z", z, T, shape),
-                      _maybe("dt_bias", dt_bias, f32, (D,)), yp, B, D, N, G, int(dt_softplus), code, _handle(stream, u))
+                      0 if Dskip is None else _tight("Dskip", Dskip, f32, (D,)),
+                      0 if z is None else _tight("z", z, T, shape),
+                      0 if dt_bias is None else _tight("dt_bias", dt_bias, f32, (D,)), yp, B, D, N, G,
+                      int(dt_softplus), code, _handle(stream, u))
     _check(lib.lion_scan_step(a))
     return y
 
