@@ -137,6 +137,10 @@ __device__ __forceinline__ f2 gate2(f2 o, float z0, float z1) {
   return mul2(mul2(o, pack2(z0, z1)), sigmoid2(z0, z1));
 }
 
+// For a kernel launched as a dependent (launch_dependent): the launch before it
+// has ended and its writes are there.
+__device__ __forceinline__ void wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Whether rows of es-byte elements, `stride` elements apart, all start on 16 bytes.
 inline bool rows_wide(const void* p, long long stride, int es) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * es % 16 == 0;

@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(ScanP p, T* dB, T* dC) {
   const long long tok = k / N2 / p.G;   // b * L + t
   const int b = (int)(tok / p.L), t = (int)(tok - (long long)b * p.L);
   float s = 0.f;
+  wait_prior();
   if (!p.lengths || t < p.lengths[b])
     for (int q = 0; q < p.nblk; ++q) s += p.part_bc[(size_t)q * n + k];
   (v < p.N ? dB : dC)[k / N2 * p.N + v % p.N] = from_f32<T>(s);
@@ -549,8 +550,8 @@ cudaError_t run_bwd(const ScanP& p, cudaStream_t s) {
 template <typename T>
 cudaError_t run_bc(const ScanP& p, void* dB, void* dC, cudaStream_t s) {
   const long long n = (long long)p.B * p.L * p.G * 2 * p.N;
-  scan_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, static_cast<T*>(dB), static_cast<T*>(dC));
-  return cudaGetLastError();
+  return launch_dependent(scan_bc_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p, static_cast<T*>(dB),
+                          static_cast<T*>(dC));
 }
 
 // The workspace's parts: the forward's own, the states, the segments, the

@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, (N == 64 ? 8 : 12) / kFwdWarps
   };
   if (a0 < a1) fetch_tile(sm.raw[0], a0);
   if (MAIN) {
+    if (p.nseg > 1) wait_prior();
     const float* from = p.nseg > 1 ? p.seg_state + ((size_t)w.b * p.nseg + w.seg) * p.D * N
                         : p.h0     ? p.h0 + (size_t)w.b * p.D * N
                                    : nullptr;
@@ -335,7 +336,9 @@ cudaError_t run_kernel(const ScanP& p, cudaStream_t s) {
   auto kern = scan_fwd_kernel<T, N, MAIN>;
   const size_t smem = sizeof(FwdWarp<T, N>) * kFwdWarps;
   static_assert(sizeof(FwdWarp<T, N>) * kFwdWarps <= 48 * 1024, "more shared memory has to be asked for");
-  kern<<<(unsigned)p.nblk * p.G * p.nseg * p.B, 32 * kFwdWarps, smem, s>>>(p);
+  const dim3 grid((unsigned)p.nblk * p.G * p.nseg * p.B);
+  if (MAIN && p.nseg > 1) return launch_dependent(kern, grid, dim3(32 * kFwdWarps), smem, s, p);   // of the chain
+  kern<<<grid, 32 * kFwdWarps, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -447,6 +450,7 @@ __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, cons
   f2 A[2], x[2];
   load_pair(p.A + (size_t)d * p.N + n0, true, A, kLog2e);
   load_pair(first + bd * p.N + n0, first != nullptr, x);
+  wait_prior();
   for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
     f2 own[kAhead][2];
     float sum[kAhead];
@@ -478,8 +482,7 @@ __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, cons
 
 cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cudaStream_t s) {
   const long long n = (long long)p.B * p.D * (p.N / 4);
-  scan_chain_kernel<<<(unsigned)((n + 63) / 64), 64, 0, s>>>(p, back, first);
-  return cudaGetLastError();
+  return launch_dependent(scan_chain_kernel, dim3((unsigned)((n + 63) / 64)), dim3(64), 0, s, p, back, first);
 }
 
 // Cuts sequences into segments so that the SMs' slots for CTAs are filled in
