@@ -356,17 +356,26 @@ cudaError_t run_fwd(const ScanP& p, cudaStream_t s) {
 // bound by the states' traffic, read and written once, 16 bytes a thread and
 // sequence with the rows' reads in flight together.  Of a channel's lanes the
 // r-th takes what there is one of for row r: the step size and the gate.  256 x
-// 2048 x 16, 67 MB of states: 10.3 us with them in L2, 20.4 from HBM (every lane
-// taking both: 12.3 and 22; four rows or rows read ahead in a loop: no faster).
+// 2048 x 16, 67 MB of states: 10.3 us with them in L2, 18.7 from HBM (every lane
+// taking both: 12.3 and 22; B and C value by value: 19.2; four rows, larger
+// CTAs, or rows read ahead in a loop: no faster).
 constexpr int kStepRows = 2;   // at most the lanes of a channel at N = 8
 
-template <typename T>
-__device__ __forceinline__ float4 four(const T* p) {
+// Four values of B or C, in one read where they lie aligned.
+__device__ __forceinline__ float4 four(const float* p, bool wide) {
+  return wide ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+}
+__device__ __forceinline__ float4 four(const __nv_bfloat16* p, bool wide) {
+  if (wide) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
   return make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
 }
 
 template <typename T, int N>
-__global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a) {
+__global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a, bool bc_wide) {
   constexpr int LN = N / 4;
   const unsigned item = blockIdx.x * 128 + threadIdx.x;
   const int lane = threadIdx.x & 31, ln = item % LN, d = item / LN;
@@ -396,8 +405,8 @@ __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a) {
 #pragma unroll
     for (int r = 0; r < kStepRows; ++r)
       if (b0 + r < a.B) {
-        Bv[r] = four(static_cast<const T*>(a.Bm) + bc + r * bc_hop);
-        Cv[r] = four(static_cast<const T*>(a.Cm) + bc + r * bc_hop);
+        Bv[r] = four(static_cast<const T*>(a.Bm) + bc + r * bc_hop, bc_wide);
+        Cv[r] = four(static_cast<const T*>(a.Cm) + bc + r * bc_hop, bc_wide);
       }
   }
   if (a.dt_softplus) dt = softplus(dt);
@@ -428,7 +437,9 @@ template <typename T, int N>
 cudaError_t run_step(const lion_scan_step_args& a, cudaStream_t s) {
   const long long n = (long long)a.D * (N / 4);
   const int rows = (a.B + kStepRows - 1) / kStepRows;
-  scan_step_kernel<T, N><<<dim3((unsigned)((n + 127) / 128), rows), 128, 0, s>>>(a);
+  const int bc_align = std::min(rows_align(a.Bm, 0, 0, sizeof(T)), rows_align(a.Cm, 0, 0, sizeof(T)));
+  const bool bc_wide = bc_align >= 4 * (int)sizeof(T);
+  scan_step_kernel<T, N><<<dim3((unsigned)((n + 127) / 128), rows), 128, 0, s>>>(a, bc_wide);
   return cudaGetLastError();
 }
 

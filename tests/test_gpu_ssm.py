@@ -311,6 +311,22 @@ def test_scan_steps(N, G, dtype):
     _check("h", h, r["h"], tol * m["h"])
 
 
+def test_scan_step_of_unaligned_rows():
+    """B and C off their vectors' alignment: the aligned copies' bits."""
+    B, D, N = 5, 33, 8
+    a, _ = _scan_inputs(B, 1, D, N, 1, "bf16", True, True, True, True, True, seed=6)
+    dev = {k: v.cuda() for k, v in a.items()}
+    args = {k: dev[k][:, 0].contiguous() for k in ("u", "dt", "Bm", "Cm", "z")}
+    rest = {k: dev[k] for k in ("A", "Dskip", "dt_bias")}
+    h1, h2 = dev["h0"].clone(), dev["h0"].clone()
+    want = ssm.scan_step(h1, **args, **rest)
+    for k in ("u", "dt", "Bm", "Cm", "z"):
+        flat = torch.empty(args[k].numel() + 1, dtype=torch.bfloat16, device="cuda")
+        flat[1:] = args[k].flatten()
+        args[k] = flat[1:].view(args[k].shape)
+    assert torch.equal(ssm.scan_step(h2, **args, **rest), want) and torch.equal(h1, h2)
+
+
 def test_scan_step_captured_in_a_graph():
     B, D, N = 2, 48, 16
     a, _ = _scan_inputs(B, 1, D, N, 1, "bf16", True, True, True, True, True, seed=5)
