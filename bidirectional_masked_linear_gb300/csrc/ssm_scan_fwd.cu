@@ -14,8 +14,8 @@
 // 126 us of exponentials, 90 us of bytes).  With packed pairs a scheduler
 // reaches about 45 clocks for the exponentials and products of 16 channels'
 // token against 32 at the pipes' rates; loads, softplus, gate and stores add
-// about 40.  Measured: 86 clocks, 329 us (14.5e12 operations a second with the
-// segments' pass, 559 us; 1576 in the first form).  32 states a lane are what
+// about 40.  Measured: 86 clocks, 330 us (14.5e12 operations a second with the
+// segments' pass, 552 us; 1576 in the first form).  32 states a lane are what
 // keeps shared memory from being the bound: a token costs a lane one read of
 // delta and one of delta u for them, and B and C are broadcasts (four states of
 // four channels a lane: 689 us, bound by shared-memory reads; of two: 865).
@@ -505,7 +505,7 @@ cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cud
 // the host does not see, are taken to fill half of the tokens in CTAs that end
 // at any time: only the last one's time counts in full, which asks for short
 // segments (16 prompts of up to 4096 tokens x 1024 channels: 509 us with two
-// whole rounds, 331 us so).  Up to kMaxSegments, of 64 tokens at least.
+// whole rounds, 328 us so).  Up to kMaxSegments, of 64 tokens at least.
 ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slots, float whole, bool ragged) {
   constexpr int kMaxSegments = 512;
   ScanPlan r;
