@@ -505,7 +505,7 @@ cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cud
 // the host does not see, are taken to fill half of the tokens in CTAs that end
 // at any time: only the last one's time counts in full, which asks for short
 // segments (16 prompts of up to 4096 tokens x 1024 channels: 509 us with two
-// whole rounds, 328 us so).  Up to kMaxSegments, of 64 tokens at least.
+// whole rounds, 328 to 335 us so).  Up to kMaxSegments, of 64 tokens at least.
 ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slots, float whole, bool ragged) {
   constexpr int kMaxSegments = 512;
   ScanPlan r;
