@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
               if (GATE) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
             }
           }
+          if (LN > 1) __syncwarp();       // the channel's lanes have read this dy and delta u; a shuffle orders no memory
           sm.dy[t * CW + c[0]] = gb[0];   // lanes of one parity hold the same sums
           sm.du[t * CW + c[0]] = qa[0];
           if (GATE) sm.y[t * CW + c[0]] = y[0];

@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, (N == 64 ? 8 : 12) / kFwdWarps
             float r = v[0] + __shfl_xor_sync(0xffffffffu, v[1], 1);
 #pragma unroll
             for (int o = 2; o < LN; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-            yo[odd] = r;   // lanes of one parity hold the same sum
+            __syncwarp();   // the channel's lanes have read this delta; a shuffle orders no memory
+            yo[odd] = r;    // lanes of one parity hold the same sum
           } else if (RC == 4) {
             *reinterpret_cast<float4*>(yo) = make_float4(v[0], v[1], v[RC - 2], v[RC - 1]);
           } else {
