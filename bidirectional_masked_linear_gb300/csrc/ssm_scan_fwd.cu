@@ -452,6 +452,16 @@ cudaError_t run_step(const lion_scan_step_args& a, cudaStream_t s) {
 // of a channel and reads kAhead segments ahead.
 namespace {
 constexpr int kAhead = 16;
+
+// 2^s x + own.  A growing state's factor can pass fp32 where the state, 0 or tiny, does not: what 2^s has above 2^126
+// is multiplied in first, in finite parts, so that the product overflows only if 2^s x does (2^378 takes the least
+// positive x there).
+__device__ __forceinline__ float grow(float s, float x, float own) {
+  if (s > 126.f) x *= ex2(fminf(s - 126.f, 126.f));
+  if (s > 252.f) x *= ex2(fminf(s - 252.f, 126.f));
+  return fmaf(ex2(s > 126.f ? 126.f : s), x, own);   // a NaN stays one
+}
+
 __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, const float* first) {
   const int per = p.N / 4;
   const long long k = (long long)blockIdx.x * 64 + threadIdx.x;
@@ -483,9 +493,8 @@ __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, cons
       const f2 s2 = pack2(sum[q], sum[q]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        // a growing state's factor can overflow where nothing has grown yet
-        const f2 f = ex2_2(mul2(s2, A[e]));
-        x[e] = fma2(pack2(x[e].x == 0.f ? 0.f : f.x, x[e].y == 0.f ? 0.f : f.y), x[e], own[q][e]);
+        const f2 s = mul2(s2, A[e]);
+        x[e] = pack2(grow(s.x, x[e].x, own[q][e].x), grow(s.y, x[e].y, own[q][e].y));
       }
     }
   }

@@ -34,3 +34,61 @@ def test_equal_sequences_give_equal_bits(N, dtype):
     for name, t in (("out", f.out), ("h", f.h), ("states", f.states), ("du", g.du), ("ddt", g.ddt), ("dB", g.dB),
                     ("dC", g.dC), ("dz", g.dz), ("dh0", g.dh0)):
         assert torch.equal(t, t[:1].expand_as(t)), name
+
+
+# ------------------------------------------------------ factors that overflow
+
+def _growth(L=1600, D=8, N=16):
+    """Two adjacent tokens that each multiply a state by exp(64): their product, the factor of the segment that they
+    lie in, is past fp32, what they make of a state of 1e-36 is not."""
+    dt, A = torch.zeros(1, L, D, device="cuda"), torch.full((D, N), 64.0, device="cuda")
+    dt[:, 200:202] = 1.0
+    return dt, A, torch.ones(1, L, N, device="cuda"), 1e-36 * np.exp(128.0)
+
+
+# two exponents of 92 in base 2 and one of 185, each rounded and each error a factor of ln 2
+GROWTH_TOL = 512 * E
+
+
+def test_scan_chain_of_a_tiny_state():
+    dt, A, ones, want = _growth()
+    h0 = torch.full((1, 8, 16), 1e-36, device="cuda")
+    f = ssm.scan_fwd(torch.zeros_like(dt), dt, A, ones, ones, dt_softplus=False, h0=h0, return_state=True)
+    assert float((f.h / want - 1).abs().max()) <= GROWTH_TOL
+    assert float((f.out[:, 201:] / (16 * want) - 1).abs().max()) <= GROWTH_TOL
+
+
+def test_scan_chain_of_a_tiny_gradient():
+    dt, A, ones, want = _growth()
+    u, dout = torch.zeros_like(dt), torch.zeros_like(dt)
+    u[:, 0] = 1.0   # its step is 0: it adds nothing, but its step's gradient is u sum_n G B
+    dout[:, -1] = 1e-36
+    h0 = torch.zeros(1, 8, 16, device="cuda")
+    g = ssm.scan_bwd(dout, u, dt, A, ones, ones, dt_softplus=False, h0=h0)
+    assert float((g.dh0 / want - 1).abs().max()) <= GROWTH_TOL
+    assert float((g.ddt[:, 0] / (16 * want) - 1).abs().max()) <= GROWTH_TOL
+    for t in (g.du[:, :200], g.du[:, 202:], g.ddt[:, 1:], g.dA, g.dB, g.dC):
+        assert bool((t == 0).all())
+
+
+@pytest.mark.parametrize("sign", (1, -1))
+def test_scan_chain_past_overflow(sign):
+    """Segments whose factor overflows: of a state that is 0 they make 0, of any other what the walk does, inf."""
+    L, D, N = 1600, 8, 16
+    u, dt = torch.zeros(1, L, D, device="cuda"), torch.ones(1, L, D, device="cuda")
+    u[:, -20:] = sign
+    A, ones = torch.full((D, N), 2.0, device="cuda"), torch.ones(1, L, N, device="cuda")
+    f = ssm.scan_fwd(u, dt, A, ones, ones, dt_softplus=False, return_state=True)
+    want = sign * sum(np.exp(2.0 * k) for k in range(20))
+    assert bool((f.out[:, :-20] == 0).all())
+    assert float((f.h / want - 1).abs().max()) <= 20 * 16 * E
+    dout = torch.zeros_like(u)
+    dout[:, :20] = sign
+    h0 = torch.zeros(1, D, N, device="cuda")
+    g = ssm.scan_bwd(dout, u, dt, A, ones, ones, dt_softplus=False, h0=h0)
+    want = sign * sum(np.exp(2.0 * (k + 1)) for k in range(20))
+    assert float((g.dh0 / want - 1).abs().max()) <= 21 * 16 * E
+    assert bool((g.du[:, 20:] == 0).all())
+    f = ssm.scan_fwd(torch.zeros_like(u), dt, A, ones, ones, dt_softplus=False, h0=sign * torch.ones_like(h0),
+                     return_state=True)
+    assert bool((f.h == sign * float("inf")).all())
