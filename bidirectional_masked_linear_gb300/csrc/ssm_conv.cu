@@ -290,8 +290,9 @@ __global__ void __launch_bounds__(32 * kBwdRows, 2) conv_bwd_kernel(ConvP p) {
     Quad win[K], dp[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) dp[k] = zero4();
+    // (the state before a sequence without tokens meets no gradient, whatever it holds)
 #pragma unroll
-    for (int k = 1; k < K; ++k) win[k] = l.at(p, i0 - K + k).get();
+    for (int k = 1; k < K; ++k) win[k] = l.len > 0 ? l.at(p, i0 - K + k).get() : zero4();
     const int last = mine + K - 1;   // steps until the run's last dx is complete
     for (int j = 0; j < last; j += A) {
       Raw4<T> vx[A], vy[A];

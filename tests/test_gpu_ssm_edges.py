@@ -92,3 +92,21 @@ def test_scan_chain_past_overflow(sign):
     f = ssm.scan_fwd(torch.zeros_like(u), dt, A, ones, ones, dt_softplus=False, h0=sign * torch.ones_like(h0),
                      return_state=True)
     assert bool((f.h == sign * float("inf")).all())
+
+
+# ------------------------------------------------------------ empty sequences
+
+@pytest.mark.parametrize("dtype", ("bf16", "fp32"))
+@pytest.mark.parametrize("bad", (float("nan"), float("inf")))
+def test_conv_gradients_of_an_empty_sequence(bad, dtype):
+    """The state before a sequence without tokens reaches no output, whatever it holds."""
+    B, L, D, K = 3, 9, 20, 4
+    x, dy = (torch.randn(B, L, D, device="cuda").to(T[dtype]) for _ in range(2))
+    w, b = torch.randn(D, K, device="cuda"), torch.randn(D, device="cuda")
+    st = torch.randn(B, K - 1, D, device="cuda").to(T[dtype])
+    lens = torch.tensor([9, 0, 2], dtype=torch.int32, device="cuda")
+    want = ssm.conv_bwd(dy, x, w, b, state=st, lengths=lens)
+    st[1] = bad
+    got = ssm.conv_bwd(dy, x, w, b, state=st, lengths=lens)
+    assert all(torch.equal(p, s) for p, s in zip(got, want))
+    assert bool((got.dstate[1] == 0).all())
