@@ -114,11 +114,22 @@ __device__ __forceinline__ void load_bc(const ScanP& p, const ScanAt& w, const v
   }
 }
 
-// The state's four values of a channel, or of the decays (scaled by log2 e).
-__device__ __forceinline__ void load_pair(const float* src, bool there, f2 (&v)[2], float scale = 1.f) {
+// The state's four values of a channel.
+__device__ __forceinline__ void load_pair(const float* src, bool there, f2 (&v)[2]) {
   const float4 x = there ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-  v[0] = pack2(x.x * scale, x.y * scale);
-  v[1] = pack2(x.z * scale, x.w * scale);
+  v[0] = pack2(x.x, x.y);
+  v[1] = pack2(x.z, x.w);
+}
+// A as the kernels use it: times log2 e.  -inf (a state that keeps nothing) becomes a finite value that keeps as
+// little: the step of a place without a token is 0, and 0 times it has to be 0.
+__device__ __forceinline__ float decay(float a) {
+  const float x = a * kLog2e;
+  return x < -3e38f ? -3e38f : x;   // a NaN stays one
+}
+__device__ __forceinline__ void load_decays(const float* src, bool there, f2 (&v)[2]) {
+  load_pair(src, there, v);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) v[k] = pack2(decay(v[k].x), decay(v[k].y));
 }
 __device__ __forceinline__ void store_pair(float* dst, const f2 (&v)[2]) {
   const float2 a = unpack2(v[0]), b = unpack2(v[1]);

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(32 * W) scan_bwd_segment_kernel(ScanP p) {
   f2 A[2][2], g[2][2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    load_pair(p.A + (size_t)d[k] * N + 4 * ln, live[k], A[k], kLog2e);
+    load_decays(p.A + (size_t)d[k] * N + 4 * ln, live[k], A[k]);
     g[k][0] = g[k][1] = pack2(0.f, 0.f);
   }
   float total[8];
@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   typename BwdSmem<T, N>::Warp& sm = sh.warp[warp];
   ScanAt w = scan_at(p, S::CB);
-  const int cta_d0 = w.d0;
   w.d0 += warp * CW;
   w.nch = max(0, min(CW, w.nch - warp * CW));   // a warp without channels goes along: the CTA has barriers
   // element role: VL vectors of four channels, 32 / VT tokens apart
@@ -177,13 +176,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
     live[k] = c[k] < w.nch;
   }
   const int n0 = ln * RN + 4 * flip, n1 = ln * RN + 4 * (flip ^ 1);   // the first and the second block's states
-  auto load_h = [&](const float* from, bool have, f2 (&v)[RC][4], float scale) {
+  auto load_h = [&](const float* from, bool have, f2 (&v)[RC][4]) {
 #pragma unroll
     for (int k = 0; k < RC; ++k) {
       f2 a[2], b[2];
       const float* row = from + (size_t)(w.d0 + c[k]) * N;
-      load_pair(row + n0, have && live[k], a, scale);
-      load_pair(row + n1, have && live[k], b, scale);
+      load_pair(row + n0, have && live[k], a);
+      load_pair(row + n1, have && live[k], b);
       v[k][0] = a[0]; v[k][1] = a[1]; v[k][2] = b[0]; v[k][3] = b[1];
     }
   };
@@ -198,13 +197,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
     }
   };
   f2 A[RC][4], g[RC][4], dA[RC][4];
-  load_h(p.A, true, A, kLog2e);
+  load_h(p.A, true, A);
   // what the segments after this one pass back into it
-  load_h(p.nseg > 1 ? p.seg_state + ((size_t)w.b * p.nseg + w.seg) * p.D * N : p.A, p.nseg > 1, g, 1.f);
+  load_h(p.nseg > 1 ? p.seg_state + ((size_t)w.b * p.nseg + w.seg) * p.D * N : p.A, p.nseg > 1, g);
 #pragma unroll
   for (int k = 0; k < RC; ++k)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) dA[k][q] = pack2(0.f, 0.f);
+    for (int q = 0; q < 4; ++q) {
+      A[k][q] = pack2(decay(A[k][q].x), decay(A[k][q].y));
+      dA[k][q] = pack2(0.f, 0.f);
+    }
   float bias[4], skip[4], dskip[4], dbias[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       f2 h[RC][4];
-      load_h(p.states + ((size_t)w.b * p.nst + i0 / TT) * p.D * N, true, h, 1.f);
+      load_h(p.states + ((size_t)w.b * p.nst + i0 / TT) * p.D * N, true, h);
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
       for (int k = tid; k < TT * N; k += NT) {

@@ -80,11 +80,11 @@ __device__ __forceinline__ void get_some(const float* p, float (&v)[R]) {
 
 // RN states of a channel (fp32, 16-byte aligned) as pairs.
 template <int RN>
-__device__ __forceinline__ void load_states(const float* src, bool there, f2 (&v)[RN / 2], float scale = 1.f) {
+__device__ __forceinline__ void load_states(const float* src, bool there, f2 (&v)[RN / 2]) {
 #pragma unroll
   for (int k = 0; k < RN / 4; ++k) {
     f2 x[2];
-    load_pair(src + 4 * k, there, x, scale);
+    load_pair(src + 4 * k, there, x);
     v[2 * k] = x[0];
     v[2 * k + 1] = x[1];
   }
@@ -126,9 +126,12 @@ __global__ void __launch_bounds__(32 * kFwdWarps, (N == 64 ? 8 : 12) / kFwdWarps
 #pragma unroll
   for (int k = 0; k < RC; ++k) {
     live[k] = c0 + (k ^ odd) < w.nch;
-    load_states<RN>(p.A + state_at + (k ^ odd) * N, live[k], A[k], kLog2e);
+    load_states<RN>(p.A + state_at + (k ^ odd) * N, live[k], A[k]);
 #pragma unroll
-    for (int q = 0; q < RN / 2; ++q) h[k][q] = pack2(0.f, 0.f);
+    for (int q = 0; q < RN / 2; ++q) {
+      A[k][q] = pack2(decay(A[k][q].x), decay(A[k][q].y));
+      h[k][q] = pack2(0.f, 0.f);
+    }
   }
   float total[4], bias[4], skip[4];
 #pragma unroll
@@ -403,6 +406,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a, b
       if (a.Dskip) skip = a.Dskip[d];
     }
     A = *reinterpret_cast<const float4*>(a.A + (size_t)d * N + 4 * ln);
+    A = make_float4(decay(A.x), decay(A.y), decay(A.z), decay(A.w));
 #pragma unroll
     for (int r = 0; r < kStepRows; ++r)
       if (b0 + r < a.B) {
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a, b
 #pragma unroll
   for (int r = 0; r < kStepRows; ++r) {
     const int from = lane - ln + r;   // the lane that has row r's step size
-    const float s = __shfl_sync(0xffffffffu, dt, from) * kLog2e, x = __shfl_sync(0xffffffffu, du, from);
+    const float s = __shfl_sync(0xffffffffu, dt, from), x = __shfl_sync(0xffffffffu, du, from);
     h[r].x = fmaf(ex2(s * A.x), h[r].x, x * Bv[r].x);
     h[r].y = fmaf(ex2(s * A.y), h[r].y, x * Bv[r].y);
     h[r].z = fmaf(ex2(s * A.z), h[r].z, x * Bv[r].z);
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, cons
   const long long bd = k / per;
   const int b = (int)(bd / p.D), d = (int)(bd - (long long)b * p.D);
   f2 A[2], x[2];
-  load_pair(p.A + (size_t)d * p.N + n0, true, A, kLog2e);
+  load_decays(p.A + (size_t)d * p.N + n0, true, A);
   load_pair(first + bd * p.N + n0, first != nullptr, x);
   wait_prior();
   for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {

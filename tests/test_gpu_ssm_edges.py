@@ -110,3 +110,35 @@ def test_conv_gradients_of_an_empty_sequence(bad, dtype):
     got = ssm.conv_bwd(dy, x, w, b, state=st, lengths=lens)
     assert all(torch.equal(p, s) for p, s in zip(got, want))
     assert bool((got.dstate[1] == 0).all())
+
+
+# ---------------------------------------------------- states that forget at once
+
+@pytest.mark.parametrize("dtype", ("bf16", "fp32"))
+@pytest.mark.parametrize("L,D,reverse", ((20, 33, False), (20, 33, True), (600, 24, False), (600, 24, True)))
+def test_scan_of_states_without_memory(L, D, reverse, dtype):
+    """A = -inf keeps nothing (exp(delta A) = 0), and the tokens that a sequence does not have change nothing."""
+    N, n = 16, [L, L // 3 + 1]
+    a, dout = _scan_inputs(2, L, D, N, 1, dtype, True, True, True, True, True, seed=L)
+    a["A"][:, 1::3] = -float("inf")
+    lens = torch.tensor(n, dtype=torch.int32)
+    A64 = {k: _f64(v) for k, v in a.items()}
+    r = ref.scan(**A64, lengths=n, reverse=reverse)
+    m = ref.scan(**A64, lengths=n, reverse=reverse, absolute=True)
+    dev = {k: v.cuda() for k, v in a.items()}
+    how = dict(lengths=lens.cuda(), reverse=reverse)
+    f = ssm.scan_fwd(**dev, **how, return_state=True, save_states=True)
+    tol = E * (64 + 16 * L + 2 * (N + D + 2 * L))
+    _check("out", f.out, r["out"], tol * m["out"])
+    _check("h", f.h, r["h"], tol * m["h"])
+    # the gradients are those of a decay that is as good as none
+    g = ssm.scan_bwd(dout.cuda(), **dev, **how, states=f.states)
+    dev["A"].clamp_(min=-1e30)
+    want = ssm.scan_bwd(dout.cuda(), **dev, **how, states=f.states)
+    assert all(torch.equal(p, s) for p, s in zip(g, want))
+    # one token after these
+    one = {k: dev[k][:, 0].contiguous() for k in ("u", "dt", "Bm", "Cm", "z")}
+    rest = {k: dev[k] for k in ("Dskip", "dt_bias")}
+    h1, h2 = f.h.clone(), f.h.clone()
+    assert torch.equal(ssm.scan_step(h1, **one, A=a["A"].cuda(), **rest), ssm.scan_step(h2, **one, A=dev["A"], **rest))
+    assert torch.equal(h1, h2)
