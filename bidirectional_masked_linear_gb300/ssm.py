@@ -217,6 +217,34 @@ def _workspace(workspace, like, stream, name, *sizes):
     return ws.data_ptr(), n, ws
 
 
+# ------------------------------------------------------------ first derivatives
+
+class _Refuse(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, needs, grad):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the state space block's gradients cannot be differentiated again")
+
+
+def _first_only(backward):
+    """Gradients that raise if they are differentiated, as the kernels' are
+    not: without this a second derivative would lack their terms.  (PyTorch's
+    own ``once_differentiable`` looks at the incoming gradient alone, which may
+    be a constant.)"""
+    @functools.wraps(backward)
+    def first(ctx, dy):
+        with torch.no_grad():
+            grads = backward(ctx, dy)
+        if not torch.is_grad_enabled():
+            return grads
+        needs = next((t for t in (dy, *ctx.saved_tensors) if t is not None and t.requires_grad), None)
+        return tuple(g if g is None or needs is None else _Refuse.apply(needs, g) for g in grads)
+    return first
+
+
 # ------------------------------------------------------------------ layer norm
 
 def _rows(x):
@@ -282,6 +310,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_only
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = layernorm_bwd(dy.contiguous(), x, weight, mean, rstd, ctx.bias)
@@ -375,6 +404,7 @@ class CausalConv(torch.autograd.Function):
         return conv_fwd(x, weight, bias, activation, state, lengths, reverse)
 
     @staticmethod
+    @_first_only
     def backward(ctx, dy):
         x, weight, bias, state, lengths = ctx.saved_tensors
         activation, reverse = ctx.how
@@ -517,6 +547,7 @@ class SelectiveScan(torch.autograd.Function):
         return f.out
 
     @staticmethod
+    @_first_only
     def backward(ctx, dout):
         u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lengths, states = ctx.saved_tensors
         softplus, reverse = ctx.how
