@@ -4,23 +4,32 @@
 
 #include "../../include/lion.h"
 #include "lion_internal.h"
+#include "ssm_check.h"
 
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-bool device_accessible(const void* p) {
-  cudaPointerAttributes at;
-  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
+// Checks of a call's pointers: aligned to `a` bytes and memory that the current device's kernels can use.
+class Pointers {
+ public:
+  Pointers() {
+    if (cudaGetDevice(&device_) != cudaSuccess) cudaGetLastError();   // no device: no pointer passes
   }
-  if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) return true;
-  return at.type == cudaMemoryTypeHost && at.devicePointer != nullptr;
-}
+  bool need(const void* p, size_t a) const { return p && aligned(p, a) && usable(p); }
+  bool maybe(const void* p, size_t a) const { return !p || need(p, a); }
 
-bool need(const void* p, size_t a) { return p && aligned(p, a) && device_accessible(p); }
-bool maybe(const void* p, size_t a) { return !p || (aligned(p, a) && device_accessible(p)); }
+ private:
+  bool usable(const void* p) const {
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    return lion::usable_on(at, device_);
+  }
+  int device_ = -1;
+};
 bool dtype_ok(int t) { return t == LION_DTYPE_BF16 || t == LION_DTYPE_FP32; }
 size_t esize(int t) { return t == LION_DTYPE_BF16 ? 2 : 4; }
 bool flag(int v) { return v == 0 || v == 1; }
@@ -39,7 +48,7 @@ template <typename F>
 lion_status with_workspace(void* ws, size_t ws_bytes, size_t want, cudaStream_t s, F go) {
   if (want == 0) return from_cuda(go(nullptr));
   if (ws) {
-    if (!aligned(ws, 256) || !device_accessible(ws) || ws_bytes < want) return LION_ERR_INVALID_ARG;
+    if (!Pointers().need(ws, 256) || ws_bytes < want) return LION_ERR_INVALID_ARG;
     return from_cuda(go(ws));
   }
   cudaError_t e = cudaMallocAsync(&ws, want, s);
@@ -84,9 +93,10 @@ lion_status lion_layernorm_fwd(const lion_layernorm_args* a) {
   if (!a) return LION_ERR_INVALID_ARG;
   const lion_status st = norm_sizes(a->rows, a->cols, a->x_row, a->dtype);
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(a->dtype);
-  if (!need(a->x, es) || !need(a->weight, 4) || !maybe(a->bias, 4) || !need(a->y, es) || !maybe(a->mean, 4) ||
-      !maybe(a->rstd, 4) || !a->mean != !a->rstd || !(a->eps >= 0.f))
+  if (!ptr.need(a->x, es) || !ptr.need(a->weight, 4) || !ptr.maybe(a->bias, 4) || !ptr.need(a->y, es) ||
+      !ptr.maybe(a->mean, 4) || !ptr.maybe(a->rstd, 4) || !a->mean != !a->rstd || !(a->eps >= 0.f))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_layernorm_fwd(*a, a->stream));
@@ -101,9 +111,10 @@ lion_status lion_layernorm_bwd(const lion_layernorm_bwd_args* a) {
   if (!a) return LION_ERR_INVALID_ARG;
   const lion_status st = norm_sizes(a->rows, a->cols, a->x_row, a->dtype);
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(a->dtype);
-  if (!need(a->dy, es) || !need(a->x, es) || !need(a->weight, 4) || !need(a->mean, 4) || !need(a->rstd, 4) ||
-      !need(a->dx, es) || !need(a->dweight, 4) || !maybe(a->dbias, 4))
+  if (!ptr.need(a->dy, es) || !ptr.need(a->x, es) || !ptr.need(a->weight, 4) || !ptr.need(a->mean, 4) ||
+      !ptr.need(a->rstd, 4) || !ptr.need(a->dx, es) || !ptr.need(a->dweight, 4) || !ptr.maybe(a->dbias, 4))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(a->workspace, a->workspace_bytes, lion::layernorm_bwd_workspace_bytes(a->rows, a->cols),
@@ -114,9 +125,11 @@ lion_status lion_conv_fwd(const lion_conv_args* a) {
   if (!a) return LION_ERR_INVALID_ARG;
   const lion_status st = conv_sizes(a->B, a->L, a->D, a->K, a->act, a->reverse, a->dtype, a->x_token);
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(a->dtype);
-  if (!need(a->x, es) || !need(a->weight, 4) || !maybe(a->bias, 4) || !maybe(a->state, es) || !maybe(a->lengths, 4) ||
-      !need(a->y, es) || !maybe(a->state_out, es) || (a->state && a->state_out == a->state))
+  if (!ptr.need(a->x, es) || !ptr.need(a->weight, 4) || !ptr.maybe(a->bias, 4) || !ptr.maybe(a->state, es) ||
+      !ptr.maybe(a->lengths, 4) || !ptr.need(a->y, es) || !ptr.maybe(a->state_out, es) ||
+      (a->state && a->state_out == a->state))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_conv_fwd(*a, a->stream));
@@ -131,10 +144,11 @@ lion_status lion_conv_bwd(const lion_conv_bwd_args* a) {
   if (!a) return LION_ERR_INVALID_ARG;
   const lion_status st = conv_sizes(a->B, a->L, a->D, a->K, a->act, a->reverse, a->dtype, a->x_token);
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(a->dtype);
-  if (!need(a->dy, es) || !need(a->x, es) || !need(a->weight, 4) || !maybe(a->bias, 4) || !maybe(a->state, es) ||
-      !maybe(a->lengths, 4) || !need(a->dx, es) || !need(a->dweight, 4) || !maybe(a->dbias, 4) ||
-      !maybe(a->dstate, es))
+  if (!ptr.need(a->dy, es) || !ptr.need(a->x, es) || !ptr.need(a->weight, 4) || !ptr.maybe(a->bias, 4) ||
+      !ptr.maybe(a->state, es) || !ptr.maybe(a->lengths, 4) || !ptr.need(a->dx, es) || !ptr.need(a->dweight, 4) ||
+      !ptr.maybe(a->dbias, 4) || !ptr.maybe(a->dstate, es))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(a->workspace, a->workspace_bytes, lion::conv_bwd_workspace_bytes(a->B, a->L, a->D, a->K),
@@ -145,8 +159,9 @@ lion_status lion_conv_step(const void* x, void* state, const float* weight, cons
                            int K, int act, int dtype, cudaStream_t stream) {
   const lion_status st = conv_sizes(B, 1, D, K, act, 0, dtype, 0);
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(dtype);
-  if (!need(x, es) || !need(state, es) || !need(weight, 4) || !maybe(bias, 4) || !need(y, es))
+  if (!ptr.need(x, es) || !ptr.need(state, es) || !ptr.need(weight, 4) || !ptr.maybe(bias, 4) || !ptr.need(y, es))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_conv_step(x, state, weight, bias, y, B, D, K, act, dtype, stream));
@@ -161,14 +176,16 @@ lion_status lion_scan_fwd(const lion_scan_args* a) {
   if (!a) return LION_ERR_INVALID_ARG;
   const lion_status st = scan_sizes(a->B, a->L, a->D, a->N, a->G, a->dt_softplus, a->reverse, a->dtype);
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(a->dtype);
   const long long gn = (long long)a->G * a->N;
   if (!stride_ok(a->u_token, a->D) || !stride_ok(a->dt_token, a->D) || !stride_ok(a->z_token, a->D) ||
       !stride_ok(a->b_token, gn) || !stride_ok(a->c_token, gn))
     return LION_ERR_INVALID_ARG;
-  if (!need(a->u, es) || !need(a->dt, es) || !need(a->A, 16) || !need(a->Bm, es) || !need(a->Cm, es) ||
-      !maybe(a->Dskip, 4) || !maybe(a->z, es) || !maybe(a->dt_bias, 4) || !maybe(a->h0, 16) ||
-      !maybe(a->lengths, 4) || !need(a->out, es) || !maybe(a->h_out, 16) || !maybe(a->states, 16))
+  if (!ptr.need(a->u, es) || !ptr.need(a->dt, es) || !ptr.need(a->A, 16) || !ptr.need(a->Bm, es) ||
+      !ptr.need(a->Cm, es) || !ptr.maybe(a->Dskip, 4) || !ptr.maybe(a->z, es) || !ptr.maybe(a->dt_bias, 4) ||
+      !ptr.maybe(a->h0, 16) || !ptr.maybe(a->lengths, 4) || !ptr.need(a->out, es) || !ptr.maybe(a->h_out, 16) ||
+      !ptr.maybe(a->states, 16))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(a->workspace, a->workspace_bytes, lion::scan_workspace_bytes(a->B, a->L, a->D, a->N, a->G),
@@ -184,16 +201,18 @@ lion_status lion_scan_bwd(const lion_scan_bwd_args* a) {
   if (!a) return LION_ERR_INVALID_ARG;
   const lion_status st = scan_sizes(a->B, a->L, a->D, a->N, a->G, a->dt_softplus, a->reverse, a->dtype);
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(a->dtype);
   const long long gn = (long long)a->G * a->N;
   if (!stride_ok(a->u_token, a->D) || !stride_ok(a->dt_token, a->D) || !stride_ok(a->z_token, a->D) ||
       !stride_ok(a->b_token, gn) || !stride_ok(a->c_token, gn))
     return LION_ERR_INVALID_ARG;
-  if (!need(a->dout, es) || !need(a->u, es) || !need(a->dt, es) || !need(a->A, 16) || !need(a->Bm, es) ||
-      !need(a->Cm, es) || !maybe(a->Dskip, 4) || !maybe(a->z, es) || !maybe(a->dt_bias, 4) || !maybe(a->h0, 16) ||
-      !maybe(a->lengths, 4) || !maybe(a->states, 16) || !need(a->du, es) || !need(a->ddt, es) || !need(a->dA, 16) ||
-      !need(a->dB, es) || !need(a->dC, es) || !maybe(a->dDskip, 4) || !maybe(a->dz, es) || !a->z != !a->dz ||
-      !maybe(a->ddt_bias, 4) || !maybe(a->dh0, 16))
+  if (!ptr.need(a->dout, es) || !ptr.need(a->u, es) || !ptr.need(a->dt, es) || !ptr.need(a->A, 16) ||
+      !ptr.need(a->Bm, es) || !ptr.need(a->Cm, es) || !ptr.maybe(a->Dskip, 4) || !ptr.maybe(a->z, es) ||
+      !ptr.maybe(a->dt_bias, 4) || !ptr.maybe(a->h0, 16) || !ptr.maybe(a->lengths, 4) || !ptr.maybe(a->states, 16) ||
+      !ptr.need(a->du, es) || !ptr.need(a->ddt, es) || !ptr.need(a->dA, 16) || !ptr.need(a->dB, es) ||
+      !ptr.need(a->dC, es) || !ptr.maybe(a->dDskip, 4) || !ptr.maybe(a->dz, es) || !a->z != !a->dz ||
+      !ptr.maybe(a->ddt_bias, 4) || !ptr.maybe(a->dh0, 16))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(a->workspace, a->workspace_bytes,
@@ -206,9 +225,11 @@ lion_status lion_scan_step(const lion_scan_step_args* a) {
   lion_status st = scan_sizes(a->B, 1, a->D, a->N, a->G, a->dt_softplus, 0, a->dtype);
   if (st == LION_OK && a->B > 2 * 65535) st = LION_ERR_UNSUPPORTED;   // two sequences a CTA on a grid's second axis
   if (st == LION_ERR_INVALID_ARG) return st;
+  const Pointers ptr;
   const size_t es = esize(a->dtype);
-  if (!need(a->h, 16) || !need(a->u, es) || !need(a->dt, es) || !need(a->A, 16) || !need(a->Bm, es) ||
-      !need(a->Cm, es) || !maybe(a->Dskip, 4) || !maybe(a->z, es) || !maybe(a->dt_bias, 4) || !need(a->out, es))
+  if (!ptr.need(a->h, 16) || !ptr.need(a->u, es) || !ptr.need(a->dt, es) || !ptr.need(a->A, 16) ||
+      !ptr.need(a->Bm, es) || !ptr.need(a->Cm, es) || !ptr.maybe(a->Dskip, 4) || !ptr.maybe(a->z, es) ||
+      !ptr.maybe(a->dt_bias, 4) || !ptr.need(a->out, es))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_scan_step(*a, a->stream));

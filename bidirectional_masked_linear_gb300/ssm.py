@@ -11,6 +11,8 @@ sequences evenly laid out.
 
 ``stream``: the stream to run on (the current one by default).  Outputs and
 workspaces belong to it; inputs made on another stream have to be ready on it.
+Tensors and stream belong to the current device (``torch.cuda.device``), on
+which the library launches; any other is refused.
 """
 from __future__ import annotations
 
@@ -123,10 +125,13 @@ def load():
 
 _CODES = {torch.bfloat16: lion.DTYPE_BF16, torch.float32: lion.DTYPE_FP32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _handle(stream, x):
     if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {x.device}")
         return stream.cuda_stream
     if _raw_stream is None:
         return torch.cuda.current_stream(x.device).cuda_stream
@@ -147,6 +152,8 @@ def _code(x):
         raise TypeError(f"activations must be bfloat16 or float32, got {x.dtype}")
     if not x.is_cuda:
         raise ValueError("tensors must be on the GPU")
+    if x.get_device() != _current_device():
+        raise ValueError(f"tensors are on {x.device}, the current device is cuda:{_current_device()}")
     return code
 
 

@@ -428,6 +428,9 @@ size_t lion_attn_reordered_bwd_workspace_bytes(int B, int H, int L, int d);
  *     with atomics: the same call gives the same bits.
  *   - workspace: device, 256-byte aligned, of the queried size, or NULL for a
  *     stream-ordered allocation.
+ *   - Pointers are memory of the current device, managed memory or mapped host
+ *     memory, and the stream is the current device's; another device's memory
+ *     is refused (LION_ERR_INVALID_ARG).
  */
 
 /* Largest row lion_layernorm_* take. */

@@ -1,5 +1,8 @@
 """The state space block's Python binding without a GPU: what its autograd
 functions and argument checks do before anything reaches the library."""
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -38,3 +41,60 @@ def test_second_derivatives_are_refused(monkeypatch, name):
     # nor is one with nothing to differentiate
     dy = torch.ones_like(x)
     assert not torch.autograd.grad(f(x), x, dy)[0].requires_grad
+
+
+class _On:
+    """What the checks look at of a tensor on GPU `k`."""
+    dtype, is_cuda, shape = torch.float32, True, (2, 4, 8)
+
+    def __init__(self, k):
+        self.k, self.device = k, torch.device("cuda", k)
+
+    def get_device(self):
+        return self.k
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The library launches on the current device: tensors of another one must not get that far."""
+    monkeypatch.setattr(ssm, "_current_device", lambda: 0)
+    monkeypatch.setattr(ssm, "load", lambda: None)
+    assert ssm._code(_On(0)) == 1
+    x = _On(1)
+    for call in (lambda: ssm._code(x), lambda: ssm.layernorm_fwd(x, x), lambda: ssm.layernorm_bwd(x, x, x, x, x),
+                 lambda: ssm.conv_fwd(x, x), lambda: ssm.conv_bwd(x, x, x), lambda: ssm.conv_step(x, x, x),
+                 lambda: ssm.scan_fwd(x, x, x, x, x), lambda: ssm.scan_bwd(x, x, x, x, x, x),
+                 lambda: ssm.scan_step(x, x, x, x, x, x)):
+        with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+            call()
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 7
+
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        ssm._handle(Stream, _On(0))
+    assert ssm._handle(Stream, x) == 7
+
+
+def test_memory_that_a_device_can_use(tmp_path):
+    """The library's own check of every pointer (ssm_check.h): another device's memory is refused."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "check.cpp"
+    src.write_text(
+        '#include <cstdio>\n#include <initializer_list>\n#include "ssm_check.h"\n'
+        "int main() {\n"
+        "  for (int type : {cudaMemoryTypeUnregistered, cudaMemoryTypeHost, cudaMemoryTypeDevice,"
+        " cudaMemoryTypeManaged})\n"
+        "    for (int device = 0; device < 2; ++device) for (int mapped = 0; mapped < 2; ++mapped) {\n"
+        "      cudaPointerAttributes at = {};\n"
+        "      at.type = (cudaMemoryType)type; at.device = device;\n"
+        "      at.devicePointer = mapped ? &at : nullptr;\n"
+        '      printf("%d", (int)lion::usable_on(at, 1));\n'
+        "    }\n"
+        "}\n")
+    exe = tmp_path / "check"
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(root, "bidirectional_masked_linear_gb300", "csrc"),
+                    "-I", os.path.join(cuda, "include"), str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    # (device 0 unmapped, mapped; device 1 unmapped, mapped) of each kind
+    assert got == "0000" "0101" "0011" "1111"
