@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(32 * kBwdRows, 2) conv_bwd_kernel(ConvP p) {
 #pragma unroll
   for (int k = 0; k < K; ++k) dw[k] = zero4();
   const long long x_hop = p.reverse ? -p.x_ld : p.x_ld, d_hop = p.reverse ? -p.D : p.D;
-  const int lines = p.B * p.runs;
-  for (int line = blockIdx.y * kBwdRows + r; live && line < lines; line += gridDim.y * kBwdRows) {
-    const int b = line / p.runs, i0 = (line - b * p.runs) * p.run;
+  const unsigned runs = p.runs, lines = p.B * runs;   // fewer than 2^31: a step past them stays in 32 bits
+  for (unsigned line = blockIdx.y * kBwdRows + r; live && line < lines; line += gridDim.y * kBwdRows) {
+    const int b = (int)(line / runs), i0 = (int)(line - b * runs) * p.run;
     const Line<T, K> l(p, b, c0);
     const int i1 = min(i0 + p.run, p.L), mine = min(i1, l.len) - i0;
     // the sums that end in the run need dp up to K-1 tokens behind it

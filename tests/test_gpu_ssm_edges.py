@@ -142,3 +142,27 @@ def test_scan_of_states_without_memory(L, D, reverse, dtype):
     h1, h2 = f.h.clone(), f.h.clone()
     assert torch.equal(ssm.scan_step(h1, **one, A=a["A"].cuda(), **rest), ssm.scan_step(h2, **one, A=dev["A"], **rest))
     assert torch.equal(h1, h2)
+
+
+# ------------------------------------------------------- sizes past 32 bits
+
+def _room(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes * 1e9:
+        pytest.skip("not enough free memory")
+
+
+def test_conv_of_two_to_the_31_sequences():
+    """As many runs as the calls take, one less than 2^31: the gradients' walk over them ends."""
+    _room(40)
+    B = 2 ** 31 - 1
+    x = torch.zeros(B, 1, 1, dtype=torch.bfloat16, device="cuda")
+    x[-1000:] = 1.0
+    dy = torch.ones_like(x)
+    w = torch.tensor([[0.5, -0.75]], device="cuda")
+    y = ssm.conv_fwd(x, w, activation="none")
+    assert bool((y[-1000:] == -0.75).all()) and float(y[:-1000].float().abs().max()) == 0
+    del y
+    g = ssm.conv_bwd(dy, x, w, activation="none")
+    assert float(g.dx.min()) == float(g.dx.max()) == -0.75
+    assert g.dweight.tolist() == [[0.0, 1000.0]]
