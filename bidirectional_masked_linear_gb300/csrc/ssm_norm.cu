@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(32 * NW * RS) layernorm_bwd_kernel(NormP p) {
 template <typename T, int TPR, int NV>
 cudaError_t run_fwd(const NormP& p, cudaStream_t s) {
   constexpr int RPC = TPR == 32 ? 4 : 1;
-  layernorm_fwd_kernel<T, TPR, NV><<<(unsigned)((p.rows + RPC - 1) / RPC), TPR == 32 ? 128 : TPR, 0, s>>>(p);
+  layernorm_fwd_kernel<T, TPR, NV><<<(unsigned)(((long long)p.rows + RPC - 1) / RPC), TPR == 32 ? 128 : TPR, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int NW, int NV, int RS>

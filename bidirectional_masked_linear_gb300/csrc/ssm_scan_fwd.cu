@@ -537,7 +537,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slot
   float best = whole * rounds(ctas) * ((float)L + 6.f);
   const int most = std::min(kMaxSegments, L / 64);
   for (int n = 2; n <= most; ++n) {
-    const int len = ((L + n - 1) / n + 15) / 16 * 16, real = (L + len - 1) / len;   // whole tiles
+    const int len = ((L + n - 1) / n + 15) / 16 * 16, real = (L - 1) / len + 1;   // whole tiles
     if (real != n) continue;
     const float cost = rounds(ctas * n) * ((float)len + 6.f) + (0.18f + states) * (float)n;
     if (cost < best) {

@@ -166,3 +166,18 @@ def test_conv_of_two_to_the_31_sequences():
     g = ssm.conv_bwd(dy, x, w, activation="none")
     assert float(g.dx.min()) == float(g.dx.max()) == -0.75
     assert g.dweight.tolist() == [[0.0, 1000.0]]
+
+
+def test_layernorm_of_two_to_the_31_rows():
+    _room(40)
+    rows = 2 ** 31 - 1
+    x = torch.ones(rows, 1, dtype=torch.bfloat16, device="cuda")
+    w, b = torch.ones(1, device="cuda"), torch.full((1,), 0.25, device="cuda")
+    y, mean, rstd = ssm.layernorm_fwd(x, w, b, 1.0, save_stats=True)   # x - mean is 0
+    assert float(y.min()) == float(y.max()) == 0.25
+    del y
+    x[:-1000] = 0.0   # as dy
+    dx, dw, db = ssm.layernorm_bwd(x, x, w, torch.zeros_like(mean), rstd)
+    assert bool((dx[-1000:] == -1).all())   # xh = 1 there with a mean of 0: 1 - 1 - 1 * 1
+    assert float(dx[:-1000].min()) == float(dx[:-1000].max()) == 0
+    assert dw.tolist() == db.tolist() == [1000.0]

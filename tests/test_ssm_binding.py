@@ -98,3 +98,14 @@ def test_memory_that_a_device_can_use(tmp_path):
     got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
     # (device 0 unmapped, mapped; device 1 unmapped, mapped) of each kind
     assert got == "0000" "0101" "0011" "1111"
+
+
+def test_token_counts_near_32_bits_are_refused():
+    """Past LION_SSM_MAX_TOKENS an index plus a segment's length would not fit an int."""
+    from bidirectional_masked_linear_gb300 import build, lion
+    lion.load(build.build())
+    most = 2 ** 31 - 2 ** 16
+    for L, taken in ((most, True), (most + 1, False), (2 ** 31 - 1, False)):
+        assert (ssm.conv_bwd_workspace_bytes(1, L, 8, 4) > 0) is taken
+        assert (ssm.scan_workspace_bytes(1, L, 8, 16) > 0) is taken
+        assert (ssm.scan_bwd_workspace_bytes(1, L, 8, 16) > 0) is taken
