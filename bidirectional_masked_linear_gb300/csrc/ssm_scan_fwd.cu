@@ -381,9 +381,9 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* p, bool wide) {
 template <typename T, int N>
 __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a, bool bc_wide) {
   constexpr int LN = N / 4;
-  const unsigned item = blockIdx.x * 128 + threadIdx.x;
-  const int lane = threadIdx.x & 31, ln = item % LN, d = item / LN;
-  const bool live = d < a.D;
+  const unsigned long long item = (unsigned long long)blockIdx.x * 128 + threadIdx.x;   // D N / 4 can pass 32 bits
+  const int lane = threadIdx.x & 31, ln = (int)(item % LN), d = (int)(item / LN);
+  const bool live = item / LN < (unsigned)a.D;
   const int b0 = blockIdx.y * kStepRows;
   float4* hp = reinterpret_cast<float4*>(a.h + ((size_t)b0 * a.D + d) * N) + ln;
   const size_t h_hop = (size_t)a.D * N / 4, bc_hop = (size_t)a.G * N;

@@ -181,3 +181,17 @@ def test_layernorm_of_two_to_the_31_rows():
     assert bool((dx[-1000:] == -1).all())   # xh = 1 there with a mean of 0: 1 - 1 - 1 * 1
     assert float(dx[:-1000].min()) == float(dx[:-1000].max()) == 0
     assert dw.tolist() == db.tolist() == [1000.0]
+
+
+def test_scan_step_of_two_to_the_34_states():
+    """More groups of four states than 32 bits count: each channel steps once."""
+    _room(160)
+    D, N = 2 ** 28 + 40, 64
+    A = torch.full((D, N), -1.0, device="cuda")
+    h = torch.ones(1, D, N, device="cuda")
+    u, dt = torch.zeros(1, D, dtype=torch.bfloat16, device="cuda"), torch.ones(1, D, dtype=torch.bfloat16, device="cuda")
+    Bm = torch.ones(1, N, dtype=torch.bfloat16, device="cuda")
+    y = ssm.scan_step(h, u, dt, A, Bm, Bm, dt_softplus=False)
+    want = float(np.exp(-1.0))
+    assert abs(float(h.min()) / want - 1) <= 64 * E and abs(float(h.max()) / want - 1) <= 64 * E
+    assert float(y.min()) == float(y.max()) == float(torch.tensor(64 * want).bfloat16())
