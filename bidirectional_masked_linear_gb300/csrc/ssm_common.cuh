@@ -4,11 +4,11 @@
 #pragma once
 
 #include "lion_common.cuh"
+#include "scan_plan.h"
 
 namespace lion {
 namespace {
 
-constexpr int kSmCount = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

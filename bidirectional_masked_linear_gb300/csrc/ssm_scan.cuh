@@ -10,6 +10,7 @@
 #pragma once
 
 #include "lion_internal.h"
+#include "scan_plan.h"
 #include "ssm_common.cuh"
 
 namespace lion {
@@ -276,17 +277,10 @@ inline int rows_align(const void* p, long long stride, long long group, int es) 
   return x % 16 == 0 ? 16 : x % 8 == 0 ? 8 : x % 4 == 0 ? 4 : 2;
 }
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-inline int scan_channels(int N, int W) { return W * 2 * 32 / (N / 4); }
 
 }  // namespace
 
-// Segments of a sequence for kernels whose CTAs hold `cb` channels.
-struct ScanPlan {
-  int nblk, nseg, seglen;
-};
 void fill_scan(ScanP& p, const lion_scan_args& a);   // everything but the plan and the workspace
-ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slots, float whole,
-                   bool ragged);
 cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cudaStream_t s);
 
 }  // namespace lion

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(32 * W) scan_bwd_segment_kernel(ScanP p) {
   }
 }
 
-constexpr int kBwdWarps = 4;
+constexpr int kBwdWarps = kScanBwdWarps;
 constexpr int kBlock = 4;   // tokens whose states and decays are held in registers
 
 // A lane holds eight states of RC channels: sixteen products a token, as many
@@ -122,6 +122,7 @@ struct BwdTile {
   static constexpr int LC = 32 / LN;                  // channel lanes
   static constexpr int CW = LC * RC;                  // channels of a warp
   static constexpr int CB = kBwdWarps * CW;           // and of a CTA
+  static_assert(CB == scan_bwd_channels(N), "the plan cuts the channels alike");
   static constexpr int TT = kStateEvery;
   static constexpr int VT = CW / 4, VL = TT * VT / 32;
   static constexpr int NB = TT / kBlock;
@@ -565,7 +566,7 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(int B, int L, int D, int N, int G, bool have_states, bool ragged) {
   BwdPlan q;
-  q.r = scan_plan(B, L, D, N, G, kBwdWarps * (N == 8 ? 32 : 512 / N), 2 * kSmCount, 0.85f, ragged);
+  q.r = scan_bwd_plan(B, L, D, N, G, ragged);
   size_t at = 0;
   auto take = [&](size_t floats) {
     const size_t here = at;

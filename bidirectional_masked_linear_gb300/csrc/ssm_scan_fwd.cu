@@ -35,7 +35,7 @@
 namespace lion {
 namespace {
 
-constexpr int kFwdWarps = 1;   // CTAs of one warp spread best: 64 x 197 x 1536 x 16 529 -> 525 us (both ways) against four
+constexpr int kFwdWarps = kScanFwdWarps;
 
 template <typename T, int N_>
 struct FwdTile {
@@ -45,6 +45,7 @@ struct FwdTile {
   static constexpr int RC = 32 / RN;                  // adjacent channels of a lane
   static constexpr int CW = 32 / LN * RC;             // channels of a warp
   static constexpr int TT = N == 64 ? 16 : 512 / CW;  // tokens of a tile
+  static_assert(kFwdWarps * CW == scan_fwd_channels(N), "the plan cuts the channels alike");
   static constexpr int VT = CW / 4;                   // vectors of four channels: of a token,
   static constexpr int VL = TT * VT / 32;             // and of a lane, 32 / VT tokens apart
   static constexpr bool kConvert = sizeof(T) == 2;    // B and C: fp32 copies of raw bf16
@@ -510,55 +511,10 @@ cudaError_t launch_scan_chain(const ScanP& p, bool back, const float* first, cud
   return launch_dependent(scan_chain_kernel, dim3((unsigned)((n + 63) / 64)), dim3(64), 0, s, p, back, first);
 }
 
-// Cuts sequences into segments so that the SMs' slots for CTAs are filled in
-// whole rounds.  The cost, in tokens of a round: rounds x (a segment's tokens +
-// what a CTA takes to start), a round that is not full counting for 0.4 plus
-// 0.6 of its fill (fewer CTAs on an SM run faster), plus the chain over the
-// segments and their states' way through HBM; a sequence left whole is spared the pass over the segments' own
-// contributions and costs `whole` of that.  Ragged sequences, whose lengths
-// the host does not see, are taken to fill half of the tokens in CTAs that end
-// at any time: only the last one's time counts in full, which asks for short
-// segments (16 prompts of up to 4096 tokens x 1024 channels: 509 us with two
-// whole rounds, 328 to 335 us so).  Up to kMaxSegments, of 64 tokens at least.
-ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slots, float whole, bool ragged) {
-  constexpr int kMaxSegments = 512;
-  ScanPlan r;
-  r.nblk = (D / G + cta_channels - 1) / cta_channels;
-  const long long ctas = (long long)B * G * r.nblk;
-  auto rounds = [&](long long n) {
-    if (ragged) return 0.5f * (float)n / (float)slots + 0.8f;
-    const long long full = n / slots, rest = n % slots;
-    return (float)full + (rest ? 0.4f + 0.6f * (float)rest / (float)slots : 0.f);
-  };
-  // a token of a round is some 0.85 us; a segment's states cross HBM four times
-  const float states = 4.f * 4.f * (float)B * (float)D * (float)N / (6.7e6f * 0.85f);
-  r.nseg = 1;
-  r.seglen = (L + 15) / 16 * 16;
-  float best = whole * rounds(ctas) * ((float)L + 6.f);
-  const int most = std::min(kMaxSegments, L / 64);
-  for (int n = 2; n <= most; ++n) {
-    const int len = ((L + n - 1) / n + 15) / 16 * 16, real = (L - 1) / len + 1;   // whole tiles
-    if (real != n) continue;
-    const float cost = rounds(ctas * n) * ((float)len + 6.f) + (0.18f + states) * (float)n;
-    if (cost < best) {
-      best = cost;
-      r.nseg = n;
-      r.seglen = len;
-    }
-  }
-  return r;
-}
-namespace {
-ScanPlan fwd_plan(int B, int L, int D, int N, int G, bool ragged) {
-  const int cw = N == 8 ? 128 : 1024 / N;
-  return scan_plan(B, L, D, N, G, kFwdWarps * cw, kSmCount * (N == 64 ? 8 : 12) / kFwdWarps, 0.6f, ragged);
-}
-}  // namespace
-
 size_t scan_workspace_bytes(int B, int L, int D, int N, int G) {
   size_t most = 0;
   for (int ragged = 0; ragged < 2; ++ragged) {
-    const size_t nseg = fwd_plan(B, L, D, N, G, ragged).nseg;
+    const size_t nseg = scan_fwd_plan(B, L, D, N, G, ragged).nseg;
     if (nseg > 1) most = std::max(most, up256(sizeof(float) * B * nseg * D * N) + up256(sizeof(float) * B * nseg * D));
   }
   return most;
@@ -605,7 +561,7 @@ void fill_scan(ScanP& p, const lion_scan_args& a) {
 cudaError_t launch_scan_fwd(const lion_scan_args& a, void* ws, cudaStream_t s) {
   ScanP p = {};
   fill_scan(p, a);
-  const ScanPlan r = fwd_plan(a.B, a.L, a.D, a.N, a.G, a.lengths != nullptr);
+  const ScanPlan r = scan_fwd_plan(a.B, a.L, a.D, a.N, a.G, a.lengths != nullptr);
   p.nblk = r.nblk;
   p.nseg = r.nseg;
   p.seglen = r.seglen;
