@@ -36,7 +36,8 @@ bool flag(int v) { return v == 0 || v == 1; }
 bool stride_ok(long long ld, long long width) { return ld == 0 || ld >= width; }
 
 constexpr long long kMaxGrid = 0x7fffffffLL;
-constexpr int kMaxTokens = LION_SSM_MAX_TOKENS;   // a token index plus a tile's, run's or segment's length stays an int
+// A token's or channel's index plus a tile's, run's, segment's or block's extent stays an int.
+constexpr int kMaxExtent = LION_SSM_MAX_EXTENT;
 
 lion_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return LION_OK;
@@ -71,7 +72,7 @@ lion_status conv_sizes(int B, int L, int D, int K, int act, int reverse, int dty
   if (B < 1 || L < 1 || D < 1 || K < 1 || !dtype_ok(dtype) || !flag(reverse) || !stride_ok(x_token, D) ||
       (act != LION_ACT_NONE && act != LION_ACT_SILU))
     return LION_ERR_INVALID_ARG;
-  if (K < 2 || K > 4 || L > kMaxTokens) return LION_ERR_UNSUPPORTED;
+  if (K < 2 || K > 4 || L > kMaxExtent || D > kMaxExtent) return LION_ERR_UNSUPPORTED;
   // a CTA for 128 vectors of four channels of a run of tokens, on one grid axis
   if ((long long)B * (L / 5 + 1) > kMaxGrid || (long long)B * (L / 5 + 1) > kMaxGrid / (((long long)D + 3) / 4) * 128) return LION_ERR_UNSUPPORTED;
   return LION_OK;
@@ -80,7 +81,8 @@ lion_status conv_sizes(int B, int L, int D, int K, int act, int reverse, int dty
 lion_status scan_sizes(int B, int L, int D, int N, int G, int softplus, int reverse, int dtype) {
   if (B < 1 || L < 1 || D < 1 || N < 1 || G < 1 || D % G != 0 || !flag(softplus) || !flag(reverse) || !dtype_ok(dtype))
     return LION_ERR_INVALID_ARG;
-  if ((N != 8 && N != 16 && N != 32 && N != 64) || L > kMaxTokens) return LION_ERR_UNSUPPORTED;
+  if (N != 8 && N != 16 && N != 32 && N != 64) return LION_ERR_UNSUPPORTED;
+  if (L > kMaxExtent || D > kMaxExtent || (long long)G * N > kMaxExtent) return LION_ERR_UNSUPPORTED;
   // CTAs on one grid axis, with as many segments as a sequence can have
   if ((long long)B * G > kMaxGrid / ((long long)D / G + 1) / ((long long)L / 64 + 1)) return LION_ERR_UNSUPPORTED;
   return LION_OK;

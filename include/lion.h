@@ -422,7 +422,8 @@ size_t lion_attn_reordered_bwd_workspace_bytes(int B, int H, int L, int d);
  *   - lengths: NULL, or device int32 [B]: only the first lengths[b] tokens of
  *     sequence b exist (values outside 0..L are clamped into it).  The rest
  *     is not used: it advances no state, its outputs and gradients are 0.
- *   - L is at most LION_SSM_MAX_TOKENS (else LION_ERR_UNSUPPORTED).
+ *   - L, D and the scan's G * N are at most LION_SSM_MAX_EXTENT (else
+ *     LION_ERR_UNSUPPORTED).
  *   - reverse: 0 walks a sequence from its first token, 1 from its last one
  *     (the second direction of a bidirectional block).
  *   - Outputs must not overlap inputs or each other.  No entry point reduces
@@ -434,7 +435,7 @@ size_t lion_attn_reordered_bwd_workspace_bytes(int B, int H, int L, int d);
  *     is refused (LION_ERR_INVALID_ARG).
  */
 
-#define LION_SSM_MAX_TOKENS 2147418112   /* 2^31 - 2^16 */
+#define LION_SSM_MAX_EXTENT 2147418112   /* 2^31 - 2^16 */
 
 /* Largest row lion_layernorm_* take. */
 #define LION_LAYERNORM_MAX_COLS 16384

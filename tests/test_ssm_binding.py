@@ -101,7 +101,7 @@ def test_memory_that_a_device_can_use(tmp_path):
 
 
 def test_token_counts_near_32_bits_are_refused():
-    """Past LION_SSM_MAX_TOKENS an index plus a segment's length would not fit an int."""
+    """Past LION_SSM_MAX_EXTENT an index plus a segment's length would not fit an int."""
     from bidirectional_masked_linear_gb300 import build, lion
     lion.load(build.build())
     most = 2 ** 31 - 2 ** 16
@@ -109,3 +109,15 @@ def test_token_counts_near_32_bits_are_refused():
         assert (ssm.conv_bwd_workspace_bytes(1, L, 8, 4) > 0) is taken
         assert (ssm.scan_workspace_bytes(1, L, 8, 16) > 0) is taken
         assert (ssm.scan_bwd_workspace_bytes(1, L, 8, 16) > 0) is taken
+
+
+def test_channel_counts_near_32_bits_are_refused():
+    """Past LION_SSM_MAX_EXTENT a channel's place, or that of a group's row of B, would not fit an int."""
+    from bidirectional_masked_linear_gb300 import build, lion
+    lion.load(build.build())
+    most = 2 ** 31 - 2 ** 16
+    for D, taken in ((most, True), (most + 1, False), (2 ** 31 - 2, False)):
+        assert (ssm.conv_bwd_workspace_bytes(1, 1, D, 4) > 0) is taken
+        assert (ssm.scan_bwd_workspace_bytes(1, 1, D, 8) > 0) is taken
+    assert ssm.scan_bwd_workspace_bytes(1, 1, 2 ** 24, 64, 2 ** 24) > 0
+    assert ssm.scan_bwd_workspace_bytes(1, 1, 2 ** 25, 64, 2 ** 25) == 0
