@@ -454,18 +454,12 @@ cudaError_t run_step(const lion_scan_step_args& a, cudaStream_t s) {
 // Turns the segments' own contributions into the states that enter them, in
 // place: X_{s+1} = exp(A sum_s) X_s + own_s from the walk's start, or, back,
 // X_{s-1} = exp(A sum_s) X_s + own_s from its end.  A thread has four states
-// of a channel and reads kAhead segments ahead.
+// of a channel and reads kAhead segments ahead.  A growing state's factor can
+// pass fp32 where the state, 0 or tiny, does not: it is the cube of a finite
+// one, multiplied in one by one, so that a product overflows only if the whole
+// does (2^378 takes the least positive state there).
 namespace {
 constexpr int kAhead = 16;
-
-// 2^s x + own.  A growing state's factor can pass fp32 where the state, 0 or tiny, does not: what 2^s has above 2^126
-// is multiplied in first, in finite parts, so that the product overflows only if 2^s x does (2^378 takes the least
-// positive x there).
-__device__ __forceinline__ float grow(float s, float x, float own) {
-  if (s > 126.f) x *= ex2(fminf(s - 126.f, 126.f));
-  if (s > 252.f) x *= ex2(fminf(s - 252.f, 126.f));
-  return fmaf(ex2(s > 126.f ? 126.f : s), x, own);   // a NaN stays one
-}
 
 __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, const float* first) {
   const int per = p.N / 4;
@@ -476,6 +470,8 @@ __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, cons
   const int b = (int)(bd / p.D), d = (int)(bd - (long long)b * p.D);
   f2 A[2], x[2];
   load_decays(p.A + (size_t)d * p.N + n0, true, A);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) A[e] = mul2(A[e], pack2(1.f / 3.f, 1.f / 3.f));
   load_pair(first + bd * p.N + n0, first != nullptr, x);
   wait_prior();
   for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
@@ -498,8 +494,9 @@ __global__ void __launch_bounds__(64) scan_chain_kernel(ScanP p, bool back, cons
       const f2 s2 = pack2(sum[q], sum[q]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const f2 s = mul2(s2, A[e]);
-        x[e] = pack2(grow(s.x, x[e].x, own[q][e].x), grow(s.y, x[e].y, own[q][e].y));
+        const f2 t = mul2(s2, A[e]);
+        const f2 f = ex2_2(pack2(t.x > 126.f ? 126.f : t.x, t.y > 126.f ? 126.f : t.y));   // a NaN stays one
+        x[e] = fma2(f, mul2(f, mul2(f, x[e])), own[q][e]);
       }
     }
   }
