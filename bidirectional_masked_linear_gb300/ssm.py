@@ -216,6 +216,8 @@ def _workspace(workspace, like, stream, name, *sizes):
     """(address, bytes, owner) of the caller's workspace, or of one from
     PyTorch's allocator (which reuses it once the stream has passed the call)."""
     if workspace is not None:
+        if not workspace.is_contiguous():   # its elements would not be the bytes that it has
+            raise ValueError("workspace must be contiguous")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     n = _query(name, *sizes)
     if n == 0:

@@ -121,3 +121,12 @@ def test_channel_counts_near_32_bits_are_refused():
         assert (ssm.scan_bwd_workspace_bytes(1, 1, D, 8) > 0) is taken
     assert ssm.scan_bwd_workspace_bytes(1, 1, 2 ** 24, 64, 2 ** 24) > 0
     assert ssm.scan_bwd_workspace_bytes(1, 1, 2 ** 25, 64, 2 ** 25) == 0
+
+
+def test_workspace_counts_bytes_that_it_has():
+    """An expanded tensor has more elements than memory behind them."""
+    ws = torch.zeros(64, dtype=torch.uint8)
+    assert ssm._workspace(ws, None, None, "scan") == (ws.data_ptr(), 64, ws)
+    for bad in (ws[:1].expand(4096), ws.view(8, 8).t(), ws[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            ssm._workspace(bad, None, None, "scan")
