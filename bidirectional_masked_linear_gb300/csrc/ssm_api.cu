@@ -132,7 +132,7 @@ lion_status lion_conv_fwd(const lion_conv_args* a) {
   const size_t es = esize(a->dtype);
   if (!ptr.need(a->x, es) || !ptr.need(a->weight, 4) || !ptr.maybe(a->bias, 4) || !ptr.maybe(a->state, es) ||
       !ptr.maybe(a->lengths, 4) || !ptr.need(a->y, es) || !ptr.maybe(a->state_out, es) ||
-      (a->state && a->state_out == a->state))
+      (a->state && a->state_out == a->state) || a->y == a->x)   // other runs still read these
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_conv_fwd(*a, a->stream));
@@ -151,7 +151,7 @@ lion_status lion_conv_bwd(const lion_conv_bwd_args* a) {
   const size_t es = esize(a->dtype);
   if (!ptr.need(a->dy, es) || !ptr.need(a->x, es) || !ptr.need(a->weight, 4) || !ptr.maybe(a->bias, 4) ||
       !ptr.maybe(a->state, es) || !ptr.maybe(a->lengths, 4) || !ptr.need(a->dx, es) || !ptr.need(a->dweight, 4) ||
-      !ptr.maybe(a->dbias, 4) || !ptr.maybe(a->dstate, es))
+      !ptr.maybe(a->dbias, 4) || !ptr.maybe(a->dstate, es) || a->dx == a->x || a->dx == a->dy)
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(a->workspace, a->workspace_bytes, lion::conv_bwd_workspace_bytes(a->B, a->L, a->D, a->K),

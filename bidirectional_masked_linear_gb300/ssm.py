@@ -12,7 +12,8 @@ sequences evenly laid out.
 ``stream``: the stream to run on (the current one by default).  Outputs and
 workspaces belong to it; inputs made on another stream have to be ready on it.
 Tensors and stream belong to the current device (``torch.cuda.device``), on
-which the library launches; any other is refused.
+which the library launches; any other is refused.  ``out``: the tensor to
+write to, which must not overlap an input.
 """
 from __future__ import annotations
 

@@ -501,6 +501,8 @@ typedef enum { LION_ACT_NONE = 0, LION_ACT_SILU = 1 } lion_act;
  *              oldest first, or NULL for zeros.
  *   state_out  [B][K-1][D]: the last K-1 inputs, to go on from, or NULL.  May
  *              not be `state` itself.
+ *   y may not be x: runs of tokens are walked side by side, each reading the
+ *   K-1 inputs before it.
  */
 typedef struct {
   const void* x;

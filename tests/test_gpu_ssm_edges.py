@@ -195,3 +195,17 @@ def test_scan_step_of_two_to_the_34_states():
     want = float(np.exp(-1.0))
     assert abs(float(h.min()) / want - 1) <= 64 * E and abs(float(h.max()) / want - 1) <= 64 * E
     assert float(y.min()) == float(y.max()) == float(torch.tensor(64 * want).bfloat16())
+
+
+def test_conv_in_place_is_refused():
+    """A run would read the outputs of the one before it."""
+    from bidirectional_masked_linear_gb300 import lion
+    x, w = torch.randn(2, 300, 64, device="cuda"), torch.randn(64, 4, device="cuda")
+    before = x.clone()
+    with pytest.raises(lion.LionError) as e:
+        ssm.conv_fwd(x, w, out=x)
+    assert e.value.status == lion.ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.equal(x, before)
+    y = torch.empty_like(x)
+    assert ssm.conv_fwd(x, w, out=y) is y and torch.equal(y, ssm.conv_fwd(x, w))
