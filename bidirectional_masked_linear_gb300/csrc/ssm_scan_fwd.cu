@@ -382,9 +382,9 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* p, bool wide) {
 template <typename T, int N>
 __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a, bool bc_wide) {
   constexpr int LN = N / 4;
-  const unsigned long long item = (unsigned long long)blockIdx.x * 128 + threadIdx.x;   // D N / 4 can pass 32 bits
-  const int lane = threadIdx.x & 31, ln = (int)(item % LN), d = (int)(item / LN);
-  const bool live = item / LN < (unsigned)a.D;
+  // a CTA has 128 / LN channels (their lanes' number, D N / 4, can pass 32 bits)
+  const int lane = threadIdx.x & 31, ln = threadIdx.x % LN, d = (int)(blockIdx.x * (128 / LN) + threadIdx.x / LN);
+  const bool live = d < a.D;
   const int b0 = blockIdx.y * kStepRows;
   float4* hp = reinterpret_cast<float4*>(a.h + ((size_t)b0 * a.D + d) * N) + ln;
   const size_t h_hop = (size_t)a.D * N / 4, bc_hop = (size_t)a.G * N;
@@ -407,7 +407,6 @@ __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a, b
       if (a.Dskip) skip = a.Dskip[d];
     }
     A = *reinterpret_cast<const float4*>(a.A + (size_t)d * N + 4 * ln);
-    A = make_float4(decay(A.x), decay(A.y), decay(A.z), decay(A.w));
 #pragma unroll
     for (int r = 0; r < kStepRows; ++r)
       if (b0 + r < a.B) {
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(lion_scan_step_args a, b
 #pragma unroll
   for (int r = 0; r < kStepRows; ++r) {
     const int from = lane - ln + r;   // the lane that has row r's step size
-    const float s = __shfl_sync(0xffffffffu, dt, from), x = __shfl_sync(0xffffffffu, du, from);
+    const float s = __shfl_sync(0xffffffffu, dt, from) * kLog2e, x = __shfl_sync(0xffffffffu, du, from);
     h[r].x = fmaf(ex2(s * A.x), h[r].x, x * Bv[r].x);
     h[r].y = fmaf(ex2(s * A.y), h[r].y, x * Bv[r].y);
     h[r].z = fmaf(ex2(s * A.z), h[r].z, x * Bv[r].z);
