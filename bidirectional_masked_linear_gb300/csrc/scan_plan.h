@@ -22,12 +22,13 @@ struct ScanPlan {
 // whole rounds.  The cost, in tokens of a round: rounds x (a segment's tokens +
 // what a CTA takes to start), a round that is not full counting for 0.4 plus
 // 0.6 of its fill (fewer CTAs on an SM run faster), plus the chain over the
-// segments and their states' way through HBM; a sequence left whole is spared the pass over the segments' own
-// contributions and costs `whole` of that.  Ragged sequences, whose lengths
+// segments and their states' way through HBM; a sequence left whole is spared
+// the pass over the segments' own contributions and costs `whole` of that.  Ragged sequences, whose lengths
 // the host does not see, are taken to fill half of the tokens in CTAs that end
 // at any time: only the last one's time counts in full, which asks for short
 // segments (16 prompts of up to 4096 tokens x 1024 channels: 509 us with two
-// whole rounds, 328 to 335 us so).  Up to kMaxSegments, of 64 tokens at least.
+// whole rounds, 322 to 335 us so; the same batch with every length full takes
+// 510 us, and 500 without lengths).  Up to kMaxSegments, of 64 tokens at least.
 inline ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, int slots, float whole, bool ragged) {
   constexpr int kMaxSegments = 512;
   ScanPlan r;
@@ -57,6 +58,9 @@ inline ScanPlan scan_plan(int B, int L, int D, int N, int G, int cta_channels, i
   return r;
 }
 
+// The slots are those of the measured bfloat16 cases.  The forward's warps an SM hold for every type and N but float32
+// at N = 16 (11 of 12) and N = 32 (9 of 12), the gradients' two CTAs but for float32 at N = 16 and N = 64 (one): those
+// take more rounds than are counted here.
 inline ScanPlan scan_fwd_plan(int B, int L, int D, int N, int G, bool ragged) {
   return scan_plan(B, L, D, N, G, scan_fwd_channels(N), kSmCount * (N == 64 ? 8 : 12) / kScanFwdWarps, 0.6f, ragged);
 }

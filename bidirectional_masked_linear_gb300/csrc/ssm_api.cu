@@ -74,7 +74,8 @@ lion_status conv_sizes(int B, int L, int D, int K, int act, int reverse, int dty
     return LION_ERR_INVALID_ARG;
   if (K < 2 || K > 4 || L > kMaxExtent || D > kMaxExtent) return LION_ERR_UNSUPPORTED;
   // a CTA for 128 vectors of four channels of a run of tokens, on one grid axis
-  if ((long long)B * (L / 5 + 1) > kMaxGrid || (long long)B * (L / 5 + 1) > kMaxGrid / (((long long)D + 3) / 4) * 128) return LION_ERR_UNSUPPORTED;
+  const long long runs = (long long)B * (L / 5 + 1);
+  if (runs > kMaxGrid || runs > kMaxGrid / (((long long)D + 3) / 4) * 128) return LION_ERR_UNSUPPORTED;
   return LION_OK;
 }
 

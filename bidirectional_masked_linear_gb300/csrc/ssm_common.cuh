@@ -151,7 +151,7 @@ inline bool rows_wide(const void* p, long long stride, int es) {
 // out[i] = sum over p < P of part[p * stride + i] for i < n1 + n2 + n3, the
 // three ranges of i going to out1, out2 and out3 (a NULL one is dropped), in
 // an order that P alone decides.
-cudaError_t launch_sum_parts(const float* part, int P, long long stride, long long n1, float* out1, long long n2, float* out2,
-                             long long n3, float* out3, cudaStream_t s);
+cudaError_t launch_sum_parts(const float* part, int P, long long stride, long long n1, float* out1, long long n2,
+                             float* out2, long long n3, float* out3, cudaStream_t s);
 
 }  // namespace lion

@@ -54,7 +54,9 @@ struct Quad {
   f2 p[2];
   __device__ __forceinline__ Quad() {}
   __device__ __forceinline__ explicit Quad(const float (&v)[4]) { p[0] = pack2(v[0], v[1]); p[1] = pack2(v[2], v[3]); }
-  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = p[0].x; v[1] = p[0].y; v[2] = p[1].x; v[3] = p[1].y; }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = p[0].x; v[1] = p[0].y; v[2] = p[1].x; v[3] = p[1].y;
+  }
 };
 __device__ __forceinline__ Quad zero4() {
   Quad q;
@@ -418,8 +420,9 @@ cudaError_t run_step(const void* x, void* state, const float* weight, const floa
 // Tokens of a run (a multiple of eight, less what the gradients read behind
 // it): the length that fills the SMs' slots in the fewest rounds of run +
 // kStart tokens, kStart being what a thread takes to begin; a round that is
-// not full counts for 0.4 plus 0.6 of its fill.  runs_of(run): how many slots
-// the runs of that length take.
+// not full counts for 0.4 plus 0.6 of its fill.  slots_of(runs): how many times
+// that many runs a sequence fill the slots.  `lengths` are not seen here: a
+// ragged batch gets a full one's run length.
 constexpr int kStart = 8;
 template <typename F>
 int best_run(int L, int behind, F slots_of) {
@@ -437,6 +440,7 @@ int best_run(int L, int behind, F slots_of) {
   }
   return best;
 }
+// Five CTAs an SM: what bfloat16 at K = 4 and float32 up to K = 3 hold; the others hold four.
 int fwd_run(int B, int L, int D) {
   return best_run(L, 0, [&](int runs) { return (float)B * runs * ((D + 3) / 4) / (float)(kSmCount * 5 * 128); });
 }
@@ -515,7 +519,8 @@ cudaError_t launch_conv_bwd(const lion_conv_bwd_args& a, void* ws, cudaStream_t 
   const int parts = conv_parts(a.B, a.L, a.D, p.run);
   cudaError_t e = LION_CONV_DISPATCH(run_bwd, a.dtype, a.K, p, parts, s);
   if (e != cudaSuccess) return e;
-  return launch_sum_parts(p.part, parts, (long long)a.D * (a.K + 1), (long long)a.D * a.K, a.dweight, a.D, a.dbias, 0, nullptr, s);
+  return launch_sum_parts(p.part, parts, (long long)a.D * (a.K + 1), (long long)a.D * a.K, a.dweight, a.D, a.dbias, 0,
+                          nullptr, s);
 }
 
 cudaError_t launch_conv_step(const void* x, void* state, const float* weight, const float* bias, void* y, int B, int D,

@@ -239,7 +239,9 @@ cudaError_t run_bwd(const NormP& p, int ctas, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The row's threads and vectors by its length.
+// The row's threads and vectors by its length.  The gradients' registers hold
+// two vectors a thread: of four (above 8192 columns) some 100 words a thread
+// spill, and 8 of float32's two.
 template <typename T>
 cudaError_t run_fwd_any(const NormP& p, cudaStream_t s) {
   return p.cols <= 256    ? run_fwd<T, 32, 1>(p, s)
@@ -263,7 +265,11 @@ cudaError_t run_bwd_any(const NormP& p, int ctas, cudaStream_t s) {
                           : run_bwd<T, 16, 4, 1>(p, ctas, s);
 }
 
-// CTAs of the gradients: what the SMs hold at once, as far as there are rows.
+// CTAs of the gradients, as far as there are rows.  The counts an SM are those
+// of bfloat16 at 513 to 768 columns, which was measured; others hold fewer at
+// once than they are given (bfloat16: 3 of 4 up to 512 and at 1025 to 2048
+// columns, 1 of 2 at 769 to 1024 and 2049 to 4096; float32: half in every band
+// up to 4096), so that theirs take more than one round.
 int norm_ctas(int rows, int cols) {
   const int per = cols <= 256 ? 8 : cols <= 1024 ? 4 : 1;
   const int most = kSmCount * (cols <= 512 ? 4 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1);
@@ -303,8 +309,8 @@ __global__ void __launch_bounds__(32 * R) sum_parts_kernel(const float* part, in
 
 }  // namespace
 
-cudaError_t launch_sum_parts(const float* part, int P, long long stride, long long n1, float* out1, long long n2, float* out2,
-                             long long n3, float* out3, cudaStream_t s) {
+cudaError_t launch_sum_parts(const float* part, int P, long long stride, long long n1, float* out1, long long n2,
+                             float* out2, long long n3, float* out3, cudaStream_t s) {
   const long long n = n1 + n2 + n3;
   // its launch overlaps the end of the one before it.  Few parts and many
   // elements: smaller CTAs, of which more are under way (64 parts of 27648: 4.6

@@ -16,7 +16,8 @@
 // and over channels, which go through shuffles and shared memory.  The states
 // and decays of a block take the registers, so that two warps share a scheduler
 // and cover half of their latencies: measured 380 us, 47% of the issue slots,
-// 39% of the fp32 pipe.  Eight products a lane instead of sixteen doubles the
+// 39% of the fp32 pipe.  (float32 at N = 16 and 64 has one: its 129,024 and
+// 116,736 bytes of shared memory leave an SM one CTA.)  Eight products a lane instead of sixteen doubles the
 // warps and, with them, the shared-memory traffic of the sums, which then is
 // the bound (570 us); inputs read a tile ahead cost more instructions than they
 // hide (443 us).
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) scan_bwd_kernel(ScanP p) {
               if (GATE) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
             }
           }
-          if (LN > 1) __syncwarp();       // the channel's lanes have read this dy and delta u; a shuffle orders no memory
+          if (LN > 1) __syncwarp();   // the channel's lanes have read dy and delta u; a shuffle orders no memory
           sm.dy[t * CW + c[0]] = gb[0];   // lanes of one parity hold the same sums
           sm.du[t * CW + c[0]] = qa[0];
           if (GATE) sm.y[t * CW + c[0]] = y[0];
@@ -646,7 +647,8 @@ cudaError_t launch_scan_bwd(const lion_scan_bwd_args& a, void* ws, cudaStream_t 
   if (e != cudaSuccess) return e;
   e = a.dtype == DT_BF16 ? run_bc<__nv_bfloat16>(p, a.dB, a.dC, s) : run_bc<float>(p, a.dB, a.dC, s);
   if (e != cudaSuccess) return e;
-  return launch_sum_parts(p.part_par, a.B * q.r.nseg, (long long)par_stride(a.D, a.N), (long long)a.D * a.N, a.dA, a.D, a.dDskip, a.D, a.ddt_bias, s);
+  return launch_sum_parts(p.part_par, a.B * q.r.nseg, (long long)par_stride(a.D, a.N), (long long)a.D * a.N, a.dA, a.D,
+                          a.dDskip, a.D, a.ddt_bias, s);
 }
 
 }  // namespace lion

@@ -20,7 +20,7 @@
 // delta and one of delta u for them, and B and C are broadcasts (four states of
 // four channels a lane: 689 us, bound by shared-memory reads; of two: 865).
 // More warps an SM than the 12 that 168 registers leave do not help, fewer
-// hurt (8: 615 us).
+// hurt (8: 615 us).  float32's shared memory leaves 11 at N = 16 and 9 at N = 32.
 //
 // Few channels: the sequences are cut into segments.  A first launch takes each
 // segment's own contribution to the state that leaves it (the same walk without
@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, (N == 64 ? 8 : 12) / kFwdWarps
     bias[e] = p.dt_bias && e < vn ? p.dt_bias[vd + e] : 0.f;
     skip[e] = MAIN && p.Dskip && e < vn ? p.Dskip[vd + e] : 0.f;
   }
-  const bool plain = w.nch == CW && p.o_wide && (p.u_align & p.dt_align & p.b_align & p.c_align & (p.z ? p.z_align : 16)) == 16;
+  const bool plain = w.nch == CW && p.o_wide &&
+                     (p.u_align & p.dt_align & p.b_align & p.c_align & (p.z ? p.z_align : 16)) == 16;
   // the tiles that have tokens; MAIN visits the others to write zeros and states
   const int a0 = max(w.i0, w.v0 - w.v0 % TT), a1 = min(w.i1, w.v1), r0 = max(w.i0, w.v0);
   Feed<T, TT, CW> fu, fdt, fz;
@@ -562,7 +563,8 @@ cudaError_t launch_scan_fwd(const lion_scan_args& a, void* ws, cudaStream_t s) {
   p.nseg = r.nseg;
   p.seglen = r.seglen;
   p.seg_state = static_cast<float*>(ws);
-  p.seg_sum = reinterpret_cast<float*>(static_cast<char*>(ws) + up256(sizeof(float) * (size_t)a.B * r.nseg * a.D * a.N));
+  p.seg_sum =
+      reinterpret_cast<float*>(static_cast<char*>(ws) + up256(sizeof(float) * (size_t)a.B * r.nseg * a.D * a.N));
   return LION_SCAN_DISPATCH(run_fwd, a.dtype, a.N, p, s);
 }
 

@@ -568,7 +568,8 @@ lion_status lion_conv_step(const void* x, void* state, const float* weight, cons
  *   states [B][ceil(L/16)][D][N] float32 or NULL: the state before every
  *   LION_SCAN_STATE_EVERY-th processed token, which spares lion_scan_bwd the
  *   recomputation.
- *   N in {8, 16, 32, 64} (else LION_ERR_UNSUPPORTED), G divides D.
+ *   N in {8, 16, 32, 64} (else LION_ERR_UNSUPPORTED), G divides D.  A = -inf is
+ *   a state that keeps nothing, where the steps are above 0.
  */
 #define LION_SCAN_STATE_EVERY 16
 typedef struct {
