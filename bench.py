@@ -7,11 +7,12 @@ of synthetic inputs already resident in HBM.  Default workload: ViT-B
 (B=64, H=12, L=197, d=64), LION-S, chunk 128 (two chunks per head).  The
 L=24,337 high-resolution workload is measured in the same run at chunk 128
 (the pre-pass and the main pass of the long-sequence tensor-core path; the
-main pass chains the segments itself) and reported under ``secondary``; every other workload, mask, form and
-chunk length of the scope's configurations gets a line under ``configs``.
+main pass chains the segments itself) and reported under ``secondary``; every
+other workload, mask, form and chunk length of the scope's configurations gets a line under ``configs``.
 
-Prints ONE JSON line (rank 0).  ``--impl reference`` times the float64 CPU
-oracle instead, on a bounded sample of the same workload.
+Prints ONE JSON line (rank 0); the configurations' full entries go to
+stderr.  ``--impl reference`` times the float64 CPU oracle instead, on a bounded
+sample of the same workload.
 """
 from __future__ import annotations
 
@@ -621,6 +622,28 @@ def run_reference(args, dist, ws, rank):
 
 METRIC = "LION attn fwd tokens/s (chunkwise form)"
 
+
+def short_line(line):
+    """The result as one line of JSON that a log keeps whole (20 KB with
+    everything in it was cut): six digits, no spaces, and of each entry of
+    ``configs`` what names it, its time and its share of the peak."""
+    def short(x):
+        if isinstance(x, float):
+            return float(f"{x:.6g}")
+        if isinstance(x, dict):
+            return {k: short(v) for k, v in x.items()}
+        return [short(v) for v in x] if isinstance(x, list) else x
+
+    def named(c):
+        c = {k: v for k, v in c.items() if k not in ("unit", "steps", "path", "hbm")}
+        c["roofline"] = {k: c["roofline"][k] for k in ("bound", "frac")}
+        if "cpu_baseline" in c:
+            c["cpu_baseline"] = {k: c["cpu_baseline"][k] for k in ("value", "cores")}
+        return c
+
+    return json.dumps(short(dict(line, configs=line["configs"] and [named(c) for c in line["configs"]])),
+                      separators=(",", ":"))
+
 # Every workload / mask / form / chunk of the scope's configurations that is
 # not the headline, each timed for its own line: (workload, mask, form, chunk)
 CONFIG_LINES = [
@@ -924,7 +947,9 @@ def main():
             "streaming": streaming,
             "configs": configs,
         }
-        print(json.dumps(line))
+        for c in configs or []:
+            print("config " + json.dumps(c), file=sys.stderr)
+        print(short_line(line))
     if dist is not None:
         dist.destroy_process_group()
 
