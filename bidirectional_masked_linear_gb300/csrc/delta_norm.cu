@@ -1,0 +1,331 @@
+// delta_norm.cu -- norms of queries and keys for each head with the position
+// rotation in the same pass, and their gradients.
+//
+//   y = rot(x r w),  r = (sum x^2 / n + eps)^(-1/2),  n = 1 or d
+//   dx = r g - x r^3 (sum g x) / n,  g = w rot^-1(dy);  dw = sum rot^-1(dy) x r
+//
+// A lane holds eight values of a head as two runs of four: adjacent ones, or
+// those that the rotation pairs in the two halves, so that a pair never leaves
+// its lane.  d / 8 lanes make a head (of a power of two, the rest idle), a
+// warp takes a token and its groups of lanes take the heads in turn.  The four
+// angles of a lane belong to all heads of the token: the groups work them out
+// between them, one each at d = 64.
+#include "lion_internal.h"
+#include "ssm_common.cuh"
+
+namespace lion {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kSmCount = 152;
+
+struct QkP {
+  const void* x[2];        // q, k
+  const void* dy[2];
+  void* y[2];              // outputs, or dx
+  const float* w[2];
+  const float* freqs;
+  const int* positions;
+  float* part;             // [CTA][2][d]
+  long long x_ld[2];
+  long long tokens;
+  int L, H[2], d, rp;      // rp: lanes of a head whose values turn (rot / 8)
+  int interleaved;
+  float inv_n, eps;
+};
+
+// Four consecutive values; wide: p lies on four values' size.
+template <bool WIDE>
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  if (WIDE) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = p[e];
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+  if (WIDE) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __bfloat162float(p[e]);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  if (WIDE) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = v[e];
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+  if (WIDE) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+// f / (2 pi) as a fraction of a turn in units of 2^-64: the product with an
+// integer position wraps at whole turns, and 32 bits of position leave 32 of
+// the fraction exact.  1 / (2 pi) in two doubles, as the product's own error
+// and the constant's would show from positions of about 2^28 on.
+__device__ __forceinline__ unsigned long long turn_of(float f) {
+  const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
+  const double x = f, t = x * hi;
+  const double rest = fma(x, hi, -t) + x * lo;
+  const double frac = t - floor(t);   // exact
+  return (unsigned long long)(frac * 18446744073709551616.0) +
+         (unsigned long long)(long long)(rest * 18446744073709551616.0);
+}
+
+template <int LPH>
+struct Turn {
+  static constexpr int NG = 32 / LPH;                    // heads at a time
+  static constexpr int OWN = NG >= 4 ? 1 : 4 / NG;       // angles of a lane's own
+  unsigned long long u[OWN];
+
+  // lane: this thread's, p: its place in the head
+  __device__ __forceinline__ void init(const QkP& q, int lane, int p) {
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      const int e = lane / LPH + o * NG;
+      u[o] = p < q.rp && e < 4 ? turn_of(q.freqs[4 * p + e]) : 0;
+    }
+  }
+  __device__ __forceinline__ void at(int pos, int p, float (&c)[4], float (&s)[4]) const {
+    float co[OWN], so[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      const unsigned long long t = u[o] * (unsigned long long)(long long)pos;
+      sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &so[o], &co[o]);   // 2^-31: half turns
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] = __shfl_sync(0xffffffffu, co[e / NG], (e % NG) * LPH + p);
+      s[e] = __shfl_sync(0xffffffffu, so[e / NG], (e % NG) * LPH + p);
+    }
+  }
+};
+
+// v[0..3] and v[4..7] are the lane's two runs.
+__device__ __forceinline__ void turn8(float (&v)[8], const float (&c)[4], const float (&s)[4], bool interleaved,
+                                      float sign) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = interleaved ? 2 * e : e, j = interleaved ? 2 * e + 1 : e + 4;
+    const float a = v[i], b = v[j], sn = sign * s[e];
+    v[i] = a * c[e] - b * sn;
+    v[j] = a * sn + b * c[e];
+  }
+}
+__device__ __forceinline__ void turn8(float (&v)[8], const float (&c)[4], const float (&s)[4], int interleaved,
+                                      float sign) {
+  if (interleaved)
+    turn8(v, c, s, true, sign);
+  else
+    turn8(v, c, s, false, sign);
+}
+
+template <int LPH>
+__device__ __forceinline__ float head_sum(float x) {
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <typename T, int LPH, bool WIDE, bool BWD>
+__global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
+  constexpr int NG = 32 / LPH;
+  constexpr int U = BWD ? 2 : 4;   // heads a lane has under way
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int p = lane & (LPH - 1), g = lane / LPH;
+  const bool there = 8 * p < q.d, turns = p < q.rp;
+  const int a = q.interleaved || !turns ? 8 * p : 4 * p, b = q.interleaved || !turns ? 8 * p + 4 : 4 * (p + q.rp);
+  float w[2][8], dw[2][8];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[m][e] = q.w[m] && there ? q.w[m][(e < 4 ? a : b - 4) + e] : 1.f;
+      dw[m][e] = 0.f;
+    }
+  Turn<LPH> turn;
+  turn.init(q, lane, p);
+  const int heads = q.H[0] + q.H[1];
+  for (long long t = (long long)blockIdx.x * kWarps + warp; t < q.tokens; t += (long long)gridDim.x * kWarps) {
+    float c[4], s[4];
+    if (q.rp) turn.at(q.positions ? q.positions[t] : (int)(t % q.L), p, c, s);
+    for (int h0 = g; h0 < heads + g; h0 += NG * U) {   // all lanes go round equally often
+      float x[U][8], dy[BWD ? U : 1][8];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int h = h0 + i * NG;
+        const int m = h >= q.H[0], hm = m ? h - q.H[0] : h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[i][e] = 0.f;
+          if (BWD) dy[i][e] = 0.f;
+        }
+        if (there && h < heads) {
+          const T* src = static_cast<const T*>(q.x[m]) + t * q.x_ld[m] + (long long)hm * q.d;
+          load4<WIDE>(src + a, x[i]);
+          load4<WIDE>(src + b, x[i] + 4);
+          if (BWD) {
+            const T* d = static_cast<const T*>(q.dy[m]) + (t * q.H[m] + hm) * q.d;
+            load4<WIDE>(d + a, dy[i]);
+            load4<WIDE>(d + b, dy[i] + 4);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int h = h0 + i * NG;
+        if (h - g >= heads) break;   // of all lanes
+        const int m = h >= q.H[0], hm = m ? h - q.H[0] : h;
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+        const float r = 1.f / sqrtf(fmaf(head_sum<LPH>(ss), q.inv_n, q.eps));
+        float o[8];
+        if (!BWD) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = x[i][e] * r * (m ? w[1][e] : w[0][e]);
+          if (turns) turn8(o, c, s, q.interleaved, 1.f);
+        } else {
+          if (turns) turn8(dy[i], c, s, q.interleaved, -1.f);
+          float gx = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            o[e] = dy[i][e] * (m ? w[1][e] : w[0][e]);
+            gx = fmaf(o[e], x[i][e], gx);
+          }
+          if (q.part && h < heads) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float z = dy[i][e] * (x[i][e] * r);
+              dw[0][e] += m ? 0.f : z;
+              dw[1][e] += m ? z : 0.f;
+            }
+          }
+          const float k = head_sum<LPH>(gx) * q.inv_n * r * r;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-k, x[i][e], o[e]);
+        }
+        if (there && h < heads) {
+          T* dst = static_cast<T*>(q.y[m]) + (t * q.H[m] + hm) * q.d;
+          store4<WIDE>(dst + a, o);
+          store4<WIDE>(dst + b, o + 4);
+        }
+      }
+    }
+  }
+  if (!BWD || !q.part) return;
+  __shared__ float sh[kWarps][2][8 * LPH];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int o = 16; o >= LPH; o >>= 1) dw[m][e] += __shfl_xor_sync(0xffffffffu, dw[m][e], o);
+      if (g == 0 && there) sh[warp][m][(e < 4 ? a : b - 4) + e] = dw[m][e];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * q.d; i += 32 * kWarps) {
+    const int m = i >= q.d, e = m ? i - q.d : i;
+    float v = sh[0][m][e];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) v += sh[k][m][e];
+    q.part[(size_t)blockIdx.x * 2 * q.d + i] = v;
+  }
+}
+
+// CTAs: a token a warp while that fills the SMs, else eight CTAs an SM that go
+// round (the angles' frequencies and the weights are set up once a warp).
+int qknorm_ctas(long long tokens) {
+  const long long want = (tokens + kWarps - 1) / kWarps;
+  return (int)(want < 8 * kSmCount ? want : 8 * kSmCount);
+}
+
+template <typename T, bool BWD>
+cudaError_t run(const QkP& q, bool wide, cudaStream_t s) {
+  const dim3 grid(qknorm_ctas(q.tokens)), block(32 * kWarps);
+  if (q.d <= 64)
+    wide ? qknorm_kernel<T, 8, true, BWD><<<grid, block, 0, s>>>(q) : qknorm_kernel<T, 8, false, BWD><<<grid, block, 0, s>>>(q);
+  else if (q.d <= 128)
+    wide ? qknorm_kernel<T, 16, true, BWD><<<grid, block, 0, s>>>(q) : qknorm_kernel<T, 16, false, BWD><<<grid, block, 0, s>>>(q);
+  else
+    wide ? qknorm_kernel<T, 32, true, BWD><<<grid, block, 0, s>>>(q) : qknorm_kernel<T, 32, false, BWD><<<grid, block, 0, s>>>(q);
+  return cudaGetLastError();
+}
+
+template <typename Args>
+QkP fill(const Args& a) {
+  QkP q = {};
+  q.x[0] = a.q;
+  q.x[1] = a.k;
+  q.w[0] = a.q_weight;
+  q.w[1] = a.k_weight;
+  q.freqs = a.freqs;
+  q.positions = a.positions;
+  q.x_ld[0] = a.q_token ? a.q_token : (long long)a.Hq * a.d;
+  q.x_ld[1] = a.k_token ? a.k_token : (long long)a.Hk * a.d;
+  q.tokens = (long long)a.B * a.L;
+  q.L = a.L;
+  q.H[0] = a.Hq;
+  q.H[1] = a.Hk;
+  q.d = a.d;
+  q.rp = a.rot / 8;
+  q.interleaved = a.interleaved;
+  q.inv_n = a.norm == LION_QKNORM_L2 ? 1.f : 1.f / a.d;
+  q.eps = a.eps;
+  return q;
+}
+
+// Whether all runs of four values lie on their size (heads do, as d is a multiple of 8).
+bool on4(const void* p, long long ld, int es) {
+  return reinterpret_cast<uintptr_t>(p) % (4 * es) == 0 && ld % 4 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_qknorm_fwd(const lion_qknorm_args& a, cudaStream_t s) {
+  QkP q = fill(a);
+  q.y[0] = a.q_out;
+  q.y[1] = a.k_out;
+  const int es = a.dtype == DT_BF16 ? 2 : 4;
+  const bool wide = on4(a.q, q.x_ld[0], es) && on4(a.k, q.x_ld[1], es) && on4(a.q_out, 0, es) && on4(a.k_out, 0, es);
+  return a.dtype == DT_BF16 ? run<__nv_bfloat16, false>(q, wide, s) : run<float, false>(q, wide, s);
+}
+
+size_t qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d) {
+  return sizeof(float) * 2 * d * (size_t)qknorm_ctas((long long)B * L);
+}
+
+cudaError_t launch_qknorm_bwd(const lion_qknorm_bwd_args& a, void* ws, cudaStream_t s) {
+  QkP q = fill(a);
+  q.dy[0] = a.dq_out;
+  q.dy[1] = a.dk_out;
+  q.y[0] = a.dq;
+  q.y[1] = a.dk;
+  q.part = static_cast<float*>(ws);
+  const int es = a.dtype == DT_BF16 ? 2 : 4;
+  const bool wide = on4(a.q, q.x_ld[0], es) && on4(a.k, q.x_ld[1], es) && on4(a.dq, 0, es) && on4(a.dk, 0, es) &&
+                    on4(a.dq_out, 0, es) && on4(a.dk_out, 0, es);
+  const cudaError_t e = a.dtype == DT_BF16 ? run<__nv_bfloat16, true>(q, wide, s) : run<float, true>(q, wide, s);
+  if (e != cudaSuccess || !ws) return e;
+  return launch_sum_parts(q.part, qknorm_ctas(q.tokens), 2LL * a.d, a.d, a.dq_weight, a.d, a.dk_weight, 0, nullptr, s);
+}
+
+}  // namespace lion

@@ -161,6 +161,18 @@ size_t scan_bwd_workspace_bytes(int B, int L, int D, int N, int G, bool have_sta
 cudaError_t launch_scan_bwd(const lion_scan_bwd_args& a, void* ws, cudaStream_t s);
 cudaError_t launch_scan_step(const lion_scan_step_args& a, cudaStream_t s);
 
+// The delta rule's operators (delta_*.cu), on checked arguments.
+cudaError_t launch_qknorm_fwd(const lion_qknorm_args& a, cudaStream_t s);
+size_t qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d);
+cudaError_t launch_qknorm_bwd(const lion_qknorm_bwd_args& a, void* ws, cudaStream_t s);
+// `saved` as lion_delta_args has it, or else the workspace of the queried size.
+size_t delta_saved_bytes(int B, int L, int Hv, int dk, int dv, int dtype);
+size_t delta_workspace_bytes(int B, int L, int Hv, int dk, int dv, int dtype);
+cudaError_t launch_delta_fwd(const lion_delta_args& a, void* ws, cudaStream_t s);
+size_t delta_bwd_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, bool have_saved);
+cudaError_t launch_delta_bwd(const lion_delta_bwd_args& a, void* ws, cudaStream_t s);
+cudaError_t launch_delta_step(const lion_delta_step_args& a, cudaStream_t s);
+
 // y (fp32, n values) rounded to nearest even bfloat16.
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, cudaStream_t s);
 

@@ -236,7 +236,7 @@ class _Refuse(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, _):
-        raise RuntimeError("the state space block's gradients cannot be differentiated again")
+        raise RuntimeError("these operators' gradients cannot be differentiated again")
 
 
 def _first_only(backward):
@@ -245,12 +245,12 @@ def _first_only(backward):
     own ``once_differentiable`` looks at the incoming gradient alone, which may
     be a constant.)"""
     @functools.wraps(backward)
-    def first(ctx, dy):
+    def first(ctx, *dy):
         with torch.no_grad():
-            grads = backward(ctx, dy)
+            grads = backward(ctx, *dy)
         if not torch.is_grad_enabled():
             return grads
-        needs = next((t for t in (dy, *ctx.saved_tensors) if t is not None and t.requires_grad), None)
+        needs = next((t for t in (*dy, *ctx.saved_tensors) if t is not None and t.requires_grad), None)
         return tuple(g if g is None or needs is None else _Refuse.apply(needs, g) for g in grads)
     return first
 

@@ -665,6 +665,185 @@ typedef struct {
 lion_status lion_scan_step(const lion_scan_step_args* a);
 
 /*
+ * The gated delta rule beside them: the recurrence of LION-S's scalar decay
+ * whose tokens also take out what the state holds under their key, and the
+ * norms of queries and keys that it needs.  The conventions are those of the
+ * state space block above; heads are adjacent within a token ([B][L][H][d]),
+ * a field `*_token` is the distance between tokens.  Head sizes d, dk and dv
+ * are multiples of 8 (else LION_ERR_UNSUPPORTED).
+ */
+
+/* What a head is divided by: its length, or the root of its mean square. */
+typedef enum { LION_QKNORM_L2 = 0, LION_QKNORM_RMS = 1 } lion_qknorm_kind;
+
+/* Largest head lion_qknorm_* take. */
+#define LION_QKNORM_MAX_D 256
+
+/*
+ * lion_qknorm_fwd -- per token and head of q [B][L][Hq][d] and k [B][L][Hk][d]:
+ *   y = x w / sqrt(sum x^2 / n + eps),  n = 1 (L2) or d (RMS),
+ * then the first `rot` values turned by the token's position p: the pair m of
+ * rot / 2 by the angle p freqs[m], (a, b) -> (a cos - b sin, a sin + b cos).
+ * Pair m is (y[m], y[rot/2 + m]), or with interleaved = 1 (y[2m], y[2m+1]).
+ *   q_weight, k_weight  [d] float32 or NULL for ones.
+ *   freqs      [rot/2] float32 (NULL with rot = 0); rot is a multiple of 8, at
+ *              most d (else LION_ERR_INVALID_ARG above d, LION_ERR_UNSUPPORTED
+ *              off 8).  An angle is held in 64 bits as a fraction of a turn, so
+ *              that far positions keep their place.
+ *   positions  int32 [B][L] or NULL for the token's index.
+ *   q_out, k_out  [B][L][Hq][d], [B][L][Hk][d], tight.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  const float* q_weight;
+  const float* k_weight;
+  const float* freqs;
+  const int* positions;
+  void* q_out;
+  void* k_out;
+  long long q_token, k_token;
+  int B, L, Hq, Hk, d, rot;
+  int norm;                  /* lion_qknorm_kind */
+  int interleaved;
+  float eps;                 /* >= 0 */
+  int dtype;
+  cudaStream_t stream;
+} lion_qknorm_args;
+lion_status lion_qknorm_fwd(const lion_qknorm_args* a);
+
+/*
+ * lion_qknorm_bwd -- gradients of a loss through lion_qknorm_fwd's outputs,
+ * given dq_out and dk_out (tight, in dtype): dq, dk (tight, in dtype) and,
+ * where the weight is given and its gradient wanted, dq_weight, dk_weight [d]
+ * float32 (NULL otherwise).
+ */
+typedef struct {
+  const void* dq_out;
+  const void* dk_out;
+  const void* q;
+  const void* k;
+  const float* q_weight;
+  const float* k_weight;
+  const float* freqs;
+  const int* positions;
+  void* dq;
+  void* dk;
+  float* dq_weight;
+  float* dk_weight;
+  long long q_token, k_token;
+  int B, L, Hq, Hk, d, rot;
+  int norm;
+  int interleaved;
+  float eps;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} lion_qknorm_bwd_args;
+lion_status lion_qknorm_bwd(const lion_qknorm_bwd_args* a);
+/* weights: 1 if the call asks for a weight's gradient. */
+size_t lion_qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d, int weights);
+
+/* Largest dk and dv lion_delta_* take. */
+#define LION_DELTA_MAX_D 128
+
+/*
+ * lion_delta_fwd -- the gated delta rule.  Per sequence and value head h,
+ * which uses query and key head h / (Hv / Hk), with the state S [dk][dv]:
+ *   S <- e^g_t S;  S <- S + beta_t k_t (v_t - S^T k_t)^T;  out_t = scale S^T q_t
+ *   q, k  [B][L][Hk][dk];  v, out  [B][L][Hv][dv];  g, beta  [B][L][Hv] (in
+ *   dtype, g the decay's logarithm, -infinity for one of 0; the product of 32
+ *   adjacent tokens' decays has to be finite in float32).
+ *   h0, h_out  [B][Hv][dk][dv] float32 or NULL: the state before the first
+ *   token (NULL: zeros) and after the last one.  h_out may not be h0.
+ *   saved  device, 256-byte aligned, of lion_delta_saved_bytes, or NULL: what
+ *   lion_delta_bwd goes on from; with it no workspace is used.
+ *   Keys longer than sqrt(2 / beta) make the state grow.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  const float* h0;
+  const int* lengths;
+  void* out;
+  float* h_out;
+  void* saved;
+  long long q_token, k_token, v_token, g_token, beta_token;
+  int B, L, Hk, Hv, dk, dv;
+  float scale;
+  int reverse;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} lion_delta_args;
+lion_status lion_delta_fwd(const lion_delta_args* a);
+size_t lion_delta_saved_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype);
+size_t lion_delta_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype);
+
+/*
+ * lion_delta_bwd -- gradients of a loss through lion_delta_fwd's out, given
+ * dout [B][L][Hv][dv] (tight, in dtype).  Inputs as the forward's; saved: the
+ * forward's (NULL: recomputed in the workspace).
+ *   dq, dk_out [B][L][Hk][dk], dv_out [B][L][Hv][dv], dg, dbeta [B][L][Hv], tight,
+ *   in dtype;  dh0 [B][Hv][dk][dv] float32 or NULL.
+ */
+typedef struct {
+  const void* dout;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  const float* h0;
+  const int* lengths;
+  const void* saved;
+  void* dq;
+  void* dk_out;
+  void* dv_out;
+  void* dg;
+  void* dbeta;
+  float* dh0;
+  long long q_token, k_token, v_token, g_token, beta_token;
+  int B, L, Hk, Hv, dk, dv;
+  float scale;
+  int reverse;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} lion_delta_bwd_args;
+lion_status lion_delta_bwd(const lion_delta_bwd_args* a);
+/* have_saved: 1 if the call passes the forward's. */
+size_t lion_delta_bwd_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, int have_saved);
+
+/*
+ * lion_delta_step -- the gated delta rule for one token: q, k [B][Hk][dk],
+ * v, out [B][Hv][dv], g, beta [B][Hv], all tight, in dtype; value head h uses
+ * query and key head h / (Hv / Hk).  Per value head, with the state S
+ * [dk][dv] (float32, 16-byte aligned) updated in place:
+ *   S <- e^g S;  S <- S + beta k (v - S^T k)^T;  out = scale S^T q.
+ */
+typedef struct {
+  float* h;                  /* [B][Hv][dk][dv] */
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  void* out;
+  int B, Hk, Hv, dk, dv;
+  float scale;
+  int dtype;
+  cudaStream_t stream;
+} lion_delta_step_args;
+lion_status lion_delta_step(const lion_delta_step_args* a);
+
+/*
  * Testing aids for the bound on device-side waits (no counterpart in the
  * pages; not needed in normal use).
  * lion_debug_set_wait_cycles -- the bound, in SM clock cycles, on every
