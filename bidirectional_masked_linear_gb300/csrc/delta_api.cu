@@ -102,9 +102,9 @@ size_t lion_delta_saved_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int 
   return lion::delta_saved_bytes(B, L, Hv, dk, dv, dtype);
 }
 
-size_t lion_delta_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype) {
+size_t lion_delta_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, int save) {
   if (delta_sizes(B, L, Hk, Hv, dk, dv, 1.f, dtype) != LION_OK) return 0;
-  return lion::delta_workspace_bytes(B, L, Hv, dk, dv, dtype);
+  return lion::delta_workspace_bytes(B, L, Hv, dk, dv, dtype, save != 0);
 }
 
 lion_status lion_delta_fwd(const lion_delta_args* a) {
@@ -115,9 +115,9 @@ lion_status lion_delta_fwd(const lion_delta_args* a) {
   if (!ptr.need(a->out, esize(a->dtype)) || !ptr.maybe(a->h_out, 16) || (a->h0 && a->h_out == a->h0))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
-  const size_t want = a->saved ? 0 : lion::delta_workspace_bytes(a->B, a->L, a->Hv, a->dk, a->dv, a->dtype);
-  return with_workspace(a->workspace, a->workspace_bytes, want, a->stream,
-                        [&](void* ws) { return lion::launch_delta_fwd(*a, ws, a->stream); });
+  return with_workspace(a->workspace, a->workspace_bytes,
+                        lion::delta_workspace_bytes(a->B, a->L, a->Hv, a->dk, a->dv, a->dtype, a->saved != nullptr),
+                        a->stream, [&](void* ws) { return lion::launch_delta_fwd(*a, ws, a->stream); });
 }
 
 size_t lion_delta_bwd_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, int have_saved) {

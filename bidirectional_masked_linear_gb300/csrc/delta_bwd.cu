@@ -7,191 +7,196 @@
 namespace lion {
 namespace {
 
+// ------------------------------------------------------- what dO gives a chunk
+//
+// A warp a chunk: P^T dO, transposed as the chain's accumulators are, and
+// (scale e^G o dO)^T as its A operands.
+
+template <typename T, int DK>
+__global__ void __launch_bounds__(32) delta_back_prep_kernel(const DeltaP p) {
+  typedef ChunkData<T, DK, true, sizeof(T) == 4> D;
+  constexpr int NI = D::NI, NS = D::NS, NPP = D::NPP, val = kChunk * kSlice * 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const unsigned base = shared_at(smem), tiles = base + NPP * kTile;
+  const int lane = threadIdx.x, q4 = lane & 3;
+  const long long bh = blockIdx.x / p.nc;
+  const int c = (int)(blockIdx.x - bh * p.nc), b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv);
+  const int n = delta_length(p, b), i0 = c * kChunk;
+  if (i0 >= n) return;
+  const char* chunk = p.chunks + (long long)blockIdx.x * D::bytes;
+  copy_block<NPP * kTile, 32>(base, chunk + D::P, lane);
+  for (int s = 0; s < p.slices; ++s)
+    load_tile<kSlice, kChunk, 32>(tiles + s * NI * val, val,
+                                  rows_of<T>(p, p.dout, (long long)p.Hv * p.dv, (long long)hv * p.dv + s * kSlice, b, n),
+                                  i0, n, p.dv - s * kSlice, p.do_wide, lane);
+  copy_commit();
+  float2 g[2][2];
+  const float* coef = reinterpret_cast<const float*>(chunk + D::coef);
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) g[ks][h] = *reinterpret_cast<const float2*>(coef + 16 * ks + 8 * h + 2 * q4);
+  copy_wait<0>();
+  __syncwarp();
+  float4* Z = reinterpret_cast<float4*>(p.U) + (long long)blockIdx.x * p.dvp * (kChunk / 4) + lane;
+  uint4* out = p.dO + (long long)blockIdx.x * (p.dvp / 16) * 2 * NS * 32 + lane;
+  for (int mt = 0; 16 * mt < p.dvp; ++mt) {
+    float z[4][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      unsigned a[NI][4];
+      float f[2][4] = {};
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        ldsm_t(a[j], tiles + (mt >> 2) * NI * val + j * val + at_a_rows_k<kSlice>(16 * ks, 16 * (mt & 3), lane));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = unpack_bf16(a[j][e]);
+          f[e >> 1][2 * (e & 1)] += v.x;
+          f[e >> 1][2 * (e & 1) + 1] += v.y;
+        }
+      }
+#pragma unroll
+      for (int np = 0; np <= ks; ++np)
+        mma_tile<NI, NPP, true>(z[2 * np], z[2 * np + 1], a, base + at_b_rows_k<kChunk, true>(16 * ks, 16 * np, lane), kTile);
+      unsigned s[NS][4];
+      to_a<NS>(f[0], f[1], g[ks][0], g[ks][1], s);
+#pragma unroll
+      for (int y = 0; y < NS; ++y) out[((mt * 2 + ks) * NS + y) * 32] = make_uint4(s[y][0], s[y][1], s[y][2], s[y][3]);
+    }
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) Z[(mt * 4 + nb) * 32] = make_float4(z[nb][0], z[nb][1], z[nb][2], z[nb][3]);
+  }
+}
+
 // ------------------------------------------------------------- the chain back
 //
 // As delta_chain_kernel with dS^T in the registers:
-//   dU^T = e^(G_C - G) o (dS'^T K^T) + dO^T P;  dR^T = (beta o dU)^T T
-//   dS^T = e^G_C dS'^T + (scale e^G o dO)^T Q - (e^G o dR)^T K
+//   X^T = dO^T P + beta e^(G_C - G) o (dS'^T K^T);  dR^T = X^T T
+//   dS^T = e^G_C dS'^T + (scale e^G o dO)^T Q - X^T W
 
 template <typename T, int DK>
 struct Back {
-  static constexpr int NPP = Planes<T>::mid;
+  typedef ChunkData<T, DK, true, sizeof(T) == 4> D;
+  typedef Stage<T, DK, D::coef, D::bytes> L;
   static constexpr int stages = sizeof(T) == 4 ? 2 : 3;
-  static constexpr int smem = stages * ChainTiles<T, DK, NPP>::bytes + 4 * kOutBytes;
+  static constexpr int smem = stages * L::bytes + 4 * out_bytes<T>();
 };
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
-  constexpr int NPP = Back<T, DK>::NPP, NST = Back<T, DK>::stages;
-  constexpr int NI = Planes<T>::in, NS = Planes<T>::mid;
-  typedef ChainTiles<T, DK, NPP> L;
-  extern __shared__ __align__(1024) unsigned char smem[];
+  typedef Back<T, DK> C;
+  typedef typename C::D D;
+  typedef typename C::L L;
+  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, PER = kStateChunk / kChunk;
+  constexpr bool KQ = L::KQ;
+  extern __shared__ __align__(128) unsigned char smem[];
   const unsigned base = shared_at(smem);
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int q4 = lane & 3;
-  float* buf = reinterpret_cast<float*>(smem + NST * L::bytes + w * kOutBytes);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
+  unsigned char* buf = smem + NST * L::bytes + w * out_bytes<T>();
   const long long bh = blockIdx.x / p.slices;
   const int slice = (int)(blockIdx.x - bh * p.slices);
   const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
   const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
-  const long long do_ld = (long long)p.Hv * p.dv;
+  const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
+  const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
+  const Rows<T> xv = rows_of<T>(p, p.dv_out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
+  const char* chunk = p.chunks + bh * p.nc * D::bytes;
+  const long long at_last = bh * p.nc + nc - 1;
+  const float4* Z = reinterpret_cast<const float4*>(p.U) + (at_last * p.dvp + m0) * (kChunk / 4) + lane;
+  const uint4* dO = p.dO + (at_last * (p.dvp / 16) + m0 / 16) * 2 * NS * 32 + lane;
 
-  float s[DK / 8][4];   // dS^T
-#pragma unroll
-  for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+  float s[DK / 8][4] = {};   // dS^T
+  wait_prior();
 #pragma unroll
   for (int st = 0; st < NST - 1; ++st) {
-    if (st < nc)
-      load_chunk<T, DK, NPP>(p, base + st * L::bytes, nc - 1 - st, b, hv, hk, slice, n, p.dout, do_ld, p.do_wide, tid);
+    const int c = nc - 1 - st;
+    if (c >= 0) L::template load<128>(p, base + st * L::bytes, chunk + (long long)c * D::bytes, xq, xk, c * kChunk, n, tid);
     copy_commit();
   }
+  float4 znext[4];
+  uint4 onext[2][NS];
+  if (cols > 0 && nc > 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) znext[e] = Z[32 * e];
+#pragma unroll
+    for (int e = 0; e < 2 * NS; ++e) onext[e / NS][e % NS] = dO[32 * e];
+  }
   for (int step = 0; step < nc; ++step) {
-    const int c = nc - 1 - step;
+    const int c = nc - 1 - step, ahead = c - (NST - 1);
     copy_wait<NST - 2>();
     __syncthreads();
-    if (step + NST - 1 < nc)
-      load_chunk<T, DK, NPP>(p, base + (step + NST - 1) % NST * L::bytes, c - (NST - 1), b, hv, hk, slice, n, p.dout,
-                             do_ld, p.do_wide, tid);
+    if (ahead >= 0)
+      L::template load<128>(p, base + (step + NST - 1) % NST * L::bytes, chunk + (long long)ahead * D::bytes, xq, xk,
+                            ahead * kChunk, n, tid);
     copy_commit();
     if (cols <= 0) continue;
     const unsigned st = base + step % NST * L::bytes;
-    const float* coef = reinterpret_cast<const float*>(smem + step % NST * L::bytes + L::coef);
-    constexpr int PER = kStateChunk / kChunk;
-    if (step == 0 || c % PER == PER - 1) save_state<T, DK>(p, p.dstates, bh, c / PER, s, m0, cols, lane);
+    const float* coef = reinterpret_cast<const float*>(smem + step % NST * L::bytes + L::at(D::coef));
+    if (step == 0 || c % PER == PER - 1)
+      store_blocks<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK, s, lane);
 
-    // dU^T
+    float4 z[4];
+    unsigned g[2][NS][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = znext[e];
+#pragma unroll
+    for (int e = 0; e < 2 * NS; ++e) {
+      const uint4 v = onext[e / NS][e % NS];
+      unsigned(&d)[4] = g[e / NS][e % NS];
+      d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+    }
+    if (c > 0) {
+      Z -= p.dvp * (kChunk / 4);
+      dO -= (p.dvp / 16) * 2 * NS * 32;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) znext[e] = Z[32 * e];
+#pragma unroll
+      for (int e = 0; e < 2 * NS; ++e) onext[e / NS][e % NS] = dO[32 * e];
+    }
+    // X^T
     float x[4][4] = {};
 #pragma unroll
     for (int ks = 0; ks < DK / 16; ++ks) {
       unsigned a[NS][4];
       to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
 #pragma unroll
-      for (int np = 0; np < 2; ++np) {
-        const unsigned at = st + L::k + at_b_rows_n<DK>(16 * np, 16 * ks, lane);
-        unsigned bk[4];
-        ldsm(bk, at);
-        mma_planes<NS, NI, 0>(x[2 * np], x[2 * np + 1], a, bk);
-        if (NI > 1) {
-          ldsm(bk, at + L::row);
-          mma_planes<NS, NI, 1>(x[2 * np], x[2 * np + 1], a, bk);
-          ldsm(bk, at + 2 * L::row);
-          mma_planes<NS, NI, 2>(x[2 * np], x[2 * np + 1], a, bk);
-        }
-      }
+      for (int np = 0; np < 2; ++np)
+        mma_tile<NS, NI, false>(x[2 * np], x[2 * np + 1], a, st + L::k + at_b_rows_n<DK, KQ>(16 * np, 16 * ks, lane), L::row);
     }
 #pragma unroll
     for (int nb = 0; nb < 4; ++nb) {
-      const float2 l = *reinterpret_cast<const float2*>(coef + 2 * kChunk + 8 * nb + 2 * q4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[nb][e] *= e & 1 ? l.y : l.x;
+      const float2 l = *reinterpret_cast<const float2*>(coef + kChunk + 8 * nb + 2 * q4);
+      x[nb][0] = fmaf(l.x, x[nb][0], z[nb].x);
+      x[nb][1] = fmaf(l.y, x[nb][1], z[nb].y);
+      x[nb][2] = fmaf(l.x, x[nb][2], z[nb].z);
+      x[nb][3] = fmaf(l.y, x[nb][3], z[nb].w);
     }
-    unsigned g[2][NI][4];   // dO^T
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int j = 0; j < NI; ++j) ldsm_t(g[ks][j], st + L::v + j * L::val + at_a_rows_k<kSlice>(16 * ks, 16 * w, lane));
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int np = 0; np <= ks; ++np) {
-        const unsigned at = st + L::tp + NS * kTile + at_b_rows_k<kChunk>(16 * ks, 16 * np, lane);
-        unsigned bp[4];
-        ldsm_t(bp, at);
-        mma_planes<NI, NPP, 0>(x[2 * np], x[2 * np + 1], g[ks], bp);
-        ldsm_t(bp, at + kTile);
-        mma_planes<NI, NPP, 1>(x[2 * np], x[2 * np + 1], g[ks], bp);
-        if (NPP > 2) {
-          ldsm_t(bp, at + 2 * kTile);
-          mma_planes<NI, NPP, 2>(x[2 * np], x[2 * np + 1], g[ks], bp);
-        }
-      }
-    // dR^T
+    // dS^T and dR^T
+    scale_by(s, coef[2 * kChunk]);
     float y[4][4] = {};
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const float2 b0 = *reinterpret_cast<const float2*>(coef + 3 * kChunk + 16 * ks + 2 * q4);
-      const float2 b1 = *reinterpret_cast<const float2*>(coef + 3 * kChunk + 16 * ks + 8 + 2 * q4);
       unsigned a[NS][4];
-      to_a<NS>(x[2 * ks], x[2 * ks + 1], b0, b1, a);
-#pragma unroll
-      for (int np = 0; np <= ks; ++np) {
-        const unsigned at = st + L::tp + at_b_rows_k<kChunk>(16 * ks, 16 * np, lane);
-        unsigned bt[4];
-        ldsm_t(bt, at);
-        mma_planes<NS, NS, 0>(y[2 * np], y[2 * np + 1], a, bt);
-        ldsm_t(bt, at + kTile);
-        mma_planes<NS, NS, 1>(y[2 * np], y[2 * np + 1], a, bt);
-        if (NS > 2) {
-          ldsm_t(bt, at + 2 * kTile);
-          mma_planes<NS, NS, 2>(y[2 * np], y[2 * np + 1], a, bt);
-        }
-      }
-    }
-    // dS^T
-    const float last = coef[kChunk - 1];
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] *= last;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int j0 = 16 * ks + 2 * q4;
-      const float2 g0 = *reinterpret_cast<const float2*>(coef + j0), g1 = *reinterpret_cast<const float2*>(coef + j0 + 8);
-      const float2 h0 = *reinterpret_cast<const float2*>(coef + kChunk + j0);
-      const float2 h1 = *reinterpret_cast<const float2*>(coef + kChunk + j0 + 8);
-      unsigned ag[NS][4], ay[NS][4];
-      to_a<NS>(y[2 * ks], y[2 * ks + 1], make_float2(-g0.x, -g0.y), make_float2(-g1.x, -g1.y), ay);
-      float f[2][4] = {};
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = unpack_bf16(g[ks][j][e]);
-          f[e >> 1][2 * (e & 1)] += v.x;
-          f[e >> 1][2 * (e & 1) + 1] += v.y;
-        }
-      to_a<NS>(f[0], f[1], h0, h1, ag);
+      to_a<NS>(x[2 * ks], x[2 * ks + 1], a);
 #pragma unroll
       for (int nn = 0; nn < DK / 16; ++nn) {
-        const unsigned at = st + at_b_rows_k<DK>(16 * ks, 16 * nn, lane);
-        unsigned bk[4];
-        ldsm_t(bk, at + L::q);
-        mma_planes<NS, NI, 0>(s[2 * nn], s[2 * nn + 1], ag, bk);
-        ldsm_t(bk, at + L::k);
-        mma_planes<NS, NI, 0>(s[2 * nn], s[2 * nn + 1], ay, bk);
-        if (NI > 1) {
-          ldsm_t(bk, at + L::q + L::row);
-          mma_planes<NS, NI, 1>(s[2 * nn], s[2 * nn + 1], ag, bk);
-          ldsm_t(bk, at + L::k + L::row);
-          mma_planes<NS, NI, 1>(s[2 * nn], s[2 * nn + 1], ay, bk);
-          ldsm_t(bk, at + L::q + 2 * L::row);
-          mma_planes<NS, NI, 2>(s[2 * nn], s[2 * nn + 1], ag, bk);
-          ldsm_t(bk, at + L::k + 2 * L::row);
-          mma_planes<NS, NI, 2>(s[2 * nn], s[2 * nn + 1], ay, bk);
-        }
+        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], g[ks], st + L::q + at_b_rows_k<DK, KQ>(16 * ks, 16 * nn, lane), L::row);
+        mma_tile<NS, NS, true>(s[2 * nn], s[2 * nn + 1], a,
+                               st + L::at(D::W) + at_b_rows_k<DK, true>(16 * ks, 16 * nn, lane), L::row);
       }
+#pragma unroll
+      for (int np = 0; np <= ks; ++np)
+        mma_tile<NS, NS, true>(y[2 * np], y[2 * np + 1], a,
+                               st + L::at(D::Tm) + at_b_rows_k<kChunk, true>(16 * ks, 16 * np, lane), kTile);
     }
-    store_rows<T>(buf, y, lane, cols, p.dv_wide, [&](int t) -> T* {
-      const int i = c * kChunk + t;
-      if (i >= n) return nullptr;
-      return static_cast<T*>(p.dv_out) + (((long long)b * p.L + (p.reverse ? n - 1 - i : i)) * p.Hv + hv) * p.dv + m0;
-    });
+    const int i = c * kChunk + lane;
+    store_rows(buf, y, lane, cols, p.dv_wide, i < n ? const_cast<T*>(xv.at(i)) : nullptr);
   }
   copy_wait<0>();
   if (cols <= 0) return;
-  if (p.dh0) {
-    const int r = lane >> 2;
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int kx = 8 * j + 2 * q4 + (e & 1), col = r + 8 * (e >> 1);
-        if (kx < p.dk && col < cols) p.dh0[(bh * p.dk + kx) * p.dv + m0 + col] = s[j][e];
-      }
-  }
+  if (p.dh0) keep_state<DK>(p, p.dh0, bh, m0, cols, lane, s);
   zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, lane);
 }
 
@@ -229,22 +234,47 @@ struct Grad {
   static constexpr int smem = end > last ? end : last;
 };
 
+// Blocks of 8 x 8 as the chains left them: `units` rows of eight values to
+// UNITS in shared memory, zeros behind them.
+template <int UNITS, int THREADS>
+__device__ __forceinline__ void load_blocks(unsigned dst, int, const __nv_bfloat16* src, int units, int tid) {
+#pragma unroll
+  for (int k = 0; k < UNITS / THREADS; ++k) {
+    const int i = tid + k * THREADS;
+    copy16(dst + 16 * i, src + 8 * (i < units ? i : 0), i < units);
+  }
+  static_assert(UNITS % THREADS == 0, "");
+}
+template <int UNITS, int THREADS>
+__device__ __forceinline__ void load_blocks(unsigned dst, int plane, const float* src, int units, int tid) {
+#pragma unroll 2
+  for (int i = tid; i < UNITS; i += THREADS) {
+    float v[8];
+    load8(src + 8 * (long long)i, i < units ? 8 : 0, true, v);
+    store_planes(dst + 16 * i, plane, v);
+  }
+}
+
 __device__ __forceinline__ float2 pair_of(unsigned addr) {
   unsigned v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return unpack_bf16(v);
 }
-// Two adjacent values of a tile, all planes.
-template <int W, int NP>
-__device__ __forceinline__ float2 tile_pair(unsigned tile, int plane, int row, int col) {
-  float2 s = pair_of(tile + unit_at<W>(row, col >> 3) + 2 * (col & 7));
+// Two adjacent values, all planes.
+template <int NP>
+__device__ __forceinline__ float2 plane_sum(unsigned addr, int plane) {
+  float2 s = pair_of(addr);
 #pragma unroll
   for (int j = 1; j < NP; ++j) {
-    const float2 t = pair_of(tile + j * plane + unit_at<W>(row, col >> 3) + 2 * (col & 7));
+    const float2 t = pair_of(addr + j * plane);
     s.x += t.x;
     s.y += t.y;
   }
   return s;
+}
+template <int W, int NP>
+__device__ __forceinline__ float2 tile_pair(unsigned tile, int plane, int row, int col) {
+  return plane_sum<NP>(tile + unit_at<W>(row, col >> 3) + 2 * (col & 7), plane);
 }
 __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -255,7 +285,7 @@ template <typename T, int DK>
 __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) delta_grad_kernel(const DeltaP p) {
   typedef Grad<T, DK> G;
   constexpr int NI = G::NI, THREADS = 32 * G::warps;
-  extern __shared__ __align__(1024) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float2 sG[64];
   __shared__ float sGrown[64], sLeft[64], sBeta[64], sI[2][64], sW[2][64], sB[2][64], sDot[G::warps];
   __shared__ double sCarry;
@@ -293,14 +323,9 @@ __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) del
     }
     return;
   }
-  const auto rows = [&](const void* x, long long ld, long long first) {
-    return [=](int row) -> const T* {
-      return i0 + row < n ? static_cast<const T*>(x) + token(row) * ld + first : nullptr;
-    };
-  };
-  load_tile<DK, 64, THREADS>(base + G::k, G::row, static_cast<const T*>(p.k), rows(p.k, p.k_ld, (long long)hk * p.dk), p.dk,
+  load_tile<DK, 64, THREADS>(base + G::k, G::row, rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n), i0, n, p.dk,
                              p.k_wide, tid);
-  load_tile<DK, 64, THREADS>(base + G::q, G::row, static_cast<const T*>(p.q), rows(p.q, p.q_ld, (long long)hk * p.dk), p.dk,
+  load_tile<DK, 64, THREADS>(base + G::q, G::row, rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n), i0, n, p.dk,
                              p.q_wide, tid);
   // decays
   double Gs = 0.0;
@@ -333,35 +358,27 @@ __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) del
 
   float dP[8][4] = {}, N[8][4] = {}, dq[8][4] = {}, f[8][4] = {}, W[8][4] = {};
   float dot = 0.f;
-  const long long state = (bh * p.nc64 + c) * p.dv * p.dk;
-  const T* Rp = static_cast<const T*>(p.R) + ((bh * p.nc) * kChunk + i0) * p.dv;
   wait_prior();
   for (int d0 = 0; d0 < p.dv; d0 += G::dvs) {
     if (d0) __syncthreads();
-    const int cols = p.dv - d0;
-    load_tile<G::dvs, 64, THREADS>(base + G::dO, G::val, static_cast<const T*>(p.dout),
-                                   rows(p.dout, (long long)p.Hv * p.dv, (long long)hv * p.dv + d0), cols, p.do_wide, tid);
-    load_tile<G::dvs, 64, THREADS>(base + G::dR, G::val, static_cast<const T*>(p.dv_out),
-                                   rows(p.dv_out, (long long)p.Hv * p.dv, (long long)hv * p.dv + d0), cols, p.dv_wide, tid);
-    load_tile<G::dvs, 64, THREADS>(
-        base + G::R, G::val, Rp,
-        [&](int row) -> const T* { return i0 + row < n ? Rp + (long long)row * p.dv + d0 : nullptr; }, cols, true, tid);
-    const auto state_row = [&](const void* x) {
-      return [=](int row) -> const T* {
-        return d0 + row < p.dv ? static_cast<const T*>(x) + state + (long long)(d0 + row) * p.dk : nullptr;
-      };
-    };
-    load_tile<DK, G::dvs, THREADS>(base + G::S, G::sta, static_cast<const T*>(p.states), state_row(p.states), p.dk, true, tid);
-    load_tile<DK, G::dvs, THREADS>(base + G::dS, G::sta, static_cast<const T*>(p.dstates), state_row(p.dstates), p.dk, true,
-                                   tid);
+    const int cols = p.dv - d0, some = p.dvp - d0 < G::dvs ? p.dvp - d0 : G::dvs;
+    const long long ld = (long long)p.Hv * p.dv, head = (long long)hv * p.dv + d0;
+    load_tile<G::dvs, 64, THREADS>(base + G::dO, G::val, rows_of<T>(p, p.dout, ld, head, b, n), i0, n, cols, p.do_wide, tid);
+    load_tile<G::dvs, 64, THREADS>(base + G::dR, G::val, rows_of<T>(p, p.dv_out, ld, head, b, n), i0, n, cols, p.dv_wide, tid);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)   // R^T of 32 tokens each
+      load_blocks<G::dvs * 4, THREADS>(base + G::R + h * G::val / 2, G::val,
+                                       static_cast<const T*>(p.R) + ((bh * p.nc + 2 * c + h) * p.dvp + d0) * kChunk,
+                                       i0 + h * kChunk < n ? some * 4 : 0, tid);
+    const long long state = ((bh * p.nc64 + c) * p.dvp + d0) * DK;
+    load_blocks<G::dvs * DK / 8, THREADS>(base + G::S, G::sta, static_cast<const T*>(p.states) + state, some * (DK / 8), tid);
+    load_blocks<G::dvs * DK / 8, THREADS>(base + G::dS, G::sta, static_cast<const T*>(p.dstates) + state, some * (DK / 8), tid);
     copy_commit();
     copy_wait<0>();
     __syncthreads();
 #pragma unroll 4
     for (int i = tid; i < G::dvs * DK / 2; i += THREADS) {
-      const int row = i / (DK / 2), col = i % (DK / 2) * 2;
-      const float2 x = tile_pair<DK, NI>(base + G::S, G::sta, row, col);
-      const float2 y = tile_pair<DK, NI>(base + G::dS, G::sta, row, col);
+      const float2 x = plane_sum<NI>(base + G::S + 4 * i, G::sta), y = plane_sum<NI>(base + G::dS + 4 * i, G::sta);
       dot = fmaf(x.x, y.x, fmaf(x.y, y.y, dot));
     }
 #pragma unroll
@@ -372,16 +389,18 @@ __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) del
         const unsigned at = base + j * G::val + at_a_rows_m<G::dvs>(16 * rw, 16 * ks, lane);
         ldsm(ao[j], at + G::dO);
         ldsm(ad[j], at + G::dR);
-        ldsm(ar[j], at + G::R);
+        ldsm_t(ar[j], base + G::R + j * G::val + (rw >> 1) * (G::val / 2) +
+                          at_a_rows_k<kChunk, true>(16 * ks, 16 * (rw & 1), lane));
       }
 #pragma unroll
       for (int np = 0; np < 4; ++np)
         if (np <= rw) {
-          const unsigned at = base + G::R + at_b_rows_n<G::dvs>(16 * np, 16 * ks, lane);
+          const unsigned at =
+              base + G::R + (np >> 1) * (G::val / 2) + at_b_rows_k<kChunk, true>(16 * ks, 16 * (np & 1), lane);
           unsigned x[4];
 #define LION_PLANE(J)                                               \
   if (J < NI) {                                                     \
-    ldsm(x, at + J * G::val);                                       \
+    ldsm_t(x, at + J * G::val);                                     \
     mma_planes<NI, NI, J>(dP[2 * np], dP[2 * np + 1], ao, x);       \
     mma_planes<NI, NI, J>(N[2 * np], N[2 * np + 1], ad, x);         \
   }
@@ -390,7 +409,7 @@ __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) del
         }
 #pragma unroll
       for (int nn = 0; nn < 4; ++nn) {
-        const unsigned at = base + at_b_rows_k<DK>(16 * ks, 64 * half + 16 * nn, lane);
+        const unsigned at = base + at_b_rows_k<DK, true>(16 * ks, 64 * half + 16 * nn, lane);
         unsigned x[4];
 #define LION_PLANE(J)                                               \
   if (J < NI) {                                                     \
@@ -634,11 +653,16 @@ __global__ void __launch_bounds__(256) delta_heads_kernel(const float* part_q, c
 
 template <typename T, int DK>
 cudaError_t run_back(const DeltaP& p, cudaStream_t s) {
-  const auto back = delta_back_kernel<T, DK>;
-  cudaError_t e = cudaFuncSetAttribute(back, cudaFuncAttributeMaxDynamicSharedMemorySize, Back<T, DK>::smem);
+  typedef ChunkData<T, DK, true, sizeof(T) == 4> D;
+  const auto prep = delta_back_prep_kernel<T, DK>;
+  const int smem = D::NPP * kTile + p.slices * D::NI * kChunk * kSlice * 2;
+  prep<<<(unsigned)((long long)p.B * p.Hv * p.nc), 32, smem, s>>>(p);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  back<<<(unsigned)((long long)p.B * p.Hv * p.slices), 128, Back<T, DK>::smem, s>>>(p);
-  e = cudaGetLastError();
+  const auto back = delta_back_kernel<T, DK>;
+  e = cudaFuncSetAttribute(back, cudaFuncAttributeMaxDynamicSharedMemorySize, Back<T, DK>::smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(back, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)Back<T, DK>::smem, s, p);
   if (e != cudaSuccess) return e;
   const auto grad = delta_grad_kernel<T, DK>;
   e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad<T, DK>::smem);
@@ -652,16 +676,22 @@ cudaError_t run_back(const DeltaP& p, cudaStream_t s) {
                           static_cast<T*>(p.dk_out), vectors, p.dk / 8, p.Hv / p.Hk);
 }
 
+// The workspace going back: U's place, dO's fragments, dS', the parts of dq and
+// dk, and without the forward's `saved` what that would hold.
 struct BackLayout {
-  size_t dstates, parts, bytes;
+  size_t dO, dstates, parts, part, saved, bytes;
 };
 BackLayout back_layout(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, bool have_saved) {
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const DeltaLayout f = delta_layout(B, L, Hv, dk, dv, dtype, true);
+  const size_t planes = dtype == DT_BF16 ? Planes<__nv_bfloat16>::mid : Planes<float>::mid;
   BackLayout l;
-  l.dstates = have_saved ? 0 : f.bytes;
+  l.dO = f.U;
+  l.dstates = l.dO + up((size_t)B * Hv * f.nc * kChunk * f.dvp * 2 * planes);
   l.parts = l.dstates + (f.bytes - f.states);   // as large as the states
-  l.bytes = l.parts + (Hv > Hk ? 2 * up(sizeof(float) * (size_t)B * L * Hv * dk) : 0);
+  l.part = Hv > Hk ? up(sizeof(float) * (size_t)B * L * Hv * dk) : 0;
+  l.saved = l.parts + 2 * l.part;
+  l.bytes = l.saved + (have_saved ? 0 : f.bytes);
   return l;
 }
 
@@ -673,23 +703,24 @@ size_t delta_bwd_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, i
 
 cudaError_t launch_delta_bwd(const lion_delta_bwd_args& a, void* ws, cudaStream_t s) {
   const BackLayout l = back_layout(a.B, a.L, a.Hk, a.Hv, a.dk, a.dv, a.dtype, a.saved != nullptr);
-  DeltaP p = delta_params(a, a.saved ? const_cast<void*>(a.saved) : ws, true);
+  char* base = static_cast<char*>(ws);
+  DeltaP p = delta_params(a, a.saved ? static_cast<char*>(const_cast<void*>(a.saved)) : base + l.saved, base, true);
   if (!a.saved) {
     const cudaError_t e = launch_delta_chain(p, a.dtype, true, s);
     if (e != cudaSuccess) return e;
   }
-  char* base = static_cast<char*>(ws);
   p.dout = a.dout;
   p.dv_out = a.dv_out;
+  p.dO = reinterpret_cast<uint4*>(base + l.dO);
   p.dstates = base + l.dstates;
   p.dh0 = a.dh0;
   p.dq = a.dq;
   p.dk_out = a.dk_out;
   p.dg = a.dg;
   p.dbeta = a.dbeta;
-  if (a.Hv > a.Hk) {
+  if (l.part) {
     p.dq_part = reinterpret_cast<float*>(base + l.parts);
-    p.dk_part = reinterpret_cast<float*>(base + l.parts + (l.bytes - l.parts) / 2);
+    p.dk_part = reinterpret_cast<float*>(base + l.parts + l.part);
   }
   const int es = a.dtype == DT_BF16 ? 2 : 4;
   p.do_wide = rows_wide(a.dout, 0, es);

@@ -1,5 +1,5 @@
-// delta_chain.cuh -- what the chains over chunks share, forward and back: a
-// chunk's tiles in shared memory, their loads, and the way out for results.
+// delta_chain.cuh -- what the chains over chunks share, forward and back: the
+// tiles all of a head's columns read, and the ways out for results.
 #pragma once
 
 #include "delta_common.cuh"
@@ -7,63 +7,98 @@
 namespace lion {
 namespace {
 
-template <typename T, int DK, int NPP>
-struct ChainTiles {
-  static constexpr int NI = Planes<T>::in, NS = Planes<T>::mid;
-  static constexpr int row = kChunk * DK * 2, val = kChunk * kSlice * 2;   // bytes of a plane
-  static constexpr int k = 0, q = NI * row, v = 2 * NI * row, tp = v + NI * val;
-  static constexpr int coef = tp + (NS + NPP) * kTile;
-  static constexpr int bytes = coef + kCoefs * 4;
+// A chunk's tiles in shared memory: q and k, then ChunkData's bytes FROM to TO.
+template <typename T, int DK, int FROM, int TO>
+struct Stage {
+  static constexpr bool KQ = sizeof(T) == 4;
+  static constexpr int NI = Planes<T>::in, row = kChunk * DK * 2;
+  static constexpr int q = 0, k = NI * row, rest = 2 * NI * row, bytes = rest + TO - FROM;
+  static constexpr int at(int offset) { return rest + offset - FROM; }
+
+  template <int THREADS>
+  static __device__ __forceinline__ void load(const DeltaP& p, unsigned dst, const char* chunk, const Rows<T>& xq,
+                                              const Rows<T>& xk, int i0, int n, int tid) {
+    if (KQ) {
+      copy_block<2 * NI * row, THREADS>(dst, chunk, tid);
+    } else {
+      load_tile<DK, kChunk, THREADS>(dst + q, row, xq, i0, n, p.dk, p.q_wide, tid);
+      load_tile<DK, kChunk, THREADS>(dst + k, row, xk, i0, n, p.dk, p.k_wide, tid);
+    }
+    copy_block<TO - FROM, THREADS>(dst + rest, chunk + FROM, tid);
+  }
 };
-// rows of 16 of a warp's outputs on their way out, 80 bytes apart
-constexpr int kOutRow = 20;
-constexpr int kOutBytes = kChunk * kOutRow * 4;
 
-template <typename T, int DK, int NPP>
-__device__ __forceinline__ void load_chunk(const DeltaP& p, unsigned dst, int c, int b, int hv, int hk, int slice, int n,
-                                           const void* val, long long val_ld, int val_wide, int tid) {
-  typedef ChainTiles<T, DK, NPP> L;
-  const auto token = [&](int row) {
-    const int i = c * kChunk + row;
-    return i < n ? (long long)b * p.L + (p.reverse ? n - 1 - i : i) : -1LL;
-  };
-  const auto rows = [&](const void* x, long long ld, long long first) {
-    return [=](int row) -> const T* {
-      const long long t = token(row);
-      return t < 0 ? nullptr : static_cast<const T*>(x) + t * ld + first;
-    };
-  };
-  load_tile<DK, kChunk, 128>(dst + L::k, L::row, static_cast<const T*>(p.k), rows(p.k, p.k_ld, (long long)hk * p.dk),
-                             p.dk, p.k_wide, tid);
-  load_tile<DK, kChunk, 128>(dst + L::q, L::row, static_cast<const T*>(p.q), rows(p.q, p.q_ld, (long long)hk * p.dk),
-                             p.dk, p.q_wide, tid);
-  load_tile<kSlice, kChunk, 128>(dst + L::v, L::val, static_cast<const T*>(val),
-                                 rows(val, val_ld, (long long)hv * p.dv + slice * kSlice), p.dv - slice * kSlice,
-                                 val_wide, tid);
-  const char* tp = static_cast<const char*>(p.tp) + (((long long)b * p.Hv + hv) * p.nc + c) * p.tp_chunk;
-  for (int i = tid; i < (L::bytes - L::tp) / 16; i += 128) copy16(dst + L::tp + 16 * i, tp + 16 * i, true);
+// Bytes of a warp's buffer for results on their way out: tokens in rows, 48
+// bytes apart for bfloat16 and 80 for float32.
+template <typename T>
+constexpr int out_bytes() {
+  return kChunk * (sizeof(T) == 2 ? 48 : 80);
 }
-
-// A warp's [16 columns][32 tokens] accumulators to rows of a [tokens][columns] tensor: 16 values of a token a lane.
-template <typename T, typename F>
-__device__ __forceinline__ void store_rows(float* buf, const float (&o)[4][4], int lane, int cols, bool wide, F row) {
+// A warp's accumulators [16 columns][32 tokens] to rows of a token-major
+// tensor: a token a lane, to `row` (NULL: nowhere).
+__device__ __forceinline__ void store_rows(unsigned char* buf, const float (&o)[4][4], int lane, int cols, bool wide,
+                                           __nv_bfloat16* row) {
+  const unsigned at = shared_at(buf) + ((lane >> 4) * 8 + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16;
+#pragma unroll
+  for (int np = 0; np < 2; ++np)
+    stsm_t(at + np * 16 * 48, pack_bf16(o[2 * np][0], o[2 * np][1]), pack_bf16(o[2 * np][2], o[2 * np][3]),
+           pack_bf16(o[2 * np + 1][0], o[2 * np + 1][1]), pack_bf16(o[2 * np + 1][2], o[2 * np + 1][3]));
+  __syncwarp();
+  const uint4* s = reinterpret_cast<const uint4*>(buf + lane * 48);
+  const uint4 x = s[0], y = s[1];
+  if (row) {
+    if (wide) {
+      *reinterpret_cast<uint4*>(row) = x;
+      if (cols > 8) *reinterpret_cast<uint4*>(row + 8) = y;
+    } else {
+      const unsigned w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (2 * e < cols) {
+          reinterpret_cast<unsigned short*>(row)[2 * e] = (unsigned short)w[e];
+          reinterpret_cast<unsigned short*>(row)[2 * e + 1] = (unsigned short)(w[e] >> 16);
+        }
+    }
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void store_rows(unsigned char* raw, const float (&o)[4][4], int lane, int cols, bool wide,
+                                           float* row) {
+  float* buf = reinterpret_cast<float*>(raw);
   const int r = lane >> 2, q4 = lane & 3;
 #pragma unroll
   for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) buf[(8 * nb + 2 * q4 + (e & 1)) * kOutRow + r + 8 * (e >> 1)] = o[nb][e];
+    for (int e = 0; e < 4; ++e) buf[(8 * nb + 2 * q4 + (e & 1)) * 20 + r + 8 * (e >> 1)] = o[nb][e];
   __syncwarp();
-  T* dst = row(lane);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     float v[8];
-    const float4 x = *reinterpret_cast<const float4*>(buf + lane * kOutRow + 8 * u);
-    const float4 y = *reinterpret_cast<const float4*>(buf + lane * kOutRow + 8 * u + 4);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    if (dst && 8 * u < cols) store8(dst + 8 * u, 8, wide, v);
+    load8(buf + lane * 20 + 8 * u, 8, true, v);
+    if (row && 8 * u < cols) store8(row + 8 * u, 8, wide, v);
   }
   __syncwarp();
+}
+
+// Accumulators [16 columns][8 N values] as blocks of 8 x 8 in the inputs' type,
+// rows of N blocks: what the gradients' tiles are loaded from.
+template <int N>
+__device__ __forceinline__ void store_blocks(__nv_bfloat16* to, const float (&s)[N][4], int lane) {
+  unsigned* d = reinterpret_cast<unsigned*>(to) + lane;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    d[j * 32] = pack_bf16(s[j][0], s[j][1]);
+    d[(N + j) * 32] = pack_bf16(s[j][2], s[j][3]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_blocks(float* to, const float (&s)[N][4], int lane) {
+  float2* d = reinterpret_cast<float2*>(to) + lane;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    d[j * 32] = make_float2(s[j][0], s[j][1]);
+    d[(N + j) * 32] = make_float2(s[j][2], s[j][3]);
+  }
 }
 
 // Tokens that a sequence does not have, in a warp's columns.
@@ -73,29 +108,44 @@ __device__ __forceinline__ void zero_rows(const DeltaP& p, void* out, int n, int
   const float zero[8] = {};
   for (long long t = n + (lane >> 1); t < p.L; t += 16) {
     const int u = lane & 1;
-    if (8 * u < cols) store8(static_cast<T*>(out) + (((long long)b * p.L + t) * p.Hv + hv) * p.dv + m0 + 8 * u, 8, wide, zero);
+    if (8 * u < cols)
+      store8(static_cast<T*>(out) + (((long long)b * p.L + t) * p.Hv + hv) * p.dv + m0 + 8 * u, 8, wide, zero);
   }
 }
 
-// A warp's columns of S^T, two rows of 16 adjacent values a lane pair, as a saved state [dv][dk].
-template <typename T, int DK>
-__device__ __forceinline__ void save_state(const DeltaP& p, void* states, long long bh, int at, const float (&s)[DK / 8][4],
-                                           int m0, int cols, int lane) {
-  const int r = lane >> 2, q4 = lane & 3;
-  T* to = static_cast<T*>(states) + (bh * p.nc64 + at) * p.dv * p.dk;
+// A warp's columns of the [dk][dv] state of a head, as accumulators.
+template <int DK>
+__device__ __forceinline__ void load_state(const DeltaP& p, const float* h, long long bh, int m0, int cols, int lane,
+                                           float (&s)[DK / 8][4]) {
 #pragma unroll
   for (int j = 0; j < DK / 8; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int kx = 8 * j + 2 * q4, col = r + 8 * h;
-      if (kx < p.dk && col < cols) {
-        T* d = to + (long long)(m0 + col) * p.dk + kx;
-        if (sizeof(T) == 2)
-          *reinterpret_cast<unsigned*>(d) = pack_bf16(s[j][2 * h], s[j][2 * h + 1]);
-        else
-          *reinterpret_cast<float2*>(d) = make_float2(s[j][2 * h], s[j][2 * h + 1]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int kx = 8 * j + 2 * (lane & 3) + (e & 1), col = (lane >> 2) + 8 * (e >> 1);
+      s[j][e] = h && kx < p.dk && col < cols ? h[(bh * p.dk + kx) * p.dv + m0 + col] : 0.f;
     }
+}
+template <int DK>
+__device__ __forceinline__ void keep_state(const DeltaP& p, float* h, long long bh, int m0, int cols, int lane,
+                                           const float (&s)[DK / 8][4]) {
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kx = 8 * j + 2 * (lane & 3) + (e & 1), col = (lane >> 2) + 8 * (e >> 1);
+      if (kx < p.dk && col < cols) h[(bh * p.dk + kx) * p.dv + m0 + col] = s[j][e];
+    }
+}
+
+// x *= f, all of it
+template <int N>
+__device__ __forceinline__ void scale_by(float (&x)[N][4], float f) {
+  const f2 g = pack2(f, f);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const f2 a = mul2(pack2(x[j][0], x[j][1]), g), b = mul2(pack2(x[j][2], x[j][3]), g);
+    x[j][0] = a.x; x[j][1] = a.y; x[j][2] = b.x; x[j][3] = b.y;
+  }
 }
 
 }  // namespace

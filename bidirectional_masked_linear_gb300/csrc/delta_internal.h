@@ -6,30 +6,39 @@
 
 namespace lion {
 
-// Per head and chunk of 32 tokens the planes of T and P and the coefficients;
-// with `save`, as the gradients take it, P in as many planes as T, then R of
-// every token and the state before every 64th.
+// Every chunk's ChunkData; with `save`, as the gradients take them, then R of
+// every token and the state before every 64th.  U: bytes of U, beside these.
 struct DeltaLayout {
-  size_t tp_chunk, R, states, bytes;
-  int nc, nc64;
+  size_t R, states, bytes, U;
+  int nc, nc64, dvp;
 };
+template <typename T, int DK, bool SAVE>
+constexpr size_t chunk_bytes() {
+  return ChunkData<T, DK, SAVE, sizeof(T) == 4>::bytes;
+}
 inline DeltaLayout delta_layout(int B, int L, int Hv, int dk, int dv, int dtype, bool save) {
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   DeltaLayout l;
-  const size_t es = dtype == DT_BF16 ? 2 : 4, heads = (size_t)B * Hv;
-  const int mid = dtype == DT_BF16 ? Planes<__nv_bfloat16>::mid : Planes<float>::mid;
-  const int planes = mid + (save || dtype != DT_BF16 ? mid : 1);
+  const bool bf16 = dtype == DT_BF16;
+  const size_t es = bf16 ? 2 : 4, heads = (size_t)B * Hv, DK = dk <= 64 ? 64 : 128;
+  const size_t chunk =
+      bf16 ? (DK == 64 ? (save ? chunk_bytes<__nv_bfloat16, 64, true>() : chunk_bytes<__nv_bfloat16, 64, false>())
+                       : (save ? chunk_bytes<__nv_bfloat16, 128, true>() : chunk_bytes<__nv_bfloat16, 128, false>()))
+           : (DK == 64 ? (save ? chunk_bytes<float, 64, true>() : chunk_bytes<float, 64, false>())
+                       : (save ? chunk_bytes<float, 128, true>() : chunk_bytes<float, 128, false>()));
   l.nc = (L + kChunk - 1) / kChunk;
   l.nc64 = (L + kStateChunk - 1) / kStateChunk;
-  l.tp_chunk = (size_t)planes * kTile + kCoefs * sizeof(float);
-  l.R = up(heads * l.nc * l.tp_chunk);
-  l.states = l.R + (save ? up(heads * l.nc * kChunk * dv * es) : 0);
-  l.bytes = l.states + (save ? up(heads * l.nc64 * dv * dk * es) : 0);
+  l.dvp = (dv + 15) / 16 * 16;
+  l.U = up(heads * l.nc * l.dvp * kChunk * sizeof(float));
+  l.R = up(heads * l.nc * chunk);
+  l.states = l.R + (save ? up(heads * l.nc * kChunk * l.dvp * es) : 0);
+  l.bytes = l.states + (save ? up(heads * l.nc64 * l.dvp * DK * es) : 0);
   return l;
 }
 
+// kept: `bytes` of the layout, U: its `U`.
 template <typename Args>
-DeltaP delta_params(const Args& a, void* kept, bool save) {
+DeltaP delta_params(const Args& a, char* kept, char* U, bool save) {
   const DeltaLayout l = delta_layout(a.B, a.L, a.Hv, a.dk, a.dv, a.dtype, save);
   DeltaP p = {};
   p.q = a.q;
@@ -39,11 +48,11 @@ DeltaP delta_params(const Args& a, void* kept, bool save) {
   p.beta = a.beta;
   p.lengths = a.lengths;
   p.h0 = a.h0;
-  p.tp = kept;
-  p.tp_chunk = (long long)l.tp_chunk;
+  p.chunks = kept;
+  p.U = reinterpret_cast<float*>(U);
   if (save) {
-    p.R = static_cast<char*>(kept) + l.R;
-    p.states = static_cast<char*>(kept) + l.states;
+    p.R = kept + l.R;
+    p.states = kept + l.states;
   }
   p.q_ld = a.q_token ? a.q_token : (long long)a.Hk * a.dk;
   p.k_ld = a.k_token ? a.k_token : (long long)a.Hk * a.dk;
@@ -56,6 +65,7 @@ DeltaP delta_params(const Args& a, void* kept, bool save) {
   p.Hv = a.Hv;
   p.dk = a.dk;
   p.dv = a.dv;
+  p.dvp = l.dvp;
   p.nc = l.nc;
   p.nc64 = l.nc64;
   p.slices = (a.dv + kSlice - 1) / kSlice;
@@ -68,7 +78,7 @@ DeltaP delta_params(const Args& a, void* kept, bool save) {
   return p;
 }
 
-// T, P and the decays of every chunk, then the chain; p.R and p.states where `save`.
+// Every chunk's ChunkData and U, then the chain; R and states where `save`.
 cudaError_t launch_delta_chain(const DeltaP& p, int dtype, bool save, cudaStream_t s);
 
 }  // namespace lion

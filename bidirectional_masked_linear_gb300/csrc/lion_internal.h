@@ -165,9 +165,9 @@ cudaError_t launch_scan_step(const lion_scan_step_args& a, cudaStream_t s);
 cudaError_t launch_qknorm_fwd(const lion_qknorm_args& a, cudaStream_t s);
 size_t qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d);
 cudaError_t launch_qknorm_bwd(const lion_qknorm_bwd_args& a, void* ws, cudaStream_t s);
-// `saved` as lion_delta_args has it, or else the workspace of the queried size.
+// `saved` as lion_delta_args has it; a workspace of the queried size in either case.
 size_t delta_saved_bytes(int B, int L, int Hv, int dk, int dv, int dtype);
-size_t delta_workspace_bytes(int B, int L, int Hv, int dk, int dv, int dtype);
+size_t delta_workspace_bytes(int B, int L, int Hv, int dk, int dv, int dtype, bool save);
 cudaError_t launch_delta_fwd(const lion_delta_args& a, void* ws, cudaStream_t s);
 size_t delta_bwd_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, bool have_saved);
 cudaError_t launch_delta_bwd(const lion_delta_bwd_args& a, void* ws, cudaStream_t s);

@@ -83,7 +83,7 @@ def load():
         for name in ("qknorm_fwd", "qknorm_bwd", "delta_fwd", "delta_bwd", "delta_step"):
             f = getattr(lib, "lion_" + name)
             f.argtypes, f.restype = [ctypes.c_char_p], _i
-        for name, n in (("qknorm_bwd_workspace", 6), ("delta_saved", 7), ("delta_workspace", 7),
+        for name, n in (("qknorm_bwd_workspace", 6), ("delta_saved", 7), ("delta_workspace", 8),
                         ("delta_bwd_workspace", 8)):
             f = getattr(lib, f"lion_{name}_bytes")
             f.argtypes, f.restype = [_i] * n, _sz
@@ -228,9 +228,9 @@ def delta_saved_bytes(B, L, Hk, Hv, dk, dv, dtype=lion.DTYPE_BF16) -> int:
     return int(load().lion_delta_saved_bytes(B, L, Hk, Hv, dk, dv, dtype))
 
 
-def delta_workspace_bytes(B, L, Hk, Hv, dk, dv, dtype=lion.DTYPE_BF16) -> int:
+def delta_workspace_bytes(B, L, Hk, Hv, dk, dv, dtype=lion.DTYPE_BF16, save=False) -> int:
     load()
-    return _query("delta", B, L, Hk, Hv, dk, dv, dtype)
+    return _query("delta", B, L, Hk, Hv, dk, dv, dtype, int(save))
 
 
 def delta_bwd_workspace_bytes(B, L, Hk, Hv, dk, dv, dtype=lion.DTYPE_BF16, have_saved=True) -> int:
@@ -257,7 +257,7 @@ def delta_fwd(q, k, v, g, beta, scale=None, h0=None, lengths=None, reverse=False
     y = _new(stream, v.shape, q.dtype, q) if out is None else out
     h = _new(stream, (B, Hv, dk, dv), torch.float32, q) if return_state else None
     saved = _new(stream, (delta_saved_bytes(*sizes, code),), torch.uint8, q) if save else None
-    ws, nb, _keep = (0, 0, None) if save else _workspace(workspace, q, stream, "delta", *sizes, code)
+    ws, nb, _keep = _workspace(workspace, q, stream, "delta", *sizes, code, int(save))
     a = _Delta_pack(*ptrs, _tight("out", y, q.dtype, v.shape), _ptr(h), _ptr(saved), *tokens, *sizes,
                     dk ** -0.5 if scale is None else scale, int(reverse), code, ws, nb, _handle(stream, q))
     _check(lib.lion_delta_fwd(a))

@@ -758,7 +758,7 @@ size_t lion_qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d, int 
  *   h0, h_out  [B][Hv][dk][dv] float32 or NULL: the state before the first
  *   token (NULL: zeros) and after the last one.  h_out may not be h0.
  *   saved  device, 256-byte aligned, of lion_delta_saved_bytes, or NULL: what
- *   lion_delta_bwd goes on from; with it no workspace is used.
+ *   lion_delta_bwd goes on from.
  *   Keys longer than sqrt(2 / beta) make the state grow.
  */
 typedef struct {
@@ -783,7 +783,8 @@ typedef struct {
 } lion_delta_args;
 lion_status lion_delta_fwd(const lion_delta_args* a);
 size_t lion_delta_saved_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype);
-size_t lion_delta_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype);
+/* save: 1 if the call passes `saved`. */
+size_t lion_delta_workspace_bytes(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, int save);
 
 /*
  * lion_delta_bwd -- gradients of a loss through lion_delta_fwd's out, given
