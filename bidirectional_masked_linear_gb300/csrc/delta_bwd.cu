@@ -75,51 +75,58 @@ __global__ void __launch_bounds__(32) delta_back_prep_kernel(const DeltaP p) {
 //   X^T = dO^T P + beta e^(G_C - G) o (dS'^T K^T);  dR^T = X^T T
 //   dS^T = e^G_C dS'^T + (scale e^G o dO)^T Q - X^T W
 
+constexpr int kBackThreads = 256;
+
 template <typename T, int DK>
 struct Back {
   typedef ChunkData<T, DK, true, sizeof(T) == 4> D;
   typedef Stage<T, DK, D::coef, D::bytes> L;
+  typedef Swap<T, DK, 0> X;
   static constexpr int stages = sizeof(T) == 4 ? 2 : 3;
-  static constexpr int smem = stages * L::bytes + 4 * out_bytes<T>();
+  static constexpr int swap = stages * L::bytes, out = swap + 4 * X::bytes, smem = out + 8 * out_bytes<T>();
 };
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
+__global__ void __launch_bounds__(kBackThreads) delta_back_kernel(const DeltaP p) {
   typedef Back<T, DK> C;
   typedef typename C::D D;
   typedef typename C::L L;
-  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, PER = kStateChunk / kChunk;
+  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, PER = kStateChunk / kChunk, N = DK / 16;
   constexpr bool KQ = L::KQ;
   extern __shared__ __align__(128) unsigned char smem[];
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
-  unsigned char* buf = smem + NST * L::bytes + w * out_bytes<T>();
+  const int pair = w & 3, side = w >> 2;
+  unsigned char* buf = smem + C::out + w * out_bytes<T>();
+  const unsigned xs = base + C::swap + pair * C::X::bytes, xx = xs + C::X::state;   // dS^T, X^T
   const long long bh = blockIdx.x / p.slices;
   const int slice = (int)(blockIdx.x - bh * p.slices);
   const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
-  const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
+  const int m0 = slice * kSlice + 16 * pair, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
   const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xv = rows_of<T>(p, p.dv_out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
   const char* chunk = p.chunks + bh * p.nc * D::bytes;
   const long long at_last = bh * p.nc + nc - 1;
-  const float4* Z = reinterpret_cast<const float4*>(p.U) + (at_last * p.dvp + m0) * (kChunk / 4) + lane;
+  const float4* Z = reinterpret_cast<const float4*>(p.U) + (at_last * p.dvp + m0) * (kChunk / 4) + 64 * side + lane;
   const uint4* dO = p.dO + (at_last * (p.dvp / 16) + m0 / 16) * 2 * NS * 32 + lane;
 
-  float s[DK / 8][4] = {};   // dS^T
+  float s[N][4] = {};   // dS^T, this side's dk
+  if (cols > 0) put_state<DK, NS>(xs, s, side, lane);
   wait_prior();
 #pragma unroll
   for (int st = 0; st < NST - 1; ++st) {
     const int c = nc - 1 - st;
-    if (c >= 0) L::template load<128>(p, base + st * L::bytes, chunk + (long long)c * D::bytes, xq, xk, c * kChunk, n, tid);
+    if (c >= 0)
+      L::template load<kBackThreads>(p, base + st * L::bytes, chunk + (long long)c * D::bytes, xq, xk, c * kChunk, n, tid);
     copy_commit();
   }
-  float4 znext[4];
+  float4 znext[2];
   uint4 onext[2][NS];
   if (cols > 0 && nc > 0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) znext[e] = Z[32 * e];
+    for (int e = 0; e < 2; ++e) znext[e] = Z[32 * e];
 #pragma unroll
     for (int e = 0; e < 2 * NS; ++e) onext[e / NS][e % NS] = dO[32 * e];
   }
@@ -128,76 +135,72 @@ __global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
     copy_wait<NST - 2>();
     __syncthreads();
     if (ahead >= 0)
-      L::template load<128>(p, base + (step + NST - 1) % NST * L::bytes, chunk + (long long)ahead * D::bytes, xq, xk,
-                            ahead * kChunk, n, tid);
+      L::template load<kBackThreads>(p, base + (step + NST - 1) % NST * L::bytes, chunk + (long long)ahead * D::bytes, xq, xk,
+                                     ahead * kChunk, n, tid);
     copy_commit();
     if (cols <= 0) continue;
     const unsigned st = base + step % NST * L::bytes;
     const float* coef = reinterpret_cast<const float*>(smem + step % NST * L::bytes + L::at(D::coef));
     if (step == 0 || c % PER == PER - 1)
-      store_blocks<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK, s, lane);
+      store_blocks<N, DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK + side * N * 64, s, lane);
 
-    float4 z[4];
-    unsigned g[2][NS][4];
+    // this side's tokens of X^T
+    float x[2][4] = {};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = znext[e];
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      unsigned a[NS][4];
 #pragma unroll
-    for (int e = 0; e < 2 * NS; ++e) {
-      const uint4 v = onext[e / NS][e % NS];
-      unsigned(&d)[4] = g[e / NS][e % NS];
-      d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+      for (int j = 0; j < NS; ++j) get_a(xs + (ks * NS + j) * 512, a[j], lane);
+      mma_tile<NS, NI, false>(x[0], x[1], a, st + L::k + at_b_rows_n<DK, KQ>(16 * side, 16 * ks, lane), L::row);
+    }
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      const float2 l = *reinterpret_cast<const float2*>(coef + kChunk + 16 * side + 8 * nb + 2 * q4);
+      x[nb][0] = fmaf(l.x, x[nb][0], znext[nb].x);
+      x[nb][1] = fmaf(l.y, x[nb][1], znext[nb].y);
+      x[nb][2] = fmaf(l.x, x[nb][2], znext[nb].z);
+      x[nb][3] = fmaf(l.y, x[nb][3], znext[nb].w);
+    }
+    unsigned mine[NS][4];
+    to_a<NS>(x[0], x[1], mine);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) put_a(xx + (side * NS + j) * 512, mine[j], lane);
+    pair_sync(pair);
+    // dS^T, this side's dk; dR^T, this side's tokens
+    scale_by(s, coef[2 * kChunk]);
+    float y[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      unsigned a[NS][4], g[NS][4];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        get_a(xx + (ks * NS + j) * 512, a[j], lane);
+        g[j][0] = onext[ks][j].x; g[j][1] = onext[ks][j].y; g[j][2] = onext[ks][j].z; g[j][3] = onext[ks][j].w;
+      }
+#pragma unroll
+      for (int nn = 0; nn < N / 2; ++nn) {
+        const int k0 = side * (DK / 2) + 16 * nn;
+        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], g, st + L::q + at_b_rows_k<DK, KQ>(16 * ks, k0, lane), L::row);
+        mma_tile<NS, NS, true>(s[2 * nn], s[2 * nn + 1], a, st + L::at(D::W) + at_b_rows_k<DK, true>(16 * ks, k0, lane), L::row);
+      }
+      if (side <= ks)
+        mma_tile<NS, NS, true>(y[0], y[1], a, st + L::at(D::Tm) + at_b_rows_k<kChunk, true>(16 * ks, 16 * side, lane), kTile);
     }
     if (c > 0) {
       Z -= p.dvp * (kChunk / 4);
       dO -= (p.dvp / 16) * 2 * NS * 32;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) znext[e] = Z[32 * e];
+      for (int e = 0; e < 2; ++e) znext[e] = Z[32 * e];
 #pragma unroll
       for (int e = 0; e < 2 * NS; ++e) onext[e / NS][e % NS] = dO[32 * e];
     }
-    // X^T
-    float x[4][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      unsigned a[NS][4];
-      to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
-#pragma unroll
-      for (int np = 0; np < 2; ++np)
-        mma_tile<NS, NI, false>(x[2 * np], x[2 * np + 1], a, st + L::k + at_b_rows_n<DK, KQ>(16 * np, 16 * ks, lane), L::row);
-    }
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-      const float2 l = *reinterpret_cast<const float2*>(coef + kChunk + 8 * nb + 2 * q4);
-      x[nb][0] = fmaf(l.x, x[nb][0], z[nb].x);
-      x[nb][1] = fmaf(l.y, x[nb][1], z[nb].y);
-      x[nb][2] = fmaf(l.x, x[nb][2], z[nb].z);
-      x[nb][3] = fmaf(l.y, x[nb][3], z[nb].w);
-    }
-    // dS^T and dR^T
-    scale_by(s, coef[2 * kChunk]);
-    float y[4][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      unsigned a[NS][4];
-      to_a<NS>(x[2 * ks], x[2 * ks + 1], a);
-#pragma unroll
-      for (int nn = 0; nn < DK / 16; ++nn) {
-        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], g[ks], st + L::q + at_b_rows_k<DK, KQ>(16 * ks, 16 * nn, lane), L::row);
-        mma_tile<NS, NS, true>(s[2 * nn], s[2 * nn + 1], a,
-                               st + L::at(D::W) + at_b_rows_k<DK, true>(16 * ks, 16 * nn, lane), L::row);
-      }
-#pragma unroll
-      for (int np = 0; np <= ks; ++np)
-        mma_tile<NS, NS, true>(y[2 * np], y[2 * np + 1], a,
-                               st + L::at(D::Tm) + at_b_rows_k<kChunk, true>(16 * ks, 16 * np, lane), kTile);
-    }
-    const int i = c * kChunk + lane;
-    store_rows(buf, y, lane, cols, p.dv_wide, i < n ? const_cast<T*>(xv.at(i)) : nullptr);
+    put_state<DK, NS>(xs, s, side, lane);
+    store_rows(buf, y, lane, cols, p.dv_wide, xv, c * kChunk + 16 * side, n);
   }
   copy_wait<0>();
   if (cols <= 0) return;
-  if (p.dh0) keep_state<DK>(p, p.dh0, bh, m0, cols, lane, s);
-  zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, lane);
+  if (p.dh0) keep_state<N>(p, p.dh0, bh, m0, cols, side * (DK / 2), lane, s);
+  zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, side, lane);
 }
 
 // ------------------------------------------------------------- all other gradients
@@ -211,26 +214,27 @@ __global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
 // A decay g_t is in every factor that reaches over it: of tokens i >= t with
 // the state, of tokens i < t with dS', of S with dS', and of pairs i >= t > j,
 //   dg_t = sum_{i >= t} (q_i . dQ1_i + k_i . F1_i) + sum_{i < t} beta_i k_i . W1_i + e^G_C <S, dS'>
-//          + sum_{i >= t > j} beta_j (A_ij q_i . k_j + E_ij k_i . k_j)
+//          + sum_{i >= t > j} beta_j p_ij,   p_ij = A_ij q_i . k_j + E_ij k_i . k_j
 // (dQ1, F1, W1: the first terms), each sum of its own terms alone: sums over all
 // of q . dq - k . dk from t on would be shorter, but pairs on one side of t would
-// have to cancel in them, and beside a strong decay nothing else is left.
+// have to cancel in them, and beside a strong decay nothing else is left.  With
+// the pairs at hand, dbeta_j = k_j . W1_j + sum_{i >= j} p_ij.
 //
-// A warp has 16 rows and 64 of the dk columns.  R, dR, S and dS' come in the
-// inputs' type: in bfloat16 each is one rounding of 2^-9, as A and E are.
+// A warp has 16 rows and 32 of the dk columns, and of A and E every other (dk >
+// 64: every fourth) block of 16 columns.  R, dR, S and dS' come in the inputs'
+// type: in bfloat16 each is one rounding of 2^-9, as A beta and E beta are.
 
-constexpr int kPairRow = 65;
+constexpr int kPairRow = 65;   // floats of a row of p, of 64
 
-template <typename T, int DK>
+template <typename T, int DK, int DV>
 struct Grad {
   static constexpr int NI = Planes<T>::in;
-  static constexpr int halves = DK / 64, warps = 4 * halves;
-  static constexpr int dvs = sizeof(T) == 4 ? 32 : 64;   // columns of dv at a time: what shared memory holds
-  static constexpr int row = 64 * DK * 2, val = 64 * dvs * 2, sta = dvs * DK * 2, pair = 64 * 64 * 2;
+  static constexpr int groups = DK / 32, warps = 4 * groups, blocks = 4 / groups;
+  static constexpr int row = 64 * DK * 2, val = 64 * DV * 2, sta = DV * DK * 2, pair = 64 * 64 * 2;
   static constexpr int k = 0, q = NI * row, dO = 2 * NI * row, dR = dO + NI * val, R = dR + NI * val;
   static constexpr int S = R + NI * val, dS = S + NI * sta, end = dS + NI * sta;
-  static constexpr int A = dO, E = A + NI * pair;        // over the values' tiles, when they are done with
-  static constexpr int pairs = E + NI * pair, last = pairs + 64 * kPairRow * 4;   // the pairs' terms, fp32
+  static constexpr int A = dO, E = A + NI * pair, pairs = E + NI * pair;   // over the values' tiles, when they are done with
+  static constexpr int last = pairs + 64 * kPairRow * 4;
   static constexpr int smem = end > last ? end : last;
 };
 
@@ -239,11 +243,7 @@ struct Grad {
 template <int UNITS, int THREADS>
 __device__ __forceinline__ void load_blocks(unsigned dst, int, const __nv_bfloat16* src, int units, int tid) {
 #pragma unroll
-  for (int k = 0; k < UNITS / THREADS; ++k) {
-    const int i = tid + k * THREADS;
-    copy16(dst + 16 * i, src + 8 * (i < units ? i : 0), i < units);
-  }
-  static_assert(UNITS % THREADS == 0, "");
+  for (int i = tid; i < UNITS; i += THREADS) copy16(dst + 16 * i, src + 8 * (i < units ? i : 0), i < units);
 }
 template <int UNITS, int THREADS>
 __device__ __forceinline__ void load_blocks(unsigned dst, int plane, const float* src, int units, int tid) {
@@ -260,6 +260,9 @@ __device__ __forceinline__ float2 pair_of(unsigned addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return unpack_bf16(v);
 }
+__device__ __forceinline__ void put_pair(unsigned addr, unsigned v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Two adjacent values, all planes.
 template <int NP>
 __device__ __forceinline__ float2 plane_sum(unsigned addr, int plane) {
@@ -272,25 +275,22 @@ __device__ __forceinline__ float2 plane_sum(unsigned addr, int plane) {
   }
   return s;
 }
-template <int W, int NP>
-__device__ __forceinline__ float2 tile_pair(unsigned tile, int plane, int row, int col) {
-  return plane_sum<NP>(tile + unit_at<W>(row, col >> 3) + 2 * (col & 7), plane);
-}
 __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-template <typename T, int DK>
-__global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) delta_grad_kernel(const DeltaP p) {
-  typedef Grad<T, DK> G;
-  constexpr int NI = G::NI, THREADS = 32 * G::warps;
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1) delta_grad_kernel(const DeltaP p) {
+  typedef Grad<T, DK, DV> G;
+  constexpr int NI = G::NI, THREADS = 32 * G::warps, NQ = G::groups;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float2 sG[64];
-  __shared__ float sGrown[64], sLeft[64], sBeta[64], sI[2][64], sW[2][64], sB[2][64], sDot[G::warps];
+  __shared__ float sGrown[64], sLeft[64], sBeta[64], sI[NQ][64], sW[NQ][64], sCol[4][64], sDot[G::warps];
+  __shared__ float sPart[4][64];
   __shared__ double sCarry;
   const unsigned base = shared_at(smem);
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, rw = w & 3, half = w >> 2;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, rw = w & 3, grp = w >> 2;
   const int r = lane >> 2, q4 = lane & 3;
   const long long bh = blockIdx.x / p.nc64;
   const int c = (int)(blockIdx.x - bh * p.nc64);
@@ -300,22 +300,22 @@ __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) del
     const int i = i0 + row;
     return i >= p.L ? -1 : (long long)b * p.L + (i < n && p.reverse ? n - 1 - i : i);
   };
-  // the gradients of q and k: to their places, or per value head in fp32
-  const auto put = [&](void* out, float* part, int row, int col, float x, float y) {
+  // eight values of q's or k's gradient: to their place, or per value head in fp32
+  const auto put = [&](void* out, float* part, int row, int col, const float (&v)[8]) {
     const long long t = token(row);
     if (t < 0 || col >= p.dk) return;
     if (part) {
-      *reinterpret_cast<float2*>(part + (t * p.Hv + hv) * p.dk + col) = make_float2(x, y);
+      store8(part + (t * p.Hv + hv) * p.dk + col, 8, true, v);
     } else {
       T* d = static_cast<T*>(out) + (t * p.Hk + hk) * p.dk + col;
-      d[0] = from_f32<T>(x);
-      d[1] = from_f32<T>(y);
+      store8(d, 8, reinterpret_cast<uintptr_t>(d) % 16 == 0, v);
     }
   };
   if (i0 >= n) {
-    for (int i = tid; i < 64 * DK / 2; i += THREADS) {
-      put(p.dq, p.dq_part, i / (DK / 2), i % (DK / 2) * 2, 0.f, 0.f);
-      put(p.dk_out, p.dk_part, i / (DK / 2), i % (DK / 2) * 2, 0.f, 0.f);
+    const float zero[8] = {};
+    for (int i = tid; i < 64 * DK / 8; i += THREADS) {
+      put(p.dq, p.dq_part, i / (DK / 8), i % (DK / 8) * 8, zero);
+      put(p.dk_out, p.dk_part, i / (DK / 8), i % (DK / 8) * 8, zero);
     }
     if (tid < 64 && token(tid) >= 0) {
       static_cast<T*>(p.dg)[token(tid) * p.Hv + hv] = from_f32<T>(0.f);
@@ -356,143 +356,103 @@ __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) del
   __syncthreads();
   if (tid < 64) sLeft[tid] = ex2((float)(sCarry - Gs));
 
-  float dP[8][4] = {}, N[8][4] = {}, dq[8][4] = {}, f[8][4] = {}, W[8][4] = {};
+  float dP[G::blocks][2][4] = {}, N[G::blocks][2][4] = {}, dq[4][4] = {}, f[4][4] = {}, W[4][4] = {};
   float dot = 0.f;
   wait_prior();
-  for (int d0 = 0; d0 < p.dv; d0 += G::dvs) {
+  for (int d0 = 0; d0 < p.dv; d0 += DV) {
     if (d0) __syncthreads();
-    const int cols = p.dv - d0, some = p.dvp - d0 < G::dvs ? p.dvp - d0 : G::dvs;
+    const int cols = p.dv - d0, some = p.dvp - d0 < DV ? p.dvp - d0 : DV;
     const long long ld = (long long)p.Hv * p.dv, head = (long long)hv * p.dv + d0;
-    load_tile<G::dvs, 64, THREADS>(base + G::dO, G::val, rows_of<T>(p, p.dout, ld, head, b, n), i0, n, cols, p.do_wide, tid);
-    load_tile<G::dvs, 64, THREADS>(base + G::dR, G::val, rows_of<T>(p, p.dv_out, ld, head, b, n), i0, n, cols, p.dv_wide, tid);
+    load_tile<DV, 64, THREADS>(base + G::dO, G::val, rows_of<T>(p, p.dout, ld, head, b, n), i0, n, cols, p.do_wide, tid);
+    load_tile<DV, 64, THREADS>(base + G::dR, G::val, rows_of<T>(p, p.dv_out, ld, head, b, n), i0, n, cols, p.dv_wide, tid);
 #pragma unroll
     for (int h = 0; h < 2; ++h)   // R^T of 32 tokens each
-      load_blocks<G::dvs * 4, THREADS>(base + G::R + h * G::val / 2, G::val,
-                                       static_cast<const T*>(p.R) + ((bh * p.nc + 2 * c + h) * p.dvp + d0) * kChunk,
-                                       i0 + h * kChunk < n ? some * 4 : 0, tid);
+      load_blocks<DV * 4, THREADS>(base + G::R + h * G::val / 2, G::val,
+                                   static_cast<const T*>(p.R) + ((bh * p.nc + 2 * c + h) * p.dvp + d0) * kChunk,
+                                   i0 + h * kChunk < n ? some * 4 : 0, tid);
     const long long state = ((bh * p.nc64 + c) * p.dvp + d0) * DK;
-    load_blocks<G::dvs * DK / 8, THREADS>(base + G::S, G::sta, static_cast<const T*>(p.states) + state, some * (DK / 8), tid);
-    load_blocks<G::dvs * DK / 8, THREADS>(base + G::dS, G::sta, static_cast<const T*>(p.dstates) + state, some * (DK / 8), tid);
+    load_blocks<DV * DK / 8, THREADS>(base + G::S, G::sta, static_cast<const T*>(p.states) + state, some * (DK / 8), tid);
+    load_blocks<DV * DK / 8, THREADS>(base + G::dS, G::sta, static_cast<const T*>(p.dstates) + state, some * (DK / 8), tid);
     copy_commit();
     copy_wait<0>();
     __syncthreads();
 #pragma unroll 4
-    for (int i = tid; i < G::dvs * DK / 2; i += THREADS) {
+    for (int i = tid; i < DV * DK / 2; i += THREADS) {
       const float2 x = plane_sum<NI>(base + G::S + 4 * i, G::sta), y = plane_sum<NI>(base + G::dS + 4 * i, G::sta);
       dot = fmaf(x.x, y.x, fmaf(x.y, y.y, dot));
     }
 #pragma unroll
-    for (int ks = 0; ks < G::dvs / 16; ++ks) {
+    for (int ks = 0; ks < DV / 16; ++ks) {
       unsigned ao[NI][4], ad[NI][4], ar[NI][4];
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        const unsigned at = base + j * G::val + at_a_rows_m<G::dvs>(16 * rw, 16 * ks, lane);
+        const unsigned at = base + j * G::val + at_a_rows_m<DV>(16 * rw, 16 * ks, lane);
         ldsm(ao[j], at + G::dO);
         ldsm(ad[j], at + G::dR);
         ldsm_t(ar[j], base + G::R + j * G::val + (rw >> 1) * (G::val / 2) +
                           at_a_rows_k<kChunk, true>(16 * ks, 16 * (rw & 1), lane));
       }
 #pragma unroll
-      for (int np = 0; np < 4; ++np)
+      for (int i = 0; i < G::blocks; ++i) {
+        const int np = grp + NQ * i;
         if (np <= rw) {
           const unsigned at =
               base + G::R + (np >> 1) * (G::val / 2) + at_b_rows_k<kChunk, true>(16 * ks, 16 * (np & 1), lane);
-          unsigned x[4];
-#define LION_PLANE(J)                                               \
-  if (J < NI) {                                                     \
-    ldsm_t(x, at + J * G::val);                                     \
-    mma_planes<NI, NI, J>(dP[2 * np], dP[2 * np + 1], ao, x);       \
-    mma_planes<NI, NI, J>(N[2 * np], N[2 * np + 1], ad, x);         \
-  }
-          LION_PLANE(0) LION_PLANE(1) LION_PLANE(2)
-#undef LION_PLANE
+          mma_tile<NI, NI, true>(dP[i][0], dP[i][1], ao, at, G::val);
+          mma_tile<NI, NI, true>(N[i][0], N[i][1], ad, at, G::val);
         }
+      }
 #pragma unroll
-      for (int nn = 0; nn < 4; ++nn) {
-        const unsigned at = base + at_b_rows_k<DK, true>(16 * ks, 64 * half + 16 * nn, lane);
-        unsigned x[4];
-#define LION_PLANE(J)                                               \
-  if (J < NI) {                                                     \
-    ldsm_t(x, at + G::S + J * G::sta);                              \
-    mma_planes<NI, NI, J>(dq[2 * nn], dq[2 * nn + 1], ao, x);       \
-    mma_planes<NI, NI, J>(f[2 * nn], f[2 * nn + 1], ad, x);         \
-    ldsm_t(x, at + G::dS + J * G::sta);                             \
-    mma_planes<NI, NI, J>(W[2 * nn], W[2 * nn + 1], ar, x);         \
-  }
-        LION_PLANE(0) LION_PLANE(1) LION_PLANE(2)
-#undef LION_PLANE
+      for (int nn = 0; nn < 2; ++nn) {
+        const unsigned at = base + at_b_rows_k<DK, true>(16 * ks, 32 * grp + 16 * nn, lane);
+        mma_tile<NI, NI, true>(dq[2 * nn], dq[2 * nn + 1], ao, at + G::S, G::sta);
+        mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], ad, at + G::S, G::sta);
+        mma_tile<NI, NI, true>(W[2 * nn], W[2 * nn + 1], ar, at + G::dS, G::sta);
       }
     }
   }
   dot = warp_sum(dot);
   if (lane == 0) sDot[w] = dot;
 
-  // the first terms, and their products with q and k
+  // the first terms, their products with q and k, and f as dK's beginning
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int i = 16 * rw + r + 8 * h;
-    const float grown = sGrown[i], left = sLeft[i];
+    const float grown = sGrown[i], left = sLeft[i], beta = sBeta[i], gq = p.scale * grown;
     float si = 0.f, sw = 0.f;
 #pragma unroll
-    for (int nb = 0; nb < 8; ++nb) {
-      const float2 qv = tile_pair<DK, NI>(base + G::q, G::row, i, 64 * half + 8 * nb + 2 * q4);
-      const float2 kv = tile_pair<DK, NI>(base + G::k, G::row, i, 64 * half + 8 * nb + 2 * q4);
+    for (int nb = 0; nb < 4; ++nb) {
+      const unsigned at = base + unit_at<DK>(i, 4 * grp + nb) + 4 * q4;
+      const float2 qv = plane_sum<NI>(at + G::q, G::row), kv = plane_sum<NI>(at + G::k, G::row);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        dq[nb][2 * h + e] *= p.scale * grown;
-        f[nb][2 * h + e] *= -grown;
-        W[nb][2 * h + e] *= left;
-        const float qe = e ? qv.y : qv.x, ke = e ? kv.y : kv.x;
-        si = fmaf(qe, dq[nb][2 * h + e], fmaf(ke, f[nb][2 * h + e], si));
-        sw = fmaf(ke, W[nb][2 * h + e], sw);
+        float &x = dq[nb][2 * h + e], &y = f[nb][2 * h + e];
+        const float z = left * W[nb][2 * h + e], qe = e ? qv.y : qv.x, ke = e ? kv.y : kv.x;
+        x *= gq;
+        y *= -grown;
+        si = fmaf(qe, x, fmaf(ke, y, si));
+        sw = fmaf(ke, z, sw);
+        y = fmaf(beta, z, y);
       }
     }
     si = quad_sum(si);
     sw = quad_sum(sw);
     if (q4 == 0) {
-      sI[half][i] = si;
-      sW[half][i] = sw * sBeta[i];
+      sI[grp][i] = si;
+      sW[grp][i] = sw;
     }
   }
-  // A and E, in the registers of dP and N
-#pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 16 * rw + r + 8 * (e >> 1), j = 8 * nb + 2 * q4 + (e & 1);
-      const float2 gi = sG[i], gj = sG[j];
-      const float d = i >= j ? ex2((gi.x - gj.x) + (gi.y - gj.y)) : 0.f;
-      dP[nb][e] = i >= j ? p.scale * d * dP[nb][e] : 0.f;
-      N[nb][e] = i > j ? -d * N[nb][e] : 0.f;
-    }
   __syncthreads();   // the values' tiles are done with
-#pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
-    if (nb < 2 * rw + 2)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const unsigned at = base + unit_at<64>(16 * rw + r + 8 * h, nb) + 4 * q4;
-        unsigned t[NI];
-        if (half == 0) {
-          split<NI>(dP[nb][2 * h], dP[nb][2 * h + 1], t);
-#pragma unroll
-          for (int j = 0; j < NI; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + G::A + j * G::pair), "r"(t[j]) : "memory");
-        }
-        if (half == G::halves - 1) {
-          split<NI>(N[nb][2 * h], N[nb][2 * h + 1], t);
-#pragma unroll
-          for (int j = 0; j < NI; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + G::E + j * G::pair), "r"(t[j]) : "memory");
-        }
-      }
-  // the pairs' terms; with two halves each has every other block
   float* pairs = reinterpret_cast<float*>(smem + G::pairs);
 #pragma unroll
-  for (int np = 0; np < 4; ++np)
-    if (np <= rw && np % G::halves == half) {
+  for (int i = 0; i < G::blocks; ++i) {
+    const int np = grp + NQ * i;
+    float col[4] = {0.f, 0.f, 0.f, 0.f};
+    if (np <= rw) {
       float qk[2][4] = {}, kk[2][4] = {};
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks) {
-        unsigned aq[NI][4], ak[NI][4], x[4];
+        unsigned aq[NI][4], ak[NI][4];
         const unsigned aa = base + at_a_rows_m<DK>(16 * rw, 16 * ks, lane);
         const unsigned bb = base + G::k + at_b_rows_n<DK>(16 * np, 16 * ks, lane);
 #pragma unroll
@@ -500,130 +460,179 @@ __global__ void __launch_bounds__(32 * Grad<T, DK>::warps, DK == 64 ? 2 : 1) del
           ldsm(aq[j], aa + G::q + j * G::row);
           ldsm(ak[j], aa + G::k + j * G::row);
         }
-#define LION_PLANE(J)                                    \
-  if (J < NI) {                                          \
-    ldsm(x, bb + J * G::row);                            \
-    mma_planes<NI, NI, J>(qk[0], qk[1], aq, x);          \
-    mma_planes<NI, NI, J>(kk[0], kk[1], ak, x);          \
-  }
-        LION_PLANE(0) LION_PLANE(1) LION_PLANE(2)
-#undef LION_PLANE
+        mma_tile<NI, NI, false>(qk[0], qk[1], aq, bb, G::row);
+        mma_tile<NI, NI, false>(kk[0], kk[1], ak, bb, G::row);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        const int j = 16 * np + 8 * h + 2 * q4;
+        const float4 gj = *reinterpret_cast<const float4*>(&sG[j]);
+        const float2 bj = *reinterpret_cast<const float2*>(&sBeta[j]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int nb = 2 * np + h, i = 16 * rw + r + 8 * (e >> 1), j = 8 * nb + 2 * q4 + (e & 1);
-          pairs[i * kPairRow + j] = sBeta[j] * fmaf(dP[nb][e], qk[h][e], N[nb][e] * kk[h][e]);
+        for (int half = 0; half < 2; ++half) {
+          const int ii = 16 * rw + r + 8 * half;
+          const float2 gi = sG[ii];
+          float av[2], ev[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float d = ex2(e ? (gi.x - gj.z) + (gi.y - gj.w) : (gi.x - gj.x) + (gi.y - gj.y));
+            const float x = ii >= j + e ? p.scale * d * dP[i][h][2 * half + e] : 0.f;
+            const float y = ii > j + e ? -d * N[i][h][2 * half + e] : 0.f;
+            const float v = fmaf(x, qk[h][2 * half + e], y * kk[h][2 * half + e]);
+            pairs[ii * kPairRow + j + e] = v;
+            col[2 * h + e] += v;
+            av[e] = x * (e ? bj.y : bj.x);
+            ev[e] = y * (e ? bj.y : bj.x);
+          }
+          const unsigned at = base + unit_at<64>(ii, 2 * np + h) + 4 * q4;
+          unsigned t[NI];
+          split<NI>(av[0], av[1], t);
+#pragma unroll
+          for (int y = 0; y < NI; ++y) put_pair(at + G::A + y * G::pair, t[y]);
+          split<NI>(ev[0], ev[1], t);
+#pragma unroll
+          for (int y = 0; y < NI; ++y) put_pair(at + G::E + y * G::pair, t[y]);
         }
-    }
-  // dQ += (A beta) K, F += (E beta) K
-#pragma unroll
-  for (int ks = 0; ks < 4; ++ks)
-    if (ks <= rw) {
-      const int j0 = 16 * ks + 2 * q4;
-      const float2 b0 = make_float2(sBeta[j0], sBeta[j0 + 1]), b1 = make_float2(sBeta[j0 + 8], sBeta[j0 + 9]);
-      unsigned aa[NI][4], ae[NI][4];
-      to_a<NI>(dP[2 * ks], dP[2 * ks + 1], b0, b1, aa);
-      to_a<NI>(N[2 * ks], N[2 * ks + 1], b0, b1, ae);
-#pragma unroll
-      for (int nn = 0; nn < 4; ++nn) {
-        const unsigned at = base + G::k + at_b_rows_k<DK>(16 * ks, 64 * half + 16 * nn, lane);
-        unsigned x[4];
-#define LION_PLANE(J)                                               \
-  if (J < NI) {                                                     \
-    ldsm_t(x, at + J * G::row);                                     \
-    mma_planes<NI, NI, J>(dq[2 * nn], dq[2 * nn + 1], aa, x);       \
-    mma_planes<NI, NI, J>(f[2 * nn], f[2 * nn + 1], ae, x);         \
-  }
-        LION_PLANE(0) LION_PLANE(1) LION_PLANE(2)
-#undef LION_PLANE
       }
     }
 #pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      put(p.dq, p.dq_part, 16 * rw + r + 8 * h, 64 * half + 8 * nb + 2 * q4, dq[nb][2 * h], dq[nb][2 * h + 1]);
-  __syncthreads();   // A and E are there
-  if (rw >= 2 && half == 0) {   // a pair row's sums up to each token; the warps with the fewest products below
-    float* row = pairs + (tid - 64) * kPairRow;
-    float sum = 0.f;
-#pragma unroll 8
-    for (int j = 0; j < 64; ++j) {
-      const float x = j < tid - 64 ? row[j] : 0.f;
-      row[j] = sum;
-      sum += x;
+      for (int o = 4; o < 32; o <<= 1) col[e] += __shfl_xor_sync(0xffffffffu, col[e], o);
+      if (r == 0) sCol[rw][16 * np + 8 * (e >> 1) + 2 * q4 + (e & 1)] = col[e];
     }
   }
-  // W += A^T Q + E^T K
+  __syncthreads();   // A, E and p are there
+  if (tid < 256) {   // a row's sums of beta p up to each token, four threads a row
+    const int i = tid >> 2, j0 = 16 * (tid & 3);
+    float* row = pairs + i * kPairRow + j0;
+    float v[16], sum = 0.f;
 #pragma unroll
-  for (int ib = 0; ib < 4; ++ib)
-    if (ib >= rw) {
+    for (int j = 0; j < 16; ++j) {
+      v[j] = sum;
+      sum += j0 + j < i ? sBeta[j0 + j] * row[j] : 0.f;
+    }
+    float before = __shfl_up_sync(0xffffffffu, sum, 1, 4), x = q4 >= 1 ? before : 0.f;
+    before = __shfl_up_sync(0xffffffffu, sum, 2, 4);
+    x += q4 >= 2 ? before : 0.f;
+    before = __shfl_up_sync(0xffffffffu, sum, 3, 4);
+    x += q4 >= 3 ? before : 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) row[j] = v[j] + x;
+  }
+  // dQ += (A beta) K, dK += (E beta) K + (A beta)^T Q + (E beta)^T K
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    if (ks <= rw) {
       unsigned aa[NI][4], ae[NI][4];
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        const unsigned at = base + j * G::pair + at_a_rows_k<64>(16 * ib, 16 * rw, lane);
+        const unsigned at = base + j * G::pair + at_a_rows_m<64>(16 * rw, 16 * ks, lane);
+        ldsm(aa[j], at + G::A);
+        ldsm(ae[j], at + G::E);
+      }
+#pragma unroll
+      for (int nn = 0; nn < 2; ++nn) {
+        const unsigned at = base + G::k + at_b_rows_k<DK>(16 * ks, 32 * grp + 16 * nn, lane);
+        mma_tile<NI, NI, true>(dq[2 * nn], dq[2 * nn + 1], aa, at, G::row);
+        mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], ae, at, G::row);
+      }
+    }
+    if (ks >= rw) {
+      unsigned aa[NI][4], ae[NI][4];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const unsigned at = base + j * G::pair + at_a_rows_k<64>(16 * ks, 16 * rw, lane);
         ldsm_t(aa[j], at + G::A);
         ldsm_t(ae[j], at + G::E);
       }
 #pragma unroll
-      for (int nn = 0; nn < 4; ++nn) {
-        const unsigned at = base + at_b_rows_k<DK>(16 * ib, 64 * half + 16 * nn, lane);
-        unsigned x[4];
-#define LION_PLANE(J)                                               \
-  if (J < NI) {                                                     \
-    ldsm_t(x, at + G::q + J * G::row);                              \
-    mma_planes<NI, NI, J>(W[2 * nn], W[2 * nn + 1], aa, x);         \
-    ldsm_t(x, at + G::k + J * G::row);                              \
-    mma_planes<NI, NI, J>(W[2 * nn], W[2 * nn + 1], ae, x);         \
-  }
-        LION_PLANE(0) LION_PLANE(1) LION_PLANE(2)
-#undef LION_PLANE
+      for (int nn = 0; nn < 2; ++nn) {
+        const unsigned at = base + at_b_rows_k<DK>(16 * ks, 32 * grp + 16 * nn, lane);
+        mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], aa, at + G::q, G::row);
+        mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], ae, at + G::k, G::row);
       }
     }
+  }
+  __syncthreads();   // the sums of rows are there, and q and k done with
+  // dg's sums over 16 rows a thread
+  if (tid < 256) {
+    const int t = tid & 63, part = tid >> 6;
+    float sum = 0.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = 16 * rw + r + 8 * h;
-    const float beta = sBeta[i];
-    float sb = 0.f;
+    for (int x = 0; x < 16; ++x) {
+      const int i = 16 * part + x;
+      float a = 0.f, bw = 0.f;
 #pragma unroll
-    for (int nb = 0; nb < 8; ++nb) {
-      const int col = 64 * half + 8 * nb + 2 * q4;
-      const float2 kv = tile_pair<DK, NI>(base + G::k, G::row, i, col);
-      sb = fmaf(kv.x, W[nb][2 * h], fmaf(kv.y, W[nb][2 * h + 1], sb));
-      put(p.dk_out, p.dk_part, i, col, fmaf(beta, W[nb][2 * h], f[nb][2 * h]),
-          fmaf(beta, W[nb][2 * h + 1], f[nb][2 * h + 1]));
+      for (int h = 0; h < NQ; ++h) {
+        a += sI[h][i];
+        bw += sW[h][i];
+      }
+      sum += i >= t ? a + pairs[i * kPairRow + t] : sBeta[i] * bw;
     }
-    sb = quad_sum(sb);
-    if (q4 == 0) sB[half][i] = sb;
+    sPart[part][t] = sum;
+  }
+  // dQ and dK through q's and k's place, for whole rows
+  if (sizeof(T) == 2 && !p.dq_part) {
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned at = base + unit_at<DK>(16 * rw + r + 8 * h, 4 * grp + nb) + 4 * q4;
+        put_pair(at + G::q, pack_bf16(dq[nb][2 * h], dq[nb][2 * h + 1]));
+        put_pair(at + G::k, pack_bf16(f[nb][2 * h], f[nb][2 * h + 1]));
+      }
+  } else {
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const long long t = token(16 * rw + r + 8 * h);
+        const int col = 32 * grp + 8 * nb + 2 * q4;
+        if (t < 0 || col >= p.dk) continue;
+        const float2 x = make_float2(dq[nb][2 * h], dq[nb][2 * h + 1]), y = make_float2(f[nb][2 * h], f[nb][2 * h + 1]);
+        if (p.dq_part) {
+          const long long at = (t * p.Hv + hv) * p.dk + col;
+          *reinterpret_cast<float2*>(p.dq_part + at) = x;
+          *reinterpret_cast<float2*>(p.dk_part + at) = y;
+        } else {
+          const long long at = (t * p.Hk + hk) * p.dk + col;
+          float* d[2] = {reinterpret_cast<float*>(p.dq) + at, reinterpret_cast<float*>(p.dk_out) + at};
+          d[0][0] = x.x;
+          d[0][1] = x.y;
+          d[1][0] = y.x;
+          d[1][1] = y.y;
+        }
+      }
   }
   __syncthreads();
+  if (sizeof(T) == 2 && !p.dq_part) {
+#pragma unroll 2
+    for (int i = tid; i < 2 * 64 * (DK / 8); i += THREADS) {
+      const int second = i >= 64 * (DK / 8), x = i - second * 64 * (DK / 8), row = x / (DK / 8), u = x % (DK / 8);
+      const long long t = token(row);
+      if (t < 0 || 8 * u >= p.dk) continue;
+      const uint4 v = *reinterpret_cast<const uint4*>(smem + (second ? G::k : G::q) + unit_at<DK>(row, u));
+      T* d = static_cast<T*>(second ? p.dk_out : p.dq) + (t * p.Hk + hk) * p.dk + 8 * u;
+      if (reinterpret_cast<uintptr_t>(d) % 16 == 0) {
+        *reinterpret_cast<uint4*>(d) = v;
+      } else {
+        const unsigned s[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) reinterpret_cast<unsigned short*>(d)[e] = (unsigned short)(s[e >> 1] >> 16 * (e & 1));
+      }
+    }
+  }
   if (tid < 64 && token(tid) >= 0) {
     float dg = 0.f, db = 0.f;
     if (i0 + tid < n) {
-      float inner = 0.f, before = 0.f, across = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < 64; ++i) {
-        float a = 0.f, bw = 0.f;
-#pragma unroll
-        for (int h = 0; h < G::halves; ++h) {
-          a += sI[h][i];
-          bw += sW[h][i];
-        }
-        if (i >= tid) {
-          inner += a;
-          across += pairs[i * kPairRow + tid];
-        } else {
-          before += bw;
-        }
-      }
       float d = 0.f;
 #pragma unroll
       for (int k = 0; k < G::warps; ++k) d += sDot[k];
-      dg = inner + before + across + sGrown[63] * d;
+      dg = (sPart[0][tid] + sPart[1][tid]) + (sPart[2][tid] + sPart[3][tid]) + sGrown[63] * d;
+      db = (sCol[0][tid] + sCol[1][tid]) + (sCol[2][tid] + sCol[3][tid]);
 #pragma unroll
-      for (int h = 0; h < G::halves; ++h) db += sB[h][tid];
+      for (int h = 0; h < NQ; ++h) db += sW[h][tid];
     }
     static_cast<T*>(p.dg)[token(tid) * p.Hv + hv] = from_f32<T>(dg);
     static_cast<T*>(p.dbeta)[token(tid) * p.Hv + hv] = from_f32<T>(db);
@@ -651,6 +660,24 @@ __global__ void __launch_bounds__(256) delta_heads_kernel(const float* part_q, c
   store8(dst, 8, reinterpret_cast<uintptr_t>(dst) % 16 == 0, s);
 }
 
+template <typename T, int DK, int DV>
+cudaError_t run_grad(const DeltaP& p, cudaStream_t s) {
+  const auto grad = delta_grad_kernel<T, DK, DV>;
+  const cudaError_t e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad<T, DK, DV>::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(grad, dim3((unsigned)((long long)p.B * p.Hv * p.nc64)), dim3(32 * Grad<T, DK, DV>::warps),
+                          (size_t)Grad<T, DK, DV>::smem, s, p);
+}
+// Columns of dv at a time: all of them in bfloat16, what shared memory holds in three planes.
+template <int DK>
+cudaError_t run_grad_any(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
+  return p.dv <= 64 ? run_grad<__nv_bfloat16, DK, 64>(p, s) : run_grad<__nv_bfloat16, DK, 128>(p, s);
+}
+template <int DK>
+cudaError_t run_grad_any(const DeltaP& p, float*, cudaStream_t s) {
+  return run_grad<float, DK, 32>(p, s);
+}
+
 template <typename T, int DK>
 cudaError_t run_back(const DeltaP& p, cudaStream_t s) {
   typedef ChunkData<T, DK, true, sizeof(T) == 4> D;
@@ -662,13 +689,9 @@ cudaError_t run_back(const DeltaP& p, cudaStream_t s) {
   const auto back = delta_back_kernel<T, DK>;
   e = cudaFuncSetAttribute(back, cudaFuncAttributeMaxDynamicSharedMemorySize, Back<T, DK>::smem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(back, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)Back<T, DK>::smem, s, p);
+  e = launch_dependent(back, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(kBackThreads), (size_t)Back<T, DK>::smem, s, p);
   if (e != cudaSuccess) return e;
-  const auto grad = delta_grad_kernel<T, DK>;
-  e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad<T, DK>::smem);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(grad, dim3((unsigned)((long long)p.B * p.Hv * p.nc64)), dim3(32 * Grad<T, DK>::warps),
-                       (size_t)Grad<T, DK>::smem, s, p);
+  e = run_grad_any<DK>(p, (T*)nullptr, s);
   if (e != cudaSuccess || !p.dq_part) return e;
   const long long vectors = (long long)p.B * p.L * p.Hk * (p.dk / 8);
   return launch_dependent(delta_heads_kernel<T>, dim3((unsigned)((2 * vectors + 255) / 256)), dim3(256), (size_t)0, s,

@@ -302,11 +302,9 @@ __device__ __forceinline__ void store_planes(unsigned dst, int plane, const floa
 template <int W, int ROWS, int THREADS>
 __device__ __forceinline__ void load_tile(unsigned dst, int plane, Rows<float> x, int i0, int n, int cols, bool wide,
                                           int tid) {
-  constexpr int RS = THREADS / (W / 8);
-  const int u = tid % (W / 8), r0 = tid / (W / 8);
 #pragma unroll 4
-  for (int k = 0; k < ROWS / RS; ++k) {
-    const int row = r0 + k * RS;
+  for (int i = tid; i < ROWS * (W / 8); i += THREADS) {
+    const int row = i / (W / 8), u = i % (W / 8);
     float v[8];
     load8(x.at(i0 + row) + 8 * u, i0 + row < n && 8 * u < cols ? 8 : 0, wide, v);
     store_planes(dst + unit_at<W>(row, u), plane, v);

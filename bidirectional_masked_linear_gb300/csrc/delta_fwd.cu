@@ -244,126 +244,151 @@ __global__ void __launch_bounds__(32) delta_prep_kernel(const DeltaP p) {
 
 // ------------------------------------------------------------------ the chain
 //
-// A CTA holds 64 columns of a head's state, a warp 16 of them as rows of S^T;
-// all a chunk does to them stays in the warp's registers, and the tiles that
-// all columns share come through shared memory a few chunks ahead.
+// A CTA holds 64 columns of a head's state, two warps 16 of them as rows of S^T:
+// each has half of dk in its registers and, of a chunk, half of the tokens'
+// products with S.  The halves of R^T and of the new S^T pass between them in
+// shared memory; the tiles that all columns share come through it a few chunks
+// ahead.  One warp for all of a chunk's products would have the tensor core
+// wait for it three clocks of four: a step is some 700 instructions of one warp
+// or 400 of each of two (2 x 24337 x 12 x 64: 848 against XXX us).
+
+constexpr int kChainThreads = 256;
 
 template <typename T, int DK, bool SAVE>
 struct Chain {
   typedef ChunkData<T, DK, SAVE, sizeof(T) == 4> D;
   typedef Stage<T, DK, D::P, D::Tm> L;
+  static constexpr int NO = D::NI == 1 ? 1 : D::NS;   // planes of S and R that a bfloat16 output takes: a rounding of 2^-9
+  typedef Swap<T, DK, NO> X;
   static constexpr int stages = sizeof(T) == 4 ? 2 : 3;
-  static constexpr int smem = stages * L::bytes + 4 * out_bytes<T>();
+  static constexpr int swap = stages * L::bytes, out = swap + 4 * X::bytes, smem = out + 8 * out_bytes<T>();
 };
 
 template <typename T, int DK, bool SAVE>
-__global__ void __launch_bounds__(128) delta_chain_kernel(const DeltaP p) {
+__global__ void __launch_bounds__(kChainThreads) delta_chain_kernel(const DeltaP p) {
   typedef Chain<T, DK, SAVE> C;
   typedef typename C::D D;
   typedef typename C::L L;
-  constexpr int NST = C::stages, NI = D::NI, NS = D::NS;
-  constexpr int NO = NI == 1 ? 1 : NS;   // planes of S and R that a bfloat16 output takes: one rounding of 2^-9 each
+  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, NO = C::NO, N = DK / 16;
   constexpr bool KQ = L::KQ;
   extern __shared__ __align__(128) unsigned char smem[];
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
-  unsigned char* buf = smem + NST * L::bytes + w * out_bytes<T>();
+  const int pair = w & 3, side = w >> 2;
+  unsigned char* buf = smem + C::out + w * out_bytes<T>();
+  const unsigned xs = base + C::swap + pair * C::X::bytes, xr = xs + C::X::state;   // S^T, R^T
   const long long bh = blockIdx.x / p.slices;
   const int slice = (int)(blockIdx.x - bh * p.slices);
   const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
-  const int m0 = slice * kSlice + 16 * w;              // the warp's first column of the state
+  const int m0 = slice * kSlice + 16 * pair;           // the warp's first column of the state
   const int cols = p.dv - m0 < 16 ? p.dv - m0 : 16;    // 0 or less: none
   const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xo = rows_of<T>(p, p.out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
   const char* chunk = p.chunks + bh * p.nc * D::bytes;
-  const float4* U = reinterpret_cast<const float4*>(p.U) + (bh * p.nc * p.dvp + m0) * (kChunk / 4) + lane;
+  const float4* U = reinterpret_cast<const float4*>(p.U) + (bh * p.nc * p.dvp + m0) * (kChunk / 4) + 64 * side + lane;
 
-  float s[DK / 8][4];   // S^T
-  load_state<DK>(p, p.h0, bh, m0, cols, lane, s);
+  float s[N][4];   // S^T, this side's dk
+  load_state<N>(p, p.h0, bh, m0, cols, side * (DK / 2), lane, s);
+  if (cols > 0) put_state<DK, NS>(xs, s, side, lane);
   wait_prior();
 #pragma unroll
   for (int st = 0; st < NST - 1; ++st) {
     if (st < nc)
-      L::template load<128>(p, base + st * L::bytes, chunk + (long long)st * D::bytes, xq, xk, st * kChunk, n, tid);
+      L::template load<kChainThreads>(p, base + st * L::bytes, chunk + (long long)st * D::bytes, xq, xk, st * kChunk, n, tid);
     copy_commit();
   }
-  float4 next[4];
+  float4 next[2];
   if (cols > 0 && nc > 0)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) next[e] = U[32 * e];
+    for (int e = 0; e < 2; ++e) next[e] = U[32 * e];
   for (int c = 0; c < nc; ++c) {
     copy_wait<NST - 2>();
     __syncthreads();
     if (c + NST - 1 < nc)
-      L::template load<128>(p, base + (c + NST - 1) % NST * L::bytes, chunk + (long long)(c + NST - 1) * D::bytes, xq, xk,
-                            (c + NST - 1) * kChunk, n, tid);
+      L::template load<kChainThreads>(p, base + (c + NST - 1) % NST * L::bytes, chunk + (long long)(c + NST - 1) * D::bytes,
+                                      xq, xk, (c + NST - 1) * kChunk, n, tid);
     copy_commit();
     if (cols <= 0) continue;
     const unsigned st = base + c % NST * L::bytes;
-    const float* coef = reinterpret_cast<const float*>(smem + c % NST * L::bytes + L::at(D::coef));
+    const float* coef = reinterpret_cast<const float*>(smem + c % NST * L::bytes + L::at(D::coef)) + 16 * side + 2 * q4;
     if (SAVE && c % (kStateChunk / kChunk) == 0)
-      store_blocks<DK / 8>(static_cast<T*>(p.states) + ((bh * p.nc64 + c / (kStateChunk / kChunk)) * p.dvp + m0) * DK, s, lane);
+      store_blocks<N, DK / 8>(static_cast<T*>(p.states) +
+                                  ((bh * p.nc64 + c / (kStateChunk / kChunk)) * p.dvp + m0) * DK + side * N * 64,
+                              s, lane);
 
-    // R^T = U^T - S^T W^T; S^T Q^T
-    float x[4][4], o[4][4] = {};
+    // this side's tokens: R^T = U^T - S^T W^T; S^T Q^T
+    float x[2][4], o[2][4] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       x[i][0] = next[i].x; x[i][1] = next[i].y; x[i][2] = next[i].z; x[i][3] = next[i].w;
     }
     if (c + 1 < nc) {
       U += p.dvp * (kChunk / 4);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) next[e] = U[32 * e];
+      for (int e = 0; e < 2; ++e) next[e] = U[32 * e];
     }
 #pragma unroll
     for (int ks = 0; ks < DK / 16; ++ks) {
       unsigned a[NS][4], ao[NO][4];
-      to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
 #pragma unroll
-      for (int i = 0; i < NO; ++i)
+      for (int j = 0; j < NS; ++j) get_a(xs + (ks * NS + j) * 512, a[j], lane);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ao[i][e] = a[i][e];
+      for (int j = 0; j < NO; ++j)
 #pragma unroll
-      for (int np = 0; np < 2; ++np) {
-        mma_tile<NS, NS, false>(x[2 * np], x[2 * np + 1], a, st + L::at(D::W) + at_b_rows_n<DK, true>(16 * np, 16 * ks, lane),
-                                L::row);
-        mma_tile<NO, NI, false>(o[2 * np], o[2 * np + 1], ao, st + L::q + at_b_rows_n<DK, KQ>(16 * np, 16 * ks, lane), L::row);
-      }
+        for (int e = 0; e < 4; ++e) ao[j][e] = a[j][e];
+      mma_tile<NS, NS, false>(x[0], x[1], a, st + L::at(D::W) + at_b_rows_n<DK, true>(16 * side, 16 * ks, lane), L::row);
+      mma_tile<NO, NI, false>(o[0], o[1], ao, st + L::q + at_b_rows_n<DK, KQ>(16 * side, 16 * ks, lane), L::row);
     }
-    if (SAVE) store_blocks<4>(static_cast<T*>(p.R) + ((bh * p.nc + c) * p.dvp + m0) * kChunk, x, lane);
-    // S^T = e^G_C S^T + (beta left R)^T K; O^T = scale e^G (S^T Q^T) + R^T P^T
+    // R^T to the other side: times beta e^(G_C - G) in planes, and as it is for the output
+    unsigned mine[NS][4], plain[NO][4];
+    to_a<NS>(x[0], x[1], *reinterpret_cast<const float2*>(coef + kChunk), *reinterpret_cast<const float2*>(coef + kChunk + 8),
+             mine);
+    to_a<NO>(x[0], x[1], plain);
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-      const float2 g = *reinterpret_cast<const float2*>(coef + 8 * nb + 2 * q4);
+    for (int j = 0; j < NS; ++j) put_a(xr + (side * NS + j) * 512, mine[j], lane);
+    if (side == 0)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[nb][e] *= e & 1 ? g.y : g.x;
-    }
-    scale_by(s, coef[2 * kChunk]);
+      for (int j = 0; j < NO; ++j) put_a(xr + (2 * NS + j) * 512, plain[j], lane);
+    pair_sync(pair);
+    // S^T = e^G_C S^T + (beta left R)^T K, this side's dk
+    scale_by(s, coef[2 * kChunk - 16 * side - 2 * q4]);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const float* l = coef + kChunk + 16 * ks + 2 * q4;
-      unsigned a[NS][4], ao[NO][4];
-      to_a<NS>(x[2 * ks], x[2 * ks + 1], *reinterpret_cast<const float2*>(l), *reinterpret_cast<const float2*>(l + 8), a);
+      unsigned a[NS][4];
 #pragma unroll
-      for (int nn = 0; nn < DK / 16; ++nn)
-        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], a, st + L::k + at_b_rows_k<DK, KQ>(16 * ks, 16 * nn, lane), L::row);
-      to_a<NO>(x[2 * ks], x[2 * ks + 1], ao);
+      for (int j = 0; j < NS; ++j) get_a(xr + (ks * NS + j) * 512, a[j], lane);
 #pragma unroll
-      for (int np = ks; np < 2; ++np)
-        mma_tile<NO, NO, false>(o[2 * np], o[2 * np + 1], ao,
-                                st + L::at(D::P) + at_b_rows_n<kChunk, true>(16 * np, 16 * ks, lane), kTile);
+      for (int nn = 0; nn < N / 2; ++nn)
+        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], a,
+                               st + L::k + at_b_rows_k<DK, KQ>(16 * ks, side * (DK / 2) + 16 * nn, lane), L::row);
     }
-    if (p.out) {
-      const int i = c * kChunk + lane;
-      store_rows(buf, o, lane, cols, p.o_wide, i < n ? const_cast<T*>(xo.at(i)) : nullptr);
+    put_state<DK, NS>(xs, s, side, lane);
+    if (SAVE)
+      store_blocks<2, 4>(static_cast<T*>(p.R) + ((bh * p.nc + c) * p.dvp + m0) * kChunk + side * 2 * 64, x, lane);
+    if (p.out) {   // O^T = scale e^G (S^T Q^T) + R^T P^T
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        const float2 g = *reinterpret_cast<const float2*>(coef + 8 * nb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nb][e] *= e & 1 ? g.y : g.x;
+      }
+      const unsigned P = st + L::at(D::P);
+      if (side == 1) {
+        unsigned a[NO][4];
+#pragma unroll
+        for (int j = 0; j < NO; ++j) get_a(xr + (2 * NS + j) * 512, a[j], lane);
+        mma_tile<NO, NO, false>(o[0], o[1], a, P + at_b_rows_n<kChunk, true>(16, 0, lane), kTile);
+      }
+      mma_tile<NO, NO, false>(o[0], o[1], plain, P + at_b_rows_n<kChunk, true>(16 * side, 16 * side, lane), kTile);
+      store_rows(buf, o, lane, cols, p.o_wide, xo, c * kChunk + 16 * side, n);
     }
   }
   copy_wait<0>();
   if (cols <= 0) return;
-  if (p.h_out) keep_state<DK>(p, p.h_out, bh, m0, cols, lane, s);
-  if (p.out) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, lane);
+  if (p.h_out) keep_state<N>(p, p.h_out, bh, m0, cols, side * (DK / 2), lane, s);
+  if (p.out) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, side, lane);
 }
 
 template <typename T, int DK, bool SAVE>
@@ -378,7 +403,7 @@ cudaError_t run_chain(const DeltaP& p, cudaStream_t s) {
   const auto kern = delta_chain_kernel<T, DK, SAVE>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), C::smem, s, p);
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(kChainThreads), C::smem, s, p);
 }
 template <typename T>
 cudaError_t run_chain_any(const DeltaP& p, bool save, cudaStream_t s) {

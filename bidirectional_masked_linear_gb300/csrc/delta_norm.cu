@@ -7,9 +7,11 @@
 // A lane holds eight values of a head as two runs of four: adjacent ones, or
 // those that the rotation pairs in the two halves, so that a pair never leaves
 // its lane.  d / 8 lanes make a head (of a power of two, the rest idle), a
-// warp takes a token and its groups of lanes take the heads in turn.  The four
+// warp takes a token, its groups of lanes the token's heads.  The four
 // angles of a lane belong to all heads of the token: the groups work them out
 // between them, one each at d = 64.
+#include <algorithm>
+
 #include "lion_internal.h"
 #include "ssm_common.cuh"
 
@@ -29,32 +31,40 @@ struct QkP {
   float* part;             // [CTA][2][d]
   long long x_ld[2];
   long long tokens;
+  unsigned per;            // items a token
   int L, H[2], d, rp;      // rp: lanes of a head whose values turn (rot / 8)
   int interleaved;
   float inv_n, eps;
 };
 
-// Four consecutive values; wide: p lies on four values' size.
+// A lane's eight values of a head as they lie in memory: runs of four at a and
+// b.  WIDE: a run lies on its size.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+};
 template <bool WIDE>
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  if (WIDE) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = p[e];
-  }
+__device__ __forceinline__ uint2 run_of(const __nv_bfloat16* p) {
+  if (WIDE) return *reinterpret_cast<const uint2*>(p);
+  const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 template <bool WIDE>
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
-  if (WIDE) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p);
-    const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __bfloat162float(p[e]);
-  }
+__device__ __forceinline__ float4 run_of(const float* p) {
+  return WIDE ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+}
+__device__ __forceinline__ void values(uint2 r, float* v) {
+  const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void values(float4 r, float* v) {
+  v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
 }
 template <bool WIDE>
 __device__ __forceinline__ void store4(float* p, const float* v) {
@@ -145,122 +155,175 @@ __device__ __forceinline__ float head_sum(float x) {
   return x;
 }
 
+// Heads a lane has under way: some 48 registers of raw values, this item's and
+// the next one's.
+template <typename T, bool BWD>
+constexpr int heads_at_once() {
+  return sizeof(T) == 2 ? (BWD ? 3 : 6) : (BWD ? 2 : 3);
+}
+
+// An item is a token's heads as far as a warp has them under way at once; its
+// values are read while the item before it is worked on.
 template <typename T, int LPH, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
-  constexpr int NG = 32 / LPH;
-  constexpr int U = BWD ? 2 : 4;   // heads a lane has under way
+  constexpr int NG = 32 / LPH, U = heads_at_once<T, BWD>();
+  __shared__ __align__(16) float sw[2][8 * LPH];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int p = lane & (LPH - 1), g = lane / LPH;
   const bool there = 8 * p < q.d, turns = p < q.rp;
   const int a = q.interleaved || !turns ? 8 * p : 4 * p, b = q.interleaved || !turns ? 8 * p + 4 : 4 * (p + q.rp);
-  float w[2][8], dw[2][8];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[m][e] = q.w[m] && there ? q.w[m][(e < 4 ? a : b - 4) + e] : 1.f;
-      dw[m][e] = 0.f;
-    }
+  for (int i = threadIdx.x; i < 2 * 8 * LPH; i += 32 * kWarps) {
+    const int m = i / (8 * LPH), e = i % (8 * LPH);
+    sw[m][e] = q.w[m] && e < q.d ? q.w[m][e] : 1.f;
+  }
   Turn<LPH> turn;
   turn.init(q, lane, p);
+  float dw[BWD ? 2 : 1][8] = {};
   const int heads = q.H[0] + q.H[1];
-  for (long long t = (long long)blockIdx.x * kWarps + warp; t < q.tokens; t += (long long)gridDim.x * kWarps) {
-    float c[4], s[4];
-    if (q.rp) turn.at(q.positions ? q.positions[t] : (int)(t % q.L), p, c, s);
-    for (int h0 = g; h0 < heads + g; h0 += NG * U) {   // all lanes go round equally often
-      float x[U][8], dy[BWD ? U : 1][8];
+  const unsigned per = q.per;
+  __syncthreads();
+
+  Raw<T> x[U], dy[BWD ? U : 1];
+  const auto fetch = [&](long long t, unsigned part) {
+    const int h0 = (int)part * NG * U + g;
+    const T* xq = static_cast<const T*>(q.x[0]) + t * q.x_ld[0];
+    const T* xk = static_cast<const T*>(q.x[1]) + t * q.x_ld[1] - (long long)q.H[0] * q.d;
+    const T* dq = static_cast<const T*>(q.dy[0]) + t * q.H[0] * q.d;
+    const T* dk = static_cast<const T*>(q.dy[1]) + (t * q.H[1] - q.H[0]) * q.d;
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int h = h0 + i * NG;
-        const int m = h >= q.H[0], hm = m ? h - q.H[0] : h;
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * NG;
+      if (there && h < heads) {
+        const T* s = (h < q.H[0] ? xq : xk) + (long long)h * q.d;
+        x[i].a = run_of<WIDE>(s + a);
+        x[i].b = run_of<WIDE>(s + b);
+        if (BWD) {
+          const T* d = (h < q.H[0] ? dq : dk) + (long long)h * q.d;
+          dy[i].a = run_of<WIDE>(d + a);
+          dy[i].b = run_of<WIDE>(d + b);
+        }
+      } else {
+        x[i] = Raw<T>();
+        if (BWD) dy[i] = Raw<T>();
+      }
+    }
+  };
+  const unsigned hop = gridDim.x * kWarps, hop_t = hop / per, hop_part = hop % per;
+  const unsigned first = blockIdx.x * kWarps + warp;
+  long long tn = first / per;
+  unsigned pn = first % per;
+  if (tn < q.tokens) fetch(tn, pn);
+  while (tn < q.tokens) {
+    const long long t = tn;
+    const int h0 = (int)pn * NG * U + g;
+    Raw<T> xc[U], dc[BWD ? U : 1];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      xc[i] = x[i];
+      if (BWD) dc[i] = dy[i];
+    }
+    tn += hop_t;
+    pn += hop_part;
+    if (pn >= per) {
+      pn -= per;
+      ++tn;
+    }
+    if (tn < q.tokens) fetch(tn, pn);
+    float c[4], s[4];
+    if (q.rp) turn.at(q.positions ? q.positions[t] : q.tokens >> 32 ? (int)(t % q.L) : (int)((unsigned)t % (unsigned)q.L), p, c, s);
+    T* yq = static_cast<T*>(q.y[0]) + t * q.H[0] * q.d;
+    T* yk = static_cast<T*>(q.y[1]) + (t * q.H[1] - q.H[0]) * q.d;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * NG;
+      if (h - g >= heads) break;   // of all lanes
+      const int m = h >= q.H[0];
+      float v[8], w[8];
+      values(xc[i].a, v);
+      values(xc[i].b, v + 4);
+      values(*reinterpret_cast<const float4*>(&sw[m][a]), w);
+      values(*reinterpret_cast<const float4*>(&sw[m][b]), w + 4);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+      const float r = 1.f / sqrtf(fmaf(head_sum<LPH>(ss), q.inv_n, q.eps));
+      float o[8];
+      if (!BWD) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v[e] * r * w[e];
+        if (turns) turn8(o, c, s, q.interleaved, 1.f);
+      } else {
+        float z[8];
+        values(dc[i].a, z);
+        values(dc[i].b, z + 4);
+        if (turns) turn8(z, c, s, q.interleaved, -1.f);
+        float gx = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[i][e] = 0.f;
-          if (BWD) dy[i][e] = 0.f;
+          o[e] = z[e] * w[e];
+          gx = fmaf(o[e], v[e], gx);
         }
-        if (there && h < heads) {
-          const T* src = static_cast<const T*>(q.x[m]) + t * q.x_ld[m] + (long long)hm * q.d;
-          load4<WIDE>(src + a, x[i]);
-          load4<WIDE>(src + b, x[i] + 4);
-          if (BWD) {
-            const T* d = static_cast<const T*>(q.dy[m]) + (t * q.H[m] + hm) * q.d;
-            load4<WIDE>(d + a, dy[i]);
-            load4<WIDE>(d + b, dy[i] + 4);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int h = h0 + i * NG;
-        if (h - g >= heads) break;   // of all lanes
-        const int m = h >= q.H[0], hm = m ? h - q.H[0] : h;
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[i][e], x[i][e], ss);
-        const float r = 1.f / sqrtf(fmaf(head_sum<LPH>(ss), q.inv_n, q.eps));
-        float o[8];
-        if (!BWD) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = x[i][e] * r * (m ? w[1][e] : w[0][e]);
-          if (turns) turn8(o, c, s, q.interleaved, 1.f);
-        } else {
-          if (turns) turn8(dy[i], c, s, q.interleaved, -1.f);
-          float gx = 0.f;
+        if (q.part && h < heads) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            o[e] = dy[i][e] * (m ? w[1][e] : w[0][e]);
-            gx = fmaf(o[e], x[i][e], gx);
+            const float y = z[e] * (v[e] * r);
+            dw[0][e] += m ? 0.f : y;
+            dw[BWD ? 1 : 0][e] += m ? y : 0.f;
           }
-          if (q.part && h < heads) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float z = dy[i][e] * (x[i][e] * r);
-              dw[0][e] += m ? 0.f : z;
-              dw[1][e] += m ? z : 0.f;
-            }
-          }
-          const float k = head_sum<LPH>(gx) * q.inv_n * r * r;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-k, x[i][e], o[e]);
         }
-        if (there && h < heads) {
-          T* dst = static_cast<T*>(q.y[m]) + (t * q.H[m] + hm) * q.d;
-          store4<WIDE>(dst + a, o);
-          store4<WIDE>(dst + b, o + 4);
-        }
+        const float k = head_sum<LPH>(gx) * q.inv_n * r * r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-k, v[e], o[e]);
+      }
+      if (there && h < heads) {
+        T* dst = (m ? yk : yq) + (long long)h * q.d;
+        store4<WIDE>(dst + a, o);
+        store4<WIDE>(dst + b, o + 4);
       }
     }
   }
-  if (!BWD || !q.part) return;
-  __shared__ float sh[kWarps][2][8 * LPH];
+  if constexpr (BWD) {
+    if (!q.part) return;
+    __shared__ float sh[kWarps][2][8 * LPH];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 8; ++e) {
 #pragma unroll
-      for (int o = 16; o >= LPH; o >>= 1) dw[m][e] += __shfl_xor_sync(0xffffffffu, dw[m][e], o);
-      if (g == 0 && there) sh[warp][m][(e < 4 ? a : b - 4) + e] = dw[m][e];
+        for (int o = 16; o >= LPH; o >>= 1) dw[m][e] += __shfl_xor_sync(0xffffffffu, dw[m][e], o);
+        if (g == 0 && there) sh[warp][m][(e < 4 ? a : b - 4) + e] = dw[m][e];
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * q.d; i += 32 * kWarps) {
+      const int m = i >= q.d, e = m ? i - q.d : i;
+      float v = sh[0][m][e];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) v += sh[k][m][e];
+      q.part[(size_t)blockIdx.x * 2 * q.d + i] = v;
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * q.d; i += 32 * kWarps) {
-    const int m = i >= q.d, e = m ? i - q.d : i;
-    float v = sh[0][m][e];
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) v += sh[k][m][e];
-    q.part[(size_t)blockIdx.x * 2 * q.d + i] = v;
   }
 }
 
-// CTAs: a token a warp while that fills the SMs, else eight CTAs an SM that go
-// round (the angles' frequencies and the weights are set up once a warp).
-int qknorm_ctas(long long tokens) {
-  const long long want = (tokens + kWarps - 1) / kWarps;
-  return (int)(want < 8 * kSmCount ? want : 8 * kSmCount);
+int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+// Warps' items a token.
+int items_of(int heads, int d, int at_once) {
+  const int by = 32 / lanes_of(d) * at_once;
+  return (heads + by - 1) / by;
+}
+// CTAs: an item a warp while that fills the SMs, else four CTAs an SM that go
+// round, as registers have room for (the angles' frequencies are set up once a warp).
+int qknorm_ctas(long long items) {
+  const long long want = (items + kWarps - 1) / kWarps;
+  return (int)(want < 4 * kSmCount ? want : 4 * kSmCount);
+}
+int bwd_at_once(int dtype) {
+  return dtype == DT_BF16 ? heads_at_once<__nv_bfloat16, true>() : heads_at_once<float, true>();
 }
 
 template <typename T, bool BWD>
-cudaError_t run(const QkP& q, bool wide, cudaStream_t s) {
-  const dim3 grid(qknorm_ctas(q.tokens)), block(32 * kWarps);
+cudaError_t run(QkP q, bool wide, cudaStream_t s) {
+  q.per = items_of(q.H[0] + q.H[1], q.d, heads_at_once<T, BWD>());
+  const dim3 grid(qknorm_ctas(q.tokens * q.per)), block(32 * kWarps);
   if (q.d <= 64)
     wide ? qknorm_kernel<T, 8, true, BWD><<<grid, block, 0, s>>>(q) : qknorm_kernel<T, 8, false, BWD><<<grid, block, 0, s>>>(q);
   else if (q.d <= 128)
@@ -309,8 +372,10 @@ cudaError_t launch_qknorm_fwd(const lion_qknorm_args& a, cudaStream_t s) {
   return a.dtype == DT_BF16 ? run<__nv_bfloat16, false>(q, wide, s) : run<float, false>(q, wide, s);
 }
 
+// Of the type that makes more items; they go round on as many CTAs at most.
 size_t qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d) {
-  return sizeof(float) * 2 * d * (size_t)qknorm_ctas((long long)B * L);
+  const int per = items_of(Hq + Hk, d, std::min(bwd_at_once(DT_BF16), bwd_at_once(DT_FP32)));
+  return sizeof(float) * 2 * d * (size_t)qknorm_ctas((long long)B * L * per);
 }
 
 cudaError_t launch_qknorm_bwd(const lion_qknorm_bwd_args& a, void* ws, cudaStream_t s) {
@@ -325,7 +390,8 @@ cudaError_t launch_qknorm_bwd(const lion_qknorm_bwd_args& a, void* ws, cudaStrea
                     on4(a.dq_out, 0, es) && on4(a.dk_out, 0, es);
   const cudaError_t e = a.dtype == DT_BF16 ? run<__nv_bfloat16, true>(q, wide, s) : run<float, true>(q, wide, s);
   if (e != cudaSuccess || !ws) return e;
-  return launch_sum_parts(q.part, qknorm_ctas(q.tokens), 2LL * a.d, a.d, a.dq_weight, a.d, a.dk_weight, 0, nullptr, s);
+  const int ctas = qknorm_ctas(q.tokens * items_of(a.Hq + a.Hk, a.d, bwd_at_once(a.dtype)));
+  return launch_sum_parts(q.part, ctas, 2LL * a.d, a.d, a.dq_weight, a.d, a.dk_weight, 0, nullptr, s);
 }
 
 }  // namespace lion

@@ -177,15 +177,13 @@ def test_delta(B, L, Hk, Hv, dk, dv, lens, state, reverse, decay, dtype):
     how = dict(scale=scale, h0=h0.cuda() if state else None, reverse=reverse,
                lengths=torch.tensor(lens, dtype=torch.int32, device="cuda") if lens else None)
     f = delta.delta_fwd(**dev, **how, return_state=True, save=True)
-    _check("out", f.out, r["out"], r["~out"])
-    _check("h", f.h, r["h"], r["~h"])
     g = delta.delta_bwd(dout.cuda(), **dev, **how, saved=f.saved)
-    for x in ("dq", "dk", "dv", "dg", "dbeta"):
-        _check(x, getattr(g, x), r[x], r["~" + x])
-    if state:
-        _check("dh0", g.dh0, r["dh0"], r["~dh0"])
-    else:
-        assert g.dh0 is None
+    assert (g.dh0 is not None) == state
+    for x, y in (("out", f.out), ("h", f.h), *((x, getattr(g, x)) for x in ("dq", "dk", "dv", "dg", "dbeta", "dh0"))):
+        if y is not None:
+            _check(x, y, r[x], r["~" + x])
+            if x in ("out", "dv") or y.dtype == torch.float32:
+                _exact_enough(x, y, r[x])
     # without what the forward kept, into workspaces of the caller's, and again
     plain = delta.delta_fwd(**dev, **how, return_state=True)
     assert plain.saved is None and _equal(plain[:2], f[:2])
@@ -197,11 +195,20 @@ def test_delta(B, L, Hk, Hv, dk, dv, lens, state, reverse, decay, dtype):
     assert _equal(delta.delta_fwd(**dev, **how, workspace=ws)[:1], f[:1])
 
 
-@pytest.mark.parametrize("dtype,limit", (("bf16", 5e-3), ("fp32", 1e-5)))
+def _exact_enough(name, got, want):
+    """What the bounds of single values, in which all errors add up, leave open.  The 2-norm of the error, where
+    roundings add as their squares do: bfloat16 results are five roundings of at most 2^-9 off (four factors' and their
+    own), 2^-9 sqrt(5) of the norm of their terms, float32 results, a bfloat16 call's states among them, 1e-5.  The
+    terms of dq, dk, dg and dbeta come from both sides of a token and may cancel where there are two or three of them;
+    of many tokens' sums they are as large as the result."""
+    off = np.linalg.norm(_f64(got) - want)
+    limit = 1e-5 if got.dtype == torch.float32 else 5 ** 0.5 * 2.0 ** -9
+    assert off <= limit * np.linalg.norm(want), (name, off / np.linalg.norm(want))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "fp32"))
 @pytest.mark.parametrize("L,dk,dv", ((513, 64, 64), (300, 128, 128)))
-def test_delta_is_as_exact_as_its_type(L, dk, dv, dtype, limit):
-    """The 2-norm of the error: bfloat16 results are a few roundings of 2^-9 / sqrt(3) off (limit: three of them and the
-    last), float32 ones, the states of bfloat16 calls among them, 1e-5."""
+def test_delta_over_many_chunks(L, dk, dv, dtype):
     a, h0, dout = _inputs(2, L, 1, 2, dk, dv, dtype, 11)
     r = ref.delta(**{x: _f64(y) for x, y in a.items()}, scale=dk ** -0.5, h0=_f64(h0), dout=_f64(dout))
     dev = {x: y.cuda() for x, y in a.items()}
@@ -209,8 +216,7 @@ def test_delta_is_as_exact_as_its_type(L, dk, dv, dtype, limit):
     g = delta.delta_bwd(dout.cuda(), **dev, h0=h0.cuda(), saved=f.saved)
     for x, y in (("out", f.out), ("h", f.h), ("dq", g.dq), ("dk", g.dk), ("dv", g.dv), ("dg", g.dg),
                  ("dbeta", g.dbeta), ("dh0", g.dh0)):
-        off = np.linalg.norm(_f64(y) - r[x]) / np.linalg.norm(r[x])
-        assert off <= (1e-5 if y.dtype == torch.float32 else limit), (x, off)
+        _exact_enough(x, y, r[x])
 
 
 @pytest.mark.parametrize("dtype", ("bf16", "fp32"))
