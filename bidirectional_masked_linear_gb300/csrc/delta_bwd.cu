@@ -75,58 +75,51 @@ __global__ void __launch_bounds__(32) delta_back_prep_kernel(const DeltaP p) {
 //   X^T = dO^T P + beta e^(G_C - G) o (dS'^T K^T);  dR^T = X^T T
 //   dS^T = e^G_C dS'^T + (scale e^G o dO)^T Q - X^T W
 
-constexpr int kBackThreads = 256;
-
 template <typename T, int DK>
 struct Back {
   typedef ChunkData<T, DK, true, sizeof(T) == 4> D;
   typedef Stage<T, DK, D::coef, D::bytes> L;
-  typedef Swap<T, DK, 0> X;
   static constexpr int stages = sizeof(T) == 4 ? 2 : 3;
-  static constexpr int swap = stages * L::bytes, out = swap + 4 * X::bytes, smem = out + 8 * out_bytes<T>();
+  static constexpr int smem = stages * L::bytes + 4 * out_bytes<T>();
 };
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(kBackThreads) delta_back_kernel(const DeltaP p) {
+__global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
   typedef Back<T, DK> C;
   typedef typename C::D D;
   typedef typename C::L L;
-  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, PER = kStateChunk / kChunk, N = DK / 16;
+  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, PER = kStateChunk / kChunk;
   constexpr bool KQ = L::KQ;
   extern __shared__ __align__(128) unsigned char smem[];
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
-  const int pair = w & 3, side = w >> 2;
-  unsigned char* buf = smem + C::out + w * out_bytes<T>();
-  const unsigned xs = base + C::swap + pair * C::X::bytes, xx = xs + C::X::state;   // dS^T, X^T
+  unsigned char* buf = smem + NST * L::bytes + w * out_bytes<T>();
   const long long bh = blockIdx.x / p.slices;
   const int slice = (int)(blockIdx.x - bh * p.slices);
   const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
-  const int m0 = slice * kSlice + 16 * pair, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
+  const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
   const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xv = rows_of<T>(p, p.dv_out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
   const char* chunk = p.chunks + bh * p.nc * D::bytes;
   const long long at_last = bh * p.nc + nc - 1;
-  const float4* Z = reinterpret_cast<const float4*>(p.U) + (at_last * p.dvp + m0) * (kChunk / 4) + 64 * side + lane;
+  const float4* Z = reinterpret_cast<const float4*>(p.U) + (at_last * p.dvp + m0) * (kChunk / 4) + lane;
   const uint4* dO = p.dO + (at_last * (p.dvp / 16) + m0 / 16) * 2 * NS * 32 + lane;
 
-  float s[N][4] = {};   // dS^T, this side's dk
-  if (cols > 0) put_state<DK, NS>(xs, s, side, lane);
+  float s[DK / 8][4] = {};   // dS^T
   wait_prior();
 #pragma unroll
   for (int st = 0; st < NST - 1; ++st) {
     const int c = nc - 1 - st;
-    if (c >= 0)
-      L::template load<kBackThreads>(p, base + st * L::bytes, chunk + (long long)c * D::bytes, xq, xk, c * kChunk, n, tid);
+    if (c >= 0) L::template load<128>(p, base + st * L::bytes, chunk + (long long)c * D::bytes, xq, xk, c * kChunk, n, tid);
     copy_commit();
   }
-  float4 znext[2];
+  float4 znext[4];
   uint4 onext[2][NS];
   if (cols > 0 && nc > 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) znext[e] = Z[32 * e];
+    for (int e = 0; e < 4; ++e) znext[e] = Z[32 * e];
 #pragma unroll
     for (int e = 0; e < 2 * NS; ++e) onext[e / NS][e % NS] = dO[32 * e];
   }
@@ -135,72 +128,250 @@ __global__ void __launch_bounds__(kBackThreads) delta_back_kernel(const DeltaP p
     copy_wait<NST - 2>();
     __syncthreads();
     if (ahead >= 0)
-      L::template load<kBackThreads>(p, base + (step + NST - 1) % NST * L::bytes, chunk + (long long)ahead * D::bytes, xq, xk,
-                                     ahead * kChunk, n, tid);
+      L::template load<128>(p, base + (step + NST - 1) % NST * L::bytes, chunk + (long long)ahead * D::bytes, xq, xk,
+                            ahead * kChunk, n, tid);
     copy_commit();
     if (cols <= 0) continue;
     const unsigned st = base + step % NST * L::bytes;
     const float* coef = reinterpret_cast<const float*>(smem + step % NST * L::bytes + L::at(D::coef));
     if (step == 0 || c % PER == PER - 1)
-      store_blocks<N, DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK + side * N * 64, s, lane);
+      store_blocks<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK, s, lane);
 
-    // this side's tokens of X^T
-    float x[2][4] = {};
+    float4 z[4];
+    unsigned g[2][NS][4];
 #pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      unsigned a[NS][4];
+    for (int e = 0; e < 4; ++e) z[e] = znext[e];
 #pragma unroll
-      for (int j = 0; j < NS; ++j) get_a(xs + (ks * NS + j) * 512, a[j], lane);
-      mma_tile<NS, NI, false>(x[0], x[1], a, st + L::k + at_b_rows_n<DK, KQ>(16 * side, 16 * ks, lane), L::row);
-    }
-#pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      const float2 l = *reinterpret_cast<const float2*>(coef + kChunk + 16 * side + 8 * nb + 2 * q4);
-      x[nb][0] = fmaf(l.x, x[nb][0], znext[nb].x);
-      x[nb][1] = fmaf(l.y, x[nb][1], znext[nb].y);
-      x[nb][2] = fmaf(l.x, x[nb][2], znext[nb].z);
-      x[nb][3] = fmaf(l.y, x[nb][3], znext[nb].w);
-    }
-    unsigned mine[NS][4];
-    to_a<NS>(x[0], x[1], mine);
-#pragma unroll
-    for (int j = 0; j < NS; ++j) put_a(xx + (side * NS + j) * 512, mine[j], lane);
-    pair_sync(pair);
-    // dS^T, this side's dk; dR^T, this side's tokens
-    scale_by(s, coef[2 * kChunk]);
-    float y[2][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      unsigned a[NS][4], g[NS][4];
-#pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        get_a(xx + (ks * NS + j) * 512, a[j], lane);
-        g[j][0] = onext[ks][j].x; g[j][1] = onext[ks][j].y; g[j][2] = onext[ks][j].z; g[j][3] = onext[ks][j].w;
-      }
-#pragma unroll
-      for (int nn = 0; nn < N / 2; ++nn) {
-        const int k0 = side * (DK / 2) + 16 * nn;
-        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], g, st + L::q + at_b_rows_k<DK, KQ>(16 * ks, k0, lane), L::row);
-        mma_tile<NS, NS, true>(s[2 * nn], s[2 * nn + 1], a, st + L::at(D::W) + at_b_rows_k<DK, true>(16 * ks, k0, lane), L::row);
-      }
-      if (side <= ks)
-        mma_tile<NS, NS, true>(y[0], y[1], a, st + L::at(D::Tm) + at_b_rows_k<kChunk, true>(16 * ks, 16 * side, lane), kTile);
+    for (int e = 0; e < 2 * NS; ++e) {
+      const uint4 v = onext[e / NS][e % NS];
+      unsigned(&d)[4] = g[e / NS][e % NS];
+      d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
     }
     if (c > 0) {
       Z -= p.dvp * (kChunk / 4);
       dO -= (p.dvp / 16) * 2 * NS * 32;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) znext[e] = Z[32 * e];
+      for (int e = 0; e < 4; ++e) znext[e] = Z[32 * e];
 #pragma unroll
       for (int e = 0; e < 2 * NS; ++e) onext[e / NS][e % NS] = dO[32 * e];
     }
-    put_state<DK, NS>(xs, s, side, lane);
-    store_rows(buf, y, lane, cols, p.dv_wide, xv, c * kChunk + 16 * side, n);
+    // X^T
+    float x[4][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      unsigned a[NS][4];
+      to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
+#pragma unroll
+      for (int np = 0; np < 2; ++np)
+        mma_tile<NS, NI, false>(x[2 * np], x[2 * np + 1], a, st + L::k + at_b_rows_n<DK, KQ>(16 * np, 16 * ks, lane), L::row);
+    }
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      const float2 l = *reinterpret_cast<const float2*>(coef + kChunk + 8 * nb + 2 * q4);
+      x[nb][0] = fmaf(l.x, x[nb][0], z[nb].x);
+      x[nb][1] = fmaf(l.y, x[nb][1], z[nb].y);
+      x[nb][2] = fmaf(l.x, x[nb][2], z[nb].z);
+      x[nb][3] = fmaf(l.y, x[nb][3], z[nb].w);
+    }
+    // dS^T and dR^T
+    scale_by(s, coef[2 * kChunk]);
+    float y[4][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      unsigned a[NS][4];
+      to_a<NS>(x[2 * ks], x[2 * ks + 1], a);
+#pragma unroll
+      for (int nn = 0; nn < DK / 16; ++nn) {
+        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], g[ks], st + L::q + at_b_rows_k<DK, KQ>(16 * ks, 16 * nn, lane), L::row);
+        mma_tile<NS, NS, true>(s[2 * nn], s[2 * nn + 1], a,
+                               st + L::at(D::W) + at_b_rows_k<DK, true>(16 * ks, 16 * nn, lane), L::row);
+      }
+#pragma unroll
+      for (int np = 0; np <= ks; ++np)
+        mma_tile<NS, NS, true>(y[2 * np], y[2 * np + 1], a,
+                               st + L::at(D::Tm) + at_b_rows_k<kChunk, true>(16 * ks, 16 * np, lane), kTile);
+    }
+    const int i = c * kChunk + lane;
+    store_rows(buf, y, lane, cols, p.dv_wide, i < n ? const_cast<T*>(xv.at(i)) : nullptr);
   }
   copy_wait<0>();
   if (cols <= 0) return;
-  if (p.dh0) keep_state<N>(p, p.dh0, bh, m0, cols, side * (DK / 2), lane, s);
-  zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, side, lane);
+  if (p.dh0) keep_state<DK>(p, p.dh0, bh, m0, cols, lane, s);
+  zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, lane);
+}
+
+// The same in bfloat16 with a helper to each warp, which has the loads, dR, what
+// the other gradients take, and dO's part of the next dS, ready when the warp
+// has X.
+
+template <int DK>
+struct BackTeam {
+  typedef __nv_bfloat16 T;
+  typedef ChunkData<T, DK, true, false> D;
+  static constexpr int row = kChunk * DK * 2;
+  // a stage: k, q, coefficients, -W and T, the slice of P^T dO
+  static constexpr int k = 0, q = row, coef = 2 * row, W = coef + (D::W - D::coef), Tm = W + (D::Tm - D::W);
+  static constexpr int Z = Tm + (D::bytes - D::Tm), bytes = Z + kSlice * kChunk * 4;
+  static constexpr int stages = 3;
+  static constexpr int S = 0, X = DK / 16 * 512, swap = X + 4 * 512;   // a warp's buffer to its helper
+  static constexpr int Y = DK / 8 * 512;                               // and back: dO's part of dS^T
+  static constexpr int swaps = stages * bytes, ys = swaps + 2 * 4 * swap, out = ys + 4 * Y;
+  static constexpr int smem = out + 4 * out_bytes<T>();
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const DeltaP p) {
+  typedef __nv_bfloat16 T;
+  typedef BackTeam<DK> C;
+  typedef typename C::D D;
+  constexpr int NST = C::stages, NS = 2, PER = kStateChunk / kChunk;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const unsigned base = shared_at(smem);
+  const int tid = threadIdx.x & 127, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
+  const bool helper = threadIdx.x >= 128;
+  const long long bh = blockIdx.x / p.slices;
+  const int slice = (int)(blockIdx.x - bh * p.slices);
+  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
+  const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
+  const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer 4 swaps behind
+  const unsigned ys = base + C::ys + w * C::Y;
+  wait_prior();
+  if (helper) {
+    const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
+    const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
+    const Rows<T> xv = rows_of<T>(p, p.dv_out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
+    const char* chunks = p.chunks + bh * p.nc * D::bytes;
+    const float* Zs = p.U + (bh * p.nc * p.dvp + slice * kSlice) * kChunk;
+    const uint4* dO = p.dO + (bh * p.nc * (p.dvp / 16) + m0 / 16) * 2 * NS * 32 + lane;
+    const int rows = p.dvp - slice * kSlice < kSlice ? p.dvp - slice * kSlice : kSlice;
+    unsigned char* buf = smem + C::out + w * out_bytes<T>();
+    const auto load = [&](int i) {   // the i-th chunk from the end
+      const int c = nc - 1 - i;
+      const unsigned st = base + i % NST * C::bytes;
+      load_tile<DK, kChunk, 128>(st + C::k, 0, xk, c * kChunk, n, p.dk, p.k_wide, tid);
+      load_tile<DK, kChunk, 128>(st + C::q, 0, xq, c * kChunk, n, p.dk, p.q_wide, tid);
+      copy_block<D::bytes - D::coef, 128>(st + C::coef, chunks + (long long)c * D::bytes + D::coef, tid);
+      copy_slice<128>(st + C::Z, Zs + (long long)c * p.dvp * kChunk, rows, tid);
+    };
+    uint4 g[2][NS];
+    const auto fetch = [&](int i) {
+      const uint4* s = dO + (long long)(nc - 1 - i) * (p.dvp / 16) * 2 * NS * 32;
+#pragma unroll
+      for (int e = 0; e < 2 * NS; ++e) g[e / NS][e % NS] = s[32 * e];
+    };
+    if (nc > 0) {
+      load(0);
+      if (cols > 0) fetch(0);
+    }
+    copy_commit();
+    for (int i = 0; i <= nc; ++i) {
+      copy_wait<0>();
+      __syncthreads();
+      if (i + 1 < nc) load(i + 1);
+      copy_commit();
+      if (i < nc && cols > 0) {   // (scale e^G o dO)^T Q
+        const unsigned st = base + i % NST * C::bytes;
+        float y[DK / 8][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          unsigned a[NS][4];
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            a[j][0] = g[ks][j].x; a[j][1] = g[ks][j].y; a[j][2] = g[ks][j].z; a[j][3] = g[ks][j].w;
+          }
+#pragma unroll
+          for (int nn = 0; nn < DK / 16; ++nn)
+            mma_tile<NS, 1, true>(y[2 * nn], y[2 * nn + 1], a, st + C::q + at_b_rows_k<DK>(16 * ks, 16 * nn, lane), 0);
+        }
+#pragma unroll
+        for (int nb = 0; nb < DK / 8; ++nb)
+          asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(ys + nb * 512 + 16 * lane), "f"(y[nb][0]), "f"(y[nb][1]),
+                       "f"(y[nb][2]), "f"(y[nb][3])
+                       : "memory");
+        asm volatile("barrier.cta.arrive %0, 64;" ::"r"(1 + w) : "memory");
+        if (i + 1 < nc) fetch(i + 1);
+      }
+      if (i == 0 || cols <= 0) continue;
+      const int j = i - 1, c = nc - 1 - j;
+      const unsigned st = base + j % NST * C::bytes, x = swap + (j & 1) * 4 * C::swap;
+      if (j == 0 || c % PER == PER - 1) {
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+          unsigned a[4];
+          get_a(x + C::S + ks * 512, a, lane);
+          store_a<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK + ks * 128, a, lane);
+        }
+      }
+      float y[4][4] = {};   // dR^T
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        unsigned a[NS][4];
+#pragma unroll
+        for (int e = 0; e < NS; ++e) get_a(x + C::X + (ks * NS + e) * 512, a[e], lane);
+#pragma unroll
+        for (int np = 0; np <= ks; ++np)
+          mma_tile<NS, NS, true>(y[2 * np], y[2 * np + 1], a,
+                                 st + C::Tm + at_b_rows_k<kChunk, true>(16 * ks, 16 * np, lane), kTile);
+      }
+      const int t = c * kChunk + lane;
+      store_rows(buf, y, lane, cols, p.dv_wide, t < n ? const_cast<T*>(xv.at(t)) : nullptr);
+    }
+    if (cols > 0) zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, lane);
+    return;
+  }
+  float s[DK / 8][4] = {};   // dS^T
+  for (int i = 0; i <= nc; ++i) {
+    __syncthreads();
+    if (i == nc || cols <= 0) continue;
+    const unsigned st = base + i % NST * C::bytes, x = swap + (i & 1) * 4 * C::swap;
+    const float* coef = reinterpret_cast<const float*>(smem + i % NST * C::bytes + C::coef);
+    // X^T
+    float r[4][4] = {};
+    unsigned plain[DK / 16][4], a[2][NS][4];   // to the helper at the end, as in the forward walk
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      unsigned d[NS][4];
+      to_a<NS>(s[2 * ks], s[2 * ks + 1], d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) plain[ks][e] = d[0][e];
+#pragma unroll
+      for (int np = 0; np < 2; ++np)
+        mma_tile<NS, 1, false>(r[2 * np], r[2 * np + 1], d, st + C::k + at_b_rows_n<DK>(16 * np, 16 * ks, lane), 0);
+    }
+    scale_by(s, coef[2 * kChunk]);
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      const float2 l = *reinterpret_cast<const float2*>(coef + kChunk + 8 * nb + 2 * q4);
+      const float4 z = get_f4(st + C::Z + (w * 4 + nb) * 512, lane);
+      r[nb][0] = fmaf(l.x, r[nb][0], z.x);
+      r[nb][1] = fmaf(l.y, r[nb][1], z.y);
+      r[nb][2] = fmaf(l.x, r[nb][2], z.z);
+      r[nb][3] = fmaf(l.y, r[nb][3], z.w);
+    }
+    // dS^T
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      to_a<NS>(r[2 * ks], r[2 * ks + 1], a[ks]);
+#pragma unroll
+      for (int nn = 0; nn < DK / 16; ++nn)
+        mma_tile<NS, NS, true>(s[2 * nn], s[2 * nn + 1], a[ks], st + C::W + at_b_rows_k<DK, true>(16 * ks, 16 * nn, lane), C::row);
+    }
+    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + w) : "memory");
+#pragma unroll
+    for (int nb = 0; nb < DK / 8; ++nb) {
+      const float4 y = get_f4(ys + nb * 512, lane);
+      s[nb][0] += y.x;
+      s[nb][1] += y.y;
+      s[nb][2] += y.z;
+      s[nb][3] += y.w;
+    }
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) put_a(x + C::S + ks * 512, plain[ks], lane);
+#pragma unroll
+    for (int e = 0; e < 2 * NS; ++e) put_a(x + C::X + e * 512, a[e / NS][e % NS], lane);
+  }
+  if (p.dh0 && cols > 0) keep_state<DK>(p, p.dh0, bh, m0, cols, lane, s);
 }
 
 // ------------------------------------------------------------- all other gradients
@@ -220,8 +391,9 @@ __global__ void __launch_bounds__(kBackThreads) delta_back_kernel(const DeltaP p
 // have to cancel in them, and beside a strong decay nothing else is left.  With
 // the pairs at hand, dbeta_j = k_j . W1_j + sum_{i >= j} p_ij.
 //
-// A warp has 16 rows and 32 of the dk columns, and of A and E every other (dk >
-// 64: every fourth) block of 16 columns.  R, dR, S and dS' come in the inputs'
+// A warp has 16 rows and half or a quarter of the dk columns, and of A and E
+// two blocks or one of 16 columns: eight warps and two CTAs an SM in bfloat16 up
+// to dk = 64 (16 x 4096 x 8 x 64: 269 us, sixteen warps 310), else sixteen.  R, dR, S and dS' come in the inputs'
 // type: in bfloat16 each is one rounding of 2^-9, as A beta and E beta are.
 
 constexpr int kPairRow = 65;   // floats of a row of p, of 64
@@ -229,7 +401,8 @@ constexpr int kPairRow = 65;   // floats of a row of p, of 64
 template <typename T, int DK, int DV>
 struct Grad {
   static constexpr int NI = Planes<T>::in;
-  static constexpr int groups = DK / 32, warps = 4 * groups, blocks = 4 / groups;
+  static constexpr int groups = DK == 64 && sizeof(T) == 2 ? 2 : 4, blocks = 4 / groups, threads = 128 * groups;
+  static constexpr int N = DK / 8 / groups;   // a warp's blocks of eight columns
   static constexpr int row = 64 * DK * 2, val = 64 * DV * 2, sta = DV * DK * 2, pair = 64 * 64 * 2;
   static constexpr int k = 0, q = NI * row, dO = 2 * NI * row, dR = dO + NI * val, R = dR + NI * val;
   static constexpr int S = R + NI * val, dS = S + NI * sta, end = dS + NI * sta;
@@ -281,13 +454,13 @@ __device__ __forceinline__ float quad_sum(float x) {
 }
 
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1) delta_grad_kernel(const DeltaP p) {
+__global__ void __launch_bounds__(Grad<T, DK, DV>::threads, Grad<T, DK, DV>::groups == 2 ? 2 : 1) delta_grad_kernel(const DeltaP p) {
   typedef Grad<T, DK, DV> G;
-  constexpr int NI = G::NI, THREADS = 32 * G::warps, NQ = G::groups;
+  constexpr int NI = G::NI, THREADS = G::threads, NQ = G::groups, N = G::N, PARTS = THREADS / 64;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float2 sG[64];
-  __shared__ float sGrown[64], sLeft[64], sBeta[64], sI[NQ][64], sW[NQ][64], sCol[4][64], sDot[G::warps];
-  __shared__ float sPart[4][64];
+  __shared__ float sGrown[64], sLeft[64], sBeta[64], sI[NQ][64], sW[NQ][64], sB[64], sCol[4][64], sDot[4 * NQ];
+  __shared__ float sPart[PARTS][64];
   __shared__ double sCarry;
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, rw = w & 3, grp = w >> 2;
@@ -356,7 +529,7 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
   __syncthreads();
   if (tid < 64) sLeft[tid] = ex2((float)(sCarry - Gs));
 
-  float dP[G::blocks][2][4] = {}, N[G::blocks][2][4] = {}, dq[4][4] = {}, f[4][4] = {}, W[4][4] = {};
+  float dP[G::blocks][2][4] = {}, dN[G::blocks][2][4] = {}, dq[N][4] = {}, f[N][4] = {}, W[N][4] = {};
   float dot = 0.f;
   wait_prior();
   for (int d0 = 0; d0 < p.dv; d0 += DV) {
@@ -395,18 +568,15 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < G::blocks; ++i) {
         const int np = grp + NQ * i;
-        if (np <= rw) {
-          const unsigned at =
-              base + G::R + (np >> 1) * (G::val / 2) + at_b_rows_k<kChunk, true>(16 * ks, 16 * (np & 1), lane);
-          mma_tile<NI, NI, true>(dP[i][0], dP[i][1], ao, at, G::val);
-          mma_tile<NI, NI, true>(N[i][0], N[i][1], ad, at, G::val);
-        }
+        if (np <= rw)
+          mma_tile2<NI, NI, true>(
+              dP[i][0], dP[i][1], ao, dN[i][0], dN[i][1], ad,
+              base + G::R + (np >> 1) * (G::val / 2) + at_b_rows_k<kChunk, true>(16 * ks, 16 * (np & 1), lane), G::val);
       }
 #pragma unroll
-      for (int nn = 0; nn < 2; ++nn) {
-        const unsigned at = base + at_b_rows_k<DK, true>(16 * ks, 32 * grp + 16 * nn, lane);
-        mma_tile<NI, NI, true>(dq[2 * nn], dq[2 * nn + 1], ao, at + G::S, G::sta);
-        mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], ad, at + G::S, G::sta);
+      for (int nn = 0; nn < N / 2; ++nn) {
+        const unsigned at = base + at_b_rows_k<DK, true>(16 * ks, 8 * N * grp + 16 * nn, lane);
+        mma_tile2<NI, NI, true>(dq[2 * nn], dq[2 * nn + 1], ao, f[2 * nn], f[2 * nn + 1], ad, at + G::S, G::sta);
         mma_tile<NI, NI, true>(W[2 * nn], W[2 * nn + 1], ar, at + G::dS, G::sta);
       }
     }
@@ -421,8 +591,8 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
     const float grown = sGrown[i], left = sLeft[i], beta = sBeta[i], gq = p.scale * grown;
     float si = 0.f, sw = 0.f;
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-      const unsigned at = base + unit_at<DK>(i, 4 * grp + nb) + 4 * q4;
+    for (int nb = 0; nb < N; ++nb) {
+      const unsigned at = base + unit_at<DK>(i, N * grp + nb) + 4 * q4;
       const float2 qv = plane_sum<NI>(at + G::q, G::row), kv = plane_sum<NI>(at + G::k, G::row);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -443,6 +613,17 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
     }
   }
   __syncthreads();   // the values' tiles are done with
+  if (tid < 64) {
+    float si = sI[0][tid], sw = sW[0][tid];
+#pragma unroll
+    for (int h = 1; h < NQ; ++h) {
+      si += sI[h][tid];
+      sw += sW[h][tid];
+    }
+    sI[0][tid] = si;
+    sB[tid] = sw;
+    sW[0][tid] = sw * sBeta[tid];
+  }
   float* pairs = reinterpret_cast<float*>(smem + G::pairs);
 #pragma unroll
   for (int i = 0; i < G::blocks; ++i) {
@@ -454,14 +635,13 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
       for (int ks = 0; ks < DK / 16; ++ks) {
         unsigned aq[NI][4], ak[NI][4];
         const unsigned aa = base + at_a_rows_m<DK>(16 * rw, 16 * ks, lane);
-        const unsigned bb = base + G::k + at_b_rows_n<DK>(16 * np, 16 * ks, lane);
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           ldsm(aq[j], aa + G::q + j * G::row);
           ldsm(ak[j], aa + G::k + j * G::row);
         }
-        mma_tile<NI, NI, false>(qk[0], qk[1], aq, bb, G::row);
-        mma_tile<NI, NI, false>(kk[0], kk[1], ak, bb, G::row);
+        mma_tile2<NI, NI, false>(qk[0], qk[1], aq, kk[0], kk[1], ak, base + G::k + at_b_rows_n<DK>(16 * np, 16 * ks, lane),
+                                 G::row);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -477,7 +657,7 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
           for (int e = 0; e < 2; ++e) {
             const float d = ex2(e ? (gi.x - gj.z) + (gi.y - gj.w) : (gi.x - gj.x) + (gi.y - gj.y));
             const float x = ii >= j + e ? p.scale * d * dP[i][h][2 * half + e] : 0.f;
-            const float y = ii > j + e ? -d * N[i][h][2 * half + e] : 0.f;
+            const float y = ii > j + e ? -d * dN[i][h][2 * half + e] : 0.f;
             const float v = fmaf(x, qk[h][2 * half + e], y * kk[h][2 * half + e]);
             pairs[ii * kPairRow + j + e] = v;
             col[2 * h + e] += v;
@@ -503,8 +683,8 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
     }
   }
   __syncthreads();   // A, E and p are there
-  if (tid < 256) {   // a row's sums of beta p up to each token, four threads a row
-    const int i = tid >> 2, j0 = 16 * (tid & 3);
+  if (NQ == 2 || rw >= 2) {   // a row's sums of beta p up to each token, four threads a row
+    const int i = (NQ == 2 ? tid : (rw - 2) * 32 + grp * 64 + lane) >> 2, j0 = 16 * (lane & 3);
     float* row = pairs + i * kPairRow + j0;
     float v[16], sum = 0.f;
 #pragma unroll
@@ -532,11 +712,9 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
         ldsm(ae[j], at + G::E);
       }
 #pragma unroll
-      for (int nn = 0; nn < 2; ++nn) {
-        const unsigned at = base + G::k + at_b_rows_k<DK>(16 * ks, 32 * grp + 16 * nn, lane);
-        mma_tile<NI, NI, true>(dq[2 * nn], dq[2 * nn + 1], aa, at, G::row);
-        mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], ae, at, G::row);
-      }
+      for (int nn = 0; nn < N / 2; ++nn)
+        mma_tile2<NI, NI, true>(dq[2 * nn], dq[2 * nn + 1], aa, f[2 * nn], f[2 * nn + 1], ae,
+                                base + G::k + at_b_rows_k<DK>(16 * ks, 8 * N * grp + 16 * nn, lane), G::row);
     }
     if (ks >= rw) {
       unsigned aa[NI][4], ae[NI][4];
@@ -547,48 +725,42 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
         ldsm_t(ae[j], at + G::E);
       }
 #pragma unroll
-      for (int nn = 0; nn < 2; ++nn) {
-        const unsigned at = base + at_b_rows_k<DK>(16 * ks, 32 * grp + 16 * nn, lane);
+      for (int nn = 0; nn < N / 2; ++nn) {
+        const unsigned at = base + at_b_rows_k<DK>(16 * ks, 8 * N * grp + 16 * nn, lane);
         mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], aa, at + G::q, G::row);
         mma_tile<NI, NI, true>(f[2 * nn], f[2 * nn + 1], ae, at + G::k, G::row);
       }
     }
   }
   __syncthreads();   // the sums of rows are there, and q and k done with
-  // dg's sums over 16 rows a thread
-  if (tid < 256) {
+  // dg's sums, some rows a thread
+  {
     const int t = tid & 63, part = tid >> 6;
     float sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      const int i = 16 * part + x;
-      float a = 0.f, bw = 0.f;
-#pragma unroll
-      for (int h = 0; h < NQ; ++h) {
-        a += sI[h][i];
-        bw += sW[h][i];
-      }
-      sum += i >= t ? a + pairs[i * kPairRow + t] : sBeta[i] * bw;
+    for (int x = 0; x < 64 / PARTS; ++x) {
+      const int i = 64 / PARTS * part + x;
+      sum += i >= t ? sI[0][i] + pairs[i * kPairRow + t] : sW[0][i];
     }
     sPart[part][t] = sum;
   }
   // dQ and dK through q's and k's place, for whole rows
   if (sizeof(T) == 2 && !p.dq_part) {
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb)
+    for (int nb = 0; nb < N; ++nb)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const unsigned at = base + unit_at<DK>(16 * rw + r + 8 * h, 4 * grp + nb) + 4 * q4;
+        const unsigned at = base + unit_at<DK>(16 * rw + r + 8 * h, N * grp + nb) + 4 * q4;
         put_pair(at + G::q, pack_bf16(dq[nb][2 * h], dq[nb][2 * h + 1]));
         put_pair(at + G::k, pack_bf16(f[nb][2 * h], f[nb][2 * h + 1]));
       }
   } else {
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb)
+    for (int nb = 0; nb < N; ++nb)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const long long t = token(16 * rw + r + 8 * h);
-        const int col = 32 * grp + 8 * nb + 2 * q4;
+        const int col = 8 * N * grp + 8 * nb + 2 * q4;
         if (t < 0 || col >= p.dk) continue;
         const float2 x = make_float2(dq[nb][2 * h], dq[nb][2 * h + 1]), y = make_float2(f[nb][2 * h], f[nb][2 * h + 1]);
         if (p.dq_part) {
@@ -628,11 +800,11 @@ __global__ void __launch_bounds__(32 * Grad<T, DK, DV>::warps, DK == 64 ? 2 : 1)
     if (i0 + tid < n) {
       float d = 0.f;
 #pragma unroll
-      for (int k = 0; k < G::warps; ++k) d += sDot[k];
-      dg = (sPart[0][tid] + sPart[1][tid]) + (sPart[2][tid] + sPart[3][tid]) + sGrown[63] * d;
-      db = (sCol[0][tid] + sCol[1][tid]) + (sCol[2][tid] + sCol[3][tid]);
+      for (int k = 0; k < 4 * NQ; ++k) d += sDot[k];
 #pragma unroll
-      for (int h = 0; h < NQ; ++h) db += sW[h][tid];
+      for (int k = 0; k < PARTS; ++k) dg += sPart[k][tid];
+      dg += sGrown[63] * d;
+      db = sB[tid] + ((sCol[0][tid] + sCol[1][tid]) + (sCol[2][tid] + sCol[3][tid]));
     }
     static_cast<T*>(p.dg)[token(tid) * p.Hv + hv] = from_f32<T>(dg);
     static_cast<T*>(p.dbeta)[token(tid) * p.Hv + hv] = from_f32<T>(db);
@@ -665,7 +837,7 @@ cudaError_t run_grad(const DeltaP& p, cudaStream_t s) {
   const auto grad = delta_grad_kernel<T, DK, DV>;
   const cudaError_t e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad<T, DK, DV>::smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(grad, dim3((unsigned)((long long)p.B * p.Hv * p.nc64)), dim3(32 * Grad<T, DK, DV>::warps),
+  return launch_dependent(grad, dim3((unsigned)((long long)p.B * p.Hv * p.nc64)), dim3(Grad<T, DK, DV>::threads),
                           (size_t)Grad<T, DK, DV>::smem, s, p);
 }
 // Columns of dv at a time: all of them in bfloat16, what shared memory holds in three planes.
@@ -678,6 +850,23 @@ cudaError_t run_grad_any(const DeltaP& p, float*, cudaStream_t s) {
   return run_grad<float, DK, 32>(p, s);
 }
 
+template <int DK>
+cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
+  const auto kern = delta_back_team_kernel<DK>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BackTeam<DK>::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(kTeamThreads),
+                          (size_t)BackTeam<DK>::smem, s, p);
+}
+template <int DK>
+cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
+  const auto kern = delta_back_kernel<float, DK>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Back<float, DK>::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)Back<float, DK>::smem,
+                          s, p);
+}
+
 template <typename T, int DK>
 cudaError_t run_back(const DeltaP& p, cudaStream_t s) {
   typedef ChunkData<T, DK, true, sizeof(T) == 4> D;
@@ -686,10 +875,7 @@ cudaError_t run_back(const DeltaP& p, cudaStream_t s) {
   prep<<<(unsigned)((long long)p.B * p.Hv * p.nc), 32, smem, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const auto back = delta_back_kernel<T, DK>;
-  e = cudaFuncSetAttribute(back, cudaFuncAttributeMaxDynamicSharedMemorySize, Back<T, DK>::smem);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(back, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(kBackThreads), (size_t)Back<T, DK>::smem, s, p);
+  e = run_walk<DK>(p, (T*)nullptr, s);
   if (e != cudaSuccess) return e;
   e = run_grad_any<DK>(p, (T*)nullptr, s);
   if (e != cudaSuccess || !p.dq_part) return e;

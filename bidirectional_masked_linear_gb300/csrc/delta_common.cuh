@@ -56,6 +56,7 @@ struct DeltaP {
 
 namespace {
 
+constexpr int kSmCount = 152;
 constexpr int kChunk = 32;          // tokens of a step of the chains
 constexpr int kSlice = 64;          // columns of the state a chain's CTA holds, 16 a warp
 constexpr int kStateChunk = 64;     // tokens between saved states, and of a block of the gradients
@@ -192,6 +193,26 @@ __device__ __forceinline__ void mma_tile(float (&c0)[4], float (&c1)[4], const u
   if (NB > 2) {
     TRANS ? ldsm_t(b, at + 2 * plane) : ldsm(b, at + 2 * plane);
     mma_planes<NA, NB, 2>(c0, c1, a, b);
+  }
+}
+
+// Two A operands on the same B.
+template <int NA, int NB, bool TRANS>
+__device__ __forceinline__ void mma_tile2(float (&c0)[4], float (&c1)[4], const unsigned (&a)[NA][4], float (&d0)[4],
+                                          float (&d1)[4], const unsigned (&e)[NA][4], unsigned at, int plane) {
+  unsigned b[4];
+  TRANS ? ldsm_t(b, at) : ldsm(b, at);
+  mma_planes<NA, NB, 0>(c0, c1, a, b);
+  mma_planes<NA, NB, 0>(d0, d1, e, b);
+  if (NB > 1) {
+    TRANS ? ldsm_t(b, at + plane) : ldsm(b, at + plane);
+    mma_planes<NA, NB, 1>(c0, c1, a, b);
+    mma_planes<NA, NB, 1>(d0, d1, e, b);
+  }
+  if (NB > 2) {
+    TRANS ? ldsm_t(b, at + 2 * plane) : ldsm(b, at + 2 * plane);
+    mma_planes<NA, NB, 2>(c0, c1, a, b);
+    mma_planes<NA, NB, 2>(d0, d1, e, b);
   }
 }
 

@@ -244,166 +244,310 @@ __global__ void __launch_bounds__(32) delta_prep_kernel(const DeltaP p) {
 
 // ------------------------------------------------------------------ the chain
 //
-// A CTA holds 64 columns of a head's state, two warps 16 of them as rows of S^T:
-// each has half of dk in its registers and, of a chunk, half of the tokens'
-// products with S.  The halves of R^T and of the new S^T pass between them in
-// shared memory; the tiles that all columns share come through it a few chunks
-// ahead.  One warp for all of a chunk's products would have the tensor core
-// wait for it three clocks of four: a step is some 700 instructions of one warp
-// or 400 of each of two (2 x 24337 x 12 x 64: 848 against XXX us).
-
-constexpr int kChainThreads = 256;
+// A CTA holds 64 columns of a head's state, a warp 16 of them as rows of S^T;
+// all a chunk does to them stays in the warp's registers, and the tiles that
+// all columns share come through shared memory a few chunks ahead.
 
 template <typename T, int DK, bool SAVE>
 struct Chain {
   typedef ChunkData<T, DK, SAVE, sizeof(T) == 4> D;
   typedef Stage<T, DK, D::P, D::Tm> L;
-  static constexpr int NO = D::NI == 1 ? 1 : D::NS;   // planes of S and R that a bfloat16 output takes: a rounding of 2^-9
-  typedef Swap<T, DK, NO> X;
   static constexpr int stages = sizeof(T) == 4 ? 2 : 3;
-  static constexpr int swap = stages * L::bytes, out = swap + 4 * X::bytes, smem = out + 8 * out_bytes<T>();
+  static constexpr int smem = stages * L::bytes + 4 * out_bytes<T>();
 };
 
 template <typename T, int DK, bool SAVE>
-__global__ void __launch_bounds__(kChainThreads) delta_chain_kernel(const DeltaP p) {
+__global__ void __launch_bounds__(128) delta_chain_kernel(const DeltaP p) {
   typedef Chain<T, DK, SAVE> C;
   typedef typename C::D D;
   typedef typename C::L L;
-  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, NO = C::NO, N = DK / 16;
+  constexpr int NST = C::stages, NI = D::NI, NS = D::NS;
+  constexpr int NO = NI == 1 ? 1 : NS;   // planes of S and R that a bfloat16 output takes: one rounding of 2^-9 each
   constexpr bool KQ = L::KQ;
   extern __shared__ __align__(128) unsigned char smem[];
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
-  const int pair = w & 3, side = w >> 2;
-  unsigned char* buf = smem + C::out + w * out_bytes<T>();
-  const unsigned xs = base + C::swap + pair * C::X::bytes, xr = xs + C::X::state;   // S^T, R^T
+  unsigned char* buf = smem + NST * L::bytes + w * out_bytes<T>();
   const long long bh = blockIdx.x / p.slices;
   const int slice = (int)(blockIdx.x - bh * p.slices);
   const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
-  const int m0 = slice * kSlice + 16 * pair;           // the warp's first column of the state
+  const int m0 = slice * kSlice + 16 * w;              // the warp's first column of the state
   const int cols = p.dv - m0 < 16 ? p.dv - m0 : 16;    // 0 or less: none
   const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
   const Rows<T> xo = rows_of<T>(p, p.out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
   const char* chunk = p.chunks + bh * p.nc * D::bytes;
-  const float4* U = reinterpret_cast<const float4*>(p.U) + (bh * p.nc * p.dvp + m0) * (kChunk / 4) + 64 * side + lane;
+  const float4* U = reinterpret_cast<const float4*>(p.U) + (bh * p.nc * p.dvp + m0) * (kChunk / 4) + lane;
 
-  float s[N][4];   // S^T, this side's dk
-  load_state<N>(p, p.h0, bh, m0, cols, side * (DK / 2), lane, s);
-  if (cols > 0) put_state<DK, NS>(xs, s, side, lane);
+  float s[DK / 8][4];   // S^T
+  load_state<DK>(p, p.h0, bh, m0, cols, lane, s);
   wait_prior();
 #pragma unroll
   for (int st = 0; st < NST - 1; ++st) {
     if (st < nc)
-      L::template load<kChainThreads>(p, base + st * L::bytes, chunk + (long long)st * D::bytes, xq, xk, st * kChunk, n, tid);
+      L::template load<128>(p, base + st * L::bytes, chunk + (long long)st * D::bytes, xq, xk, st * kChunk, n, tid);
     copy_commit();
   }
-  float4 next[2];
+  float4 next[4];
   if (cols > 0 && nc > 0)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) next[e] = U[32 * e];
+    for (int e = 0; e < 4; ++e) next[e] = U[32 * e];
   for (int c = 0; c < nc; ++c) {
     copy_wait<NST - 2>();
     __syncthreads();
     if (c + NST - 1 < nc)
-      L::template load<kChainThreads>(p, base + (c + NST - 1) % NST * L::bytes, chunk + (long long)(c + NST - 1) * D::bytes,
-                                      xq, xk, (c + NST - 1) * kChunk, n, tid);
+      L::template load<128>(p, base + (c + NST - 1) % NST * L::bytes, chunk + (long long)(c + NST - 1) * D::bytes, xq, xk,
+                            (c + NST - 1) * kChunk, n, tid);
     copy_commit();
     if (cols <= 0) continue;
     const unsigned st = base + c % NST * L::bytes;
-    const float* coef = reinterpret_cast<const float*>(smem + c % NST * L::bytes + L::at(D::coef)) + 16 * side + 2 * q4;
+    const float* coef = reinterpret_cast<const float*>(smem + c % NST * L::bytes + L::at(D::coef));
     if (SAVE && c % (kStateChunk / kChunk) == 0)
-      store_blocks<N, DK / 8>(static_cast<T*>(p.states) +
-                                  ((bh * p.nc64 + c / (kStateChunk / kChunk)) * p.dvp + m0) * DK + side * N * 64,
-                              s, lane);
+      store_blocks<DK / 8>(static_cast<T*>(p.states) + ((bh * p.nc64 + c / (kStateChunk / kChunk)) * p.dvp + m0) * DK, s, lane);
 
-    // this side's tokens: R^T = U^T - S^T W^T; S^T Q^T
-    float x[2][4], o[2][4] = {};
+    // R^T = U^T - S^T W^T; S^T Q^T
+    float x[4][4], o[4][4] = {};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       x[i][0] = next[i].x; x[i][1] = next[i].y; x[i][2] = next[i].z; x[i][3] = next[i].w;
     }
     if (c + 1 < nc) {
       U += p.dvp * (kChunk / 4);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) next[e] = U[32 * e];
+      for (int e = 0; e < 4; ++e) next[e] = U[32 * e];
     }
 #pragma unroll
     for (int ks = 0; ks < DK / 16; ++ks) {
       unsigned a[NS][4], ao[NO][4];
+      to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
 #pragma unroll
-      for (int j = 0; j < NS; ++j) get_a(xs + (ks * NS + j) * 512, a[j], lane);
+      for (int i = 0; i < NO; ++i)
 #pragma unroll
-      for (int j = 0; j < NO; ++j)
+        for (int e = 0; e < 4; ++e) ao[i][e] = a[i][e];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ao[j][e] = a[j][e];
-      mma_tile<NS, NS, false>(x[0], x[1], a, st + L::at(D::W) + at_b_rows_n<DK, true>(16 * side, 16 * ks, lane), L::row);
-      mma_tile<NO, NI, false>(o[0], o[1], ao, st + L::q + at_b_rows_n<DK, KQ>(16 * side, 16 * ks, lane), L::row);
+      for (int np = 0; np < 2; ++np) {
+        mma_tile<NS, NS, false>(x[2 * np], x[2 * np + 1], a, st + L::at(D::W) + at_b_rows_n<DK, true>(16 * np, 16 * ks, lane),
+                                L::row);
+        mma_tile<NO, NI, false>(o[2 * np], o[2 * np + 1], ao, st + L::q + at_b_rows_n<DK, KQ>(16 * np, 16 * ks, lane), L::row);
+      }
     }
-    // R^T to the other side: times beta e^(G_C - G) in planes, and as it is for the output
-    unsigned mine[NS][4], plain[NO][4];
-    to_a<NS>(x[0], x[1], *reinterpret_cast<const float2*>(coef + kChunk), *reinterpret_cast<const float2*>(coef + kChunk + 8),
-             mine);
-    to_a<NO>(x[0], x[1], plain);
+    if (SAVE) store_blocks<4>(static_cast<T*>(p.R) + ((bh * p.nc + c) * p.dvp + m0) * kChunk, x, lane);
+    // S^T = e^G_C S^T + (beta left R)^T K; O^T = scale e^G (S^T Q^T) + R^T P^T
 #pragma unroll
-    for (int j = 0; j < NS; ++j) put_a(xr + (side * NS + j) * 512, mine[j], lane);
-    if (side == 0)
+    for (int nb = 0; nb < 4; ++nb) {
+      const float2 g = *reinterpret_cast<const float2*>(coef + 8 * nb + 2 * q4);
 #pragma unroll
-      for (int j = 0; j < NO; ++j) put_a(xr + (2 * NS + j) * 512, plain[j], lane);
-    pair_sync(pair);
-    // S^T = e^G_C S^T + (beta left R)^T K, this side's dk
-    scale_by(s, coef[2 * kChunk - 16 * side - 2 * q4]);
+      for (int e = 0; e < 4; ++e) o[nb][e] *= e & 1 ? g.y : g.x;
+    }
+    scale_by(s, coef[2 * kChunk]);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      unsigned a[NS][4];
+      const float* l = coef + kChunk + 16 * ks + 2 * q4;
+      unsigned a[NS][4], ao[NO][4];
+      to_a<NS>(x[2 * ks], x[2 * ks + 1], *reinterpret_cast<const float2*>(l), *reinterpret_cast<const float2*>(l + 8), a);
 #pragma unroll
-      for (int j = 0; j < NS; ++j) get_a(xr + (ks * NS + j) * 512, a[j], lane);
+      for (int nn = 0; nn < DK / 16; ++nn)
+        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], a, st + L::k + at_b_rows_k<DK, KQ>(16 * ks, 16 * nn, lane), L::row);
+      to_a<NO>(x[2 * ks], x[2 * ks + 1], ao);
 #pragma unroll
-      for (int nn = 0; nn < N / 2; ++nn)
-        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], a,
-                               st + L::k + at_b_rows_k<DK, KQ>(16 * ks, side * (DK / 2) + 16 * nn, lane), L::row);
+      for (int np = ks; np < 2; ++np)
+        mma_tile<NO, NO, false>(o[2 * np], o[2 * np + 1], ao,
+                                st + L::at(D::P) + at_b_rows_n<kChunk, true>(16 * np, 16 * ks, lane), kTile);
     }
-    put_state<DK, NS>(xs, s, side, lane);
-    if (SAVE)
-      store_blocks<2, 4>(static_cast<T*>(p.R) + ((bh * p.nc + c) * p.dvp + m0) * kChunk + side * 2 * 64, x, lane);
-    if (p.out) {   // O^T = scale e^G (S^T Q^T) + R^T P^T
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const float2 g = *reinterpret_cast<const float2*>(coef + 8 * nb);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[nb][e] *= e & 1 ? g.y : g.x;
-      }
-      const unsigned P = st + L::at(D::P);
-      if (side == 1) {
-        unsigned a[NO][4];
-#pragma unroll
-        for (int j = 0; j < NO; ++j) get_a(xr + (2 * NS + j) * 512, a[j], lane);
-        mma_tile<NO, NO, false>(o[0], o[1], a, P + at_b_rows_n<kChunk, true>(16, 0, lane), kTile);
-      }
-      mma_tile<NO, NO, false>(o[0], o[1], plain, P + at_b_rows_n<kChunk, true>(16 * side, 16 * side, lane), kTile);
-      store_rows(buf, o, lane, cols, p.o_wide, xo, c * kChunk + 16 * side, n);
+    if (p.out) {
+      const int i = c * kChunk + lane;
+      store_rows(buf, o, lane, cols, p.o_wide, i < n ? const_cast<T*>(xo.at(i)) : nullptr);
     }
   }
   copy_wait<0>();
   if (cols <= 0) return;
-  if (p.h_out) keep_state<N>(p, p.h_out, bh, m0, cols, side * (DK / 2), lane, s);
-  if (p.out) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, side, lane);
+  if (p.h_out) keep_state<DK>(p, p.h_out, bh, m0, cols, lane, s);
+  if (p.out) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, lane);
+}
+
+// The same in bfloat16 with a helper to each warp: the warp has the two
+// products between one state and the next, the helper the loads, the output and
+// what the gradients keep.  One warp for all of it is 1206 ns a chunk at 2 x
+// 24337 x 12 x 64, of which the loads are 256, the output 227, U's read 146;
+// two warps with half of the tokens and of dk each took longer (1430), as every
+// half has to pass between them within a chunk.
+
+template <int DK, bool SAVE>
+struct Team {
+  typedef __nv_bfloat16 T;
+  typedef ChunkData<T, DK, SAVE, false> D;
+  static constexpr int row = kChunk * DK * 2;
+  // a stage: q, k, P's first plane, coefficients and -W, the slice of U
+  static constexpr int q = 0, k = row, P = 2 * row, coef = P + kTile, W = coef + (D::W - D::coef);
+  static constexpr int U = W + (D::Tm - D::W), bytes = U + kSlice * kChunk * 4, stages = 3;
+  static constexpr int S = 0, R = DK / 16 * 512, swap = R + 2 * 512;   // a warp's buffer to its helper
+  static constexpr int swaps = stages * bytes, out = swaps + 2 * 4 * swap, smem = out + 4 * out_bytes<T>();
+};
+
+template <int DK, bool SAVE, int CTAS>   // CTAS: of an SM, by registers
+__global__ void __launch_bounds__(kTeamThreads, CTAS) delta_team_kernel(const DeltaP p) {
+  typedef __nv_bfloat16 T;
+  typedef Team<DK, SAVE> C;
+  typedef typename C::D D;
+  constexpr int NST = C::stages, NS = 2, PER = kStateChunk / kChunk;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const unsigned base = shared_at(smem);
+  const int tid = threadIdx.x & 127, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
+  const bool helper = threadIdx.x >= 128;
+  const long long bh = blockIdx.x / p.slices;
+  const int slice = (int)(blockIdx.x - bh * p.slices);
+  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
+  const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
+  const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer 4 swaps behind
+  wait_prior();
+  if (helper) {
+    const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
+    const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
+    const Rows<T> xo = rows_of<T>(p, p.out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
+    const char* chunks = p.chunks + bh * p.nc * D::bytes;
+    const float* Us = p.U + (bh * p.nc * p.dvp + slice * kSlice) * kChunk;
+    const int rows = p.dvp - slice * kSlice < kSlice ? p.dvp - slice * kSlice : kSlice;
+    unsigned char* buf = smem + C::out + w * out_bytes<T>();
+    const auto load = [&](int c) {
+      const unsigned st = base + c % NST * C::bytes;
+      const char* chunk = chunks + (long long)c * D::bytes;
+      load_tile<DK, kChunk, 128>(st + C::k, 0, xk, c * kChunk, n, p.dk, p.k_wide, tid);
+      load_tile<DK, kChunk, 128>(st + C::q, 0, xq, c * kChunk, n, p.dk, p.q_wide, tid);
+      copy_block<kTile, 128>(st + C::P, chunk + D::P, tid);
+      copy_block<D::Tm - D::coef, 128>(st + C::coef, chunk + D::coef, tid);
+      copy_slice<128>(st + C::U, Us + (long long)c * p.dvp * kChunk, rows, tid);
+    };
+    if (nc > 0) load(0);
+    copy_commit();
+    for (int i = 0; i <= nc; ++i) {
+      copy_wait<0>();
+      __syncthreads();
+      if (i + 1 < nc) load(i + 1);
+      copy_commit();
+      if (i == 0 || cols <= 0) continue;
+      const int c = i - 1;
+      const unsigned st = base + c % NST * C::bytes, x = swap + (c & 1) * 4 * C::swap;
+      const float* coef = reinterpret_cast<const float*>(smem + c % NST * C::bytes + C::coef);
+      // O^T = scale e^G (S^T Q^T) + R^T P^T
+      float o[4][4] = {};
+      unsigned a[DK / 16][1][4], r[2][1][4];
+#pragma unroll
+      for (int ks = 0; ks < DK / 16; ++ks) get_a(x + C::S + ks * 512, a[ks][0], lane);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) get_a(x + C::R + ks * 512, r[ks][0], lane);
+#pragma unroll
+      for (int ks = 0; ks < DK / 16; ++ks)
+#pragma unroll
+        for (int np = 0; np < 2; ++np)
+          mma_tile<1, 1, false>(o[2 * np], o[2 * np + 1], a[ks], st + C::q + at_b_rows_n<DK>(16 * np, 16 * ks, lane), 0);
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        const float2 g = *reinterpret_cast<const float2*>(coef + 8 * nb + 2 * q4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nb][e] *= e & 1 ? g.y : g.x;
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int np = ks; np < 2; ++np)
+          mma_tile<1, 1, false>(o[2 * np], o[2 * np + 1], r[ks],
+                                st + C::P + at_b_rows_n<kChunk, true>(16 * np, 16 * ks, lane), 0);
+      if (SAVE) {
+        if (c % PER == 0)
+#pragma unroll
+          for (int ks = 0; ks < DK / 16; ++ks)
+            store_a<DK / 8>(static_cast<T*>(p.states) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK + ks * 128, a[ks][0], lane);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          store_a<4>(static_cast<T*>(p.R) + ((bh * p.nc + c) * p.dvp + m0) * kChunk + ks * 128, r[ks][0], lane);
+      }
+      if (p.out) {
+        const int t = c * kChunk + lane;
+        store_rows(buf, o, lane, cols, p.o_wide, t < n ? const_cast<T*>(xo.at(t)) : nullptr);
+      }
+    }
+    if (p.out && cols > 0) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, lane);
+    return;
+  }
+  float s[DK / 8][4];   // S^T
+  load_state<DK>(p, p.h0, bh, m0, cols, lane, s);
+  for (int i = 0; i <= nc; ++i) {
+    __syncthreads();
+    if (i == nc || cols <= 0) continue;
+    const unsigned st = base + i % NST * C::bytes, x = swap + (i & 1) * 4 * C::swap;
+    const float* coef = reinterpret_cast<const float*>(smem + i % NST * C::bytes + C::coef);
+    float r[4][4];
+    unsigned plain[DK / 16][4], rplain[2][1][4];   // to the helper at the end: a store would hold back the reads behind it
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      const float4 u = get_f4(st + C::U + (w * 4 + nb) * 512, lane);
+      r[nb][0] = u.x; r[nb][1] = u.y; r[nb][2] = u.z; r[nb][3] = u.w;
+    }
+    // R^T = U^T - S^T W^T
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      unsigned a[NS][4];
+      to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) plain[ks][e] = a[0][e];
+#pragma unroll
+      for (int np = 0; np < 2; ++np)
+        mma_tile<NS, NS, false>(r[2 * np], r[2 * np + 1], a, st + C::W + at_b_rows_n<DK, true>(16 * np, 16 * ks, lane), C::row);
+    }
+    // S^T = e^G_C S^T + (beta left R)^T K
+    scale_by(s, coef[2 * kChunk]);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const float* l = coef + kChunk + 16 * ks + 2 * q4;
+      unsigned a[NS][4];
+      to_a<NS>(r[2 * ks], r[2 * ks + 1], *reinterpret_cast<const float2*>(l), *reinterpret_cast<const float2*>(l + 8), a);
+      to_a<1>(r[2 * ks], r[2 * ks + 1], rplain[ks]);
+#pragma unroll
+      for (int nn = 0; nn < DK / 16; ++nn)
+        mma_tile<NS, 1, true>(s[2 * nn], s[2 * nn + 1], a, st + C::k + at_b_rows_k<DK>(16 * ks, 16 * nn, lane), 0);
+    }
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) put_a(x + C::S + ks * 512, plain[ks], lane);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) put_a(x + C::R + ks * 512, rplain[ks][0], lane);
+  }
+  if (p.h_out && cols > 0) keep_state<DK>(p, p.h_out, bh, m0, cols, lane, s);
+}
+
+template <int DK, bool SAVE, int CTAS>
+cudaError_t run_team(const DeltaP& p, unsigned ctas, cudaStream_t s) {
+  const auto kern = delta_team_kernel<DK, SAVE, CTAS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Team<DK, SAVE>::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(ctas), dim3(kTeamThreads), (size_t)Team<DK, SAVE>::smem, s, p);
+}
+// More CTAs than SMs: two an SM, whose 128 registers a thread take a warp alone
+// from 613 to 735 ns a chunk; shared memory has room for one at dk > 64.
+template <int DK, bool SAVE>
+cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
+  const unsigned ctas = (unsigned)((long long)p.B * p.Hv * p.slices);
+  return DK == 64 && ctas > kSmCount ? run_team<DK, SAVE, DK == 64 ? 2 : 1>(p, ctas, s) : run_team<DK, SAVE, 1>(p, ctas, s);
+}
+template <int DK, bool SAVE>
+cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
+  typedef Chain<float, DK, SAVE> C;
+  const auto kern = delta_chain_kernel<float, DK, SAVE>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)C::smem, s, p);
 }
 
 template <typename T, int DK, bool SAVE>
 cudaError_t run_chain(const DeltaP& p, cudaStream_t s) {
-  typedef Chain<T, DK, SAVE> C;
   const auto prep = delta_prep_kernel<T, DK, SAVE>;
   cudaError_t e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, Prep<T, DK>::smem(2));
   if (e != cudaSuccess) return e;
   prep<<<(unsigned)((long long)p.B * p.Hv * p.nc), 32, Prep<T, DK>::smem(p.slices), s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const auto kern = delta_chain_kernel<T, DK, SAVE>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(kChainThreads), C::smem, s, p);
+  return run_walk<DK, SAVE>(p, (T*)nullptr, s);
 }
 template <typename T>
 cudaError_t run_chain_any(const DeltaP& p, bool save, cudaStream_t s) {
