@@ -270,6 +270,14 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
       __syncthreads();
       if (i + 1 < nc) load(i + 1);
       copy_commit();
+      if (i + 2 < nc) {   // as in the forward walk
+        const long long c = nc - 3 - i;
+        to_l2<D::bytes - D::coef, 128>(chunks + c * D::bytes + D::coef, D::bytes - D::coef, tid);
+        to_l2<kSlice * kChunk * 4, 128>(Zs + c * p.dvp * kChunk, rows * kChunk * 4, tid);
+        rows_to_l2(xk, (int)c * kChunk, n, tid - 64);
+        rows_to_l2(xq, (int)c * kChunk, n, tid - 96);
+        if (cols > 0) to_l2<2 * NS * 512, 32>(dO - lane + c * (p.dvp / 16) * 2 * NS * 32, 2 * NS * 512, lane);
+      }
       if (i < nc && cols > 0) {   // (scale e^G o dO)^T Q
         const unsigned st = base + i % NST * C::bytes;
         float y[DK / 8][4] = {};
@@ -895,7 +903,7 @@ BackLayout back_layout(int B, int L, int Hk, int Hv, int dk, int dv, int dtype, 
   const DeltaLayout f = delta_layout(B, L, Hv, dk, dv, dtype, true);
   const size_t planes = dtype == DT_BF16 ? Planes<__nv_bfloat16>::mid : Planes<float>::mid;
   BackLayout l;
-  l.dO = f.U;
+  l.dO = f.beside;
   l.dstates = l.dO + up((size_t)B * Hv * f.nc * kChunk * f.dvp * 2 * planes);
   l.parts = l.dstates + (f.bytes - f.states);   // as large as the states
   l.part = Hv > Hk ? up(sizeof(float) * (size_t)B * L * Hv * dk) : 0;

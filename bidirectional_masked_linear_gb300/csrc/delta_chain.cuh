@@ -137,6 +137,18 @@ __device__ __forceinline__ void store_a(__nv_bfloat16* to, const unsigned (&a)[4
   d[32] = a[2];
   d[(ROW + 1) * 32] = a[3];
 }
+// `bytes`, at most MOST, on their way to L2, a line of 128 a thread.
+template <int MOST, int THREADS>
+__device__ __forceinline__ void to_l2(const void* p, int bytes, int tid) {
+#pragma unroll
+  for (int i = 0; i < (MOST / 128 + THREADS) / THREADS; ++i)
+    if (128 * (tid + i * THREADS) < bytes)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + 128 * (tid + i * THREADS)));
+}
+// A chunk's rows, a line a thread (of longer rows their beginnings).
+__device__ __forceinline__ void rows_to_l2(const Rows<__nv_bfloat16>& x, int i0, int n, int row) {
+  if (row >= 0 && row < kChunk && i0 + row < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(x.at(i0 + row)));
+}
 // A slice's fragments of a chunk: `rows` columns of 32 floats to shared memory.
 template <int THREADS>
 __device__ __forceinline__ void copy_slice(unsigned dst, const float* src, int rows, int tid) {

@@ -49,6 +49,8 @@ struct DeltaP {
   float *dq_part, *dk_part;   // per value head, [B][L][Hv][dk], where a query head has several
   long long q_ld, k_ld, v_ld, g_ld, beta_ld;
   int B, L, Hk, Hv, dk, dv, dvp, nc, nc64, slices;   // dvp: dv up to whole warps' 16
+  int nseg, seglen;        // the forward walk's segments, of seglen chunks
+  float *moves, *starts;   // per head and segment: what it makes of a state, [dk][dvp + dk]; the state before it, [dk][dv]
   float scale;
   int reverse;
   int q_wide, k_wide, v_wide, o_wide, do_wide, dv_wide;
@@ -56,7 +58,6 @@ struct DeltaP {
 
 namespace {
 
-constexpr int kSmCount = 152;
 constexpr int kChunk = 32;          // tokens of a step of the chains
 constexpr int kSlice = 64;          // columns of the state a chain's CTA holds, 16 a warp
 constexpr int kStateChunk = 64;     // tokens between saved states, and of a block of the gradients

@@ -385,8 +385,8 @@ struct Team {
   static constexpr int swaps = stages * bytes, out = swaps + 2 * 4 * swap, smem = out + 4 * out_bytes<T>();
 };
 
-template <int DK, bool SAVE, int CTAS>   // CTAS: of an SM, by registers
-__global__ void __launch_bounds__(kTeamThreads, CTAS) delta_team_kernel(const DeltaP p) {
+template <int DK, bool SAVE>
+__global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_kernel(const DeltaP p) {
   typedef __nv_bfloat16 T;
   typedef Team<DK, SAVE> C;
   typedef typename C::D D;
@@ -395,10 +395,12 @@ __global__ void __launch_bounds__(kTeamThreads, CTAS) delta_team_kernel(const De
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x & 127, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
   const bool helper = threadIdx.x >= 128;
-  const long long bh = blockIdx.x / p.slices;
-  const int slice = (int)(blockIdx.x - bh * p.slices);
+  const long long part = blockIdx.x / p.slices, bh = part / p.nseg;
+  const int slice = (int)(blockIdx.x - part * p.slices), seg = (int)(part - bh * p.nseg);
   const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
-  const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
+  const int n = delta_length(p, b), all = (n + kChunk - 1) / kChunk, c0 = seg * p.seglen;
+  const bool ends = seg == p.nseg - 1;
+  const int nc = all - c0 < 0 ? 0 : ends || all - c0 < p.seglen ? all - c0 : p.seglen;   // chunks of the segment, from c0 on
   const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
   const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer 4 swaps behind
   wait_prior();
@@ -406,15 +408,15 @@ __global__ void __launch_bounds__(kTeamThreads, CTAS) delta_team_kernel(const De
     const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
     const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
     const Rows<T> xo = rows_of<T>(p, p.out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
-    const char* chunks = p.chunks + bh * p.nc * D::bytes;
-    const float* Us = p.U + (bh * p.nc * p.dvp + slice * kSlice) * kChunk;
+    const char* chunks = p.chunks + (bh * p.nc + c0) * D::bytes;
+    const float* Us = p.U + ((bh * p.nc + c0) * p.dvp + slice * kSlice) * kChunk;
     const int rows = p.dvp - slice * kSlice < kSlice ? p.dvp - slice * kSlice : kSlice;
     unsigned char* buf = smem + C::out + w * out_bytes<T>();
     const auto load = [&](int c) {
       const unsigned st = base + c % NST * C::bytes;
       const char* chunk = chunks + (long long)c * D::bytes;
-      load_tile<DK, kChunk, 128>(st + C::k, 0, xk, c * kChunk, n, p.dk, p.k_wide, tid);
-      load_tile<DK, kChunk, 128>(st + C::q, 0, xq, c * kChunk, n, p.dk, p.q_wide, tid);
+      load_tile<DK, kChunk, 128>(st + C::k, 0, xk, (c0 + c) * kChunk, n, p.dk, p.k_wide, tid);
+      load_tile<DK, kChunk, 128>(st + C::q, 0, xq, (c0 + c) * kChunk, n, p.dk, p.q_wide, tid);
       copy_block<kTile, 128>(st + C::P, chunk + D::P, tid);
       copy_block<D::Tm - D::coef, 128>(st + C::coef, chunk + D::coef, tid);
       copy_slice<128>(st + C::U, Us + (long long)c * p.dvp * kChunk, rows, tid);
@@ -426,10 +428,16 @@ __global__ void __launch_bounds__(kTeamThreads, CTAS) delta_team_kernel(const De
       __syncthreads();
       if (i + 1 < nc) load(i + 1);
       copy_commit();
+      if (i + 2 < nc) {   // a load has a chunk's time, which covers L2's latency and not HBM's
+        to_l2<D::Tm - D::P, 128>(chunks + (long long)(i + 2) * D::bytes + D::P, D::Tm - D::P, tid);
+        to_l2<kSlice * kChunk * 4, 128>(Us + (long long)(i + 2) * p.dvp * kChunk, rows * kChunk * 4, tid);
+        rows_to_l2(xk, (c0 + i + 2) * kChunk, n, tid - 64);
+        rows_to_l2(xq, (c0 + i + 2) * kChunk, n, tid - 96);
+      }
       if (i == 0 || cols <= 0) continue;
-      const int c = i - 1;
-      const unsigned st = base + c % NST * C::bytes, x = swap + (c & 1) * 4 * C::swap;
-      const float* coef = reinterpret_cast<const float*>(smem + c % NST * C::bytes + C::coef);
+      const unsigned st = base + (i - 1) % NST * C::bytes, x = swap + (i - 1 & 1) * 4 * C::swap;
+      const float* coef = reinterpret_cast<const float*>(smem + (i - 1) % NST * C::bytes + C::coef);
+      const int c = c0 + i - 1;
       // O^T = scale e^G (S^T Q^T) + R^T P^T
       float o[4][4] = {};
       unsigned a[DK / 16][1][4], r[2][1][4];
@@ -468,11 +476,11 @@ __global__ void __launch_bounds__(kTeamThreads, CTAS) delta_team_kernel(const De
         store_rows(buf, o, lane, cols, p.o_wide, t < n ? const_cast<T*>(xo.at(t)) : nullptr);
       }
     }
-    if (p.out && cols > 0) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, lane);
+    if (p.out && cols > 0 && ends) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, lane);
     return;
   }
   float s[DK / 8][4];   // S^T
-  load_state<DK>(p, p.h0, bh, m0, cols, lane, s);
+  seg > 0 ? load_state<DK>(p, p.starts, bh * p.nseg + seg, m0, cols, lane, s) : load_state<DK>(p, p.h0, bh, m0, cols, lane, s);
   for (int i = 0; i <= nc; ++i) {
     __syncthreads();
     if (i == nc || cols <= 0) continue;
@@ -513,22 +521,180 @@ __global__ void __launch_bounds__(kTeamThreads, CTAS) delta_team_kernel(const De
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) put_a(x + C::R + ks * 512, rplain[ks][0], lane);
   }
-  if (p.h_out && cols > 0) keep_state<DK>(p, p.h_out, bh, m0, cols, lane, s);
+  if (p.h_out && cols > 0 && ends) keep_state<DK>(p, p.h_out, bh, m0, cols, lane, s);
 }
 
-template <int DK, bool SAVE, int CTAS>
-cudaError_t run_team(const DeltaP& p, unsigned ctas, cudaStream_t s) {
-  const auto kern = delta_team_kernel<DK, SAVE, CTAS>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Team<DK, SAVE>::smem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(ctas), dim3(kTeamThreads), (size_t)Team<DK, SAVE>::smem, s, p);
+// ------------------------------------------------------------------- segments
+//
+// Few heads leave most SMs idle, and a head's chunks follow one another.  Then
+// a sequence is cut into segments.  A segment makes S' = M S + N of the state
+// before it; N is its walk from zeros (the first one's from the state that is
+// given), M the walk of the identity with U = 0, both without outputs and all
+// segments' at once.  A second launch chains them, and the walks with outputs
+// start from there.  Three walks' work for one, so only where it finds idle SMs.
+
+constexpr int kMoveThreads = 256;
+
+template <int DK>
+struct Move {
+  typedef __nv_bfloat16 T;
+  static constexpr int row = kChunk * DK * 2;
+  static constexpr int k = 0, coef = row, W = coef + kCoefs * 4, bytes = W + 2 * row, stages = 3, smem = stages * bytes;
+};
+
+// CTAs for 8 x 16 columns of [N | M] of a segment.
+template <int DK, bool SAVE>
+__global__ void __launch_bounds__(kMoveThreads, 2) delta_move_kernel(const DeltaP p, int groups) {
+  typedef __nv_bfloat16 T;
+  typedef Move<DK> C;
+  typedef ChunkData<T, DK, SAVE, false> D;
+  constexpr int NST = C::stages, NS = 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const unsigned base = shared_at(smem);
+  const int tid = threadIdx.x, lane = tid & 31, q4 = lane & 3;
+  const long long part = blockIdx.x / groups, bh = part / (p.nseg - 1);
+  const int group = (int)(blockIdx.x - part * groups), seg = (int)(part - bh * (p.nseg - 1));
+  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const int n = delta_length(p, b), all = (n + kChunk - 1) / kChunk, c0 = seg * p.seglen;
+  const int nc = all - c0 < 0 ? 0 : all - c0 < p.seglen ? all - c0 : p.seglen;
+  const int m0 = 16 * (group * 8 + (tid >> 5));        // the warp's first column of [N | M]
+  const bool move = m0 >= p.dvp;                       // of M
+  const bool mine = move ? seg > 0 && m0 - p.dvp < p.dk : true;
+  const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
+  const char* chunks = p.chunks + (bh * p.nc + c0) * D::bytes;
+  const float4* U = reinterpret_cast<const float4*>(p.U) + ((bh * p.nc + c0) * p.dvp + m0) * (kChunk / 4) + lane;
+  float s[DK / 8][4];
+  if (move) {
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = 8 * j + 2 * q4 + (e & 1) == m0 - p.dvp + (lane >> 2) + 8 * (e >> 1) ? 1.f : 0.f;
+  } else {
+    load_state<DK>(p, seg == 0 ? p.h0 : nullptr, bh, m0, p.dv - m0 < 16 ? p.dv - m0 : 16, lane, s);
+  }
+  const auto load = [&](int c) {
+    const unsigned st = base + c % NST * C::bytes;
+    load_tile<DK, kChunk, kMoveThreads>(st + C::k, 0, xk, (c0 + c) * kChunk, n, p.dk, p.k_wide, tid);
+    copy_block<D::Tm - D::coef, kMoveThreads>(st + C::coef, chunks + (long long)c * D::bytes + D::coef, tid);
+  };
+  wait_prior();
+#pragma unroll
+  for (int c = 0; c < NST - 1; ++c) {
+    if (c < nc) load(c);
+    copy_commit();
+  }
+  float4 next[4] = {};
+  if (mine && !move && nc > 0)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) next[e] = U[32 * e];
+  for (int c = 0; c < nc; ++c) {
+    copy_wait<NST - 2>();
+    __syncthreads();
+    if (c + NST - 1 < nc) load(c + NST - 1);
+    copy_commit();
+    if (!mine) continue;
+    const unsigned st = base + c % NST * C::bytes;
+    const float* coef = reinterpret_cast<const float*>(smem + c % NST * C::bytes + C::coef);
+    float r[4][4];
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      r[nb][0] = next[nb].x; r[nb][1] = next[nb].y; r[nb][2] = next[nb].z; r[nb][3] = next[nb].w;
+    }
+    if (!move && c + 1 < nc) {
+      U += p.dvp * (kChunk / 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) next[e] = U[32 * e];
+    }
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      unsigned a[NS][4];
+      to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
+#pragma unroll
+      for (int np = 0; np < 2; ++np)
+        mma_tile<NS, NS, false>(r[2 * np], r[2 * np + 1], a, st + C::W + at_b_rows_n<DK, true>(16 * np, 16 * ks, lane), C::row);
+    }
+    scale_by(s, coef[2 * kChunk]);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const float* l = coef + kChunk + 16 * ks + 2 * q4;
+      unsigned a[NS][4];
+      to_a<NS>(r[2 * ks], r[2 * ks + 1], *reinterpret_cast<const float2*>(l), *reinterpret_cast<const float2*>(l + 8), a);
+#pragma unroll
+      for (int nn = 0; nn < DK / 16; ++nn)
+        mma_tile<NS, 1, true>(s[2 * nn], s[2 * nn + 1], a, st + C::k + at_b_rows_k<DK>(16 * ks, 16 * nn, lane), 0);
+    }
+  }
+  copy_wait<0>();
+  if (!mine) return;
+  const int width = p.dvp + p.dk, cols = width - m0 < 16 ? width - m0 : 16;
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kx = 8 * j + 2 * q4 + (e & 1), col = (lane >> 2) + 8 * (e >> 1);
+      if (kx < p.dk && col < cols) p.moves[((bh * p.nseg + seg) * p.dk + kx) * width + m0 + col] = s[j][e];
+    }
 }
-// More CTAs than SMs: two an SM, whose 128 registers a thread take a warp alone
-// from 613 to 735 ns a chunk; shared memory has room for one at dk > 64.
+
+// The states before the segments: a CTA for 16 columns of a head, a thread for
+// four of them and every 64th row; the state before passes through shared memory.
+__global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
+  __shared__ float4 sh[LION_DELTA_MAX_D][4];
+  const int tiles = p.dvp / 16, width = p.dvp + p.dk;
+  const long long bh = blockIdx.x / tiles;
+  const int col = 16 * (int)(blockIdx.x - bh * tiles) + 4 * (threadIdx.x & 3), row = threadIdx.x >> 2;
+  wait_prior();
+  for (int seg = 0; seg < p.nseg - 1; ++seg) {
+    const float* m = p.moves + (bh * p.nseg + seg) * p.dk * width;
+    float4 x[LION_DELTA_MAX_D / 64];
+#pragma unroll
+    for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i) {
+      const int r = row + 64 * i;
+      if (r >= p.dk) continue;
+      x[i] = *reinterpret_cast<const float4*>(m + (long long)r * width + col);
+      if (seg == 0) continue;
+#pragma unroll 8
+      for (int k = 0; k < p.dk; ++k) {
+        const float a = m[(long long)r * width + p.dvp + k];
+        const float4 y = sh[k][threadIdx.x & 3];
+        x[i].x = fmaf(a, y.x, x[i].x);
+        x[i].y = fmaf(a, y.y, x[i].y);
+        x[i].z = fmaf(a, y.z, x[i].z);
+        x[i].w = fmaf(a, y.w, x[i].w);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i) {
+      const int r = row + 64 * i;
+      if (r >= p.dk) continue;
+      sh[r][threadIdx.x & 3] = x[i];
+      if (col < p.dv)
+        *reinterpret_cast<float4*>(p.starts + ((bh * p.nseg + seg + 1) * p.dk + r) * p.dv + col) = x[i];
+    }
+    __syncthreads();
+  }
+}
+
 template <int DK, bool SAVE>
 cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
-  const unsigned ctas = (unsigned)((long long)p.B * p.Hv * p.slices);
-  return DK == 64 && ctas > kSmCount ? run_team<DK, SAVE, DK == 64 ? 2 : 1>(p, ctas, s) : run_team<DK, SAVE, 1>(p, ctas, s);
+  typedef Team<DK, SAVE> C;
+  const unsigned heads = (unsigned)((long long)p.B * p.Hv);
+  cudaError_t e;
+  if (p.nseg > 1) {
+    const auto move = delta_move_kernel<DK, SAVE>;
+    e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, Move<DK>::smem);
+    if (e != cudaSuccess) return e;
+    const int groups = (p.dvp + p.dk + 127) / 128;
+    e = launch_dependent(move, dim3(heads * (p.nseg - 1) * groups), dim3(kMoveThreads), (size_t)Move<DK>::smem, s, p, groups);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(delta_starts_kernel, dim3(heads * (p.dvp / 16)), dim3(256), (size_t)0, s, p);
+    if (e != cudaSuccess) return e;
+  }
+  const auto kern = delta_team_kernel<DK, SAVE>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(heads * p.nseg * p.slices), dim3(kTeamThreads), (size_t)C::smem, s, p);
 }
 template <int DK, bool SAVE>
 cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
@@ -566,14 +732,14 @@ size_t delta_saved_bytes(int B, int L, int Hv, int dk, int dv, int dtype) {
 }
 size_t delta_workspace_bytes(int B, int L, int Hv, int dk, int dv, int dtype, bool save) {
   const DeltaLayout l = delta_layout(B, L, Hv, dk, dv, dtype, save);
-  return l.U + (save ? 0 : l.bytes);
+  return l.beside + (save ? 0 : l.bytes);
 }
 
 cudaError_t launch_delta_fwd(const lion_delta_args& a, void* ws, cudaStream_t s) {
   const bool save = a.saved != nullptr;
   const DeltaLayout l = delta_layout(a.B, a.L, a.Hv, a.dk, a.dv, a.dtype, save);
-  char* U = static_cast<char*>(ws);
-  DeltaP p = delta_params(a, save ? static_cast<char*>(a.saved) : U + l.U, U, save);
+  char* beside = static_cast<char*>(ws);
+  DeltaP p = delta_params(a, save ? static_cast<char*>(a.saved) : beside + l.beside, beside, save);
   p.out = a.out;
   p.h_out = a.h_out;
   const int es = a.dtype == DT_BF16 ? 2 : 4;

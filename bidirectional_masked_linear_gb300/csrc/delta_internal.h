@@ -2,15 +2,19 @@
 // layout of what a forward call keeps, and the parameters of its kernels.
 #pragma once
 
+#include <algorithm>
+
 #include "delta_common.cuh"
 
 namespace lion {
 
 // Every chunk's ChunkData; with `save`, as the gradients take them, then R of
-// every token and the state before every 64th.  U: bytes of U, beside these.
+// every token and the state before every 64th.  Beside these U, and where the
+// walk is cut into segments what they make of a state and the states before them.
 struct DeltaLayout {
-  size_t R, states, bytes, U;
-  int nc, nc64, dvp;
+  size_t R, states, bytes;        // offsets of R and the states, and all of it
+  size_t moves, starts, beside;   // the same of U's neighbours
+  int nc, nc64, dvp, nseg, seglen;
 };
 template <typename T, int DK, bool SAVE>
 constexpr size_t chunk_bytes() {
@@ -29,16 +33,26 @@ inline DeltaLayout delta_layout(int B, int L, int Hv, int dk, int dv, int dtype,
   l.nc = (L + kChunk - 1) / kChunk;
   l.nc64 = (L + kStateChunk - 1) / kStateChunk;
   l.dvp = (dv + 15) / 16 * 16;
-  l.U = up(heads * l.nc * l.dvp * kChunk * sizeof(float));
+  // Segments: walks for half of the SMs' places and more are not cut, as two walks
+  // more have to be made up for; else as many as fill them, of 16 chunks at least
+  // (2 x 24337 x 12 x 64: 12 segments).
+  const long long ctas = (long long)heads * ((dv + kSlice - 1) / kSlice);
+  const long long most = bf16 && 4 * ctas <= kSmCount ? std::min<long long>(2 * kSmCount / ctas, l.nc / 16) : 1;
+  l.seglen = most >= 3 ? (int)((l.nc + most - 1) / most) : l.nc;
+  l.nseg = (l.nc + l.seglen - 1) / l.seglen;
+  const size_t cut = l.nseg > 1 ? heads * l.nseg * dk * sizeof(float) : 0;
+  l.moves = up(heads * l.nc * l.dvp * kChunk * sizeof(float));
+  l.starts = l.moves + up(cut * (l.dvp + dk));
+  l.beside = l.starts + up(cut * dv);
   l.R = up(heads * l.nc * chunk);
   l.states = l.R + (save ? up(heads * l.nc * kChunk * l.dvp * es) : 0);
   l.bytes = l.states + (save ? up(heads * l.nc64 * l.dvp * DK * es) : 0);
   return l;
 }
 
-// kept: `bytes` of the layout, U: its `U`.
+// kept: `bytes` of the layout, beside: its `beside`.
 template <typename Args>
-DeltaP delta_params(const Args& a, char* kept, char* U, bool save) {
+DeltaP delta_params(const Args& a, char* kept, char* beside, bool save) {
   const DeltaLayout l = delta_layout(a.B, a.L, a.Hv, a.dk, a.dv, a.dtype, save);
   DeltaP p = {};
   p.q = a.q;
@@ -49,7 +63,11 @@ DeltaP delta_params(const Args& a, char* kept, char* U, bool save) {
   p.lengths = a.lengths;
   p.h0 = a.h0;
   p.chunks = kept;
-  p.U = reinterpret_cast<float*>(U);
+  p.U = reinterpret_cast<float*>(beside);
+  p.moves = reinterpret_cast<float*>(beside + l.moves);
+  p.starts = reinterpret_cast<float*>(beside + l.starts);
+  p.nseg = l.nseg;
+  p.seglen = l.seglen;
   if (save) {
     p.R = kept + l.R;
     p.states = kept + l.states;
