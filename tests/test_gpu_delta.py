@@ -464,3 +464,25 @@ def test_delta_of_more_than_two_to_the_31_values():
         e = delta.delta_bwd(one[2], *one, saved=s.saved)
         for x in ("dq", "dk", "dv", "dg", "dbeta"):
             assert torch.equal(getattr(e, x), getattr(r, x)[:, :, h:h + 1]), x
+
+
+@pytest.mark.parametrize("reverse", (False, True))
+@pytest.mark.parametrize("dk,dv", ((64, 64), (128, 72), (24, 8)))
+def test_delta_in_segments(dk, dv, reverse):
+    """Long sequences of few heads are walked in segments; some of the batch end before the last ones, one has none."""
+    n = (1700, 620, 32, 0)
+    a, h0, dout = _inputs(4, 1700, 1, 1, dk, dv, "bf16", dk, decay=6.0)
+    r = ref.delta(**{x: _f64(y) for x, y in a.items()}, scale=dk ** -0.5, h0=_f64(h0), lengths=n, reverse=reverse,
+                  dout=_f64(dout), bf16=True)
+    for b in range(4):
+        for x in (*a.values(), dout):
+            x[b, n[b]:] = float("nan")
+    dev = {x: y.cuda() for x, y in a.items()}
+    how = dict(h0=h0.cuda(), lengths=torch.tensor(n, dtype=torch.int32, device="cuda"), reverse=reverse)
+    f = delta.delta_fwd(**dev, **how, return_state=True, save=True)
+    g = delta.delta_bwd(dout.cuda(), **dev, **how, saved=f.saved)
+    for x, y in (("out", f.out), ("h", f.h), ("dq", g.dq), ("dk", g.dk), ("dv", g.dv), ("dg", g.dg),
+                 ("dbeta", g.dbeta), ("dh0", g.dh0)):
+        _exact_enough(x, y, r[x])
+    assert torch.equal(f.h[3], h0[3].cuda()) and bool((f.out[2, 32:] == 0).all())
+    assert _equal(delta.delta_fwd(**dev, **how, return_state=True)[:2], f[:2])
