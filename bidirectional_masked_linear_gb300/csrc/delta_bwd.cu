@@ -858,8 +858,16 @@ cudaError_t run_grad_any(const DeltaP& p, float*, cudaStream_t s) {
   return run_grad<float, DK, 32>(p, s);
 }
 
+template <typename T, int DK>
+cudaError_t run_alone(const DeltaP& p, cudaStream_t s) {
+  const auto kern = delta_back_kernel<T, DK>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Back<T, DK>::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)Back<T, DK>::smem, s, p);
+}
 template <int DK>
 cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
+  if (crowded(p)) return run_alone<__nv_bfloat16, DK>(p, s);
   const auto kern = delta_back_team_kernel<DK>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BackTeam<DK>::smem);
   if (e != cudaSuccess) return e;
@@ -868,11 +876,7 @@ cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
 }
 template <int DK>
 cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
-  const auto kern = delta_back_kernel<float, DK>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Back<float, DK>::smem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)Back<float, DK>::smem,
-                          s, p);
+  return run_alone<float, DK>(p, s);
 }
 
 template <typename T, int DK>

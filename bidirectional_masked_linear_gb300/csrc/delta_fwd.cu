@@ -701,11 +701,27 @@ __global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
   copy_wait<0>();
 }
 
+template <typename T, int DK, bool SAVE>
+cudaError_t run_alone(const DeltaP& p, cudaStream_t s) {
+  typedef Chain<T, DK, SAVE> C;
+  const auto kern = delta_chain_kernel<T, DK, SAVE>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)C::smem, s, p);
+}
+template <int DK, bool SAVE>
+cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
+  return run_alone<float, DK, SAVE>(p, s);
+}
+// Helpers make a chunk's walk shorter and an SM hold fewer of them: with more
+// CTAs than two an SM warps alone are ahead (64 x 197 x 12 x 64, 768 CTAs: 47
+// against 52 us, back 55 against 67; 16 x 4096 x 8 x 64, 128: 172 against 146).
 template <int DK, bool SAVE>
 cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
   typedef Team<DK, SAVE> C;
   const unsigned heads = (unsigned)((long long)p.B * p.Hv);
   cudaError_t e;
+  if (crowded(p)) return run_alone<__nv_bfloat16, DK, SAVE>(p, s);
   if (p.nseg > 1) {
     const auto move = delta_move_kernel<DK, SAVE>;
     e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, Move<DK>::smem);
@@ -723,15 +739,6 @@ cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(heads * p.nseg * p.slices), dim3(kTeamThreads), (size_t)C::smem, s, p);
 }
-template <int DK, bool SAVE>
-cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
-  typedef Chain<float, DK, SAVE> C;
-  const auto kern = delta_chain_kernel<float, DK, SAVE>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)C::smem, s, p);
-}
-
 template <typename T, int DK, bool SAVE>
 cudaError_t run_chain(const DeltaP& p, cudaStream_t s) {
   const auto prep = delta_prep_kernel<T, DK, SAVE>;
