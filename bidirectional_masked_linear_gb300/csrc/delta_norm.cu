@@ -10,8 +10,6 @@
 // warp takes a token, its groups of lanes the token's heads.  The four
 // angles of a lane belong to all heads of the token: the groups work them out
 // between them, one each at d = 64.
-#include <algorithm>
-
 #include "lion_internal.h"
 #include "ssm_common.cuh"
 
@@ -31,7 +29,7 @@ struct QkP {
   float* part;             // [CTA][2][d]
   long long x_ld[2];
   long long tokens;
-  unsigned per;            // items a token
+  int per, at_once;        // a token's parts, and of each the heads a lane has
   int L, H[2], d, rp;      // rp: lanes of a head whose values turn (rot / 8)
   int interleaved;
   float inv_n, eps;
@@ -162,8 +160,9 @@ constexpr int heads_at_once() {
   return sizeof(T) == 2 ? (BWD ? 3 : 6) : (BWD ? 2 : 3);
 }
 
-// An item is a token's heads as far as a warp has them under way at once; its
-// values are read while the item before it is worked on.
+// A warp goes through its tokens' heads in parts, as many at a time as a lane
+// holds (evenly: 8 of them in two parts are 4 and 4); a part's values are read
+// while the part before it is worked on.
 template <typename T, int LPH, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
   constexpr int NG = 32 / LPH, U = heads_at_once<T, BWD>();
@@ -180,12 +179,11 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
   turn.init(q, lane, p);
   float dw[BWD ? 2 : 1][8] = {};
   const int heads = q.H[0] + q.H[1];
-  const unsigned per = q.per;
   __syncthreads();
 
   Raw<T> x[U], dy[BWD ? U : 1];
-  const auto fetch = [&](long long t, unsigned part) {
-    const int h0 = (int)part * NG * U + g;
+  const auto fetch = [&](long long t, int part) {
+    const int h0 = part * NG * q.at_once + g;
     const T* xq = static_cast<const T*>(q.x[0]) + t * q.x_ld[0];
     const T* xk = static_cast<const T*>(q.x[1]) + t * q.x_ld[1] - (long long)q.H[0] * q.d;
     const T* dq = static_cast<const T*>(q.dy[0]) + t * q.H[0] * q.d;
@@ -193,7 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int h = h0 + i * NG;
-      if (there && h < heads) {
+      if (there && i < q.at_once && h < heads) {
         const T* s = (h < q.H[0] ? xq : xk) + (long long)h * q.d;
         x[i].a = run_of<WIDE>(s + a);
         x[i].b = run_of<WIDE>(s + b);
@@ -208,35 +206,33 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
       }
     }
   };
-  const unsigned hop = gridDim.x * kWarps, hop_t = hop / per, hop_part = hop % per;
-  const unsigned first = blockIdx.x * kWarps + warp;
-  long long tn = first / per;
-  unsigned pn = first % per;
-  if (tn < q.tokens) fetch(tn, pn);
+  const long long hop = (long long)gridDim.x * kWarps;
+  long long tn = (long long)blockIdx.x * kWarps + warp;
+  int pn = 0;
+  float c[4], s[4];
+  if (tn < q.tokens) fetch(tn, 0);
   while (tn < q.tokens) {
     const long long t = tn;
-    const int h0 = (int)pn * NG * U + g;
+    const int part = pn, h0 = part * NG * q.at_once + g;
     Raw<T> xc[U], dc[BWD ? U : 1];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       xc[i] = x[i];
       if (BWD) dc[i] = dy[i];
     }
-    tn += hop_t;
-    pn += hop_part;
-    if (pn >= per) {
-      pn -= per;
-      ++tn;
+    if (++pn == q.per) {
+      pn = 0;
+      tn += hop;
     }
     if (tn < q.tokens) fetch(tn, pn);
-    float c[4], s[4];
-    if (q.rp) turn.at(q.positions ? q.positions[t] : q.tokens >> 32 ? (int)(t % q.L) : (int)((unsigned)t % (unsigned)q.L), p, c, s);
+    if (q.rp && part == 0)
+      turn.at(q.positions ? q.positions[t] : q.tokens >> 32 ? (int)(t % q.L) : (int)((unsigned)t % (unsigned)q.L), p, c, s);
     T* yq = static_cast<T*>(q.y[0]) + t * q.H[0] * q.d;
     T* yk = static_cast<T*>(q.y[1]) + (t * q.H[1] - q.H[0]) * q.d;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int h = h0 + i * NG;
-      if (h - g >= heads) break;   // of all lanes
+      if (i >= q.at_once || h - g >= heads) break;   // of all lanes
       const int m = h >= q.H[0];
       float v[8], w[8];
       values(xc[i].a, v);
@@ -246,7 +242,7 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-      const float r = 1.f / sqrtf(fmaf(head_sum<LPH>(ss), q.inv_n, q.eps));
+      const float r = rsqrtf(fmaf(head_sum<LPH>(ss), q.inv_n, q.eps));   // to 2^-22
       float o[8];
       if (!BWD) {
 #pragma unroll
@@ -305,25 +301,19 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
 }
 
 int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
-// Warps' items a token.
-int items_of(int heads, int d, int at_once) {
-  const int by = 32 / lanes_of(d) * at_once;
-  return (heads + by - 1) / by;
-}
-// CTAs: an item a warp while that fills the SMs, else four CTAs an SM that go
+// CTAs: a token a warp while that fills the SMs, else four CTAs an SM that go
 // round, as registers have room for (the angles' frequencies are set up once a warp).
-int qknorm_ctas(long long items) {
-  const long long want = (items + kWarps - 1) / kWarps;
+int qknorm_ctas(long long tokens) {
+  const long long want = (tokens + kWarps - 1) / kWarps;
   return (int)(want < 4 * kSmCount ? want : 4 * kSmCount);
-}
-int bwd_at_once(int dtype) {
-  return dtype == DT_BF16 ? heads_at_once<__nv_bfloat16, true>() : heads_at_once<float, true>();
 }
 
 template <typename T, bool BWD>
 cudaError_t run(QkP q, bool wide, cudaStream_t s) {
-  q.per = items_of(q.H[0] + q.H[1], q.d, heads_at_once<T, BWD>());
-  const dim3 grid(qknorm_ctas(q.tokens * q.per)), block(32 * kWarps);
+  const int by = 32 / lanes_of(q.d), turns = (q.H[0] + q.H[1] + by - 1) / by;
+  q.per = (turns + heads_at_once<T, BWD>() - 1) / heads_at_once<T, BWD>();
+  q.at_once = (turns + q.per - 1) / q.per;
+  const dim3 grid(qknorm_ctas(q.tokens)), block(32 * kWarps);
   if (q.d <= 64)
     wide ? qknorm_kernel<T, 8, true, BWD><<<grid, block, 0, s>>>(q) : qknorm_kernel<T, 8, false, BWD><<<grid, block, 0, s>>>(q);
   else if (q.d <= 128)
@@ -372,10 +362,8 @@ cudaError_t launch_qknorm_fwd(const lion_qknorm_args& a, cudaStream_t s) {
   return a.dtype == DT_BF16 ? run<__nv_bfloat16, false>(q, wide, s) : run<float, false>(q, wide, s);
 }
 
-// Of the type that makes more items; they go round on as many CTAs at most.
-size_t qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d) {
-  const int per = items_of(Hq + Hk, d, std::min(bwd_at_once(DT_BF16), bwd_at_once(DT_FP32)));
-  return sizeof(float) * 2 * d * (size_t)qknorm_ctas((long long)B * L * per);
+size_t qknorm_bwd_workspace_bytes(int B, int L, int, int, int d) {
+  return sizeof(float) * 2 * d * (size_t)qknorm_ctas((long long)B * L);
 }
 
 cudaError_t launch_qknorm_bwd(const lion_qknorm_bwd_args& a, void* ws, cudaStream_t s) {
@@ -390,7 +378,7 @@ cudaError_t launch_qknorm_bwd(const lion_qknorm_bwd_args& a, void* ws, cudaStrea
                     on4(a.dq_out, 0, es) && on4(a.dk_out, 0, es);
   const cudaError_t e = a.dtype == DT_BF16 ? run<__nv_bfloat16, true>(q, wide, s) : run<float, true>(q, wide, s);
   if (e != cudaSuccess || !ws) return e;
-  const int ctas = qknorm_ctas(q.tokens * items_of(a.Hq + a.Hk, a.d, bwd_at_once(a.dtype)));
+  const int ctas = qknorm_ctas(q.tokens);
   return launch_sum_parts(q.part, ctas, 2LL * a.d, a.d, a.dq_weight, a.d, a.dk_weight, 0, nullptr, s);
 }
 
