@@ -94,9 +94,11 @@ __global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
   unsigned char* buf = smem + NST * L::bytes + w * out_bytes<T>();
-  const long long bh = blockIdx.x / p.slices;
-  const int slice = (int)(blockIdx.x - bh * p.slices);
-  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const long long at = blockIdx.x / p.slices;
+  const int slice = (int)(blockIdx.x - at * p.slices), rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv);
+  const int b = by_length(p, rank);
+  const long long bh = (long long)b * p.Hv + hv;
+  const int hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
   const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
   const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
@@ -229,9 +231,11 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x & 127, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
   const bool helper = threadIdx.x >= 128;
-  const long long bh = blockIdx.x / p.slices;
-  const int slice = (int)(blockIdx.x - bh * p.slices);
-  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const long long at = blockIdx.x / p.slices;
+  const int slice = (int)(blockIdx.x - at * p.slices), rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv);
+  const int b = by_length(p, rank);
+  const long long bh = (long long)b * p.Hv + hv;
+  const int hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
   const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
   const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer 4 swaps behind

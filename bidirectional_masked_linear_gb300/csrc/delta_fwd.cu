@@ -268,9 +268,11 @@ __global__ void __launch_bounds__(128) delta_chain_kernel(const DeltaP p) {
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
   unsigned char* buf = smem + NST * L::bytes + w * out_bytes<T>();
-  const long long bh = blockIdx.x / p.slices;
-  const int slice = (int)(blockIdx.x - bh * p.slices);
-  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const long long at = blockIdx.x / p.slices;
+  const int slice = (int)(blockIdx.x - at * p.slices), rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv);
+  const int b = by_length(p, rank);
+  const long long bh = (long long)b * p.Hv + hv;
+  const int hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
   const int m0 = slice * kSlice + 16 * w;              // the warp's first column of the state
   const int cols = p.dv - m0 < 16 ? p.dv - m0 : 16;    // 0 or less: none
@@ -395,9 +397,11 @@ __global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_ker
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x & 127, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
   const bool helper = threadIdx.x >= 128;
-  const long long part = blockIdx.x / p.slices, bh = part / p.nseg;
-  const int slice = (int)(blockIdx.x - part * p.slices), seg = (int)(part - bh * p.nseg);
-  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const long long part = blockIdx.x / p.slices, at = part / p.nseg;
+  const int slice = (int)(blockIdx.x - part * p.slices), seg = (int)(part - at * p.nseg);
+  const int rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv), b = by_length(p, rank);
+  const long long bh = (long long)b * p.Hv + hv;
+  const int hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), all = (n + kChunk - 1) / kChunk, c0 = seg * p.seglen;
   const bool ends = seg == p.nseg - 1;
   const int nc = all - c0 < 0 ? 0 : ends || all - c0 < p.seglen ? all - c0 : p.seglen;   // chunks of the segment, from c0 on
