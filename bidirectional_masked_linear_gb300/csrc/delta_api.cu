@@ -70,7 +70,8 @@ lion_status lion_qknorm_fwd(const lion_qknorm_args* a) {
   if (st == LION_ERR_INVALID_ARG) return st;
   const Pointers ptr;
   const size_t es = esize(a->dtype);
-  if (!ptr.need(a->q_out, es) || !ptr.need(a->k_out, es)) return LION_ERR_INVALID_ARG;
+  if (!ptr.need(a->q_out, es) || !ptr.need(a->k_out, es) || a->q_out == a->q || a->k_out == a->k)   // lines on their way
+    return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_qknorm_fwd(*a, a->stream));
 }
@@ -87,6 +88,7 @@ lion_status lion_qknorm_bwd(const lion_qknorm_bwd_args* a) {
   const Pointers ptr;
   const size_t es = esize(a->dtype);
   if (!ptr.need(a->dq_out, es) || !ptr.need(a->dk_out, es) || !ptr.need(a->dq, es) || !ptr.need(a->dk, es) ||
+      a->dq == a->q || a->dk == a->k || a->dq == a->dq_out || a->dk == a->dk_out ||
       !ptr.maybe(a->dq_weight, 4) || !ptr.maybe(a->dk_weight, 4) || (a->dq_weight && !a->q_weight) ||
       (a->dk_weight && !a->k_weight))
     return LION_ERR_INVALID_ARG;
@@ -112,7 +114,8 @@ lion_status lion_delta_fwd(const lion_delta_args* a) {
   const lion_status st = delta_check(*a);
   if (st == LION_ERR_INVALID_ARG) return st;
   const Pointers ptr;
-  if (!ptr.need(a->out, esize(a->dtype)) || !ptr.maybe(a->h_out, 16) || (a->h0 && a->h_out == a->h0))
+  if (!ptr.need(a->out, esize(a->dtype)) || !ptr.maybe(a->h_out, 16) || (a->h0 && a->h_out == a->h0) ||
+      a->out == a->q || a->out == a->k || a->out == a->v)
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(a->workspace, a->workspace_bytes,
@@ -132,7 +135,8 @@ lion_status lion_delta_bwd(const lion_delta_bwd_args* a) {
   const Pointers ptr;
   const size_t es = esize(a->dtype);
   if (!ptr.need(a->dout, es) || !ptr.need(a->dq, es) || !ptr.need(a->dk_out, es) || !ptr.need(a->dv_out, es) ||
-      !ptr.need(a->dg, es) || !ptr.need(a->dbeta, es) || !ptr.maybe(a->dh0, 16))
+      !ptr.need(a->dg, es) || !ptr.need(a->dbeta, es) || !ptr.maybe(a->dh0, 16) || a->dv_out == a->dout ||
+      a->dq == a->q || a->dk_out == a->k || a->dg == a->g || a->dbeta == a->beta)   // other CTAs still read these
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(

@@ -757,9 +757,13 @@ size_t lion_qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d, int 
  *   adjacent tokens' decays has to be finite in float32).
  *   h0, h_out  [B][Hv][dk][dv] float32 or NULL: the state before the first
  *   token (NULL: zeros) and after the last one.  h_out may not be h0.
+ *   Values of the tokens that a sequence has are finite: others reach all
+ *   tokens that share their 32, earlier ones among them.
  *   saved  device, 256-byte aligned, of lion_delta_saved_bytes, or NULL: what
  *   lion_delta_bwd goes on from.
  *   Keys longer than sqrt(2 / beta) make the state grow.
+ *   Long sequences of few heads are walked in segments, whose number B, Hv, L
+ *   and the head sizes decide: results of other batches then differ by roundings.
  */
 typedef struct {
   const void* q;
