@@ -486,3 +486,57 @@ def test_delta_in_segments(dk, dv, reverse):
         _exact_enough(x, y, r[x])
     assert torch.equal(f.h[3], h0[3].cuda()) and bool((f.out[2, 32:] == 0).all())
     assert _equal(delta.delta_fwd(**dev, **how, return_state=True)[:2], f[:2])
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "fp32"))
+@pytest.mark.parametrize("B,Hv,dk,dv,reverse", ((160, 2, 64, 64, False), (102, 3, 40, 24, True), (90, 2, 128, 128, False)))
+def test_delta_of_many_sequences(B, Hv, dk, dv, reverse, dtype):
+    """More walks than an SM holds at once, of batches above and below the 128 sequences that are ordered by length."""
+    L = 70
+    a, h0, dout = _inputs(B, L, 1, Hv, dk, dv, dtype, B)
+    n = [(37 * b) % (L + 1) for b in range(B)]
+    r = ref.delta(**{x: _f64(y) for x, y in a.items()}, scale=dk ** -0.5, h0=_f64(h0), lengths=n, reverse=reverse,
+                  dout=_f64(dout), bf16=dtype == "bf16")
+    for b in range(B):
+        for x in (*a.values(), dout):
+            x[b, n[b]:] = float("nan")
+    dev = {x: y.cuda() for x, y in a.items()}
+    how = dict(h0=h0.cuda(), lengths=torch.tensor(n, dtype=torch.int32, device="cuda"), reverse=reverse)
+    f = delta.delta_fwd(**dev, **how, return_state=True, save=True)
+    g = delta.delta_bwd(dout.cuda(), **dev, **how, saved=f.saved)
+    for x, y in (("out", f.out), ("h", f.h), ("dq", g.dq), ("dk", g.dk), ("dv", g.dv), ("dg", g.dg),
+                 ("dbeta", g.dbeta), ("dh0", g.dh0)):
+        _check(x, y, r[x], r["~" + x])
+        _exact_enough(x, y, r[x])
+    assert _equal(delta.delta_fwd(**dev, **how, return_state=True)[:2], f[:2])
+
+
+def test_results_in_place_of_inputs_are_refused():
+    """A token's results are written while others are still read."""
+    a, h0, _ = _inputs(1, 40, 1, 1, 64, 64, "bf16", 1)
+    dev = {x: y.cuda() for x, y in a.items()}
+    before = {x: y.clone() for x, y in dev.items()}
+    for call in (*(lambda x=x: delta.delta_fwd(**dev, out=dev[x]) for x in "qkv"),
+                 lambda: delta.qknorm_fwd(dev["q"], dev["k"], q_out=dev["q"]),
+                 lambda: delta.qknorm_fwd(dev["q"], dev["k"], k_out=dev["k"])):
+        with pytest.raises(lion.LionError) as e:
+            call()
+        assert e.value.status == lion.ERR_INVALID_ARG and _equal(before.values(), dev.values())
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspaces, do not meet."""
+    sets = [_inputs(2, 900, 2, 4, 64, 64, "bf16", s) for s in (1, 2)]
+    sets = [({x: y.cuda() for x, y in a.items()}, h.cuda(), d.cuda()) for a, h, d in sets]
+
+    def train(a, h0, dout, s=None):
+        f = delta.delta_fwd(**a, h0=h0, return_state=True, save=True, stream=s)
+        return (*f[:2], *delta.delta_bwd(dout, **a, h0=h0, saved=f.saved, stream=s))
+
+    want = [train(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = [train(*x, s) for x, s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        assert all(_equal(x, y) for x, y in zip(got, want))
