@@ -91,6 +91,21 @@ def load():
     return _lib
 
 
+def _like(stream, x):
+    """An uninitialised contiguous tensor of x's shape and type that belongs to `stream`."""
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _new(stream, x.shape, x.dtype, x)
+
+
+def _result(name, out, stream, x):
+    """The caller's tensor for a result like x, or a new one, and its address."""
+    if out is None:
+        out = _like(stream, x)
+        return out, out.data_ptr()
+    return out, _tight(name, out, x.dtype, x.shape)
+
+
 # ------------------------------------------------------- norms of q and k
 
 class QKNormGrads(NamedTuple):
@@ -143,10 +158,9 @@ def qknorm_fwd(q, k, q_weight=None, k_weight=None, norm="l2", eps=1e-6, freqs=No
     of the same place or, with ``interleaved``, adjacent ones."""
     lib, code = load(), _code(q)
     sizes, tokens, ptrs = _qknorm_args(q, k, q_weight, k_weight, freqs, positions)
-    qo = _new(stream, q.shape, q.dtype, q) if q_out is None else q_out
-    ko = _new(stream, k.shape, q.dtype, q) if k_out is None else k_out
-    a = _QKNorm_pack(*ptrs, _tight("q_out", qo, q.dtype, q.shape), _tight("k_out", ko, q.dtype, k.shape), *tokens,
-                     *sizes, _norm_kind(norm), int(interleaved), eps, code, _handle(stream, q))
+    qo, qp = _result("q_out", q_out, stream, q)
+    ko, kp = _result("k_out", k_out, stream, k)
+    a = _QKNorm_pack(*ptrs, qp, kp, *tokens, *sizes, _norm_kind(norm), int(interleaved), eps, code, _handle(stream, q))
     _check(lib.lion_qknorm_fwd(a))
     return qo, ko
 
@@ -157,11 +171,11 @@ def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm="l2", ep
     is None where there is no weight)."""
     lib, code = load(), _code(q)
     sizes, tokens, ptrs = _qknorm_args(q, k, q_weight, k_weight, freqs, positions)
-    T, f32 = q.dtype, torch.float32
+    T = q.dtype
     dqp, dkp = _tight("dq_out", dq_out, T, q.shape), _tight("dk_out", dk_out, T, k.shape)
-    dq, dk = _new(stream, q.shape, T, q), _new(stream, k.shape, T, q)
-    dwq = None if q_weight is None else _new(stream, q_weight.shape, f32, q)
-    dwk = None if k_weight is None else _new(stream, k_weight.shape, f32, q)
+    dq, dk = _like(stream, q), _like(stream, k)
+    dwq = None if q_weight is None else _like(stream, q_weight)
+    dwk = None if k_weight is None else _like(stream, k_weight)
     weights = int(dwq is not None or dwk is not None)
     ws, nb, _keep = _workspace(workspace, q, stream, "qknorm_bwd", *sizes[:5], weights)
     a = _QKNormBwd_pack(dqp, dkp, *ptrs, dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), *tokens, *sizes,
@@ -254,11 +268,11 @@ def delta_fwd(q, k, v, g, beta, scale=None, h0=None, lengths=None, reverse=False
     lib, code = load(), _code(q)
     sizes, tokens, ptrs = _delta_args(q, k, v, g, beta, h0, lengths)
     B, L, Hk, Hv, dk, dv = sizes
-    y = _new(stream, v.shape, q.dtype, q) if out is None else out
+    y, yp = _result("out", out, stream, v)
     h = _new(stream, (B, Hv, dk, dv), torch.float32, q) if return_state else None
     saved = _new(stream, (delta_saved_bytes(*sizes, code),), torch.uint8, q) if save else None
     ws, nb, _keep = _workspace(workspace, q, stream, "delta", *sizes, code, int(save))
-    a = _Delta_pack(*ptrs, _tight("out", y, q.dtype, v.shape), _ptr(h), _ptr(saved), *tokens, *sizes,
+    a = _Delta_pack(*ptrs, yp, _ptr(h), _ptr(saved), *tokens, *sizes,
                     dk ** -0.5 if scale is None else scale, int(reverse), code, ws, nb, _handle(stream, q))
     _check(lib.lion_delta_fwd(a))
     return DeltaOut(y, h, saved)
@@ -274,8 +288,8 @@ def delta_bwd(dout, q, k, v, g, beta, scale=None, h0=None, lengths=None, reverse
     T = q.dtype
     dop = _tight("dout", dout, T, v.shape)
     sp = 0 if saved is None else _tight("saved", saved, torch.uint8, (delta_saved_bytes(*sizes, code),))
-    dq, dk, dv, dg, db = (_new(stream, t.shape, T, q) for t in (q, k, v, g, beta))
-    dh0 = None if h0 is None else _new(stream, h0.shape, torch.float32, q)
+    dq, dk, dv, dg, db = (_like(stream, t) for t in (q, k, v, g, beta))
+    dh0 = None if h0 is None else _like(stream, h0)
     ws, nb, _keep = _workspace(workspace, q, stream, "delta_bwd", *sizes, code, int(saved is not None))
     a = _DeltaBwd_pack(dop, *ptrs, sp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), db.data_ptr(),
                        _ptr(dh0), *tokens, *sizes, sizes[4] ** -0.5 if scale is None else scale, int(reverse), code, ws,
@@ -293,11 +307,7 @@ def delta_step(h, q, k, v, g, beta, scale=None, out=None, stream=None):
     T, f32 = q.dtype, torch.float32
     B, Hk, dk = q.shape
     Hv, dv = v.shape[1:]
-    if out is None:
-        y = _new(stream, (B, Hv, dv), T, q)
-        yp = y.data_ptr()
-    else:
-        y, yp = out, _tight("out", out, T, (B, Hv, dv))
+    y, yp = _result("out", out, stream, v)
     a = _DeltaStep_pack(_tight("h", h, f32, (B, Hv, dk, dv)), _tight("q", q, T, (B, Hk, dk)),
                         _tight("k", k, T, (B, Hk, dk)), _tight("v", v, T, (B, Hv, dv)), _tight("g", g, T, (B, Hv)),
                         _tight("beta", beta, T, (B, Hv)), yp, B, Hk, Hv, dk, dv, dk ** -0.5 if scale is None else scale,

@@ -193,10 +193,11 @@ def _token(name, t, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     B, L = shape[:2]
     s, run = t.stride(), 1
-    for k in range(t.dim() - 1, 1, -1):
-        if t.shape[k] != 1 and s[k] != run:
-            raise ValueError(f"{name}: the values of a token must be adjacent")
-        run *= t.shape[k]
+    if s[-1] != 1 or len(s) == 4 and s[2] != shape[3]:   # not so of dimensions of one element, whose strides do not matter
+        for k in range(t.dim() - 1, 1, -1):
+            if shape[k] != 1 and s[k] != run:
+                raise ValueError(f"{name}: the values of a token must be adjacent")
+            run *= shape[k]
     if L == 1:
         ld = s[0] if B > 1 else width
     else:
