@@ -75,8 +75,7 @@ __global__ void __launch_bounds__(32) delta_back_prep_kernel(const DeltaP p) {
 // As delta_chain_kernel with dS^T in the registers:
 //   X^T = dO^T P + beta e^(G_C - G) o (dS'^T K^T);  dR^T = X^T T
 //   dS^T = e^G_C dS'^T + (scale e^G o dO)^T Q - X^T W
-// Bound as that one is: 64 x 197 x 12 x 64 in bfloat16 54 us, 3 x 1021 x 6 x 40 x
-// 72 in float32 76.
+// Bound as that one is: 64 x 197 x 12 x 64 in bfloat16 54 us.
 
 template <typename T, int DK>
 struct Back {
@@ -205,44 +204,47 @@ __global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
   zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, lane);
 }
 
-// The same in bfloat16 with a helper to each warp, which has the loads, dR, what
-// the other gradients take, and dO's part of the next dS, ready when the warp
-// has X: 1330 ns a chunk of 64 columns where an SM has one CTA (16 x 4096 x 8 x 64:
-// 171 us, 34% of the tensor cores', 30% of the issue slots).
+// The same with a helper to each warp, which has the loads, dR, what the other
+// gradients take, and dO's part of the next dS, ready when the warp has X: 1330 ns
+// a chunk of 64 columns where an SM has one CTA (16 x 4096 x 8 x 64: 171 us, 34%
+// of the tensor cores', 30% of the issue slots).
 
-template <int DK>
+template <typename T, int DK, int PAIRS>
 struct BackTeam {
-  typedef __nv_bfloat16 T;
-  typedef ChunkData<T, DK, true, false> D;
+  static constexpr int width = 16 * PAIRS, half = 32 * PAIRS;
+  static constexpr bool KQ = sizeof(T) == 4;
+  typedef ChunkData<T, DK, true, KQ> D;
   static constexpr int row = kChunk * DK * 2;
-  // a stage: k, q, coefficients, -W and T, the slice of P^T dO
-  static constexpr int k = 0, q = row, coef = 2 * row, W = coef + (D::W - D::coef), Tm = W + (D::Tm - D::W);
-  static constexpr int Z = Tm + (D::bytes - D::Tm), bytes = Z + kSlice * kChunk * 4;
+  // a stage: q, k, coefficients, -W and T, the slice of P^T dO
+  static constexpr int q = 0, k = D::NI * row, coef = 2 * D::NI * row, W = coef + (D::W - D::coef), Tm = W + (D::Tm - D::W);
+  static constexpr int Z = Tm + (D::bytes - D::Tm), bytes = Z + width * kChunk * 4;
   static constexpr int stages = 3;
-  static constexpr int S = 0, X = DK / 16 * 512, swap = X + 4 * 512;   // a warp's buffer to its helper
+  static constexpr int S = 0, X = KQ ? 0 : DK / 16 * 512, swap = X + 2 * D::NS * 512;   // a warp's buffer to its helper
   static constexpr int Y = DK / 8 * 512;                               // and back: dO's part of dS^T
-  static constexpr int swaps = stages * bytes, ys = swaps + 2 * 4 * swap, out = ys + 4 * Y;
-  static constexpr int smem = out + 4 * out_bytes<T>();
+  static constexpr int swaps = stages * bytes, ys = swaps + 2 * PAIRS * swap, out = ys + PAIRS * Y;
+  static constexpr int smem = out + PAIRS * out_bytes<T>();
+  static_assert(smem <= 227 * 1024 - 1024);
 };
 
-template <int DK>
-__global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const DeltaP p) {
-  typedef __nv_bfloat16 T;
-  typedef BackTeam<DK> C;
+template <typename T, int DK, int PAIRS>
+__global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const DeltaP p, int slices) {
+  typedef BackTeam<T, DK, PAIRS> C;
   typedef typename C::D D;
-  constexpr int NST = C::stages, NS = 2, PER = kStateChunk / kChunk;
+  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, PER = kStateChunk / kChunk;
+  constexpr int HALF = C::half;
+  constexpr bool KQ = C::KQ;
   extern __shared__ __align__(128) unsigned char smem[];
   const unsigned base = shared_at(smem);
-  const int tid = threadIdx.x & 127, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
-  const bool helper = threadIdx.x >= 128;
-  const long long at = blockIdx.x / p.slices;
-  const int slice = (int)(blockIdx.x - at * p.slices), rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv);
+  const int tid = threadIdx.x & (HALF - 1), lane = tid & 31, w = tid >> 5, q4 = lane & 3;
+  const bool helper = threadIdx.x >= HALF;
+  const long long at = blockIdx.x / slices;
+  const int slice = (int)(blockIdx.x - at * slices), rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv);
   const int b = by_length(p, rank);
   const long long bh = (long long)b * p.Hv + hv;
   const int hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
-  const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
-  const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer 4 swaps behind
+  const int m0 = slice * C::width + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
+  const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer PAIRS swaps behind
   const unsigned ys = base + C::ys + w * C::Y;
   wait_prior();
   if (helper) {
@@ -250,17 +252,21 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
     const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
     const Rows<T> xv = rows_of<T>(p, p.dv_out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
     const char* chunks = p.chunks + bh * p.nc * D::bytes;
-    const float* Zs = p.U + (bh * p.nc * p.dvp + slice * kSlice) * kChunk;
+    const float* Zs = p.U + (bh * p.nc * p.dvp + slice * C::width) * kChunk;
     const uint4* dO = p.dO + (bh * p.nc * (p.dvp / 16) + m0 / 16) * 2 * NS * 32 + lane;
-    const int rows = p.dvp - slice * kSlice < kSlice ? p.dvp - slice * kSlice : kSlice;
+    const int rows = p.dvp - slice * C::width < C::width ? p.dvp - slice * C::width : C::width;
     unsigned char* buf = smem + C::out + w * out_bytes<T>();
     const auto load = [&](int i) {   // the i-th chunk from the end
       const int c = nc - 1 - i;
       const unsigned st = base + i % NST * C::bytes;
-      load_tile<DK, kChunk, 128>(st + C::k, 0, xk, c * kChunk, n, p.dk, p.k_wide, tid);
-      load_tile<DK, kChunk, 128>(st + C::q, 0, xq, c * kChunk, n, p.dk, p.q_wide, tid);
-      copy_block<D::bytes - D::coef, 128>(st + C::coef, chunks + (long long)c * D::bytes + D::coef, tid);
-      copy_slice<128>(st + C::Z, Zs + (long long)c * p.dvp * kChunk, rows, tid);
+      if (KQ) {
+        copy_block<2 * NI * C::row, HALF>(st, chunks + (long long)c * D::bytes, tid);
+      } else {
+        load_tile<DK, kChunk, HALF>(st + C::k, 0, xk, c * kChunk, n, p.dk, p.k_wide, tid);
+        load_tile<DK, kChunk, HALF>(st + C::q, 0, xq, c * kChunk, n, p.dk, p.q_wide, tid);
+      }
+      copy_block<D::bytes - D::coef, HALF>(st + C::coef, chunks + (long long)c * D::bytes + D::coef, tid);
+      copy_slice<C::width, HALF>(st + C::Z, Zs + (long long)c * p.dvp * kChunk, rows, tid);
     };
     uint4 g[2][NS];
     const auto fetch = [&](int i) {
@@ -280,10 +286,14 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
       copy_commit();
       if (i + 2 < nc) {   // as in the forward walk
         const long long c = nc - 3 - i;
-        to_l2<D::bytes - D::coef, 128>(chunks + c * D::bytes + D::coef, D::bytes - D::coef, tid);
-        to_l2<kSlice * kChunk * 4, 128>(Zs + c * p.dvp * kChunk, rows * kChunk * 4, tid);
-        rows_to_l2(xk, (int)c * kChunk, n, tid - 64);
-        rows_to_l2(xq, (int)c * kChunk, n, tid - 96);
+        to_l2<D::bytes - D::coef, HALF>(chunks + c * D::bytes + D::coef, D::bytes - D::coef, tid);
+        to_l2<C::width * kChunk * 4, HALF>(Zs + c * p.dvp * kChunk, rows * kChunk * 4, tid);
+        if constexpr (KQ) {
+          to_l2<2 * NI * C::row, HALF>(chunks + c * D::bytes, 2 * NI * C::row, tid);
+        } else {
+          rows_to_l2(xk, (int)c * kChunk, n, tid - (HALF - 64));
+          rows_to_l2(xq, (int)c * kChunk, n, tid - (HALF - 32));
+        }
         if (cols > 0) to_l2<2 * NS * 512, 32>(dO - lane + c * (p.dvp / 16) * 2 * NS * 32, 2 * NS * 512, lane);
       }
       if (i < nc && cols > 0) {   // (scale e^G o dO)^T Q
@@ -298,26 +308,23 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
           }
 #pragma unroll
           for (int nn = 0; nn < DK / 16; ++nn)
-            mma_tile<NS, 1, true>(y[2 * nn], y[2 * nn + 1], a, st + C::q + at_b_rows_k<DK>(16 * ks, 16 * nn, lane), 0);
+            mma_tile<NS, NI, true>(y[2 * nn], y[2 * nn + 1], a, st + C::q + at_b_rows_k<DK, KQ>(16 * ks, 16 * nn, lane), C::row);
         }
-#pragma unroll
-        for (int nb = 0; nb < DK / 8; ++nb)
-          asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(ys + nb * 512 + 16 * lane), "f"(y[nb][0]), "f"(y[nb][1]),
-                       "f"(y[nb][2]), "f"(y[nb][3])
-                       : "memory");
+        put_sums(ys, y, lane);
         asm volatile("barrier.cta.arrive %0, 64;" ::"r"(1 + w) : "memory");
         if (i + 1 < nc) fetch(i + 1);
       }
       if (i == 0 || cols <= 0) continue;
       const int j = i - 1, c = nc - 1 - j;
-      const unsigned st = base + j % NST * C::bytes, x = swap + (j & 1) * 4 * C::swap;
-      if (j == 0 || c % PER == PER - 1) {
+      const unsigned st = base + j % NST * C::bytes, x = swap + (j & 1) * PAIRS * C::swap;
+      if constexpr (!KQ) {
+        if (j == 0 || c % PER == PER - 1)
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-          unsigned a[4];
-          get_a(x + C::S + ks * 512, a, lane);
-          store_a<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK + ks * 128, a, lane);
-        }
+          for (int ks = 0; ks < DK / 16; ++ks) {
+            unsigned a[4];
+            get_a(x + C::S + ks * 512, a, lane);
+            store_a<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK + ks * 128, a, lane);
+          }
       }
       float y[4][4] = {};   // dR^T
 #pragma unroll
@@ -340,8 +347,13 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
   for (int i = 0; i <= nc; ++i) {
     __syncthreads();
     if (i == nc || cols <= 0) continue;
-    const unsigned st = base + i % NST * C::bytes, x = swap + (i & 1) * 4 * C::swap;
+    const unsigned st = base + i % NST * C::bytes, x = swap + (i & 1) * PAIRS * C::swap;
     const float* coef = reinterpret_cast<const float*>(smem + i % NST * C::bytes + C::coef);
+    if constexpr (KQ) {
+      const int c = nc - 1 - i;
+      if (i == 0 || c % PER == PER - 1)
+        store_blocks<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK, s, lane);
+    }
     // X^T
     float r[4][4] = {};
     unsigned plain[DK / 16][4], a[2][NS][4];   // to the helper at the end, as in the forward walk
@@ -353,7 +365,7 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
       for (int e = 0; e < 4; ++e) plain[ks][e] = d[0][e];
 #pragma unroll
       for (int np = 0; np < 2; ++np)
-        mma_tile<NS, 1, false>(r[2 * np], r[2 * np + 1], d, st + C::k + at_b_rows_n<DK>(16 * np, 16 * ks, lane), 0);
+        mma_tile<NS, NI, false>(r[2 * np], r[2 * np + 1], d, st + C::k + at_b_rows_n<DK, KQ>(16 * np, 16 * ks, lane), C::row);
     }
     scale_by(s, coef[2 * kChunk]);
 #pragma unroll
@@ -382,8 +394,9 @@ __global__ void __launch_bounds__(kTeamThreads) delta_back_team_kernel(const Del
       s[nb][2] += y.z;
       s[nb][3] += y.w;
     }
+    if (!KQ)
 #pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) put_a(x + C::S + ks * 512, plain[ks], lane);
+      for (int ks = 0; ks < DK / 16; ++ks) put_a(x + C::S + ks * 512, plain[ks], lane);
 #pragma unroll
     for (int e = 0; e < 2 * NS; ++e) put_a(x + C::X + e * 512, a[e / NS][e % NS], lane);
   }
@@ -440,11 +453,18 @@ __device__ __forceinline__ void load_blocks(unsigned dst, int, const __nv_bfloat
 }
 template <int UNITS, int THREADS>
 __device__ __forceinline__ void load_blocks(unsigned dst, int plane, const float* src, int units, int tid) {
-#pragma unroll 2
-  for (int i = tid; i < UNITS; i += THREADS) {
-    float v[8];
-    load8(src + 8 * (long long)i, i < units ? 8 : 0, true, v);
-    store_planes(dst + 16 * i, plane, v);
+  constexpr int N = (UNITS + THREADS - 1) / THREADS, AHEAD = N < 4 ? N : 4;
+#pragma unroll 1
+  for (int i = tid; i < UNITS; i += AHEAD * THREADS) {
+    float v[AHEAD][8];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int k = i + j * THREADS;
+      load8(src + 8 * (long long)k, k < units ? 8 : 0, true, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i + j * THREADS < UNITS) store_planes(dst + 16 * (i + j * THREADS), plane, v[j]);
   }
 }
 
@@ -877,17 +897,26 @@ cudaError_t run_alone(const DeltaP& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)Back<T, DK>::smem, s, p);
 }
+template <typename T, int DK, int PAIRS>
+cudaError_t run_team(const DeltaP& p, cudaStream_t s) {
+  typedef BackTeam<T, DK, PAIRS> C;
+  const auto kern = delta_back_team_kernel<T, DK, PAIRS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  if (e != cudaSuccess) return e;
+  const int slices = (p.dv + C::width - 1) / C::width;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * slices)), dim3(2 * C::half), (size_t)C::smem, s,
+                          p, slices);
+}
+// Helpers where the forward walk has them.
 template <int DK>
 cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
   if (crowded(p)) return run_alone<__nv_bfloat16, DK>(p, s);
-  const auto kern = delta_back_team_kernel<DK>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BackTeam<DK>::smem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(kTeamThreads),
-                          (size_t)BackTeam<DK>::smem, s, p);
+  return few(p) ? run_team<__nv_bfloat16, DK, 2>(p, s) : run_team<__nv_bfloat16, DK, 4>(p, s);
 }
 template <int DK>
 cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
+  if constexpr (DK == 64)
+    if (few(p)) return run_team<float, DK, 2>(p, s);
   return run_alone<float, DK>(p, s);
 }
 

@@ -103,12 +103,10 @@ __device__ __forceinline__ void store_blocks(float* to, const float (&s)[N][4], 
 
 // ------------------------------------------------- two warps for 16 columns
 //
-// In bfloat16 a warp that carries the state has a second one beside it, its
-// helper, for all that the next chunk does not wait for: outputs, what the
-// gradients keep, the loads.  Between them lie A operands in shared memory, a
+// A warp that carries the state has a second one beside it, its helper, for all
+// that the next chunk does not wait for: outputs, what the gradients keep, the
+// loads.  Between them lie A operands, or float32's sums, in shared memory, a
 // register quad a lane, in two buffers: the helper works on the chunk before.
-
-constexpr int kTeamThreads = 256;   // four warps and their helpers
 
 __device__ __forceinline__ void put_a(unsigned at, const unsigned (&a)[4], int lane) {
   store16(at + 16 * lane, make_uint4(a[0], a[1], a[2], a[3]));
@@ -126,6 +124,22 @@ __device__ __forceinline__ float4 get_f4(unsigned at, int lane) {
                : "r"(at + 16 * lane)
                : "memory");
   return v;
+}
+template <int N>
+__device__ __forceinline__ void put_sums(unsigned at, const float (&s)[N][4], int lane) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at + j * 512 + 16 * lane), "f"(s[j][0]), "f"(s[j][1]),
+                 "f"(s[j][2]), "f"(s[j][3])
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void get_sums(unsigned at, float (&s)[N][4], int lane) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float4 v = get_f4(at + j * 512, lane);
+    s[j][0] = v.x; s[j][1] = v.y; s[j][2] = v.z; s[j][3] = v.w;
+  }
 }
 // An A operand [16 columns][16 values] as four of the blocks of 8 x 8 that
 // store_blocks writes, in rows of ROW blocks.
@@ -150,10 +164,10 @@ __device__ __forceinline__ void rows_to_l2(const Rows<__nv_bfloat16>& x, int i0,
   if (row >= 0 && row < kChunk && i0 + row < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(x.at(i0 + row)));
 }
 // A slice's fragments of a chunk: `rows` columns of 32 floats to shared memory.
-template <int THREADS>
+template <int COLS, int THREADS>
 __device__ __forceinline__ void copy_slice(unsigned dst, const float* src, int rows, int tid) {
 #pragma unroll
-  for (int i = 0; i < kSlice * kChunk / 4 / THREADS; ++i) {
+  for (int i = 0; i < COLS * kChunk / 4 / THREADS; ++i) {
     const int u = tid + i * THREADS;
     copy16(dst + 16 * u, src + (u < rows * (kChunk / 4) ? 4 * u : 0), u < rows * (kChunk / 4));
   }

@@ -324,12 +324,20 @@ __device__ __forceinline__ void store_planes(unsigned dst, int plane, const floa
 template <int W, int ROWS, int THREADS>
 __device__ __forceinline__ void load_tile(unsigned dst, int plane, Rows<float> x, int i0, int n, int cols, bool wide,
                                           int tid) {
-#pragma unroll 4
-  for (int i = tid; i < ROWS * (W / 8); i += THREADS) {
-    const int row = i / (W / 8), u = i % (W / 8);
-    float v[8];
-    load8(x.at(i0 + row) + 8 * u, i0 + row < n && 8 * u < cols ? 8 : 0, wide, v);
-    store_planes(dst + unit_at<W>(row, u), plane, v);
+  constexpr int UNITS = ROWS * (W / 8), N = (UNITS + THREADS - 1) / THREADS, AHEAD = N < 4 ? N : 4;   // reads under way
+#pragma unroll 1
+  for (int i = tid; i < UNITS; i += AHEAD * THREADS) {
+    float v[AHEAD][8];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int k = i + j * THREADS, row = k / (W / 8), u = k % (W / 8);
+      load8(x.at(i0 + row) + 8 * u, k < UNITS && i0 + row < n && 8 * u < cols ? 8 : 0, wide, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int k = i + j * THREADS;
+      if (k < UNITS) store_planes(dst + unit_at<W>(k / (W / 8), k % (W / 8)), plane, v[j]);
+    }
   }
 }
 

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(32) delta_prep_kernel(const DeltaP p) {
 // all columns share come through shared memory a few chunks ahead.  Two products
 // that wait for one another bound it, and what stands beside them in one warp's
 // order: 64 x 197 x 12 x 64 in bfloat16, five CTAs one after the other on an SM,
-// 47 us; 3 x 1021 x 6 x 40 x 72 in float32, 36 CTAs with six products for one, 84.
+// 47 us.
 
 template <typename T, int DK, bool SAVE>
 struct Chain {
@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(128) delta_chain_kernel(const DeltaP p) {
   if (p.out) zero_rows<T>(p, p.out, n, b, hv, m0, cols, p.o_wide, lane);
 }
 
-// The same in bfloat16 with a helper to each warp: the warp has the two
-// products between one state and the next, the helper the loads, the output and
-// what the gradients keep.  One warp for all of it is 1206 ns a chunk at 2 x
+// The same with a helper to each warp: the warp has the two products between one
+// state and the next, the helper the loads, the output and what the gradients
+// keep.  One warp for all of it is 1206 ns a chunk at 2 x
 // 24337 x 12 x 64, of which the loads are 256, the output 227, U's read 146;
 // two warps with half of the tokens and of dk each took longer (1430), as every
 // half has to pass between them within a chunk.  With helpers, and the tiles two
@@ -385,59 +385,75 @@ __global__ void __launch_bounds__(128) delta_chain_kernel(const DeltaP p) {
 // SM has one CTA (16 x 4096 x 8 x 64: 145 us): 32% of the tensor cores' and 32% of
 // the issue slots, the rest what one product waits for another, shared memory
 // and the chunk's barrier.  Copies by the bulk engine into rings two chunks
-// ahead were no faster (1066 to 1108 against 1066).  In float32 helpers gain 7 us
-// of 84 here and lose 6 of 76 going back, where six products for one leave the
-// tensor cores no room for theirs: float32 has none.
+// ahead were no faster (1066 to 1108 against 1066).
+//
+// Four pairs put a warp and its helper on each of an SM's four schedulers, two
+// pairs (32 columns) every warp on one of its own: for walks of no more such CTAs
+// than SMs, 3 heads of 197 x 64 in bfloat16 7.7 us against 9.4, and in float32,
+// where six products for one keep a scheduler's tensor core busy, 3 x 1021 x 6 x
+// 40 x 72 52 us, back 49, against 77 and 83 with four pairs and 84 and 76 without
+// helpers.  Float32's longer walks than that have none.
 
-template <int DK, bool SAVE>
+// PAIRS: of a warp and its helper in a CTA.
+template <typename T, int DK, bool SAVE, int PAIRS>
 struct Team {
-  typedef __nv_bfloat16 T;
-  typedef ChunkData<T, DK, SAVE, false> D;
+  static constexpr int width = 16 * PAIRS, half = 32 * PAIRS;   // columns; threads of the warps, and of the helpers
+  static constexpr bool KQ = sizeof(T) == 4;
+  typedef ChunkData<T, DK, SAVE, KQ> D;
+  static constexpr int NO = D::NI == 1 ? 1 : D::NS;   // planes of S, R and P that the output takes, as above
   static constexpr int row = kChunk * DK * 2;
-  // a stage: q, k, P's first plane, coefficients and -W, the slice of U
-  static constexpr int q = 0, k = row, P = 2 * row, coef = P + kTile, W = coef + (D::W - D::coef);
-  static constexpr int U = W + (D::Tm - D::W), bytes = U + kSlice * kChunk * 4, stages = 3;
-  static constexpr int S = 0, R = DK / 16 * 512, swap = R + 2 * 512;   // a warp's buffer to its helper
-  static constexpr int swaps = stages * bytes, out = swaps + 2 * 4 * swap, smem = out + 4 * out_bytes<T>();
+  // a stage: q, k, P, coefficients and -W, the slice of U
+  static constexpr int q = 0, k = D::NI * row, P = 2 * D::NI * row, coef = P + NO * kTile, W = coef + (D::W - D::coef);
+  static constexpr int U = W + (D::Tm - D::W), bytes = U + width * kChunk * 4, stages = 3;
+  // a warp's buffer to its helper: operands in bfloat16, float32's sums as they are
+  static constexpr int S = 0, R = DK / 16 * (KQ ? 1024 : 512), swap = R + 2 * (KQ ? 1024 : 512);
+  static constexpr int swaps = stages * bytes, out = swaps + 2 * PAIRS * swap, smem = out + PAIRS * out_bytes<T>();
+  static_assert(smem <= 227 * 1024 - 1024);
 };
 
-template <int DK, bool SAVE>
-__global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_kernel(const DeltaP p) {
-  typedef __nv_bfloat16 T;
-  typedef Team<DK, SAVE> C;
+template <typename T, int DK, bool SAVE, int PAIRS>
+__global__ void __launch_bounds__(64 * PAIRS, DK == 64 && sizeof(T) == 2 ? 2 : 1)
+    delta_team_kernel(const DeltaP p, int slices) {
+  typedef Team<T, DK, SAVE, PAIRS> C;
   typedef typename C::D D;
-  constexpr int NST = C::stages, NS = 2, PER = kStateChunk / kChunk;
+  constexpr int NST = C::stages, NI = D::NI, NS = D::NS, NO = C::NO, PER = kStateChunk / kChunk;
+  constexpr int HALF = C::half;
+  constexpr bool KQ = C::KQ;
   extern __shared__ __align__(128) unsigned char smem[];
   const unsigned base = shared_at(smem);
-  const int tid = threadIdx.x & 127, lane = tid & 31, w = tid >> 5, q4 = lane & 3;
-  const bool helper = threadIdx.x >= 128;
-  const long long part = blockIdx.x / p.slices, at = part / p.nseg;
-  const int slice = (int)(blockIdx.x - part * p.slices), seg = (int)(part - at * p.nseg);
+  const int tid = threadIdx.x & (HALF - 1), lane = tid & 31, w = tid >> 5, q4 = lane & 3;
+  const bool helper = threadIdx.x >= HALF;
+  const long long part = blockIdx.x / slices, at = part / p.nseg;
+  const int slice = (int)(blockIdx.x - part * slices), seg = (int)(part - at * p.nseg);
   const int rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv), b = by_length(p, rank);
   const long long bh = (long long)b * p.Hv + hv;
   const int hk = hv / (p.Hv / p.Hk);
   const int n = delta_length(p, b), all = (n + kChunk - 1) / kChunk, c0 = seg * p.seglen;
   const bool ends = seg == p.nseg - 1;
   const int nc = all - c0 < 0 ? 0 : ends || all - c0 < p.seglen ? all - c0 : p.seglen;   // chunks of the segment, from c0 on
-  const int m0 = slice * kSlice + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
-  const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer 4 swaps behind
+  const int m0 = slice * C::width + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
+  const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer PAIRS swaps behind
   wait_prior();
   if (helper) {
     const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
     const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
     const Rows<T> xo = rows_of<T>(p, p.out, (long long)p.Hv * p.dv, (long long)hv * p.dv + m0, b, n);
     const char* chunks = p.chunks + (bh * p.nc + c0) * D::bytes;
-    const float* Us = p.U + ((bh * p.nc + c0) * p.dvp + slice * kSlice) * kChunk;
-    const int rows = p.dvp - slice * kSlice < kSlice ? p.dvp - slice * kSlice : kSlice;
+    const float* Us = p.U + ((bh * p.nc + c0) * p.dvp + slice * C::width) * kChunk;
+    const int rows = p.dvp - slice * C::width < C::width ? p.dvp - slice * C::width : C::width;
     unsigned char* buf = smem + C::out + w * out_bytes<T>();
     const auto load = [&](int c) {
       const unsigned st = base + c % NST * C::bytes;
       const char* chunk = chunks + (long long)c * D::bytes;
-      load_tile<DK, kChunk, 128>(st + C::k, 0, xk, (c0 + c) * kChunk, n, p.dk, p.k_wide, tid);
-      load_tile<DK, kChunk, 128>(st + C::q, 0, xq, (c0 + c) * kChunk, n, p.dk, p.q_wide, tid);
-      copy_block<kTile, 128>(st + C::P, chunk + D::P, tid);
-      copy_block<D::Tm - D::coef, 128>(st + C::coef, chunk + D::coef, tid);
-      copy_slice<128>(st + C::U, Us + (long long)c * p.dvp * kChunk, rows, tid);
+      if (KQ) {
+        copy_block<2 * NI * C::row, HALF>(st, chunk, tid);
+      } else {
+        load_tile<DK, kChunk, HALF>(st + C::k, 0, xk, (c0 + c) * kChunk, n, p.dk, p.k_wide, tid);
+        load_tile<DK, kChunk, HALF>(st + C::q, 0, xq, (c0 + c) * kChunk, n, p.dk, p.q_wide, tid);
+      }
+      copy_block<NO * kTile, HALF>(st + C::P, chunk + D::P, tid);
+      copy_block<D::Tm - D::coef, HALF>(st + C::coef, chunk + D::coef, tid);
+      copy_slice<C::width, HALF>(st + C::U, Us + (long long)c * p.dvp * kChunk, rows, tid);
     };
     if (nc > 0) load(0);
     copy_commit();
@@ -447,27 +463,46 @@ __global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_ker
       if (i + 1 < nc) load(i + 1);
       copy_commit();
       if (i + 2 < nc) {   // a load has a chunk's time, which covers L2's latency and not HBM's
-        to_l2<D::Tm - D::P, 128>(chunks + (long long)(i + 2) * D::bytes + D::P, D::Tm - D::P, tid);
-        to_l2<kSlice * kChunk * 4, 128>(Us + (long long)(i + 2) * p.dvp * kChunk, rows * kChunk * 4, tid);
-        rows_to_l2(xk, (c0 + i + 2) * kChunk, n, tid - 64);
-        rows_to_l2(xq, (c0 + i + 2) * kChunk, n, tid - 96);
+        to_l2<D::Tm - D::P, HALF>(chunks + (long long)(i + 2) * D::bytes + D::P, D::Tm - D::P, tid);
+        to_l2<C::width * kChunk * 4, HALF>(Us + (long long)(i + 2) * p.dvp * kChunk, rows * kChunk * 4, tid);
+        if constexpr (KQ) {
+          to_l2<2 * NI * C::row, HALF>(chunks + (long long)(i + 2) * D::bytes, 2 * NI * C::row, tid);
+        } else {
+          rows_to_l2(xk, (c0 + i + 2) * kChunk, n, tid - (HALF - 64));
+          rows_to_l2(xq, (c0 + i + 2) * kChunk, n, tid - (HALF - 32));
+        }
       }
       if (i == 0 || cols <= 0) continue;
-      const unsigned st = base + (i - 1) % NST * C::bytes, x = swap + (i - 1 & 1) * 4 * C::swap;
+      const unsigned st = base + (i - 1) % NST * C::bytes, x = swap + (i - 1 & 1) * PAIRS * C::swap;
       const float* coef = reinterpret_cast<const float*>(smem + (i - 1) % NST * C::bytes + C::coef);
       const int c = c0 + i - 1;
       // O^T = scale e^G (S^T Q^T) + R^T P^T
       float o[4][4] = {};
-      unsigned a[DK / 16][1][4], r[2][1][4];
+      unsigned a[DK / 16][NO][4], r[2][NO][4];
+      if constexpr (KQ) {
+        float s[DK / 8][4], rs[4][4];
+        get_sums(x + C::S, s, lane);
+        get_sums(x + C::R, rs, lane);
+        if (SAVE) {
+          if (c % PER == 0)
+            store_blocks<DK / 8>(static_cast<T*>(p.states) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK, s, lane);
+          store_blocks<4>(static_cast<T*>(p.R) + ((bh * p.nc + c) * p.dvp + m0) * kChunk, rs, lane);
+        }
 #pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) get_a(x + C::S + ks * 512, a[ks][0], lane);
+        for (int ks = 0; ks < DK / 16; ++ks) to_a<NO>(s[2 * ks], s[2 * ks + 1], a[ks]);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) get_a(x + C::R + ks * 512, r[ks][0], lane);
+        for (int ks = 0; ks < 2; ++ks) to_a<NO>(rs[2 * ks], rs[2 * ks + 1], r[ks]);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) get_a(x + C::S + ks * 512, a[ks][0], lane);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) get_a(x + C::R + ks * 512, r[ks][0], lane);
+      }
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks)
 #pragma unroll
         for (int np = 0; np < 2; ++np)
-          mma_tile<1, 1, false>(o[2 * np], o[2 * np + 1], a[ks], st + C::q + at_b_rows_n<DK>(16 * np, 16 * ks, lane), 0);
+          mma_tile<NO, NI, false>(o[2 * np], o[2 * np + 1], a[ks], st + C::q + at_b_rows_n<DK, KQ>(16 * np, 16 * ks, lane), C::row);
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
         const float2 g = *reinterpret_cast<const float2*>(coef + 8 * nb + 2 * q4);
@@ -478,9 +513,9 @@ __global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_ker
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int np = ks; np < 2; ++np)
-          mma_tile<1, 1, false>(o[2 * np], o[2 * np + 1], r[ks],
-                                st + C::P + at_b_rows_n<kChunk, true>(16 * np, 16 * ks, lane), 0);
-      if (SAVE) {
+          mma_tile<NO, NO, false>(o[2 * np], o[2 * np + 1], r[ks],
+                                  st + C::P + at_b_rows_n<kChunk, true>(16 * np, 16 * ks, lane), kTile);
+      if constexpr (SAVE && !KQ) {
         if (c % PER == 0)
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
@@ -502,8 +537,9 @@ __global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_ker
   for (int i = 0; i <= nc; ++i) {
     __syncthreads();
     if (i == nc || cols <= 0) continue;
-    const unsigned st = base + i % NST * C::bytes, x = swap + (i & 1) * 4 * C::swap;
+    const unsigned st = base + i % NST * C::bytes, x = swap + (i & 1) * PAIRS * C::swap;
     const float* coef = reinterpret_cast<const float*>(smem + i % NST * C::bytes + C::coef);
+    if (KQ) put_sums(x + C::S, s, lane);
     float r[4][4];
     unsigned plain[DK / 16][4], rplain[2][1][4];   // to the helper at the end: a store would hold back the reads behind it
 #pragma unroll
@@ -522,6 +558,7 @@ __global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_ker
       for (int np = 0; np < 2; ++np)
         mma_tile<NS, NS, false>(r[2 * np], r[2 * np + 1], a, st + C::W + at_b_rows_n<DK, true>(16 * np, 16 * ks, lane), C::row);
     }
+    if (KQ) put_sums(x + C::R, r, lane);
     // S^T = e^G_C S^T + (beta left R)^T K
     scale_by(s, coef[2 * kChunk]);
 #pragma unroll
@@ -532,12 +569,14 @@ __global__ void __launch_bounds__(kTeamThreads, DK == 64 ? 2 : 1) delta_team_ker
       to_a<1>(r[2 * ks], r[2 * ks + 1], rplain[ks]);
 #pragma unroll
       for (int nn = 0; nn < DK / 16; ++nn)
-        mma_tile<NS, 1, true>(s[2 * nn], s[2 * nn + 1], a, st + C::k + at_b_rows_k<DK>(16 * ks, 16 * nn, lane), 0);
+        mma_tile<NS, NI, true>(s[2 * nn], s[2 * nn + 1], a, st + C::k + at_b_rows_k<DK, KQ>(16 * ks, 16 * nn, lane), C::row);
     }
+    if constexpr (!KQ) {
 #pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) put_a(x + C::S + ks * 512, plain[ks], lane);
+      for (int ks = 0; ks < DK / 16; ++ks) put_a(x + C::S + ks * 512, plain[ks], lane);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) put_a(x + C::R + ks * 512, rplain[ks][0], lane);
+      for (int ks = 0; ks < 2; ++ks) put_a(x + C::R + ks * 512, rplain[ks][0], lane);
+    }
   }
   if (p.h_out && cols > 0 && ends) keep_state<DK>(p, p.h_out, bh, m0, cols, lane, s);
 }
@@ -729,16 +768,28 @@ cudaError_t run_alone(const DeltaP& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.slices)), dim3(128), (size_t)C::smem, s, p);
 }
-template <int DK, bool SAVE>
-cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
-  return run_alone<float, DK, SAVE>(p, s);
+template <typename T, int DK, bool SAVE, int PAIRS>
+cudaError_t run_team(const DeltaP& p, cudaStream_t s) {
+  typedef Team<T, DK, SAVE, PAIRS> C;
+  const auto kern = delta_team_kernel<T, DK, SAVE, PAIRS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  if (e != cudaSuccess) return e;
+  const int slices = (p.dv + C::width - 1) / C::width;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.nseg * slices)), dim3(2 * C::half),
+                          (size_t)C::smem, s, p, slices);
 }
 // Helpers make a chunk's walk shorter and an SM hold fewer of them: with more
-// CTAs than two an SM warps alone are ahead (64 x 197 x 12 x 64, 768 CTAs: 47
-// against 52 us, back 55 against 67; 16 x 4096 x 8 x 64, 128: 172 against 146).
+// CTAs than an SM holds of these at dk = 64, warps alone are ahead (64 x 197 x
+// 12 x 64, 768 CTAs: 47 against 52 us, back 55 against 67; 16 x 4096 x 8 x 64,
+// 128: 172 against 146).  In float32 at dk > 64 three stages do not fit.
+template <int DK, bool SAVE>
+cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
+  if constexpr (DK == 64)
+    if (few(p)) return run_team<float, DK, SAVE, 2>(p, s);
+  return run_alone<float, DK, SAVE>(p, s);
+}
 template <int DK, bool SAVE>
 cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
-  typedef Team<DK, SAVE> C;
   const unsigned heads = (unsigned)((long long)p.B * p.Hv);
   cudaError_t e;
   if (crowded(p)) return run_alone<__nv_bfloat16, DK, SAVE>(p, s);
@@ -754,11 +805,9 @@ cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
     e = launch_dependent(delta_starts_kernel, dim3(heads * (p.dvp / 16)), dim3(256), (size_t)starts_smem(p.dk), s, p);
     if (e != cudaSuccess) return e;
   }
-  const auto kern = delta_team_kernel<DK, SAVE>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(heads * p.nseg * p.slices), dim3(kTeamThreads), (size_t)C::smem, s, p);
+  return few(p) ? run_team<__nv_bfloat16, DK, SAVE, 2>(p, s) : run_team<__nv_bfloat16, DK, SAVE, 4>(p, s);
 }
+
 template <typename T, int DK, bool SAVE>
 cudaError_t run_chain(const DeltaP& p, cudaStream_t s) {
   const auto prep = delta_prep_kernel<T, DK, SAVE>;

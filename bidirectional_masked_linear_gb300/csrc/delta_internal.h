@@ -98,6 +98,8 @@ DeltaP delta_params(const Args& a, char* kept, char* beside, bool save) {
 
 // Whether the walks' CTAs are more than two an SM.
 inline bool crowded(const DeltaP& p) { return (long long)p.B * p.Hv * p.slices > 2 * kSmCount; }
+// Whether CTAs of 32 columns are no more than the SMs.
+inline bool few(const DeltaP& p) { return (long long)p.B * p.Hv * p.nseg * ((p.dv + 31) / 32) <= kSmCount; }
 
 // Every chunk's ChunkData and U, then the chain; R and states where `save`.
 cudaError_t launch_delta_chain(const DeltaP& p, int dtype, bool save, cudaStream_t s);
