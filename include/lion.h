@@ -762,8 +762,9 @@ size_t lion_qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d, int 
  *   saved  device, 256-byte aligned, of lion_delta_saved_bytes, or NULL: what
  *   lion_delta_bwd goes on from.
  *   Keys longer than sqrt(2 / beta) make the state grow.
- *   Long sequences of few heads are walked in segments, whose number B, Hv, L
- *   and the head sizes decide: results of other batches then differ by roundings.
+ *   Long sequences of few heads are walked in segments, and gradients of many
+ *   heads add their terms in another order than those of few; B, Hv, L, the head
+ *   sizes and the type decide: results of other batches then differ by roundings.
  */
 typedef struct {
   const void* q;
