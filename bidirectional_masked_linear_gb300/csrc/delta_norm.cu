@@ -17,7 +17,7 @@ namespace lion {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kSmCount = 152;
+constexpr int kSmCount = 152, kPerSm = 4;   // CTAs an SM
 
 struct QkP {
   const void* x[2];        // q, k
@@ -57,31 +57,31 @@ template <bool WIDE>
 __device__ __forceinline__ float4 run_of(const float* p) {
   return WIDE ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
 }
-__device__ __forceinline__ void values(uint2 r, float* v) {
-  const float2 a = unpack_bf16(r.x), b = unpack_bf16(r.y);
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+__device__ __forceinline__ void values(uint2 r, f2* v) {
+  v[0] = unpack_bf16(r.x);
+  v[1] = unpack_bf16(r.y);
 }
-__device__ __forceinline__ void values(float4 r, float* v) {
-  v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+__device__ __forceinline__ void values(float4 r, f2* v) {
+  v[0] = pack2(r.x, r.y);
+  v[1] = pack2(r.z, r.w);
 }
 template <bool WIDE>
-__device__ __forceinline__ void store4(float* p, const float* v) {
+__device__ __forceinline__ void store4(float* p, const f2* v) {
   if (WIDE) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
   } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = v[e];
+    p[0] = v[0].x; p[1] = v[0].y; p[2] = v[1].x; p[3] = v[1].y;
   }
 }
 template <bool WIDE>
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const f2* v) {
   if (WIDE) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    const __nv_bfloat162 a = __float22bfloat162_rn(v[0]), b = __float22bfloat162_rn(v[1]);
     *reinterpret_cast<uint2*>(p) =
         make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = __float2bfloat16_rn(v[e]);
+    for (int e = 0; e < 4; ++e) p[e] = __float2bfloat16_rn(e & 1 ? v[e >> 1].y : v[e >> 1].x);
   }
 }
 
@@ -112,38 +112,48 @@ struct Turn {
       u[o] = p < q.rp && e < 4 ? turn_of(q.freqs[4 * p + e]) : 0;
     }
   }
-  __device__ __forceinline__ void at(int pos, int p, float (&c)[4], float (&s)[4]) const {
+  // cosines and sines (back: of the angles' negatives)
+  template <bool BWD>
+  __device__ __forceinline__ void at(int pos, int p, f2 (&c)[2], f2 (&s)[2], f2 (&minus)[2]) const {
     float co[OWN], so[OWN];
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
       const unsigned long long t = u[o] * (unsigned long long)(long long)pos;
       sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &so[o], &co[o]);   // 2^-31: half turns
     }
+    float ca[4], sa[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      c[e] = __shfl_sync(0xffffffffu, co[e / NG], (e % NG) * LPH + p);
-      s[e] = __shfl_sync(0xffffffffu, so[e / NG], (e % NG) * LPH + p);
+      ca[e] = __shfl_sync(0xffffffffu, co[e / NG], (e % NG) * LPH + p);
+      sa[e] = __shfl_sync(0xffffffffu, so[e / NG], (e % NG) * LPH + p);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      c[e] = pack2(ca[2 * e], ca[2 * e + 1]);
+      const f2 x = pack2(sa[2 * e], sa[2 * e + 1]), y = pack2(-sa[2 * e], -sa[2 * e + 1]);
+      s[e] = BWD ? y : x;
+      minus[e] = BWD ? x : y;
     }
   }
 };
 
-// v[0..3] and v[4..7] are the lane's two runs.
-__device__ __forceinline__ void turn8(float (&v)[8], const float (&c)[4], const float (&s)[4], bool interleaved,
-                                      float sign) {
+// v[0], v[1] and v[2], v[3] are the lane's two runs; minus: the sines' negatives.
+__device__ __forceinline__ void turn8(f2 (&v)[4], const f2 (&c)[2], const f2 (&s)[2], const f2 (&minus)[2],
+                                      int interleaved) {
+  if (interleaved) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int i = interleaved ? 2 * e : e, j = interleaved ? 2 * e + 1 : e + 4;
-    const float a = v[i], b = v[j], sn = sign * s[e];
-    v[i] = a * c[e] - b * sn;
-    v[j] = a * sn + b * c[e];
+    for (int e = 0; e < 4; ++e) {
+      const float a = v[e].x, b = v[e].y, ce = e & 1 ? c[e >> 1].y : c[e >> 1].x, se = e & 1 ? s[e >> 1].y : s[e >> 1].x;
+      v[e] = pack2(a * ce - b * se, a * se + b * ce);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const f2 a = v[e], b = v[e + 2];
+      v[e] = fma2(a, c[e], mul2(b, minus[e]));
+      v[e + 2] = fma2(a, s[e], mul2(b, c[e]));
+    }
   }
-}
-__device__ __forceinline__ void turn8(float (&v)[8], const float (&c)[4], const float (&s)[4], int interleaved,
-                                      float sign) {
-  if (interleaved)
-    turn8(v, c, s, true, sign);
-  else
-    turn8(v, c, s, false, sign);
 }
 
 template <int LPH>
@@ -167,7 +177,7 @@ constexpr int heads_at_once() {
 // at 5.6 TB/s; 32 x 512 x 16 + 16 x 64 with rotation 33 us forward (4.1 TB/s), 51
 // back (3.9).
 template <typename T, int LPH, bool WIDE, bool BWD>
-__global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) qknorm_kernel(const QkP q) {
   constexpr int NG = 32 / LPH, U = heads_at_once<T, BWD>();
   __shared__ __align__(16) float sw[2][8 * LPH];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
   }
   Turn<LPH> turn;
   turn.init(q, lane, p);
-  float dw[BWD ? 2 : 1][8] = {};
+  f2 dw[BWD ? 2 : 1][4] = {};
   const int heads = q.H[0] + q.H[1];
   __syncthreads();
 
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
   const long long hop = (long long)gridDim.x * kWarps;
   long long tn = (long long)blockIdx.x * kWarps + warp;
   int pn = 0;
-  float c[4], s[4];
+  f2 c[2] = {}, s[2] = {}, minus[2] = {};
   if (tn < q.tokens) fetch(tn, 0);
   while (tn < q.tokens) {
     const long long t = tn;
@@ -229,7 +239,8 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
     }
     if (tn < q.tokens) fetch(tn, pn);
     if (q.rp && part == 0)
-      turn.at(q.positions ? q.positions[t] : q.tokens >> 32 ? (int)(t % q.L) : (int)((unsigned)t % (unsigned)q.L), p, c, s);
+      turn.template at<BWD>(q.positions ? q.positions[t] : q.tokens >> 32 ? (int)(t % q.L) : (int)((unsigned)t % (unsigned)q.L), p, c, s,
+              minus);
     T* yq = static_cast<T*>(q.y[0]) + t * q.H[0] * q.d;
     T* yk = static_cast<T*>(q.y[1]) + (t * q.H[1] - q.H[0]) * q.d;
 #pragma unroll
@@ -237,47 +248,50 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
       const int h = h0 + i * NG;
       if (i >= q.at_once || h - g >= heads) break;   // of all lanes
       const int m = h >= q.H[0];
-      float v[8], w[8];
+      f2 v[4], w[4], o[4];
       values(xc[i].a, v);
-      values(xc[i].b, v + 4);
+      values(xc[i].b, v + 2);
       values(*reinterpret_cast<const float4*>(&sw[m][a]), w);
-      values(*reinterpret_cast<const float4*>(&sw[m][b]), w + 4);
-      float ss = 0.f;
+      values(*reinterpret_cast<const float4*>(&sw[m][b]), w + 2);
+      f2 sum = mul2(v[0], v[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-      const float r = rsqrtf(fmaf(head_sum<LPH>(ss), q.inv_n, q.eps));   // to 2^-22
-      float o[8];
+      for (int e = 1; e < 4; ++e) sum = fma2(v[e], v[e], sum);
+      const float r = rsqrtf(fmaf(head_sum<LPH>(sum.x + sum.y), q.inv_n, q.eps));   // to 2^-22
+      const f2 r2 = pack2(r, r);
       if (!BWD) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = v[e] * r * w[e];
-        if (turns) turn8(o, c, s, q.interleaved, 1.f);
+        for (int e = 0; e < 4; ++e) o[e] = mul2(mul2(v[e], r2), w[e]);
+        if (turns) turn8(o, c, s, minus, q.interleaved);
       } else {
-        float z[8];
+        f2 z[4];
         values(dc[i].a, z);
-        values(dc[i].b, z + 4);
-        if (turns) turn8(z, c, s, q.interleaved, -1.f);
-        float gx = 0.f;
+        values(dc[i].b, z + 2);
+        if (turns) turn8(z, c, s, minus, q.interleaved);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          o[e] = z[e] * w[e];
-          gx = fmaf(o[e], v[e], gx);
+        for (int e = 0; e < 4; ++e) {
+          o[e] = mul2(z[e], w[e]);
+          sum = e ? fma2(o[e], v[e], sum) : mul2(o[e], v[e]);
         }
         if (q.part && h < heads) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float y = z[e] * (v[e] * r);
-            dw[0][e] += m ? 0.f : y;
-            dw[BWD ? 1 : 0][e] += m ? y : 0.f;
+          for (int e = 0; e < 4; ++e) z[e] = mul2(z[e], mul2(v[e], r2));
+          if (m) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dw[BWD ? 1 : 0][e] = add2(dw[BWD ? 1 : 0][e], z[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dw[0][e] = add2(dw[0][e], z[e]);
           }
         }
-        const float k = head_sum<LPH>(gx) * q.inv_n * r * r;
+        const float k = -(head_sum<LPH>(sum.x + sum.y) * q.inv_n * r * r);
+        const f2 k2 = pack2(k, k);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-k, v[e], o[e]);
+        for (int e = 0; e < 4; ++e) o[e] = mul2(r2, fma2(k2, v[e], o[e]));
       }
       if (there && h < heads) {
         T* dst = (m ? yk : yq) + (long long)h * q.d;
         store4<WIDE>(dst + a, o);
-        store4<WIDE>(dst + b, o + 4);
+        store4<WIDE>(dst + b, o + 2);
       }
     }
   }
@@ -288,9 +302,10 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_kernel(const QkP q) {
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        float x = e & 1 ? dw[m][e >> 1].y : dw[m][e >> 1].x;
 #pragma unroll
-        for (int o = 16; o >= LPH; o >>= 1) dw[m][e] += __shfl_xor_sync(0xffffffffu, dw[m][e], o);
-        if (g == 0 && there) sh[warp][m][(e < 4 ? a : b - 4) + e] = dw[m][e];
+        for (int o = 16; o >= LPH; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (g == 0 && there) sh[warp][m][(e < 4 ? a : b - 4) + e] = x;
       }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * q.d; i += 32 * kWarps) {
@@ -308,7 +323,7 @@ int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 // round, as registers have room for (the angles' frequencies are set up once a warp).
 int qknorm_ctas(long long tokens) {
   const long long want = (tokens + kWarps - 1) / kWarps;
-  return (int)(want < 4 * kSmCount ? want : 4 * kSmCount);
+  return (int)(want < kPerSm * kSmCount ? want : kPerSm * kSmCount);
 }
 
 template <typename T, bool BWD>
