@@ -237,12 +237,13 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x & (HALF - 1), lane = tid & 31, w = tid >> 5, q4 = lane & 3;
   const bool helper = threadIdx.x >= HALF;
-  const long long at = blockIdx.x / slices;
-  const int slice = (int)(blockIdx.x - at * slices), rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv);
-  const int b = by_length(p, rank);
+  const long long part = blockIdx.x / slices, at = part / p.nseg;
+  const int slice = (int)(blockIdx.x - part * slices), seg = (int)(part - at * p.nseg);
+  const int rank = (int)(at / p.Hv), hv = (int)(at - (long long)rank * p.Hv), b = by_length(p, rank);
   const long long bh = (long long)b * p.Hv + hv;
   const int hk = hv / (p.Hv / p.Hk);
-  const int n = delta_length(p, b), nc = (n + kChunk - 1) / kChunk;
+  const int n = delta_length(p, b), all = (n + kChunk - 1) / kChunk, c0 = seg * p.seglen;
+  const int nc = all - c0 < 0 ? 0 : all - c0 < p.seglen ? all - c0 : p.seglen, last = c0 + nc - 1;   // the segment's
   const int m0 = slice * C::width + 16 * w, cols = p.dv - m0 < 16 ? p.dv - m0 : 16;
   const unsigned swap = base + C::swaps + w * C::swap;   // the second buffer PAIRS swaps behind
   const unsigned ys = base + C::ys + w * C::Y;
@@ -256,8 +257,8 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
     const uint4* dO = p.dO + (bh * p.nc * (p.dvp / 16) + m0 / 16) * 2 * NS * 32 + lane;
     const int rows = p.dvp - slice * C::width < C::width ? p.dvp - slice * C::width : C::width;
     unsigned char* buf = smem + C::out + w * out_bytes<T>();
-    const auto load = [&](int i) {   // the i-th chunk from the end
-      const int c = nc - 1 - i;
+    const auto load = [&](int i) {   // the segment's i-th chunk from the end
+      const int c = last - i;
       const unsigned st = base + i % NST * C::bytes;
       if (KQ) {
         copy_block<2 * NI * C::row, HALF>(st, chunks + (long long)c * D::bytes, tid);
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
     };
     uint4 g[2][NS];
     const auto fetch = [&](int i) {
-      const uint4* s = dO + (long long)(nc - 1 - i) * (p.dvp / 16) * 2 * NS * 32;
+      const uint4* s = dO + (long long)(last - i) * (p.dvp / 16) * 2 * NS * 32;
 #pragma unroll
       for (int e = 0; e < 2 * NS; ++e) g[e / NS][e % NS] = s[32 * e];
     };
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
       if (i + 1 < nc) load(i + 1);
       copy_commit();
       if (i + 2 < nc) {   // as in the forward walk
-        const long long c = nc - 3 - i;
+        const long long c = last - 2 - i;
         to_l2<D::bytes - D::coef, HALF>(chunks + c * D::bytes + D::coef, D::bytes - D::coef, tid);
         to_l2<C::width * kChunk * 4, HALF>(Zs + c * p.dvp * kChunk, rows * kChunk * 4, tid);
         if constexpr (KQ) {
@@ -315,10 +316,10 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
         if (i + 1 < nc) fetch(i + 1);
       }
       if (i == 0 || cols <= 0) continue;
-      const int j = i - 1, c = nc - 1 - j;
+      const int j = i - 1, c = last - j;
       const unsigned st = base + j % NST * C::bytes, x = swap + (j & 1) * PAIRS * C::swap;
       if constexpr (!KQ) {
-        if (j == 0 || c % PER == PER - 1)
+        if (c == all - 1 || c % PER == PER - 1)
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks) {
             unsigned a[4];
@@ -340,18 +341,19 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
       const int t = c * kChunk + lane;
       store_rows(buf, y, lane, cols, p.dv_wide, t < n ? const_cast<T*>(xv.at(t)) : nullptr);
     }
-    if (cols > 0) zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, lane);
+    if (cols > 0 && seg == 0) zero_rows<T>(p, p.dv_out, n, b, hv, m0, cols, p.dv_wide, lane);
     return;
   }
-  float s[DK / 8][4] = {};   // dS^T
+  float s[DK / 8][4];   // dS^T
+  load_state<DK>(p, seg < p.nseg - 1 ? p.starts : nullptr, bh * p.nseg + seg, m0, cols, lane, s);
   for (int i = 0; i <= nc; ++i) {
     __syncthreads();
     if (i == nc || cols <= 0) continue;
     const unsigned st = base + i % NST * C::bytes, x = swap + (i & 1) * PAIRS * C::swap;
     const float* coef = reinterpret_cast<const float*>(smem + i % NST * C::bytes + C::coef);
     if constexpr (KQ) {
-      const int c = nc - 1 - i;
-      if (i == 0 || c % PER == PER - 1)
+      const int c = last - i;
+      if (c == all - 1 || c % PER == PER - 1)
         store_blocks<DK / 8>(static_cast<T*>(p.dstates) + ((bh * p.nc64 + c / PER) * p.dvp + m0) * DK, s, lane);
     }
     // X^T
@@ -400,7 +402,142 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
 #pragma unroll
     for (int e = 0; e < 2 * NS; ++e) put_a(x + C::X + e * 512, a[e / NS][e % NS], lane);
   }
-  if (p.dh0 && cols > 0) keep_state<DK>(p, p.dh0, bh, m0, cols, lane, s);
+  if (p.dh0 && cols > 0 && seg == 0) keep_state<DK>(p, p.dh0, bh, m0, cols, lane, s);
+}
+
+// Segments as in the forward walk, from their ends: dS = M dS' + N with the
+// transpose of that one's M, N the walk back from zeros: 2 x 24337 x 12 x 64, in
+// one piece 992 us, in segments 373: N and M 171, the chain 23, the walks 179.
+// CTAs for 8 x 16 columns of [N | M] of a segment; past dk = 64 one an SM, as the
+// columns of dS take half of 128 registers.
+template <int DK>
+struct BackMove {
+  static constexpr int row = kChunk * DK * 2;
+  static constexpr int q = 0, k = row, coef = 2 * row, W = coef + kCoefs * 4, bytes = W + 2 * row, stages = 3;
+  static constexpr int smem = stages * bytes;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kMoveThreads, DK == 64 ? 2 : 1) delta_back_move_kernel(const DeltaP p, int groups) {
+  typedef __nv_bfloat16 T;
+  typedef BackMove<DK> C;
+  typedef ChunkData<T, DK, true, false> D;
+  constexpr int NST = C::stages, NS = 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const unsigned base = shared_at(smem);
+  const int tid = threadIdx.x, lane = tid & 31, q4 = lane & 3;
+  const long long part = blockIdx.x / groups, bh = part / (p.nseg - 1);
+  const int group = (int)(blockIdx.x - part * groups), seg = 1 + (int)(part - bh * (p.nseg - 1));
+  const int b = (int)(bh / p.Hv), hv = (int)(bh - (long long)b * p.Hv), hk = hv / (p.Hv / p.Hk);
+  const int n = delta_length(p, b), all = (n + kChunk - 1) / kChunk, c0 = seg * p.seglen;
+  const int nc = all - c0 < 0 ? 0 : all - c0 < p.seglen ? all - c0 : p.seglen, last = c0 + nc - 1;
+  const int m0 = 16 * (group * 8 + (tid >> 5));        // the warp's first column of [N | M]
+  const bool move = m0 >= p.dvp;                       // of M
+  const bool mine = move ? seg < p.nseg - 1 && m0 - p.dvp < p.dk : true;
+  const Rows<T> xq = rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n);
+  const Rows<T> xk = rows_of<T>(p, p.k, p.k_ld, (long long)hk * p.dk, b, n);
+  const char* chunks = p.chunks + bh * p.nc * D::bytes;
+  const float4* Z = reinterpret_cast<const float4*>(p.U) + ((bh * p.nc + last) * p.dvp + m0) * (kChunk / 4) + lane;
+  const uint4* dO = p.dO + ((bh * p.nc + last) * (p.dvp / 16) + m0 / 16) * 2 * NS * 32 + lane;
+  float s[DK / 8][4];
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s[j][e] = move && 8 * j + 2 * q4 + (e & 1) == m0 - p.dvp + (lane >> 2) + 8 * (e >> 1) ? 1.f : 0.f;
+  const auto load = [&](int i) {   // the i-th from the end
+    const int c = last - i;
+    const unsigned st = base + i % NST * C::bytes;
+    load_tile<DK, kChunk, kMoveThreads>(st + C::q, 0, xq, c * kChunk, n, p.dk, p.q_wide, tid);
+    load_tile<DK, kChunk, kMoveThreads>(st + C::k, 0, xk, c * kChunk, n, p.dk, p.k_wide, tid);
+    copy_block<D::Tm - D::coef, kMoveThreads>(st + C::coef, chunks + (long long)c * D::bytes + D::coef, tid);
+  };
+  wait_prior();
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) {
+    if (i < nc) load(i);
+    copy_commit();
+  }
+  const bool given = mine && !move;
+  float4 next[4] = {};
+  if (given && nc > 0)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) next[e] = Z[32 * e];
+  for (int i = 0; i < nc; ++i) {
+    copy_wait<NST - 2>();
+    __syncthreads();
+    if (i + NST - 1 < nc) load(i + NST - 1);
+    copy_commit();
+    if (!mine) continue;
+    const unsigned st = base + i % NST * C::bytes;
+    const float* coef = reinterpret_cast<const float*>(smem + i % NST * C::bytes + C::coef);
+    uint4 g[2][NS] = {};
+    if (given)
+#pragma unroll
+      for (int e = 0; e < 2 * NS; ++e) g[e / NS][e % NS] = dO[32 * e];
+    dO -= (p.dvp / 16) * 2 * NS * 32;
+    // X^T
+    float x[4][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      unsigned a[NS][4];
+      to_a<NS>(s[2 * ks], s[2 * ks + 1], a);
+#pragma unroll
+      for (int np = 0; np < 2; ++np)
+        mma_tile<NS, 1, false>(x[2 * np], x[2 * np + 1], a, st + C::k + at_b_rows_n<DK>(16 * np, 16 * ks, lane), 0);
+    }
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      const float2 l = *reinterpret_cast<const float2*>(coef + kChunk + 8 * nb + 2 * q4);
+      x[nb][0] = fmaf(l.x, x[nb][0], next[nb].x);
+      x[nb][1] = fmaf(l.y, x[nb][1], next[nb].y);
+      x[nb][2] = fmaf(l.x, x[nb][2], next[nb].z);
+      x[nb][3] = fmaf(l.y, x[nb][3], next[nb].w);
+    }
+    if (given && i + 1 < nc) {
+      Z -= p.dvp * (kChunk / 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) next[e] = Z[32 * e];
+    }
+    // dS^T
+    scale_by(s, coef[2 * kChunk]);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      unsigned a[NS][4];
+      to_a<NS>(x[2 * ks], x[2 * ks + 1], a);
+#pragma unroll
+      for (int nn = 0; nn < DK / 16; ++nn)
+        mma_tile<NS, NS, true>(s[2 * nn], s[2 * nn + 1], a, st + C::W + at_b_rows_k<DK, true>(16 * ks, 16 * nn, lane), C::row);
+    }
+    if (given) {   // dO's part added as a whole, as above: the same bits
+      unsigned a[2][NS][4];
+#pragma unroll
+      for (int e = 0; e < 2 * NS; ++e) {
+        const uint4 v = g[e / NS][e % NS];
+        unsigned(&d)[4] = a[e / NS][e % NS];
+        d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+      }
+#pragma unroll
+      for (int nn = 0; nn < DK / 16; ++nn) {
+        float y[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          mma_tile<NS, 1, true>(y[0], y[1], a[ks], st + C::q + at_b_rows_k<DK>(16 * ks, 16 * nn, lane), 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[2 * nn + (e >> 2)][e & 3] += y[e >> 2][e & 3];
+      }
+    }
+  }
+  copy_wait<0>();
+  if (!mine) return;
+  const int width = p.dvp + p.dk, cols = width - m0 < 16 ? width - m0 : 16;
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kx = 8 * j + 2 * q4 + (e & 1), col = (lane >> 2) + 8 * (e >> 1);
+      if (kx < p.dk && col < cols) p.moves[((bh * p.nseg + seg) * p.dk + kx) * width + m0 + col] = s[j][e];
+    }
 }
 
 // ------------------------------------------------------------- all other gradients
@@ -904,13 +1041,24 @@ cudaError_t run_team(const DeltaP& p, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
   const int slices = (p.dv + C::width - 1) / C::width;
-  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * slices)), dim3(2 * C::half), (size_t)C::smem, s,
-                          p, slices);
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.nseg * slices)), dim3(2 * C::half),
+                          (size_t)C::smem, s, p, slices);
 }
 // Helpers where the forward walk has them.
 template <int DK>
 cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
   if (crowded(p)) return run_alone<__nv_bfloat16, DK>(p, s);
+  if (p.nseg > 1) {
+    const auto move = delta_back_move_kernel<DK>;
+    cudaError_t e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, BackMove<DK>::smem);
+    if (e != cudaSuccess) return e;
+    const int groups = (p.dvp + p.dk + 127) / 128;
+    e = launch_dependent(move, dim3((unsigned)((long long)p.B * p.Hv * (p.nseg - 1) * groups)), dim3(kMoveThreads),
+                         (size_t)BackMove<DK>::smem, s, p, groups);
+    if (e != cudaSuccess) return e;
+    e = run_starts<true>(p, s);
+    if (e != cudaSuccess) return e;
+  }
   return few(p) ? run_team<__nv_bfloat16, DK, 2>(p, s) : run_team<__nv_bfloat16, DK, 4>(p, s);
 }
 template <int DK>

@@ -241,5 +241,87 @@ __device__ __forceinline__ void scale_by(float (&x)[N][4], float f) {
   }
 }
 
+// ------------------------------------------------------------------- segments
+//
+// The states before the segments (BACK: dS after them), given what each makes of
+// one: a CTA for 16 columns of a head, a thread for four of them and every 64th
+// row, S' = M S + N in fp32.  The next segment's M is copied to shared memory
+// meanwhile (24 us at 2 x 24337 x 12 x 64; read from L2 as it was used 43).
+constexpr int starts_row(int dk) { return dk + 4; }   // floats of a row of M there: rows 64 apart in different banks
+inline int starts_smem(int dk) { return 2 * dk * starts_row(dk) * 4; }
+
+template <bool BACK>
+__global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float4 sh[LION_DELTA_MAX_D][4];
+  const int tiles = p.dvp / 16, width = p.dvp + p.dk, ld = starts_row(p.dk);
+  const long long bh = blockIdx.x / tiles;
+  const int c4 = threadIdx.x & 3, col = 16 * (int)(blockIdx.x - bh * tiles) + 4 * c4, row = threadIdx.x >> 2;
+  const float* moves = p.moves + bh * p.nseg * p.dk * width;
+  float* Ms = reinterpret_cast<float*>(smem);
+  const auto load = [&](int i) {   // the i-th in order
+    const float* m = moves + (long long)(BACK ? p.nseg - 1 - i : i) * p.dk * width + p.dvp;
+    for (int j = threadIdx.x; j < p.dk * (p.dk / 4); j += 256) {
+      const int r = j / (p.dk / 4), u = j - r * (p.dk / 4);
+      copy16(shared_at(Ms + ((i & 1) * p.dk + r) * ld + 4 * u), m + (long long)r * width + 4 * u, true);
+    }
+  };
+  wait_prior();
+  for (int at = 0; at < p.nseg - 1; ++at) {
+    const int seg = BACK ? p.nseg - 1 - at : at, next = BACK ? seg - 1 : seg + 1;
+    if (at + 1 < p.nseg - 1) load(at + 1);
+    copy_commit();
+    const float* n = moves + (long long)seg * p.dk * width + col;
+    float4 x[LION_DELTA_MAX_D / 64];
+#pragma unroll
+    for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i)
+      if (row + 64 * i < p.dk) x[i] = *reinterpret_cast<const float4*>(n + (long long)(row + 64 * i) * width);
+    copy_wait<1>();
+    __syncthreads();   // M is there, and S of the threads' before
+    if (at > 0) {
+#pragma unroll
+      for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i) {
+        if (row + 64 * i >= p.dk) continue;
+        const float* m = Ms + ((at & 1) * p.dk + row + 64 * i) * ld;
+#pragma unroll 2
+        for (int k = 0; k < p.dk; k += 4) {
+          const float4 a4 = *reinterpret_cast<const float4*>(m + k);
+          const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 y = sh[k + e][c4];
+            x[i].x = fmaf(a[e], y.x, x[i].x);
+            x[i].y = fmaf(a[e], y.y, x[i].y);
+            x[i].z = fmaf(a[e], y.z, x[i].z);
+            x[i].w = fmaf(a[e], y.w, x[i].w);
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i) {
+      const int r = row + 64 * i;
+      if (r >= p.dk) continue;
+      sh[r][c4] = x[i];
+      if (col < p.dv)
+        *reinterpret_cast<float4*>(p.starts + ((bh * p.nseg + next) * p.dk + r) * p.dv + col) = x[i];
+    }
+  }
+  copy_wait<0>();
+}
+
+template <bool BACK>
+cudaError_t run_starts(const DeltaP& p, cudaStream_t s) {
+  const auto kern = delta_starts_kernel<BACK>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, starts_smem(LION_DELTA_MAX_D));
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * (p.dvp / 16))), dim3(256),
+                          (size_t)starts_smem(p.dk), s, p);
+}
+
+constexpr int kMoveThreads = 256;   // of the segments' walks: 8 x 16 columns of [N | M]
+
 }  // namespace
 }  // namespace lion

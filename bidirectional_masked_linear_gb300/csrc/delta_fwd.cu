@@ -592,11 +592,8 @@ __global__ void __launch_bounds__(64 * PAIRS, DK == 64 && sizeof(T) == 2 ? 2 : 1
 // 2 x 24337 x 12 x 64, 24 heads, in one piece 896 us, in 12 segments 360: prep 93,
 // M and N 128, the chain 24, the walks 115.
 
-constexpr int kMoveThreads = 256;
-
 template <int DK>
 struct Move {
-  typedef __nv_bfloat16 T;
   static constexpr int row = kChunk * DK * 2;
   static constexpr int k = 0, coef = row, W = coef + kCoefs * 4, bytes = W + 2 * row, stages = 3, smem = stages * bytes;
 };
@@ -695,71 +692,6 @@ __global__ void __launch_bounds__(kMoveThreads, 2) delta_move_kernel(const Delta
     }
 }
 
-// The states before the segments: a CTA for 16 columns of a head, a thread for
-// four of them and every 64th row, S' = M S + N in fp32.  The next segment's M
-// is copied to shared memory meanwhile (24 us; read from L2 as it was used 43).
-constexpr int starts_row(int dk) { return dk + 4; }   // floats of a row of M there: rows 64 apart in different banks
-inline int starts_smem(int dk) { return 2 * dk * starts_row(dk) * 4; }
-
-__global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float4 sh[LION_DELTA_MAX_D][4];
-  const int tiles = p.dvp / 16, width = p.dvp + p.dk, ld = starts_row(p.dk);
-  const long long bh = blockIdx.x / tiles;
-  const int c4 = threadIdx.x & 3, col = 16 * (int)(blockIdx.x - bh * tiles) + 4 * c4, row = threadIdx.x >> 2;
-  const float* moves = p.moves + bh * p.nseg * p.dk * width;
-  float* Ms = reinterpret_cast<float*>(smem);
-  const auto load = [&](int seg) {
-    const float* m = moves + (long long)seg * p.dk * width + p.dvp;
-    for (int i = threadIdx.x; i < p.dk * (p.dk / 4); i += 256) {
-      const int r = i / (p.dk / 4), u = i - r * (p.dk / 4);
-      copy16(shared_at(Ms + ((seg & 1) * p.dk + r) * ld + 4 * u), m + (long long)r * width + 4 * u, true);
-    }
-  };
-  wait_prior();
-  for (int seg = 0; seg < p.nseg - 1; ++seg) {
-    if (seg + 1 < p.nseg - 1) load(seg + 1);
-    copy_commit();
-    const float* n = moves + (long long)seg * p.dk * width + col;
-    float4 x[LION_DELTA_MAX_D / 64];
-#pragma unroll
-    for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i)
-      if (row + 64 * i < p.dk) x[i] = *reinterpret_cast<const float4*>(n + (long long)(row + 64 * i) * width);
-    copy_wait<1>();
-    __syncthreads();   // M is there, and S of the threads' before
-    if (seg > 0) {
-#pragma unroll
-      for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i) {
-        if (row + 64 * i >= p.dk) continue;
-        const float* m = Ms + ((seg & 1) * p.dk + row + 64 * i) * ld;
-#pragma unroll 2
-        for (int k = 0; k < p.dk; k += 4) {
-          const float4 a4 = *reinterpret_cast<const float4*>(m + k);
-          const float a[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 y = sh[k + e][c4];
-            x[i].x = fmaf(a[e], y.x, x[i].x);
-            x[i].y = fmaf(a[e], y.y, x[i].y);
-            x[i].z = fmaf(a[e], y.z, x[i].z);
-            x[i].w = fmaf(a[e], y.w, x[i].w);
-          }
-        }
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i) {
-      const int r = row + 64 * i;
-      if (r >= p.dk) continue;
-      sh[r][c4] = x[i];
-      if (col < p.dv)
-        *reinterpret_cast<float4*>(p.starts + ((bh * p.nseg + seg + 1) * p.dk + r) * p.dv + col) = x[i];
-    }
-  }
-  copy_wait<0>();
-}
-
 template <typename T, int DK, bool SAVE>
 cudaError_t run_alone(const DeltaP& p, cudaStream_t s) {
   typedef Chain<T, DK, SAVE> C;
@@ -800,9 +732,7 @@ cudaError_t run_walk(const DeltaP& p, __nv_bfloat16*, cudaStream_t s) {
     const int groups = (p.dvp + p.dk + 127) / 128;
     e = launch_dependent(move, dim3(heads * (p.nseg - 1) * groups), dim3(kMoveThreads), (size_t)Move<DK>::smem, s, p, groups);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(delta_starts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, starts_smem(LION_DELTA_MAX_D));
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(delta_starts_kernel, dim3(heads * (p.dvp / 16)), dim3(256), (size_t)starts_smem(p.dk), s, p);
+    e = run_starts<false>(p, s);
     if (e != cudaSuccess) return e;
   }
   return few(p) ? run_team<__nv_bfloat16, DK, SAVE, 2>(p, s) : run_team<__nv_bfloat16, DK, SAVE, 4>(p, s);

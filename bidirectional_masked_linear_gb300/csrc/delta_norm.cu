@@ -172,10 +172,12 @@ constexpr int heads_at_once() {
 
 // A warp goes through its tokens' heads in parts, as many at a time as a lane
 // holds (evenly: 8 of them in two parts are 4 and 4); a part's values are read
-// while the part before it is worked on.  Bytes bound it, less what the angles'
-// sines and the lanes' sums take: 2 x 24337 x 12 + 12 heads of 64 in bfloat16 54 us
-// at 5.6 TB/s; 32 x 512 x 16 + 16 x 64 with rotation 33 us forward (4.1 TB/s), 51
-// back (3.9).
+// while the part before it is worked on.  2 x 24337 x 12 + 12 heads of 64 in
+// bfloat16 50 us, 5.9 TB/s, 88% of a copy's rate (five CTAs an SM 51); 32 x 512 x 16 +
+// 16 x 64 with rotation 30 us forward (4.4 TB/s), 47 back (4.3), where the issue
+// slots bound it: products of two values an instruction took 33 and 51 to that.
+// Back in float32, which then spills up to 40 bytes a thread, four CTAs an SM are
+// ahead of three (5 x 1021 x 6 + 2 x 72: 14 us against 19).
 template <typename T, int LPH, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) qknorm_kernel(const QkP q) {
   constexpr int NG = 32 / LPH, U = heads_at_once<T, BWD>();
