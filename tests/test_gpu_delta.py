@@ -540,3 +540,31 @@ def test_two_streams_at_once():
         got = [train(*x, s) for x, s in zip(sets, streams)]
         torch.cuda.synchronize()
         assert all(_equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dk,dv", ((64, 64), (40, 24)))
+def test_segments_in_a_workspace_of_the_callers(dk, dv):
+    """What a workspace held before does not matter, and gradients without the forward's `saved` are the same."""
+    B, L, Hk, Hv = 2, 1666, 1, 2
+    a, h0, dout = _inputs(B, L, Hk, Hv, dk, dv, "bf16", 17, decay=6.0)
+    dev, dout = {x: y.cuda() for x, y in a.items()}, dout.cuda()
+    how = dict(h0=h0.cuda(), lengths=torch.tensor([L, 777], dtype=torch.int32, device="cuda"))
+    f = delta.delta_fwd(**dev, **how, return_state=True, save=True)
+    g = delta.delta_bwd(dout, **dev, **how, saved=f.saved)
+    code = lion.DTYPE_BF16
+    nan = lambda n: torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+    ws = nan(delta.delta_workspace_bytes(B, L, Hk, Hv, dk, dv, code))
+    assert _equal(delta.delta_fwd(**dev, **how, return_state=True, workspace=ws)[:2], f[:2])
+    for saved in (f.saved, None):
+        ws = nan(delta.delta_bwd_workspace_bytes(B, L, Hk, Hv, dk, dv, code, saved is not None))
+        assert _equal(delta.delta_bwd(dout, **dev, **how, saved=saved, workspace=ws), g)
+    # captured and replayed on other values
+    one = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(one):
+        x = delta.delta_fwd(**dev, **how, return_state=True, save=True)
+        y = delta.delta_bwd(dout, **dev, **how, saved=x.saved)
+    dev["v"].mul_(2)
+    dout.neg_()
+    one.replay()
+    f = delta.delta_fwd(**dev, **how, return_state=True, save=True)
+    assert _equal(x[:2], f[:2]) and _equal(y, delta.delta_bwd(dout, **dev, **how, saved=f.saved))
