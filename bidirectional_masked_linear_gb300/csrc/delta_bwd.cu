@@ -639,6 +639,7 @@ __global__ void __launch_bounds__(Grad<T, DK, DV>::threads, Grad<T, DK, DV>::gro
   __shared__ float sGrown[64], sLeft[64], sBeta[64], sI[NQ][64], sW[NQ][64], sB[64], sCol[4][64], sDot[4 * NQ];
   __shared__ float sPart[PARTS][64];
   __shared__ double sCarry;
+  __shared__ bool sRoots;
   const unsigned base = shared_at(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, grp = w >> 2;
   // lower rows have more blocks left of the diagonal: a scheduler's warps take a low and a high one (float32, 3 x 1021 x
@@ -680,14 +681,17 @@ __global__ void __launch_bounds__(Grad<T, DK, DV>::threads, Grad<T, DK, DV>::gro
                              p.k_wide, tid);
   load_tile<DK, 64, THREADS>(base + G::q, G::row, rows_of<T>(p, p.q, p.q_ld, (long long)hk * p.dk, b, n), i0, n, p.dk,
                              p.q_wide, tid);
-  // decays
+  // decays; beside one above 1 each power of them is its root twice, as over 64 tokens it may be past fp32 where over 32 it
+  // is not, and what it multiplies small or 0 (for blocks with none, 16 x 4096 x 8 x 64: 258 us before this, 261 with it)
   double Gs = 0.0;
+  bool grows = false;
   if (tid < 64) {
     float beta = 0.f;
     if (i0 + tid < n) {
       const float g = to_f32(static_cast<const T*>(p.g)[token(tid) * p.g_ld + hv]);
       beta = to_f32(static_cast<const T*>(p.beta)[token(tid) * p.beta_ld + hv]);
       Gs = (g < -1000.f ? -1000.0 : (double)g) * 1.4426950408889634;
+      grows = g > 0.f;
     }
     sBeta[tid] = beta;
 #pragma unroll
@@ -697,14 +701,16 @@ __global__ void __launch_bounds__(Grad<T, DK, DV>::threads, Grad<T, DK, DV>::gro
     }
     if (tid == 31) sCarry = Gs;
   }
-  __syncthreads();
+  const bool roots = __syncthreads_or(grows);
   if (tid >= 32 && tid < 64) Gs += sCarry;
   __syncthreads();
   if (tid < 64) {
+    if (roots) Gs *= 0.5;
     const float hi = (float)Gs;
     sG[tid] = make_float2(hi, (float)(Gs - hi));
     sGrown[tid] = ex2(hi);
     if (tid == 63) sCarry = Gs;
+    if (tid == 0) sRoots = roots;
   }
   __syncthreads();
   if (tid < 64) sLeft[tid] = ex2((float)(sCarry - Gs));
@@ -762,6 +768,22 @@ __global__ void __launch_bounds__(Grad<T, DK, DV>::threads, Grad<T, DK, DV>::gro
     }
   }
   dot = warp_sum(dot);
+  if (sRoots) {   // a root once, the other below
+    dot *= sGrown[63];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 16 * rw + r + 8 * h;
+      const float grown = sGrown[row], left = sLeft[row];
+#pragma unroll
+      for (int nb = 0; nb < N; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          dq[nb][2 * h + e] *= grown;
+          f[nb][2 * h + e] *= grown;
+          W[nb][2 * h + e] *= left;
+        }
+    }
+  }
   if (lane == 0) sDot[w] = dot;
 
   // the first terms, their products with q and k, and f as dK's beginning
@@ -810,6 +832,16 @@ __global__ void __launch_bounds__(Grad<T, DK, DV>::threads, Grad<T, DK, DV>::gro
     const int np = grp + NQ * i;
     float col[4] = {0.f, 0.f, 0.f, 0.f};
     if (np <= rw) {
+      if (sRoots) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int ii = 16 * rw + r + 8 * (e >> 1 & 1), j = 16 * np + 8 * (e >> 2) + 2 * q4 + (e & 1);
+          const float2 gi = sG[ii], gj = sG[j];
+          const float d = ii >= j ? ex2((gi.x - gj.x) + (gi.y - gj.y)) : 0.f;
+          dP[i][e >> 2][e & 3] *= d;
+          dN[i][e >> 2][e & 3] *= d;
+        }
+      }
       float qk[2][4] = {}, kk[2][4] = {};
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks) {

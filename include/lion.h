@@ -753,8 +753,8 @@ size_t lion_qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d, int 
  * which uses query and key head h / (Hv / Hk), with the state S [dk][dv]:
  *   S <- e^g_t S;  S <- S + beta_t k_t (v_t - S^T k_t)^T;  out_t = scale S^T q_t
  *   q, k  [B][L][Hk][dk];  v, out  [B][L][Hv][dv];  g, beta  [B][L][Hv] (in
- *   dtype, g the decay's logarithm, -infinity for one of 0; the product of 32
- *   adjacent tokens' decays has to be finite in float32).
+ *   dtype, g the decay's logarithm, -infinity for one of 0; the product of up to
+ *   32 adjacent tokens' decays has to be finite in float32).
  *   h0, h_out  [B][Hv][dk][dv] float32 or NULL: the state before the first
  *   token (NULL: zeros) and after the last one.  h_out may not be h0.
  *   Values of the tokens that a sequence has are finite: others reach all

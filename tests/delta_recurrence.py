@@ -5,7 +5,8 @@ import torch
 
 
 def recurrence(q, k, v, g, beta, scale, h0=None, lengths=None, reverse=False, dout=None):
-    """``out``, ``h`` and, with dout, every gradient, on the inputs' device."""
+    """``out``, ``h`` and, with dout, every gradient, on the inputs' device; and what they are made of, token by token in
+    the order of the walk: ``walk`` = (states before each token and after the last, R, dR, the states' gradients)."""
     B, L, Hk, dk = q.shape
     Hv, dv = v.shape[2:]
     group, dev = Hv // Hk, q.device
@@ -42,6 +43,7 @@ def recurrence(q, k, v, g, beta, scale, h0=None, lengths=None, reverse=False, do
         return o
     DO = walk(dout)
     D = torch.zeros_like(S)
+    dstates = [D]
     dq, dk_, dR, dg, db = (torch.zeros_like(x) for x in (Q, K, V, b[..., 0], b[..., 0]))
     for i in range(L - 1, -1, -1):
         G, old = D + scale * Q[i][..., None] * DO[i][..., None, :], A[i] * states[i]
@@ -52,5 +54,7 @@ def recurrence(q, k, v, g, beta, scale, h0=None, lengths=None, reverse=False, do
         dS = G - K[i][..., None] * dR[i][..., None, :]
         dg[i] = (old * dS).sum((-1, -2))
         D = A[i] * dS
+        dstates.append(D)
+    o["walk"] = states, R, dR, dstates[::-1]
     o.update(dq=back(dq, group), dk=back(dk_, group), dv=back(dR), dg=back(dg), dbeta=back(db), dh0=D)
     return o
