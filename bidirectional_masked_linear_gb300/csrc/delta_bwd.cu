@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(kMoveThreads, DK == 64 ? 2 : 1) delta_back_mov
     load_tile<DK, kChunk, kMoveThreads>(st + C::k, 0, xk, c * kChunk, n, p.dk, p.k_wide, tid);
     copy_block<D::Tm - D::coef, kMoveThreads>(st + C::coef, chunks + (long long)c * D::bytes + D::coef, tid);
   };
+  Raised raised;
   wait_prior();
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) {
@@ -527,9 +528,11 @@ __global__ void __launch_bounds__(kMoveThreads, DK == 64 ? 2 : 1) delta_back_mov
         for (int e = 0; e < 8; ++e) s[2 * nn + (e >> 2)][e & 3] += y[e >> 2][e & 3];
       }
     }
+    if (move) raised.after(s, coef[2 * kChunk]);
   }
   copy_wait<0>();
   if (!mine) return;
+  if (m0 == p.dvp && lane == 0) p.raised[bh * p.nseg + seg] = raised.by;
   const int width = p.dvp + p.dk, cols = width - m0 < 16 ? width - m0 : 16;
 #pragma unroll
   for (int j = 0; j < DK / 8; ++j)

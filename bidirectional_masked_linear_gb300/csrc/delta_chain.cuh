@@ -242,7 +242,25 @@ __device__ __forceinline__ void scale_by(float (&x)[N][4], float f) {
 }
 
 // ------------------------------------------------------------------- segments
-//
+
+// A segment's M is a product over hundreds of tokens, which decays above 1 may take past fp32 although the state that it
+// multiplies is small there, or 0.  So a walk of M takes powers of two out of it that hold it to the 1 it starts from
+// (no more than one chunk's decays may then take it past fp32), and puts them back as decays below 1 follow.  Where
+// decays' products stay below 1 there are none.
+struct Raised {
+  float log2 = 0.f;   // of the decays' product
+  int by = 0;
+  template <int N>
+  __device__ __forceinline__ void after(float (&s)[N][4], float decay) {
+    log2 += __log2f(decay);
+    if (log2 > (float)by || (by > 0 && log2 < (float)(by - 32))) {
+      const int want = log2 > 0.f ? (int)log2 + 1 : 0, to = want < by - 64 ? by - 64 : want;
+      scale_by(s, ldexpf(1.f, by - to));
+      by = to;
+    }
+  }
+};
+
 // The states before the segments (BACK: dS after them), given what each makes of
 // one: a CTA for 16 columns of a head, a thread for four of them and every 64th
 // row, S' = M S + N in fp32.  The next segment's M is copied to shared memory
@@ -267,6 +285,7 @@ __global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
     }
   };
   wait_prior();
+  int raised = 0;   // of this segment's M; the first one's is not needed
   for (int at = 0; at < p.nseg - 1; ++at) {
     const int seg = BACK ? p.nseg - 1 - at : at, next = BACK ? seg - 1 : seg + 1;
     if (at + 1 < p.nseg - 1) load(at + 1);
@@ -276,12 +295,15 @@ __global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
 #pragma unroll
     for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i)
       if (row + 64 * i < p.dk) x[i] = *reinterpret_cast<const float4*>(n + (long long)(row + 64 * i) * width);
+    const int raised_next = at + 1 < p.nseg - 1 ? p.raised[bh * p.nseg + next] : 0;
     copy_wait<1>();
     __syncthreads();   // M is there, and S of the threads' before
     if (at > 0) {
 #pragma unroll
       for (int i = 0; i < LION_DELTA_MAX_D / 64; ++i) {
         if (row + 64 * i >= p.dk) continue;
+        const float4 given = x[i];
+        if (raised) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         const float* m = Ms + ((at & 1) * p.dk + row + 64 * i) * ld;
 #pragma unroll 2
         for (int k = 0; k < p.dk; k += 4) {
@@ -296,6 +318,9 @@ __global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
             x[i].w = fmaf(a[e], y.w, x[i].w);
           }
         }
+        if (raised)
+          x[i] = make_float4(given.x + ldexpf(x[i].x, raised), given.y + ldexpf(x[i].y, raised),
+                             given.z + ldexpf(x[i].z, raised), given.w + ldexpf(x[i].w, raised));
       }
     }
     __syncthreads();
@@ -307,6 +332,7 @@ __global__ void __launch_bounds__(256) delta_starts_kernel(const DeltaP p) {
       if (col < p.dv)
         *reinterpret_cast<float4*>(p.starts + ((bh * p.nseg + next) * p.dk + r) * p.dv + col) = x[i];
     }
+    raised = raised_next;
   }
   copy_wait<0>();
 }

@@ -51,6 +51,7 @@ struct DeltaP {
   int B, L, Hk, Hv, dk, dv, dvp, nc, nc64, slices;   // dvp: dv up to whole warps' 16
   int nseg, seglen;        // the forward walk's segments, of seglen chunks
   float *moves, *starts;   // per head and segment: what it makes of a state, [dk][dvp + dk]; the state before it, [dk][dv]
+  int* raised;             // per head and segment: M is 2^raised times what moves holds of it
   float scale;
   int reverse;
   int q_wide, k_wide, v_wide, o_wide, do_wide, dv_wide;

@@ -633,6 +633,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) delta_move_kernel(const Delta
     load_tile<DK, kChunk, kMoveThreads>(st + C::k, 0, xk, (c0 + c) * kChunk, n, p.dk, p.k_wide, tid);
     copy_block<D::Tm - D::coef, kMoveThreads>(st + C::coef, chunks + (long long)c * D::bytes + D::coef, tid);
   };
+  Raised raised;
   wait_prior();
 #pragma unroll
   for (int c = 0; c < NST - 1; ++c) {
@@ -679,9 +680,11 @@ __global__ void __launch_bounds__(kMoveThreads, 2) delta_move_kernel(const Delta
       for (int nn = 0; nn < DK / 16; ++nn)
         mma_tile<NS, 1, true>(s[2 * nn], s[2 * nn + 1], a, st + C::k + at_b_rows_k<DK>(16 * ks, 16 * nn, lane), 0);
     }
+    if (move) raised.after(s, coef[2 * kChunk]);
   }
   copy_wait<0>();
   if (!mine) return;
+  if (m0 == p.dvp && lane == 0) p.raised[bh * p.nseg + seg] = raised.by;
   const int width = p.dvp + p.dk, cols = width - m0 < 16 ? width - m0 : 16;
 #pragma unroll
   for (int j = 0; j < DK / 8; ++j)

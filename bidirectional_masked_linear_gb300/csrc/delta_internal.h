@@ -13,7 +13,7 @@ namespace lion {
 // walk is cut into segments what they make of a state and the states before them.
 struct DeltaLayout {
   size_t R, states, bytes;        // offsets of R and the states, and all of it
-  size_t moves, starts, beside;   // the same of U's neighbours
+  size_t moves, starts, raised, beside;   // the same of U's neighbours
   int nc, nc64, dvp, nseg, seglen;
 };
 template <typename T, int DK, bool SAVE>
@@ -43,7 +43,8 @@ inline DeltaLayout delta_layout(int B, int L, int Hv, int dk, int dv, int dtype,
   const size_t cut = l.nseg > 1 ? heads * l.nseg * dk * sizeof(float) : 0;
   l.moves = up(heads * l.nc * l.dvp * kChunk * sizeof(float));
   l.starts = l.moves + up(cut * (l.dvp + dk));
-  l.beside = l.starts + up(cut * dv);
+  l.raised = l.starts + up(cut * dv);
+  l.beside = l.raised + (l.nseg > 1 ? up(heads * l.nseg * sizeof(int)) : 0);
   l.R = up(heads * l.nc * chunk);
   l.states = l.R + (save ? up(heads * l.nc * kChunk * l.dvp * es) : 0);
   l.bytes = l.states + (save ? up(heads * l.nc64 * l.dvp * DK * es) : 0);
@@ -66,6 +67,7 @@ DeltaP delta_params(const Args& a, char* kept, char* beside, bool save) {
   p.U = reinterpret_cast<float*>(beside);
   p.moves = reinterpret_cast<float*>(beside + l.moves);
   p.starts = reinterpret_cast<float*>(beside + l.starts);
+  p.raised = reinterpret_cast<int*>(beside + l.raised);
   p.nseg = l.nseg;
   p.seglen = l.seglen;
   if (save) {

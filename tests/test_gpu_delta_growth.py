@@ -94,3 +94,9 @@ def test_growth_inside_a_block(dk, dv, up, reverse, dtype):
     _grown(150, dk, dv, dtype, up, (), reverse)
 
 
+# Three segments of 18 chunks, 576 tokens: all growths are in the second one.
+@pytest.mark.parametrize("reverse", (False, True))
+@pytest.mark.parametrize("down", ((), (900, 1000)))
+@pytest.mark.parametrize("dk,dv", ((64, 64), (128, 72)))
+def test_growth_inside_a_segment(dk, dv, down, reverse):
+    _grown(1700, dk, dv, "bf16", (700, 800), down, reverse)
