@@ -1,5 +1,7 @@
 // delta_api.cu -- the C ABI of the delta rule's operators declared in
 // include/lion.h: argument checks, workspaces and the launches.
+#include <initializer_list>
+
 #include "api_check.h"
 #include "lion_internal.h"
 
@@ -8,6 +10,13 @@ namespace {
 using namespace lion::api;
 
 constexpr long long kMaxWidth = LION_SSM_MAX_EXTENT;   // of a token's heads
+
+// Whether a result's memory begins where none of these do: what other CTAs still read, or write as well.
+bool apart(const void* out, std::initializer_list<const void*> others) {
+  for (const void* x : others)
+    if (out == x) return false;
+  return true;
+}
 
 // d, rot, Hq and Hk as lion_qknorm_args has them.
 lion_status qknorm_sizes(int B, int L, int Hq, int Hk, int d, int rot, int norm, int interleaved, float eps,
@@ -70,7 +79,8 @@ lion_status lion_qknorm_fwd(const lion_qknorm_args* a) {
   if (st == LION_ERR_INVALID_ARG) return st;
   const Pointers ptr;
   const size_t es = esize(a->dtype);
-  if (!ptr.need(a->q_out, es) || !ptr.need(a->k_out, es) || a->q_out == a->q || a->k_out == a->k)   // lines on their way
+  if (!ptr.need(a->q_out, es) || !ptr.need(a->k_out, es) || !apart(a->q_out, {a->q, a->k, a->k_out}) ||
+      !apart(a->k_out, {a->q, a->k}))   // heads of a token that are still to be read
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_qknorm_fwd(*a, a->stream));
@@ -88,7 +98,7 @@ lion_status lion_qknorm_bwd(const lion_qknorm_bwd_args* a) {
   const Pointers ptr;
   const size_t es = esize(a->dtype);
   if (!ptr.need(a->dq_out, es) || !ptr.need(a->dk_out, es) || !ptr.need(a->dq, es) || !ptr.need(a->dk, es) ||
-      a->dq == a->q || a->dk == a->k || a->dq == a->dq_out || a->dk == a->dk_out ||
+      !apart(a->dq, {a->q, a->k, a->dq_out, a->dk_out, a->dk}) || !apart(a->dk, {a->q, a->k, a->dq_out, a->dk_out}) ||
       !ptr.maybe(a->dq_weight, 4) || !ptr.maybe(a->dk_weight, 4) || (a->dq_weight && !a->q_weight) ||
       (a->dk_weight && !a->k_weight))
     return LION_ERR_INVALID_ARG;
@@ -115,7 +125,7 @@ lion_status lion_delta_fwd(const lion_delta_args* a) {
   if (st == LION_ERR_INVALID_ARG) return st;
   const Pointers ptr;
   if (!ptr.need(a->out, esize(a->dtype)) || !ptr.maybe(a->h_out, 16) || (a->h0 && a->h_out == a->h0) ||
-      a->out == a->q || a->out == a->k || a->out == a->v)
+      !apart(a->out, {a->q, a->k, a->v}))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(a->workspace, a->workspace_bytes,
@@ -135,8 +145,10 @@ lion_status lion_delta_bwd(const lion_delta_bwd_args* a) {
   const Pointers ptr;
   const size_t es = esize(a->dtype);
   if (!ptr.need(a->dout, es) || !ptr.need(a->dq, es) || !ptr.need(a->dk_out, es) || !ptr.need(a->dv_out, es) ||
-      !ptr.need(a->dg, es) || !ptr.need(a->dbeta, es) || !ptr.maybe(a->dh0, 16) || a->dv_out == a->dout ||
-      a->dq == a->q || a->dk_out == a->k || a->dg == a->g || a->dbeta == a->beta)   // other CTAs still read these
+      !ptr.need(a->dg, es) || !ptr.need(a->dbeta, es) || !ptr.maybe(a->dh0, 16) ||
+      !apart(a->dv_out, {a->dout, a->q, a->k, a->dq, a->dk_out}) ||   // dR, read with these by the last launch but one
+      !apart(a->dq, {a->dout, a->q, a->k, a->dk_out}) || !apart(a->dk_out, {a->dout, a->q, a->k}) ||
+      !apart(a->dg, {a->g, a->beta, a->dbeta}) || !apart(a->dbeta, {a->g, a->beta}))
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return with_workspace(
@@ -152,7 +164,8 @@ lion_status lion_delta_step(const lion_delta_step_args* a) {
   const Pointers ptr;
   const size_t es = esize(a->dtype);
   if (!ptr.need(a->h, 16) || !ptr.need(a->q, es) || !ptr.need(a->k, es) || !ptr.need(a->v, es) ||
-      !ptr.need(a->g, es) || !ptr.need(a->beta, es) || !ptr.need(a->out, es))
+      !ptr.need(a->g, es) || !ptr.need(a->beta, es) || !ptr.need(a->out, es) ||
+      !apart(a->out, {a->q, a->k, a->g, a->beta}))   // a CTA writes 32 columns, each reads all of q and k
     return LION_ERR_INVALID_ARG;
   if (st != LION_OK) return st;
   return from_cuda(lion::launch_delta_step(*a, a->stream));

@@ -670,7 +670,9 @@ lion_status lion_scan_step(const lion_scan_step_args* a);
  * norms of queries and keys that it needs.  The conventions are those of the
  * state space block above; heads are adjacent within a token ([B][L][H][d]),
  * a field `*_token` is the distance between tokens.  Head sizes d, dk and dv
- * are multiples of 8 (else LION_ERR_UNSUPPORTED).
+ * are multiples of 8 (else LION_ERR_UNSUPPORTED).  A result that begins where
+ * an input or another result does is LION_ERR_INVALID_ARG where that would be
+ * read, or written, by others still.
  */
 
 /* What a head is divided by: its length, or the root of its mean square. */
