@@ -184,9 +184,17 @@ def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm="l2", ep
     return QKNormGrads(dq, dk, dwq, dwk)
 
 
+def _no_gradient(ctx, **of):
+    """Raises if a gradient is wanted for one of these inputs (by their index), which have none here."""
+    for name, i in of.items():
+        if any(ctx.needs_input_grad[i:i + 1]):   # as many as the call had arguments
+            raise RuntimeError(f"{name} has no gradient here: pass it detached")
+
+
 class QKNorm(torch.autograd.Function):
     """The norms and rotation as a differentiable op: ``apply(q, k, q_weight,
-    k_weight, norm, eps, freqs, positions, interleaved)`` gives ``(q_out, k_out)``."""
+    k_weight, norm, eps, freqs, positions, interleaved)`` gives ``(q_out,
+    k_out)``.  ``freqs`` has no gradient: backward raises if it wants one."""
 
     @staticmethod
     def forward(ctx, q, k, q_weight=None, k_weight=None, norm="l2", eps=1e-6, freqs=None, positions=None,
@@ -198,6 +206,7 @@ class QKNorm(torch.autograd.Function):
     @staticmethod
     @_first_only
     def backward(ctx, dq_out, dk_out):
+        _no_gradient(ctx, eps=5, freqs=6)
         q, k, q_weight, k_weight, freqs, positions = ctx.saved_tensors
         norm, eps, interleaved = ctx.how
         g = qknorm_bwd(dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight, norm, eps, freqs, positions,
@@ -318,7 +327,8 @@ def delta_step(h, q, k, v, g, beta, scale=None, out=None, stream=None):
 
 class GatedDelta(torch.autograd.Function):
     """The gated delta rule as a differentiable op: ``apply(q, k, v, g, beta,
-    scale, h0, lengths, reverse)`` gives ``out``."""
+    scale, h0, lengths, reverse)`` gives ``out``.  ``scale`` has no gradient:
+    backward raises if it wants one."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, scale=None, h0=None, lengths=None, reverse=False):
@@ -330,6 +340,7 @@ class GatedDelta(torch.autograd.Function):
     @staticmethod
     @_first_only
     def backward(ctx, dout):
+        _no_gradient(ctx, scale=5)
         q, k, v, g, beta, h0, lengths, saved = ctx.saved_tensors
         scale, reverse = ctx.how
         r = delta_bwd(dout.contiguous(), q, k, v, g, beta, scale, h0, lengths, reverse, saved)
