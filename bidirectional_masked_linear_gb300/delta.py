@@ -332,7 +332,7 @@ class GatedDelta(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, scale=None, h0=None, lengths=None, reverse=False):
-        f = delta_fwd(q, k, v, g, beta, scale, h0, lengths, reverse, save=True)
+        f = delta_fwd(q, k, v, g, beta, scale, h0, lengths, reverse, save=any(ctx.needs_input_grad))
         ctx.save_for_backward(q, k, v, g, beta, h0, lengths, f.saved)
         ctx.how = scale, reverse
         return f.out

@@ -33,3 +33,13 @@ def test_a_gradient_that_there_is_none_of_raises(calls):
     q.grad = None
     delta.GatedDelta.apply(q, *rest, scale.detach()).sum().backward()
     assert torch.equal(q.grad, torch.full((3,), 2.0))
+
+
+def test_nothing_is_kept_where_no_gradient_is_wanted(calls):
+    """What the forward keeps is twice its inputs and more: 408 MB beside 201 at 16 x 4096 x 8 x 64 in bfloat16."""
+    x = [torch.ones(3)] * 5
+    delta.GatedDelta.apply(*x)
+    with torch.no_grad():
+        delta.GatedDelta.apply(*(2 * torch.ones(3, requires_grad=True) for _ in x))
+    delta.GatedDelta.apply(*x[:4], torch.ones(3, requires_grad=True)).sum().backward()
+    assert [c["save"] for c in calls] == [False, False, True]
