@@ -88,14 +88,16 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const f2* v) {
 // f / (2 pi) as a fraction of a turn in units of 2^-64: the product with an
 // integer position wraps at whole turns, and 32 bits of position leave 32 of
 // the fraction exact.  1 / (2 pi) in two doubles, as the product's own error
-// and the constant's would show from positions of about 2^28 on.
+// and the constant's would show from positions of about 2^28 on, and of f's
+// magnitude, as a fraction above 0 has more bits than what it lacks to 1.
 __device__ __forceinline__ unsigned long long turn_of(float f) {
   const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
-  const double x = f, t = x * hi;
+  const double x = fabsf(f), t = x * hi;
   const double rest = fma(x, hi, -t) + x * lo;
   const double frac = t - floor(t);   // exact
-  return (unsigned long long)(frac * 18446744073709551616.0) +
-         (unsigned long long)(long long)(rest * 18446744073709551616.0);
+  const unsigned long long u = (unsigned long long)(frac * 18446744073709551616.0) +
+                               (unsigned long long)(long long)(rest * 18446744073709551616.0);
+  return f < 0.f ? 0 - u : u;
 }
 
 template <int LPH>
