@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(128) delta_back_kernel(const DeltaP p) {
 
 // The same with a helper to each warp, which has the loads, dR, what the other
 // gradients take, and dO's part of the next dS, ready when the warp has X: 1330 ns
-// a chunk of 64 columns where an SM has one CTA (16 x 4096 x 8 x 64: 171 us, 34%
-// of the tensor cores', 30% of the issue slots).
+// a chunk of 64 columns where an SM has one CTA (16 x 4096 x 8 x 64: 174 us, 33%
+// of the tensor cores', 31% of the issue slots).
 
 template <typename T, int DK, int PAIRS>
 struct BackTeam {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(64 * PAIRS) delta_back_team_kernel(const Delta
 
 // Segments as in the forward walk, from their ends: dS = M dS' + N with the
 // transpose of that one's M, N the walk back from zeros: 2 x 24337 x 12 x 64, in
-// one piece 992 us, in segments 373: N and M 171, the chain 23, the walks 179.
+// one piece 992 us, in segments 375: N and M 171, the chain 25, the walks 179.
 // CTAs for 8 x 16 columns of [N | M] of a segment; past dk = 64 one an SM, as the
 // columns of dS take half of 128 registers.
 template <int DK>
@@ -562,10 +562,10 @@ __global__ void __launch_bounds__(kMoveThreads, DK == 64 ? 2 : 1) delta_back_mov
 //
 // A warp has 16 rows and half or a quarter of the dk columns, and of A and E
 // two blocks or one of 16 columns: eight warps and two CTAs an SM in bfloat16 up
-// to dk = 64 (16 x 4096 x 8 x 64: 257 us, sixteen warps 310), else sixteen.  R,
+// to dk = 64 (16 x 4096 x 8 x 64: 261 us, sixteen warps 310), else sixteen.  R,
 // dR, S and dS' come in the inputs' type: in bfloat16 each is one rounding of
-// 2^-9, as A beta and E beta are.  Instructions bound it, 17,700 of a warp a block
-// at 48% of the issue slots, of which one in seventeen is a product: the rest
+// 2^-9, as A beta and E beta are.  Instructions bound it, 18,100 of a warp a block
+// at 49% of the issue slots, of which one in seventeen is a product: the rest
 // makes tiles, D, p and the sums of it; 24% of the tensor cores', 29% of DRAM.  A
 // third CTA an SM would leave a thread 80 registers, as many as its sums take.
 

@@ -264,7 +264,8 @@ struct Raised {
 // The states before the segments (BACK: dS after them), given what each makes of
 // one: a CTA for 16 columns of a head, a thread for four of them and every 64th
 // row, S' = M S + N in fp32.  The next segment's M is copied to shared memory
-// meanwhile (24 us at 2 x 24337 x 12 x 64; read from L2 as it was used 43).
+// meanwhile (24 us at 2 x 24337 x 12 x 64, with M's powers of two 26; read from L2
+// as it was used 43).
 constexpr int starts_row(int dk) { return dk + 4; }   // floats of a row of M there: rows 64 apart in different banks
 inline int starts_smem(int dk) { return 2 * dk * starts_row(dk) * 4; }
 

@@ -392,7 +392,10 @@ __global__ void __launch_bounds__(128) delta_chain_kernel(const DeltaP p) {
 // than SMs, 3 heads of 197 x 64 in bfloat16 7.7 us against 9.4, and in float32,
 // where six products for one keep a scheduler's tensor core busy, 3 x 1021 x 6 x
 // 40 x 72 52 us, back 49, against 77 and 83 with four pairs and 84 and 76 without
-// helpers.  Float32's longer walks than that have none.
+// helpers.  Float32's longer walks than that have none.  At the border and twice
+// past it, in bfloat16 with two and with four pairs, forward and back: 152 CTAs (1 x
+// 480 x 76 x 64) 16 and 20 us, 20 and 23; (1 x 480 x 38 x 128) 24 and 27, 29 and 35;
+// 304 CTAs (2 x 480 x 76 x 64) 22 and 21, 27 and 25; (1 x 480 x 76 x 128) 45 and 29, 56 and 36.
 
 // PAIRS: of a warp and its helper in a CTA.
 template <typename T, int DK, bool SAVE, int PAIRS>
@@ -589,8 +592,8 @@ __global__ void __launch_bounds__(64 * PAIRS, DK == 64 && sizeof(T) == 2 ? 2 : 1
 // given), M the walk of the identity with U = 0, both without outputs and all
 // segments' at once.  A second launch chains them, and the walks with outputs
 // start from there.  Three walks' work for one, so only where it finds idle SMs:
-// 2 x 24337 x 12 x 64, 24 heads, in one piece 896 us, in 12 segments 360: prep 93,
-// M and N 128, the chain 24, the walks 115.
+// 2 x 24337 x 12 x 64, 24 heads, in one piece 896 us, in 12 segments 363: prep 93,
+// M and N 130, the chain 26, the walks 115.
 
 template <int DK>
 struct Move {
@@ -598,7 +601,9 @@ struct Move {
   static constexpr int k = 0, coef = row, W = coef + kCoefs * 4, bytes = W + 2 * row, stages = 3, smem = stages * bytes;
 };
 
-// CTAs for 8 x 16 columns of [N | M] of a segment.
+// CTAs for 8 x 16 columns of [N | M] of a segment, two an SM: past dk = 64 that
+// spills 92 bytes a thread and is as fast as one that does not (1 x 8192 x 8/16 x
+// 128: 117 us against 118).
 template <int DK, bool SAVE>
 __global__ void __launch_bounds__(kMoveThreads, 2) delta_move_kernel(const DeltaP p, int groups) {
   typedef __nv_bfloat16 T;
@@ -713,10 +718,15 @@ cudaError_t run_team(const DeltaP& p, cudaStream_t s) {
   return launch_dependent(kern, dim3((unsigned)((long long)p.B * p.Hv * p.nseg * slices)), dim3(2 * C::half),
                           (size_t)C::smem, s, p, slices);
 }
-// Helpers make a chunk's walk shorter and an SM hold fewer of them: with more
-// CTAs than an SM holds of these at dk = 64, warps alone are ahead (64 x 197 x
-// 12 x 64, 768 CTAs: 47 against 52 us, back 55 against 67; 16 x 4096 x 8 x 64,
-// 128: 172 against 146).  In float32 at dk > 64 three stages do not fit.
+// Helpers make a chunk's walk shorter, and fewer CTAs fit an SM: with them two at
+// dk = 64, one back and at dk = 128; without three, at dk = 128 two, one with
+// `saved` and back.  One rule for all, helpers for up to two walks an SM; us with
+// them and alone, forward with `saved`, then back:
+//   4 x 4096 x 38 x 64, 152 walks  152 180  178 220    4 x 4096 x 19 x 128, 152  211 233  272 288
+//   4 x 4096 x 64 x 64, 256 walks  242 248  345 276    4 x 4096 x 32 x 128, 256  411 452  535 562
+//   4 x 4096 x 77 x 64, 308 walks  380 349  515 401    4 x 4096 x 39 x 128, 312  617 675  801 844
+// and at dk = 128 without `saved` 193 249, 378 359 and 568 563.  In float32 at dk
+// > 64 three stages do not fit.
 template <int DK, bool SAVE>
 cudaError_t run_walk(const DeltaP& p, float*, cudaStream_t s) {
   if constexpr (DK == 64)

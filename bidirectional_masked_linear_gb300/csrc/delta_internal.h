@@ -33,9 +33,12 @@ inline DeltaLayout delta_layout(int B, int L, int Hv, int dk, int dv, int dtype,
   l.nc = (L + kChunk - 1) / kChunk;
   l.nc64 = (L + kStateChunk - 1) / kStateChunk;
   l.dvp = (dv + 15) / 16 * 16;
-  // Segments: walks for half of the SMs' places and more are not cut, as two walks
-  // more have to be made up for; else as many as fill them, of 16 chunks at least
-  // (2 x 24337 x 12 x 64: 12 segments).
+  // Segments: as many as fill two places an SM, of 16 chunks at least, three of
+  // them at least, for walks on a quarter of the SMs or less.  A training step's
+  // kernels whole and cut, us (of 128 a head has two walks):
+  //   heads of 64, L = 24337   24: 1893 1126   38: 2165 1669   48: 2370 2157   64: 2697 3030
+  //   heads of 64, L = 4096                    38:  381  336   48:  419  426   64:  476  556
+  //   heads of 128, L = 16384  12: 1804 1223   19: 1997 1706   24: 2143 2220   32: 2372 3001
   const long long ctas = (long long)heads * ((dv + kSlice - 1) / kSlice);
   const long long most = bf16 && 4 * ctas <= kSmCount ? std::min<long long>(2 * kSmCount / ctas, l.nc / 16) : 1;
   l.seglen = most >= 3 ? (int)((l.nc + most - 1) / most) : l.nc;

@@ -176,9 +176,10 @@ constexpr int heads_at_once() {
 // holds (evenly: 8 of them in two parts are 4 and 4); a part's values are read
 // while the part before it is worked on.  2 x 24337 x 12 + 12 heads of 64 in
 // bfloat16 50 us, 5.9 TB/s, 88% of a copy's rate (five CTAs an SM 51); 32 x 512 x 16 +
-// 16 x 64 with rotation 30 us forward (4.4 TB/s), 47 back (4.3), where the issue
-// slots bound it: products of two values an instruction took 33 and 51 to that.
-// Back in float32, which then spills up to 40 bytes a thread, four CTAs an SM are
+// 16 x 64 with rotation 31 us forward (4.3 TB/s), 47 back (4.2), with 56 and 59% of
+// the issue slots at 24% of the warps: neither is full, a warp has one part ahead.
+// Products of two values an instruction took 33 and 51 to that.
+// Back in float32, which then spills up to 36 bytes a thread, four CTAs an SM are
 // ahead of three (5 x 1021 x 6 + 2 x 72: 14 us against 19).
 template <typename T, int LPH, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) qknorm_kernel(const QkP q) {

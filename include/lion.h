@@ -668,7 +668,8 @@ lion_status lion_scan_step(const lion_scan_step_args* a);
  * The gated delta rule beside them: the recurrence of LION-S's scalar decay
  * whose tokens also take out what the state holds under their key, and the
  * norms of queries and keys that it needs.  The conventions are those of the
- * state space block above; heads are adjacent within a token ([B][L][H][d]),
+ * state space block above, but for the rule's roundings (lion_delta_fwd);
+ * heads are adjacent within a token ([B][L][H][d]),
  * a field `*_token` is the distance between tokens.  Head sizes d, dk and dv
  * are multiples of 8 (else LION_ERR_UNSUPPORTED).  A result that begins where
  * an input or another result does is LION_ERR_INVALID_ARG where that would be
@@ -760,10 +761,18 @@ size_t lion_qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d, int 
  *   h0, h_out  [B][Hv][dk][dv] float32 or NULL: the state before the first
  *   token (NULL: zeros) and after the last one.  h_out may not be h0.
  *   Values of the tokens that a sequence has are finite: others reach all
- *   tokens that share their 32, earlier ones among them.
+ *   tokens that share their 32 (of the gradients 64), earlier ones among them.
  *   saved  device, 256-byte aligned, of lion_delta_saved_bytes, or NULL: what
  *   lion_delta_bwd goes on from.
  *   Keys longer than sqrt(2 / beta) make the state grow.
+ *   Products run on the tensor cores, on factors in parts of bfloat16 with
+ *   float32 sums.  With dtype BF16 a computed factor has two parts where a
+ *   state depends on it, so that h_out and dh0 are 1e-6 to 4e-6 of their norm
+ *   off and dv_out has its own rounding alone, and one part for out and the
+ *   other gradients, which so have four or five roundings of 2^-9 at most, their
+ *   own among them: 0.003 of their norm, where one is 0.0017.  The states and
+ *   what else `saved` has of tokens are bfloat16 as well.
+ *   With FP32 a factor has three parts, and results are 1e-6 to 3e-6 off.
  *   Long sequences of few heads are walked in segments, and gradients of many
  *   heads add their terms in another order than those of few; B, Hv, L, the head
  *   sizes and the type decide: results of other batches then differ by roundings.
