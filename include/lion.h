@@ -770,8 +770,10 @@ size_t lion_qknorm_bwd_workspace_bytes(int B, int L, int Hq, int Hk, int d, int 
  *   state depends on it, so that h_out and dh0 are 1e-6 to 4e-6 of their norm
  *   off and dv_out has its own rounding alone, and one part for out and the
  *   other gradients, which so have four or five roundings of 2^-9 at most, their
- *   own among them: 0.003 of their norm, where one is 0.0017.  The states and
- *   what else `saved` has of tokens are bfloat16 as well.
+ *   own among them: 0.003 of their norm, where one is 0.0017.  They are of what
+ *   the state held within the 32 tokens (64): an output near a token that takes
+ *   out a much larger value than its own shows that value's.  The states and what
+ *   else `saved` has of tokens are bfloat16 as well.
  *   With FP32 a factor has three parts, and results are 1e-6 to 3e-6 off.
  *   Long sequences of few heads are walked in segments, and gradients of many
  *   heads add their terms in another order than those of few; B, Hv, L, the head

@@ -54,14 +54,15 @@ def _sizes(a, reverse, walk):
     return {"dg": dg.sqrt(), "dbeta": db.sqrt()}
 
 
-def _grown(L, dk, dv, dtype, up, down, reverse):
-    """Two growths of e^55 at `up`, 1e-16 before the last of them, and decays as large at `down`."""
+def _grown(L, dk, dv, dtype, up, down, reverse, by=55.0):
+    """Growths of e^by at `up`, values of 1e-16 beside them, and decays as large at `down`.  Between growths of less than
+    e^55 values are of many sizes: the tokens before the first and after the last of those are compared."""
     gen = torch.Generator().manual_seed(dk + L)
     mk = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
     unit = lambda t: t / t.norm(dim=-1, keepdim=True)  # noqa: E731
     a = dict(q=unit(mk(1, L, 1, dk)), k=unit(mk(1, L, 1, dk)), v=1e-16 * mk(1, L, 1, dv),
              g=-0.001 * torch.rand(1, L, 1, generator=gen), beta=torch.sigmoid(mk(1, L, 1)))
-    a["g"][:, list(up)], a["g"][:, list(down)] = 55.0, -55.0
+    a["g"][:, list(up)], a["g"][:, list(down)] = by, -by
     dout = 1e-16 * mk(1, L, 1, dv)
     a = {x: (y.flip(1) if reverse else y).to(T[dtype]).cuda() for x, y in a.items()}
     dout, h0 = dout.to(T[dtype]).cuda(), 1e-16 * mk(1, 1, dk, dv).cuda()
@@ -70,13 +71,14 @@ def _grown(L, dk, dv, dtype, up, down, reverse):
     f = delta.delta_fwd(**a, **how, return_state=True, save=True)
     g = delta.delta_bwd(dout, **a, **how, saved=f.saved)
     cuts = [0, *up, *down, L]
+    groups = list(zip(cuts, cuts[1:])) if by == 55.0 else [(0, up[0]), (up[-1], L)]
     sizes = _sizes(a, reverse, r["walk"])
     for x in ("h", "dh0"):
         off, size = float(((f.h if x == "h" else g.dh0).double() - r[x]).norm()), float(r[x].norm())
         assert 0 < size < 1e37 and off <= 1e-4 * size, (x, off, size)
     for x, y in (("out", f.out), *((x, getattr(g, x)) for x in ("dq", "dk", "dv", "dg", "dbeta"))):
         y, want = ((t.flip(1) if reverse else t)[0].double() for t in (y, r[x]))
-        for i, j in zip(cuts, cuts[1:]):
+        for i, j in groups:
             off, size = float((y[i:j] - want[i:j]).norm()), float(want[i:j].norm())
             if dtype == "fp32":
                 limit = 1e-4 * size
@@ -100,3 +102,10 @@ def test_growth_inside_a_block(dk, dv, up, reverse, dtype):
 @pytest.mark.parametrize("dk,dv", ((64, 64), (128, 72)))
 def test_growth_inside_a_segment(dk, dv, down, reverse):
     _grown(1700, dk, dv, "bf16", (700, 800), down, reverse)
+
+
+@pytest.mark.parametrize("reverse", (False, True))
+@pytest.mark.parametrize("L,at,dtype", ((150, 34, "fp32"), (150, 34, "bf16"), (150, 70, "bf16"), (1700, 674, "bf16")))
+def test_growth_up_to_the_bound(L, at, dtype, reverse):
+    """Ten decays of e^8.5 among 32 tokens: 8e36 of the 3e38 that their product may be."""
+    _grown(L, 64, 64, dtype, range(at, at + 20, 2), (), reverse, by=8.5)
